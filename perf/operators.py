@@ -165,7 +165,7 @@ def prepare(case, seed):
     s["z"] = rnd(T, D, dtype=dt) if gated else None
     s["state"] = rnd(N, D, S, std=0.1)
     if op == "scan":
-        s["states"] = case["states"]
+        s["states"], s["chunk_rows"] = case["states"], len(_chunk_rows(cu))
     if op == "scan_backward":
         s["d_out"] = rnd(T, D, dtype=dt)
         s["d_final"] = rnd(N, D, S)
@@ -379,7 +379,9 @@ def _run_own(s):
     args = (s["u"], s["dt"], s["A"], s["B"], s["C"])
     more = dict(D=s["D"], z=s["z"], dt_bias=s["dt_bias"])
     if op == "scan":
-        return kda.kda_ssm_scan(*args, init_state=s["state"], return_chunk_states=s["states"], **more, **seqs)
+        # a program knows its batch's lengths on the host, and so the number of chunk states
+        chunks = torch.empty((s["chunk_rows"],) + tuple(s["A"].shape), device="cuda") if s["states"] else None
+        return kda.kda_ssm_scan(*args, init_state=s["state"], chunk_states=chunks, **more, **seqs)
     if op == "step":
         return kda.kda_ssm_step(*args, s["state"], **more), s["state"]
     res = kda.kda_ssm_scan_backward(*args, s["d_out"], s["d_final"], init_state=s["state"],
