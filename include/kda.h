@@ -423,6 +423,178 @@ kda_status kda_decode(const kda_dims *dims, const void *q, const void *k, const 
                       const float *g, const float *beta, float *state_inout, void *out,
                       kda_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * State space layers and 8-bit activations
+ * ---------------------------------------------------------------------------
+ * The calls below are the sequence mixing of a selective state space layer: the
+ * same family of recurrences without the erase term, with a decay of its own for
+ * every state entry.  For channel d, state entry n and the tokens t of a sequence,
+ *
+ *   Delta_t[d] = softplus(dt_t[d] + dt_bias[d])
+ *   h_t[d,n]   = exp(Delta_t[d] A[d,n]) h_{t-1}[d,n] + Delta_t[d] u_t[d] B_t[n]
+ *   y_t[d]     = (sum_n C_t[n] h_t[d,n] + D[d] u_t[d]) * z_t[d] Sigmoid(z_t[d])
+ *
+ * where u comes from a short causal convolution.  The pages have no counterpart;
+ * these are additions for models that mix such layers with KDA layers.
+ *
+ * Conventions: as above, except that the activations are given as rows
+ * (kda_rows) whose stride the caller chooses, so that slices of a projection's
+ * output need no copy.  Inputs are fp32 or bf16 (one type a call); A, D,
+ * dt_bias, weights and states are fp32; all arithmetic is fp32, and a bf16
+ * output is rounded once.  Masked or absent work has no special value: an
+ * infinity or a NaN in an input reaches the outputs that depend on it and no
+ * other sequence or channel (the gradients of B, C and the parameters are sums
+ * over channels or tokens).  Rows of an output that belong to no sequence (tokens
+ * before cu_seqlens[0] or from cu_seqlens[N] on) are left as they were.
+ * The calls allocate nothing: a call that needs scratch takes a workspace, whose
+ * size another function gives.  Results do not depend on timing: repeated calls
+ * give the same bits.  Calls on different streams may overlap as long as they
+ * share no written buffer (workspace included); every call may be captured into
+ * a CUDA graph, whose replays use the buffers named at the capture.
+ */
+
+/* Tokens [T, channels] of an activation: row t starts at data + t * stride
+ * elements.  With scales == NULL data holds the call's input type.  Where a call
+ * says so, scales != NULL makes data int8 codes as kda_act_pack8 writes them
+ * (stride == channels) with scales fp32 [T, ceil(channels / KDA_PACK_GROUP)].
+ * data must be aligned to its element; vector accesses are used where address and
+ * stride allow. */
+typedef struct {
+    const void *data;
+    int64_t stride;
+    const float *scales;
+} kda_rows;
+
+typedef struct {
+    int32_t num_seqs;     /* N >= 0 */
+    int32_t total_tokens; /* T >= 0 (kda_ssm_step: must equal num_seqs) */
+    int32_t channels;     /* D >= 1 */
+    int32_t state_size;   /* scan: S, 1..64; convolution: taps W, 2..4 */
+    int32_t in_dtype;     /* kda_dtype of the activations read */
+    int32_t out_dtype;    /* kda_dtype of the activations (or their gradients) written */
+} kda_ssm_dims;
+
+/* What every scan call reads. */
+typedef struct {
+    kda_rows u, dt, B, C, z;   /* [T, D], [T, D], [T, S], [T, S]; z [T, D], or data NULL: no gate */
+    const float *A;            /* [D, S]; finite */
+    const float *D;            /* [D] or NULL (0) */
+    const float *dt_bias;      /* [D] or NULL (0) */
+    const int32_t *cu_seqlens; /* [N+1] or NULL (N equal sequences), as in kda_prefill */
+    int32_t delta_softplus;    /* 1: Delta = softplus(dt + dt_bias); 0: Delta = dt + dt_bias */
+} kda_ssm_inputs;
+
+/* Channels that share a scale in the 8-bit packing. */
+#define KDA_PACK_GROUP 32
+
+/*
+ * kda_act_pack8 -- an activation in 8 bits, to be kept for a gradient.
+ *
+ * Per token, each group of KDA_PACK_GROUP neighbouring channels (the last may be
+ * partial) has m = max |x|, scale = m / 127 and codes round(x * (127 / m)), half
+ * to even; code * scale is off x by at most half a scale.  A group with m below
+ * 2^-120 has scale 0 and codes 0; one that holds an infinity or a NaN has scale NaN
+ * (the rest of its codes are unspecified).
+ *
+ *   x       device, in_dtype rows [rows, channels].
+ *   codes   device int8 [rows, channels];  scales  device fp32 [rows, ceil(channels / 32)].
+ */
+kda_status kda_act_pack8(int32_t rows, int32_t channels, int32_t in_dtype, const kda_rows *x,
+                         int8_t *codes, float *scales, kda_stream_t stream);
+
+/*
+ * kda_ssm_conv -- causal per-channel convolution of W taps over each sequence, and
+ * Swish:  c_t = bias + sum_k weight[k] x_{t-(W-1-k)},  out = c_t Sigmoid(c_t)
+ * (or c_t with swish == 0).
+ *
+ *   x              in_dtype rows [T, D].
+ *   weight         device fp32 [D, W] (entry W-1 on the current token);  bias  fp32 [D] or NULL.
+ *   conv_state_in  device fp32 [N, W-1, D] or NULL (zeros): the W-1 inputs before each
+ *                  sequence's first token, oldest first.
+ *   out            device, out_dtype [T, D].
+ *   conv_state_out device fp32 [N, W-1, D] or NULL: the last W-1 inputs of each sequence
+ *                  (from conv_state_in where it is shorter).  May be conv_state_in itself.
+ *
+ * One token per sequence (cu_seqlens NULL, T == N) is the decode step: one launch
+ * that writes the output and moves the state.
+ */
+kda_status kda_ssm_conv(const kda_ssm_dims *dims, const kda_rows *x, const float *weight,
+                        const float *bias, const float *conv_state_in, const int32_t *cu_seqlens,
+                        int32_t swish, void *out, float *conv_state_out, kda_stream_t stream);
+
+/*
+ * kda_ssm_conv_backward -- gradients of kda_ssm_conv for d_out (in_dtype rows
+ * [T, D]) and d_conv_state_out (fp32 [N, W-1, D] or NULL: zero).
+ *
+ *   x              as in the forward call, or its 8-bit codes and scales: the gradients
+ *                  are then those at the values the codes stand for.
+ *   dx             device, out_dtype [T, D];  dweight  fp32 [D, W];  dbias  fp32 [D] or NULL;
+ *   d_conv_state_in  fp32 [N, W-1, D] or NULL.
+ *   workspace      kda_ssm_conv_backward_workspace(dims) bytes, 16-byte aligned.
+ */
+int64_t kda_ssm_conv_backward_workspace(const kda_ssm_dims *dims);
+kda_status kda_ssm_conv_backward(const kda_ssm_dims *dims, const kda_rows *x, const float *weight,
+                                 const float *bias, const float *conv_state_in,
+                                 const int32_t *cu_seqlens, int32_t swish, const kda_rows *d_out,
+                                 const float *d_conv_state_out, void *dx, float *dweight,
+                                 float *dbias, float *d_conv_state_in, void *workspace,
+                                 int64_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_ssm_scan -- the scan over a packed batch of prompts.
+ *
+ *   init_state   device fp32 [N, D, S] or NULL (zeros).
+ *   out          device, out_dtype [T, D].
+ *   final_state  device fp32 [N, D, S] or NULL.  May be init_state itself.
+ *   chunk_states device fp32 [chunk_capacity, D, S] or NULL (with chunk_capacity 0): the
+ *                state after every KDA_CHUNK tokens of each sequence, rows as in
+ *                kda_prefill_checkpointed with interval KDA_CHUNK; what the gradients need.
+ */
+kda_status kda_ssm_scan(const kda_ssm_dims *dims, const kda_ssm_inputs *in, const float *init_state,
+                        void *out, float *final_state, float *chunk_states, int64_t chunk_capacity,
+                        kda_stream_t stream);
+
+/*
+ * kda_ssm_step -- one token for each of N sequences: state (device fp32 [N, D, S],
+ * updated in place) and out (out_dtype [N, D]).  in->cu_seqlens must be NULL.
+ */
+kda_status kda_ssm_step(const kda_ssm_dims *dims, const kda_ssm_inputs *in, float *state, void *out,
+                        kda_stream_t stream);
+
+/* What kda_ssm_scan_backward writes: du, ddt, dz (out_dtype [T, D]; dz is needed
+ * with z), dB, dC (out_dtype [T, S]), dA (fp32 [D, S]), dD and ddt_bias (fp32 [D]
+ * or NULL), d_init_state (fp32 [N, D, S] or NULL). */
+typedef struct {
+    void *du, *ddt, *dB, *dC, *dz;
+    float *dA, *dD, *ddt_bias, *d_init_state;
+} kda_ssm_grads;
+
+/*
+ * kda_ssm_scan_backward -- gradients of kda_ssm_scan for d_out (in_dtype rows
+ * [T, D]) and d_final_state (fp32 [N, D, S] or NULL: zero).
+ *
+ *   in           as in the forward call; u and z may both be 8-bit codes and scales
+ *                (dt, B, C and d_out stay in_dtype): the gradients are then those at the
+ *                values the codes stand for, with the states run on from chunk_states.
+ *   chunk_states the forward's, chunk_capacity rows (NULL with 0 rows).  Where a row that is
+ *                needed is missing: as in kda_backward (an error where lengths are known on
+ *                the host, else the device status word).
+ *   workspace    kda_ssm_scan_backward_workspace(dims) bytes, 16-byte aligned.
+ */
+int64_t kda_ssm_scan_backward_workspace(const kda_ssm_dims *dims);
+kda_status kda_ssm_scan_backward(const kda_ssm_dims *dims, const kda_ssm_inputs *in,
+                                 const float *init_state, const float *chunk_states,
+                                 int64_t chunk_capacity, const kda_rows *d_out,
+                                 const float *d_final_state, const kda_ssm_grads *grads,
+                                 void *workspace, int64_t workspace_bytes, kda_stream_t stream);
+
+/* In all of these: no output may share a byte with an input or another output
+ * except where a call allows it.  KDA_ERR_INVALID_ARGUMENT for a NULL or misaligned
+ * pointer that is needed, a negative size, a stride below the row's length (one
+ * row excepted), an overlap, or a workspace too small; KDA_ERR_UNSUPPORTED for S
+ * outside 1..64, W outside 2..4, or sizes beyond one grid.  The workspace
+ * functions return -1 for dims that the call refuses. */
+
 /*
  * kda_get_last_device_error -- report, then clear, the device-side status.
  *

@@ -16,6 +16,16 @@ method and has no fallback: if the library is missing, every call raises.
     kda_output_gate(out, gate_logit, ...)   the output gate alone, in place
     kda_qkv_prologue(x_q, x_k, x_v, conv_weight, ...)   ShortConv, Swish, L2Norm -> q, k, v
     kda_decode(q, k, v, g, beta, state) one-token in-place state update
+
+State space layers (selective scan with its short convolution) and the 8-bit
+packing of the activations their gradients read:
+
+    kda_ssm_conv(x, weight, bias, ...)  causal convolution and Swish; one-token calls move its state
+    kda_ssm_conv_backward(...)          its gradients, from x or its 8-bit codes
+    kda_ssm_scan(u, dt, A, B, C, ...)   selective scan over a packed batch
+    kda_ssm_step(..., state)            one token, states in place
+    kda_ssm_scan_backward(...)          gradients of the scan, from u and z or their 8-bit codes
+    kda_act_pack8(x)                    an activation as int8 codes and scales
 """
 from __future__ import annotations
 
@@ -29,6 +39,8 @@ __all__ = ["KdaError", "kda_prefill", "kda_prefill_noalloc", "kda_prefill_checkp
            "kda_output_gate", "kda_qkv_prologue", "checkpoint_count", "kda_decode",
            "kda_status_string", "lib", "library_path",
            "kda_get_last_device_error", "kda_selftest_timeout",
+           "kda_act_pack8", "kda_ssm_conv", "kda_ssm_conv_backward", "kda_ssm_scan",
+           "kda_ssm_step", "kda_ssm_scan_backward", "PACK_GROUP",
            "PREFILL_DEFAULT", "PREFILL_FP32", "PREFILL_TC", "PREFILL_TC_SPLIT", "PREFILL_TC_2PASS", "Dims"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -98,6 +110,7 @@ def lib():
         L.kda_qkv_prologue.restype = ctypes.c_int
         L.kda_decode.argtypes = [ctypes.POINTER(Dims), vp, vp, vp, fp, fp, fp, vp, vp]
         L.kda_decode.restype = ctypes.c_int
+        _declare_ssm(L)
         L.kda_status_string.argtypes = [ctypes.c_int]
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_last_cuda_error.restype = ctypes.c_char_p
@@ -474,3 +487,8 @@ def kda_decode(q, k, v, g, beta, state, *, out=None, out_dtype=None, stream=None
                           _ptr(state), _ptr(out), _stream(stream))
     _check(st, "kda_decode")
     return out
+
+
+from ._ssm import (PACK_GROUP, kda_act_pack8, kda_ssm_conv, kda_ssm_conv_backward,  # noqa: E402
+                   kda_ssm_scan, kda_ssm_scan_backward, kda_ssm_step)
+from ._ssm import declare as _declare_ssm  # noqa: E402

@@ -1,54 +1,22 @@
 // kda_api.cu -- the C ABI front end: argument validation, kernel selection,
 // launch and error mapping.  Declarations and semantics: include/kda.h.
 
-#include <initializer_list>
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
 
-#include "kda_common.cuh"
+#include "kda_api_util.cuh"
 
 namespace {
 
+using kda::conflict;
+using kda::esize;
+using kda::overlaps;
+using kda::valid_dtype;
+
 thread_local char g_last_cuda_error[256] = "";
 
-kda_status cuda_fail(cudaError_t e, const char *where) {
-    snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s: %s (%s)", where,
-             cudaGetErrorName(e), cudaGetErrorString(e));
-    return KDA_ERR_CUDA;
-}
-
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-// Do the byte ranges [a, a + na) and [b, b + nb) share a byte?
-bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const char *x = (const char *)a, *y = (const char *)b;
-    return x < y + nb && y < x + na;
-}
-
-// A buffer a call touches: its address and size in bytes (a NULL buffer is empty).
-struct Span {
-    const void *p;
-    size_t n;
-};
-
-// Does a written buffer share a byte with a read buffer or with another
-// written buffer?  The kernels read inputs (some by TMA, chunks ahead) while
-// they write outputs, so any such overlap would be a race.
-bool conflict(std::initializer_list<Span> writes, std::initializer_list<Span> reads) {
-    for (const Span *w = writes.begin(); w != writes.end(); ++w) {
-        for (const Span &r : reads)
-            if (overlaps(w->p, w->n, r.p, r.n)) return true;
-        for (const Span *w2 = w + 1; w2 != writes.end(); ++w2)
-            if (overlaps(w->p, w->n, w2->p, w2->n)) return true;
-    }
-    return false;
-}
-
-size_t esize(int32_t dtype) { return dtype == KDA_DTYPE_BF16 ? 2 : 4; }
-
-bool valid_dtype(int32_t d) { return d == KDA_DTYPE_F32 || d == KDA_DTYPE_BF16; }
 
 // Shared checks of the dims struct.  Fills P on success.
 kda_status check_dims(const kda_dims *d, kda::Problem &P) {
@@ -74,7 +42,15 @@ kda_status check_dims(const kda_dims *d, kda::Problem &P) {
     return KDA_OK;
 }
 
+kda_status cuda_fail(cudaError_t e, const char *where) { return kda_cuda_fail(e, where); }
+
 }  // namespace
+
+kda_status kda_cuda_fail(cudaError_t e, const char *where) {
+    snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s: %s (%s)", where,
+             cudaGetErrorName(e), cudaGetErrorString(e));
+    return KDA_ERR_CUDA;
+}
 
 extern "C" {
 

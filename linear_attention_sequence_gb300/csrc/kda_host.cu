@@ -5,6 +5,7 @@
 
 #include "kda_common.cuh"
 #include "kda_chunk_ops.cuh"
+#include "kda_ssm_common.cuh"
 
 namespace {
 
@@ -83,5 +84,6 @@ cudaError_t kda_read_device_status(cudaStream_t stream, unsigned *status) {
     if (e == cudaSuccess) e = kda_2pass_read_status(status);
     if (e == cudaSuccess) e = kda_bwd_read_status(status);
     if (e == cudaSuccess) e = kda_bwdtc_read_status(status);
+    if (e == cudaSuccess) e = kda_ssm_read_status(status);
     return e;
 }

@@ -1,0 +1,291 @@
+// kda_ssm_common.cuh -- what the state space kernels share (sm_103a): packed
+// fp32 arithmetic, the elementary functions, and loads of rows whose address
+// or length may not allow vector accesses.
+#pragma once
+
+#include "kda_common.cuh"
+
+namespace kda {
+
+// Tokens of a scan tile, and the interval of the chunk states.
+constexpr int kSsmTile = KDA_CHUNK;
+// Channels that share one scale in the 8-bit packing.
+constexpr int kPackGroup = KDA_PACK_GROUP;
+
+// ---- packed pairs of fp32 (one issue slot for two operations)
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float &x, float &y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+    float x, y;
+    unpack2(v, x, y);
+    return x + y;
+}
+
+// 2^x, relative error below 2^-22; results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ f2 exp2_pair(f2 v) {
+    float x, y;
+    unpack2(v, x, y);
+    return pack2(exp2_fast(x), exp2_fast(y));
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Sigmoid(x) = 1 / (1 + e^-x).  e^-x = inf gives 0, the limit.
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.f + exp2_fast(-kLog2e * x)); }
+
+// softplus(x) = log(1 + e^x) = max(x, 0) + log1p(e^-|x|).  With w = e^-|x| in
+// (0, 1] and r = w / (2 + w) <= 1/3, log1p(w) = 2 artanh(r) = 2 (r + r^3/3 +
+// r^5/5 + ...); the series stops at r^15 (what is left is below 3^-16 * 2/17 of
+// r).  Small results keep their relative precision, which the logarithm of a
+// rounded 1 + w would lose: step sizes of 1e-3 and less are ordinary here.
+__device__ __forceinline__ float softplus_fast(float x) {
+    const float w = exp2_fast(-kLog2e * fabsf(x));
+    const float r = w * rcp_fast(2.f + w);
+    const float s = r * r;
+    float p = 2.f / 15.f;
+    p = fmaf(p, s, 2.f / 13.f);
+    p = fmaf(p, s, 2.f / 11.f);
+    p = fmaf(p, s, 2.f / 9.f);
+    p = fmaf(p, s, 2.f / 7.f);
+    p = fmaf(p, s, 2.f / 5.f);
+    p = fmaf(p, s, 2.f / 3.f);
+    p = fmaf(p, s, 2.f);
+    return fmaf(p, r, fmaxf(x, 0.f));
+}
+
+// ---- rows of activations as the kernels get them
+struct Rows {
+    const void *p;         // first element; nullptr: absent
+    int64_t stride;        // elements from one token's row to the next
+    const float *scales;   // != nullptr: int8 codes, [T, ngroups] scales
+    int32_t ngroups;
+    int32_t vec;           // rows may be read with 16-byte accesses
+};
+
+// E consecutive elements of a row, raw (as loaded) and as fp32.  Elements at or
+// past `have` read as 0.
+template <typename T, int E>
+struct Raw {
+    static constexpr int kBytes = E * (int)sizeof(T);
+    static constexpr int kWords = (kBytes + 3) / 4;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    // `vec`: p is aligned to min(16, kBytes) bytes and all E elements exist
+    __device__ __forceinline__ void load(const T *p, int have, bool vec) {
+        if (vec && have >= E) {
+            if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+                for (int i = 0; i < kBytes / 16; ++i) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                    w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+                }
+            } else if constexpr (kBytes % 8 == 0) {
+#pragma unroll
+                for (int i = 0; i < kBytes / 8; ++i) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+                    w[2 * i] = v.x; w[2 * i + 1] = v.y;
+                }
+            } else if constexpr (kBytes % 4 == 0) {
+#pragma unroll
+                for (int i = 0; i < kBytes / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+            } else {
+                slow(p, have);
+            }
+        } else {
+            slow(p, have);
+        }
+    }
+    __device__ __forceinline__ void slow(const T *p, int have) {
+        clear();
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (i < have) {
+                if constexpr (sizeof(T) == 4) {
+                    w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+                } else if constexpr (sizeof(T) == 2) {
+                    w[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p) + i) << (16 * (i % 2));
+                } else {
+                    w[i / 4] |= (uint32_t)__ldg(reinterpret_cast<const unsigned char *>(p) + i) << (8 * (i % 4));
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        if constexpr (sizeof(T) == 2) return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        return (float)(int)(signed char)(w[i / 4] >> (8 * (i % 4)));
+    }
+};
+
+// E consecutive results of a row.  `vec`: the address is aligned to
+// min(16, E * sizeof(T)) bytes.
+template <typename T, int E>
+__device__ __forceinline__ void store_row(T *p, const float (&v)[E], int have, bool vec) {
+    constexpr int kBytes = E * (int)sizeof(T);
+    if (vec && have >= E && kBytes % 4 == 0) {
+        uint32_t w[(kBytes + 3) / 4];
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) w[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+        }
+        if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i)
+                reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else if constexpr (kBytes % 8 == 0) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 8; ++i) reinterpret_cast<uint2 *>(p)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBytes / 4; ++i) reinterpret_cast<uint32_t *>(p)[i] = w[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (i < have) st_elem(p + i, v[i]);
+    }
+}
+
+// Sums over groups of L lanes that are `STEP` lanes apart, K values at a time:
+// each exchange keeps one half of the values and sends the other, so K values
+// cost K - K/L exchanges where L <= K.  On return v[0 .. K/L - 1] holds the sums
+// of values number (index of this lane in its group) * K/L + i.  L <= K.
+template <int L, int STEP, int K>
+__device__ __forceinline__ void reduce_scatter(float (&v)[K]) {
+    static_assert(K % L == 0, "every lane ends with as many values");
+    const int lane = threadIdx.x & 31;
+    int n = K;
+#pragma unroll
+    for (int off = L / 2; off >= 1; off /= 2) {
+        n /= 2;
+        const bool up = lane & (off * STEP);
+#pragma unroll
+        for (int i = 0; i < K / 2; ++i) {
+            if (i < n) {
+                const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off * STEP);
+            }
+        }
+    }
+}
+
+// Four states of one channel, n0 .. n0 + 3; those at or past S read as 0.
+__device__ __forceinline__ float4 load_states(const float *p, int n0, int S, bool vec) {
+    if (vec) return n0 < S ? *reinterpret_cast<const float4 *>(p + n0) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 r;
+    r.x = n0 + 0 < S ? p[n0 + 0] : 0.f;
+    r.y = n0 + 1 < S ? p[n0 + 1] : 0.f;
+    r.z = n0 + 2 < S ? p[n0 + 2] : 0.f;
+    r.w = n0 + 3 < S ? p[n0 + 3] : 0.f;
+    return r;
+}
+__device__ __forceinline__ void store_states(float *p, float4 v, int n0, int S, bool vec) {
+    if (vec) {
+        if (n0 < S) *reinterpret_cast<float4 *>(p + n0) = v;
+        return;
+    }
+    if (n0 + 0 < S) p[n0 + 0] = v.x;
+    if (n0 + 1 < S) p[n0 + 1] = v.y;
+    if (n0 + 2 < S) p[n0 + 2] = v.z;
+    if (n0 + 3 < S) p[n0 + 3] = v.w;
+}
+
+// The sequence of token t in a packed batch: its number n and its bounds.  False
+// if the token lies outside every sequence; then sa is the first token after t
+// that may lie in one (total if there is none).
+__device__ __forceinline__ bool find_seq(const int32_t *cu, int N, int64_t total, int64_t seq_len, int64_t t, int &n,
+                                         int64_t &sa, int64_t &sb) {
+    if (!cu) {
+        n = (int)(t / seq_len);   // t < total = N seq_len, so seq_len > 0
+    } else {
+        int lo = -1, hi = N;      // cu[lo] <= t < cu[hi], taking cu[-1] = -inf and cu[N] = inf
+        while (hi - lo > 1) {
+            const int m = (lo + hi) / 2;
+            if (cu[m] <= t) lo = m; else hi = m;
+        }
+        n = lo;
+        if (n < 0) {
+            sa = cu[0] < total ? cu[0] : total;
+            sb = sa;
+            return false;
+        }
+    }
+    seq_bounds(cu, n, total, seq_len, sa, sb);
+    if (t >= sa && t < sb) return true;
+    sa = sb = total;              // behind the last sequence (or a malformed array)
+    return false;
+}
+
+// Launch parameters of the state space kernels after validation.
+struct SsmProblem {
+    int32_t N, T, D, S;          // sequences, tokens, channels, states per channel (or taps)
+    int32_t in_dtype, out_dtype;
+    int64_t seq_len;             // tokens per sequence where cu is nullptr
+    const int32_t *cu;
+    Rows u, dt, B, C, z, dy;
+    const float *A, *skip, *dt_bias;
+    bool softplus;
+    bool svec;                   // state rows may be read with 16-byte accesses
+};
+
+}  // namespace kda
+
+// Launchers.
+cudaError_t kda_launch_act_pack8(int64_t rows, int32_t D, int32_t in_dtype, const kda::Rows &x, int8_t *codes,
+                                 float *scales, cudaStream_t stream);
+cudaError_t kda_launch_ssm_scan(const kda::SsmProblem &P, const float *init, void *out, float *final_state,
+                                float *chunk_states, int64_t chunk_capacity, cudaStream_t stream);
+cudaError_t kda_launch_ssm_conv(const kda::SsmProblem &P, const float *w, const float *bias, const float *cin,
+                                bool swish, void *out, float *cout, cudaStream_t stream);
+int64_t kda_ssm_conv_backward_tiles(const kda::SsmProblem &P, int *tile);
+cudaError_t kda_launch_ssm_conv_backward(const kda::SsmProblem &P, const float *w, const float *bias,
+                                         const float *cin, const float *dcout, bool swish, void *dx, float *dw,
+                                         float *dbias, float *dcin, float *workspace, cudaStream_t stream);
+int64_t kda_ssm_scan_backward_ws(const kda::SsmProblem &P);
+cudaError_t kda_launch_ssm_scan_backward(const kda::SsmProblem &P, const float *init, const float *chunk_states,
+                                         int64_t chunk_capacity, const float *d_final, void *du, void *ddt, void *dB,
+                                         void *dC, void *dz, float *dA, float *dskip, float *dbias, float *d_init,
+                                         float *workspace, cudaStream_t stream);
+cudaError_t kda_ssm_read_status(unsigned *status);
+cudaError_t kda_launch_ssm_step(const kda::SsmProblem &P, float *state, void *out, cudaStream_t stream);
