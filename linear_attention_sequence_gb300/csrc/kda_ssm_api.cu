@@ -82,7 +82,7 @@ Checked check_rows(const kda_rows *x, int64_t T, int64_t width, size_t es, bool 
 size_t cu_bytes(const SsmProblem &P) { return P.cu ? (size_t)(P.N + 1) * 4 : 0; }
 
 // Pieces that the scan kernels read of a row: a thread's share of a block's
-// channels (four threads a row), at most 16 bytes.
+// channels (at least four threads a row), at most 16 bytes.
 size_t scan_piece(int S, size_t es) {
     const int ln = S <= 8 ? 2 : S <= 16 ? 4 : S <= 32 ? 8 : 16;
     const size_t b = 32 / ln * es;
@@ -163,7 +163,7 @@ kda_status kda_ssm_conv(const kda_ssm_dims *dims, const kda_rows *x, const float
     if (st == KDA_OK) st = check_lengths(P, cu_seqlens);
     if (st != KDA_OK) return st;
     if (P.N == 0) return KDA_OK;
-    const Checked c = check_rows(x, P.T, P.D, esize(P.in_dtype), false, 16);
+    const Checked c = check_rows(x, P.T, P.D, esize(P.in_dtype), false, 4 * esize(P.in_dtype));
     if (c.st != KDA_OK) return c.st;
     if (!weight || misaligned(weight, 4) || misaligned(bias, 4) || misaligned(conv_state_in, 4) ||
         misaligned(conv_state_out, 4) || (P.T > 0 && !out) || misaligned(out, esize(P.out_dtype)))

@@ -65,22 +65,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.f + exp2_fast(-kLog2e * x)); }
 
 // softplus(x) = log(1 + e^x) = max(x, 0) + log1p(e^-|x|).  With w = e^-|x| in
-// (0, 1] and r = w / (2 + w) <= 1/3, log1p(w) = 2 artanh(r) = 2 (r + r^3/3 +
-// r^5/5 + ...); the series stops at r^15 (what is left is below 3^-16 * 2/17 of
-// r).  Small results keep their relative precision, which the logarithm of a
-// rounded 1 + w would lose: step sizes of 1e-3 and less are ordinary here.
+// (0, 1] and r = w / (2 + w) <= 1/3, log1p(w) = 2 artanh(r) = r p(r^2), p(s) = 2 (1 +
+// s/3 + s^2/5 + ...); p is a Chebyshev fit of degree 4 on [0, 1/9], off by less
+// than 8e-9 of its value.  Small results keep their relative precision, which the
+// logarithm of a rounded 1 + w would lose: step sizes of 1e-3 and less are ordinary.
 __device__ __forceinline__ float softplus_fast(float x) {
     const float w = exp2_fast(-kLog2e * fabsf(x));
     const float r = w * rcp_fast(2.f + w);
     const float s = r * r;
-    float p = 2.f / 15.f;
-    p = fmaf(p, s, 2.f / 13.f);
-    p = fmaf(p, s, 2.f / 11.f);
-    p = fmaf(p, s, 2.f / 9.f);
-    p = fmaf(p, s, 2.f / 7.f);
-    p = fmaf(p, s, 2.f / 5.f);
-    p = fmaf(p, s, 2.f / 3.f);
-    p = fmaf(p, s, 2.f);
+    float p = 0.28174657f;
+    p = fmaf(p, s, 0.27961419f);
+    p = fmaf(p, s, 0.40024854f);
+    p = fmaf(p, s, 0.66666316f);
+    p = fmaf(p, s, 2.00000001f);
     return fmaf(p, r, fmaxf(x, 0.f));
 }
 
@@ -105,30 +102,32 @@ struct Raw {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = 0;
     }
-    // `vec`: p is aligned to min(16, kBytes) bytes and all E elements exist
-    __device__ __forceinline__ void load(const T *p, int have, bool vec) {
-        if (vec && have >= E) {
-            if constexpr (kBytes % 16 == 0) {
+    // All E elements, from an address aligned to min(16, kBytes) bytes.
+    __device__ __forceinline__ void load_all(const T *p) {
+        if constexpr (kBytes % 16 == 0) {
 #pragma unroll
-                for (int i = 0; i < kBytes / 16; ++i) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-                    w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-                }
-            } else if constexpr (kBytes % 8 == 0) {
-#pragma unroll
-                for (int i = 0; i < kBytes / 8; ++i) {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
-                    w[2 * i] = v.x; w[2 * i + 1] = v.y;
-                }
-            } else if constexpr (kBytes % 4 == 0) {
-#pragma unroll
-                for (int i = 0; i < kBytes / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
-            } else {
-                slow(p, have);
+            for (int i = 0; i < kBytes / 16; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
             }
+        } else if constexpr (kBytes % 8 == 0) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 8; ++i) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+                w[2 * i] = v.x; w[2 * i + 1] = v.y;
+            }
+        } else if constexpr (kBytes % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
         } else {
-            slow(p, have);
+            slow(p, E);
         }
+    }
+    // `vec`: p is aligned to min(16, kBytes) bytes; FULL: that, and all E elements exist
+    template <bool FULL = false>
+    __device__ __forceinline__ void load(const T *p, int have, bool vec) {
+        if (FULL || (vec && have >= E)) load_all(p);
+        else slow(p, have);
     }
     __device__ __forceinline__ void slow(const T *p, int have) {
         clear();
@@ -148,16 +147,17 @@ struct Raw {
     __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
         if constexpr (sizeof(T) == 2) return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-        return (float)(int)(signed char)(w[i / 4] >> (8 * (i % 4)));
+        // the byte, made 0 .. 255, as the last place of 2^23
+        return __uint_as_float(__byte_perm(w[i / 4] ^ 0x80808080u, 0x4b000000u, 0x7440 + i % 4)) - 8388736.f;
     }
 };
 
 // E consecutive results of a row.  `vec`: the address is aligned to
-// min(16, E * sizeof(T)) bytes.
-template <typename T, int E>
+// min(16, E * sizeof(T)) bytes; FULL: that, and all E exist.
+template <typename T, int E, bool FULL = false>
 __device__ __forceinline__ void store_row(T *p, const float (&v)[E], int have, bool vec) {
     constexpr int kBytes = E * (int)sizeof(T);
-    if (vec && have >= E && kBytes % 4 == 0) {
+    if ((FULL || (vec && have >= E)) && kBytes % 4 == 0) {
         uint32_t w[(kBytes + 3) / 4];
         if constexpr (sizeof(T) == 4) {
 #pragma unroll

@@ -6,12 +6,16 @@
 //   dx_t = sum_k w[k] dc_{t+(W-1-k)},  dw[k] = sum_t dc_t x_{t-(W-1-k)},  dbias = sum_t dc_t
 //
 // with the inputs before a sequence's first token taken from its carried state.
-// HBM-bound: a thread takes V neighbouring channels (16 bytes of a bf16 row) and
-// walks a run of tokens with the W - 1 last inputs in registers, so that each
-// input is read once, but for the W - 1 rows that a run reads of its neighbour.
+// HBM-bound: a thread takes four neighbouring channels and walks a run of tokens
+// with the W - 1 last inputs in registers, so that each input is read once, but
+// for the W - 1 rows that a run reads of its neighbour.  The rows of one batch are
+// loaded while the batch before is computed (kRows rows in flight a thread).  The
+// arithmetic is on pairs of channels, one issue slot for two operations.
 // The gradient walks forward too: with dc_t known, dx of token t - (W-1) is
 // complete.  A run's share of dw and dbias goes to a workspace, and a second
 // kernel adds the runs up in their order, so the sums do not depend on timing.
+
+#include <initializer_list>
 
 #include "kda_ssm_common.cuh"
 
@@ -20,11 +24,15 @@ namespace {
 using namespace kda;
 
 constexpr int kThreads = 128;
+constexpr int V = 4;          // channels of a thread
+constexpr int NP = V / 2;     // pairs of them
+constexpr int kRows = 8;      // rows loaded ahead
 
 struct ConvArgs {
     SsmProblem P;             // P.S: taps
     const float *w, *bias, *cin;
     bool swish, ovec;
+    bool fvec;                // four fp32 neighbours may be read and written at once (weights, bias, states, shares)
     void *out;
     float *cout;
     // gradients
@@ -33,26 +41,72 @@ struct ConvArgs {
     int tile;
 };
 
-template <int V>
-__device__ __forceinline__ void load_cols(const float *p, float (&v)[V], int have) {
+// Four neighbouring fp32 values; those at or past `have`, and all of a NULL array, are 0.
+__device__ __forceinline__ void load4(const float *p, f2 (&v)[NP], int have, bool vec) {
+    float x[V];
+    if (!p) {
+        v[0] = v[1] = 0;
+        return;
+    }
+    if (vec && have >= V) {
+        const float4 q = __ldg(reinterpret_cast<const float4 *>(p));
+        v[0] = pack2(q.x, q.y);
+        v[1] = pack2(q.z, q.w);
+        return;
+    }
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = (p && i < have) ? p[i] : 0.f;
+    for (int i = 0; i < V; ++i) x[i] = i < have ? p[i] : 0.f;
+    v[0] = pack2(x[0], x[1]);
+    v[1] = pack2(x[2], x[3]);
+}
+__device__ __forceinline__ void store4(float *p, const f2 (&v)[NP], int have, bool vec) {
+    float x[V];
+    unpack2(v[0], x[0], x[1]);
+    unpack2(v[1], x[2], x[3]);
+    store_row<float, V>(p, x, have, vec);
 }
 
-// The W taps of V channels.
-template <int V, int W>
-__device__ __forceinline__ void load_taps(const ConvArgs &a, int c0, int have, float (&w)[W][V], float (&b)[V]) {
+// The W taps of four channels, which are 4 W neighbours in memory.
+template <int W>
+__device__ __forceinline__ void load_taps(const ConvArgs &a, int c0, int have, f2 (&w)[W][NP], f2 (&b)[NP]) {
+    float x[V * W];
+    const float *p = a.w + (int64_t)c0 * W;
+    if (a.fvec && have >= V) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+        for (int i = 0; i < W; ++i) {
+            const float4 q = __ldg(reinterpret_cast<const float4 *>(p) + i);
+            x[4 * i] = q.x; x[4 * i + 1] = q.y; x[4 * i + 2] = q.z; x[4 * i + 3] = q.w;
+        }
+    } else {
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[k][i] = i < have ? a.w[(int64_t)(c0 + i) * W + k] : 0.f;
-    load_cols<V>(a.bias ? a.bias + c0 : nullptr, b, have);
+        for (int i = 0; i < V * W; ++i) x[i] = i < have * W ? p[i] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+#pragma unroll
+        for (int j = 0; j < NP; ++j) w[k][j] = pack2(x[2 * j * W + k], x[(2 * j + 1) * W + k]);
+    load4(a.bias ? a.bias + c0 : nullptr, b, have, a.fvec);
+}
+
+// A row as pairs; `scale`: what a code stands for.
+template <typename IN>
+__device__ __forceinline__ void to_pairs(const Raw<IN, V> &r, float scale, f2 (&x)[NP]) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        x[j] = pack2(r.get(2 * j), r.get(2 * j + 1));
+        if constexpr (sizeof(IN) == 1) x[j] = mul2(x[j], pack2(scale, scale));
+    }
+}
+template <typename IN>
+__device__ __forceinline__ float scale_of(const Rows &u, int64_t t, int c0) {
+    if constexpr (sizeof(IN) == 1) return __ldg(u.scales + t * u.ngroups + c0 / kPackGroup);
+    return 1.f;
 }
 
 // The W - 1 inputs before token t of sequence n = [sa, sb).
-template <typename IN, int V, int W>
+template <typename IN, int W>
 __device__ __forceinline__ void load_window(const ConvArgs &a, int n, int64_t sa, int64_t t, int c0, int have,
-                                            float (&x)[W][V]) {
+                                            f2 (&x)[W][NP]) {
     const SsmProblem &P = a.P;
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
@@ -60,73 +114,115 @@ __device__ __forceinline__ void load_window(const ConvArgs &a, int n, int64_t sa
         if (u >= sa) {
             Raw<IN, V> r;
             r.load((const IN *)P.u.p + u * P.u.stride + c0, have, P.u.vec);
-            if constexpr (sizeof(IN) == 1) {
-                const float sc = P.u.scales[u * P.u.ngroups + c0 / kPackGroup];
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[k][i] = r.get(i) * sc;
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[k][i] = r.get(i);
-            }
+            to_pairs<IN>(r, scale_of<IN>(P.u, u, c0), x[k]);
         } else {
             // u - sa + W - 1 is in 0 .. W - 2
-            load_cols<V>(a.cin ? a.cin + ((int64_t)n * (W - 1) + (u - sa + W - 1)) * P.D + c0 : nullptr, x[k], have);
+            load4(a.cin ? a.cin + ((int64_t)n * (W - 1) + (u - sa + W - 1)) * P.D + c0 : nullptr, x[k], have, a.fvec);
         }
     }
 }
 
-template <int V, int W>
-__device__ __forceinline__ void shift(float (&x)[W][V]) {
+template <int W>
+__device__ __forceinline__ void shift(f2 (&x)[W][NP]) {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[k][i] = x[k + 1][i];
+        for (int j = 0; j < NP; ++j) x[k][j] = x[k + 1][j];
 }
 
-template <typename IN, typename OUT, int V, int W>
+// c_t of four channels from the window.
+template <int W>
+__device__ __forceinline__ void convolve(const f2 (&w)[W][NP], const f2 (&b)[NP], const f2 (&x)[W][NP], f2 (&c)[NP]) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        c[j] = b[j];
+#pragma unroll
+        for (int k = 0; k < W; ++k) c[j] = fma2(w[k][j], x[k][j], c[j]);
+    }
+}
+
+// Sigmoid of a pair.
+__device__ __forceinline__ f2 sigmoid_pair(f2 c) {
+    const f2 e = add2(exp2_pair(mul2(c, pack2(-kLog2e, -kLog2e))), pack2(1.f, 1.f));
+    float x, y;
+    unpack2(e, x, y);
+    return pack2(rcp_fast(x), rcp_fast(y));
+}
+
+template <typename OUT, bool FULL>
+__device__ __forceinline__ void store_pairs(OUT *p, const f2 (&v)[NP], int have, bool vec) {
+    float x[V];
+    unpack2(v[0], x[0], x[1]);
+    unpack2(v[1], x[2], x[3]);
+    store_row<OUT, V, FULL>(p, x, have, vec);
+}
+
+// Tokens [t, end) of one sequence.  FULL: every access may take four elements.
+template <typename IN, typename OUT, int W, bool FULL>
+__device__ __forceinline__ void conv_run(const ConvArgs &a, const f2 (&w)[W][NP], const f2 (&b)[NP], f2 (&x)[W][NP],
+                                         int64_t t, int64_t end, int c0, int have) {
+    const SsmProblem &P = a.P;
+    const int64_t stride = P.u.stride, D = P.D;
+    const IN *px = (const IN *)P.u.p + t * stride + c0;
+    OUT *po = (OUT *)a.out + t * D + c0;
+    auto token = [&](const Raw<IN, V> &r) {
+        f2 c[NP];
+        to_pairs<IN>(r, 1.f, x[W - 1]);
+        convolve<W>(w, b, x, c);
+        if (a.swish) {
+#pragma unroll
+            for (int j = 0; j < NP; ++j) c[j] = mul2(c[j], sigmoid_pair(c[j]));
+        }
+        store_pairs<OUT, FULL>(po, c, have, a.ovec);
+        shift<W>(x);
+        po += D;
+    };
+    int left = (int)(end - t);
+    if (left >= kRows) {
+        Raw<IN, V> next[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i, px += stride) next[i].template load<FULL>(px, have, P.u.vec);
+        for (; left >= kRows; left -= kRows) {
+            Raw<IN, V> r[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) r[i] = next[i];
+            if (left >= 2 * kRows) {
+#pragma unroll
+                for (int i = 0; i < kRows; ++i, px += stride) next[i].template load<FULL>(px, have, P.u.vec);
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) token(r[i]);
+        }
+    }
+    for (; left > 0; --left, px += stride) {
+        Raw<IN, V> r;
+        r.template load<FULL>(px, have, P.u.vec);
+        token(r);
+    }
+}
+
+template <typename IN, typename OUT, int W>
 __global__ void __launch_bounds__(kThreads) kda_ssm_conv_kernel(const ConvArgs a) {
-    constexpr int PB = 8;                      // rows in flight
     const SsmProblem &P = a.P;
     const int nvb = (P.D + V * kThreads - 1) / (V * kThreads);
     const int c0 = ((int)(blockIdx.x % nvb) * kThreads + threadIdx.x) * V;
     const int64_t t0 = (int64_t)(blockIdx.x / nvb) * a.tile, t1 = min(t0 + a.tile, (int64_t)P.T);
     const int have = P.D - c0;
     if (have <= 0) return;
-    float w[W][V], b[V], x[W][V];
-    load_taps<V, W>(a, c0, have, w, b);
+    const bool full = P.u.vec && a.ovec && have >= V;
+    f2 w[W][NP], b[NP], x[W][NP];
     int n = 0;
     int64_t sa = 0, sb = 0, t = t0;
+    load_taps<W>(a, c0, have, w, b);
     while (t < t1) {
         if (!find_seq(P.cu, P.N, P.T, P.seq_len, t, n, sa, sb)) {
             t = sa;                            // rows outside every sequence stay as they are
             continue;
         }
-        load_window<IN, V, W>(a, n, sa, t, c0, have, x);
         const int64_t end = min(sb, t1);
-        for (; t < end; t += PB) {
-            Raw<IN, V> r[PB];
-#pragma unroll
-            for (int i = 0; i < PB; ++i) {
-                r[i].clear();
-                if (t + i < end) r[i].load((const IN *)P.u.p + (t + i) * P.u.stride + c0, have, P.u.vec);
-            }
-#pragma unroll
-            for (int i = 0; i < PB; ++i) {
-                if (t + i < end) {
-                    float o[V];
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        x[W - 1][j] = r[i].get(j);
-                        float c = b[j];
-#pragma unroll
-                        for (int k = 0; k < W; ++k) c = fmaf(w[k][j], x[k][j], c);
-                        o[j] = a.swish ? c * sigmoid_fast(c) : c;
-                    }
-                    store_row<OUT, V>((OUT *)a.out + (t + i) * P.D + c0, o, have, a.ovec);
-                    shift<V, W>(x);
-                }
-            }
-        }
+        load_window<IN, W>(a, n, sa, t, c0, have, x);
+        if (full) conv_run<IN, OUT, W, true>(a, w, b, x, t, end, c0, have);
+        else conv_run<IN, OUT, W, false>(a, w, b, x, t, end, c0, have);
         t = end;
     }
 }
@@ -153,42 +249,141 @@ __global__ void __launch_bounds__(kThreads) kda_ssm_conv_state_kernel(const Conv
     for (int k = 0; k < W - 1; ++k) a.cout[((int64_t)n * (W - 1) + k) * P.D + c] = v[k];
 }
 
-// One token a sequence: output and new state in one pass.
-template <typename IN, typename OUT, int V, int W>
+// One token a sequence: output and new state in one pass (cout may be cin: a thread
+// reads what it writes).
+template <typename IN, typename OUT, int W>
 __global__ void __launch_bounds__(kThreads) kda_ssm_conv_token_kernel(const ConvArgs a) {
     const SsmProblem &P = a.P;
-    const int nv = (P.D + V - 1) / V;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t n = i / nv;
-    if (n >= P.N) return;
-    const int c0 = (int)(i - n * nv) * V, have = P.D - c0;
-    float w[W][V], b[V], x[W][V];
-    load_window<IN, V, W>(a, (int)n, n, n, c0, have, x);
+    const int nv = (P.D + V * kThreads - 1) / (V * kThreads);
+    const int64_t n = blockIdx.x / nv;
+    const int c0 = ((int)(blockIdx.x % nv) * kThreads + threadIdx.x) * V, have = P.D - c0;
+    if (have <= 0) return;
+    f2 w[W][NP], b[NP], x[W][NP], c[NP];
     Raw<IN, V> r;
     r.load((const IN *)P.u.p + n * P.u.stride + c0, have, P.u.vec);
-    load_taps<V, W>(a, c0, have, w, b);
-    float o[V];
+    load_window<IN, W>(a, (int)n, n, n, c0, have, x);
+    load_taps<W>(a, c0, have, w, b);
+    to_pairs<IN>(r, 1.f, x[W - 1]);
+    convolve<W>(w, b, x, c);
+    if (a.swish) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        x[W - 1][j] = r.get(j);
-        float c = b[j];
-#pragma unroll
-        for (int k = 0; k < W; ++k) c = fmaf(w[k][j], x[k][j], c);
-        o[j] = a.swish ? c * sigmoid_fast(c) : c;
+        for (int j = 0; j < NP; ++j) c[j] = mul2(c[j], sigmoid_pair(c[j]));
     }
-    store_row<OUT, V>((OUT *)a.out + n * P.D + c0, o, have, a.ovec);
+    store_pairs<OUT, false>((OUT *)a.out + n * P.D + c0, c, have, a.ovec);
     if (a.cout) {
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (j < have) a.cout[(n * (W - 1) + k) * P.D + c0 + j] = x[k + 1][j];
+        for (int k = 0; k < W - 1; ++k) store4(a.cout + (n * (W - 1) + k) * P.D + c0, x[k + 1], have, a.fvec);
     }
 }
 
-template <typename IN, typename DY, typename OUT, int V, int W>
+// What a run gathers.
+template <int W>
+struct Back {
+    f2 w[W][NP], b[NP], x[W][NP], dc[W][NP], dw[W][NP], db[NP];
+
+    // One step: token t's row r and gradient y.  `own`: counted by this run.
+    template <typename IN, typename DY, bool OWN>
+    __device__ __forceinline__ void step(const Raw<IN, V> &r, const Raw<DY, V> &y, float scale, bool swish) {
+        to_pairs<IN>(r, scale, x[W - 1]);
+        to_pairs<DY>(y, 1.f, dc[W - 1]);
+        if (swish) {
+            f2 c[NP];
+            convolve<W>(w, b, x, c);
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                // s + c s (1 - s) = s (1 + c (1 - s))
+                const f2 s = sigmoid_pair(c[j]);
+                const f2 e = fma2(mul2(c[j], pack2(-1.f, -1.f)), s, c[j]);
+                dc[W - 1][j] = mul2(dc[W - 1][j], fma2(s, e, s));
+            }
+        }
+        if (OWN) {
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                db[j] = add2(db[j], dc[W - 1][j]);
+#pragma unroll
+                for (int k = 0; k < W; ++k) dw[k][j] = fma2(dc[W - 1][j], x[k][j], dw[k][j]);
+            }
+        }
+    }
+    // The gradient of the position W - 1 tokens back, now complete.
+    __device__ __forceinline__ void complete(f2 (&o)[NP]) const {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            o[j] = mul2(w[W - 1][j], dc[0][j]);
+#pragma unroll
+            for (int k = 1; k < W; ++k) o[j] = fma2(w[W - 1 - k][j], dc[k][j], o[j]);
+        }
+    }
+    __device__ __forceinline__ void move() {
+        shift<W>(x);
+        shift<W>(dc);
+    }
+};
+
+// Steps [t, end) whose positions t - (W-1) are plain tokens of this run: no state in
+// or out, no end of the sequence among them.
+template <typename IN, typename DY, typename OUT, int W, bool FULL>
+__device__ __forceinline__ void back_run(const ConvArgs &a, Back<W> &k, int64_t t, int64_t end, int c0, int have) {
+    constexpr int PB = 4;                      // rows (of x and of d_out) loaded ahead
+    const SsmProblem &P = a.P;
+    const int64_t sx = P.u.stride, sy = P.dy.stride, D = P.D;
+    const IN *px = (const IN *)P.u.p + t * sx + c0;
+    const DY *py = (const DY *)P.dy.p + t * sy + c0;
+    const float *ps = P.u.scales + t * P.u.ngroups + c0 / kPackGroup;
+    OUT *po = (OUT *)a.out + (t - (W - 1)) * D + c0;
+    int left = (int)(end - t);
+    Raw<IN, V> nx[PB];
+    Raw<DY, V> ny[PB];
+    float ns[PB];
+    auto fetch = [&](int i) {
+        nx[i].template load<FULL>(px, have, P.u.vec);
+        ny[i].template load<FULL>(py, have, P.dy.vec);
+        ns[i] = 1.f;
+        if constexpr (sizeof(IN) == 1) {
+            ns[i] = __ldg(ps);
+            ps += P.u.ngroups;
+        }
+        px += sx;
+        py += sy;
+    };
+    auto token = [&](const Raw<IN, V> &x, const Raw<DY, V> &y, float s) {
+        f2 o[NP];
+        k.template step<IN, DY, true>(x, y, s, a.swish);
+        k.complete(o);
+        store_pairs<OUT, FULL>(po, o, have, a.ovec);
+        po += D;
+        k.move();
+    };
+    if (left >= PB) {
+#pragma unroll
+        for (int i = 0; i < PB; ++i) fetch(i);
+        for (; left >= PB; left -= PB) {
+            Raw<IN, V> rx[PB];
+            Raw<DY, V> ry[PB];
+            float rs[PB];
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                rx[i] = nx[i];
+                ry[i] = ny[i];
+                rs[i] = ns[i];
+            }
+            if (left >= 2 * PB) {
+#pragma unroll
+                for (int i = 0; i < PB; ++i) fetch(i);
+            }
+#pragma unroll
+            for (int i = 0; i < PB; ++i) token(rx[i], ry[i], rs[i]);
+        }
+    }
+    for (; left > 0; --left) {
+        fetch(0);
+        token(nx[0], ny[0], ns[0]);
+    }
+}
+
+template <typename IN, typename DY, typename OUT, int W>
 __global__ void __launch_bounds__(kThreads) kda_ssm_conv_backward_kernel(const ConvArgs a) {
-    constexpr int PB = 4;
     const SsmProblem &P = a.P;
     const int nvb = (P.D + V * kThreads - 1) / (V * kThreads);
     const int c0 = ((int)(blockIdx.x % nvb) * kThreads + threadIdx.x) * V;
@@ -196,13 +391,14 @@ __global__ void __launch_bounds__(kThreads) kda_ssm_conv_backward_kernel(const C
     const int64_t t0 = tile * a.tile, t1 = min(t0 + a.tile, (int64_t)P.T);
     const int have = P.D - c0;
     if (have <= 0) return;
-    float w[W][V], b[V], x[W][V], dw[W][V], db[V], dc[W][V];
-    load_taps<V, W>(a, c0, have, w, b);
+    const bool full = P.u.vec && P.dy.vec && a.ovec && have >= V;
+    Back<W> k;
+    load_taps<W>(a, c0, have, k.w, k.b);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        db[i] = 0.f;
+    for (int j = 0; j < NP; ++j) {
+        k.db[j] = 0;
 #pragma unroll
-        for (int k = 0; k < W; ++k) dw[k][i] = 0.f;
+        for (int i = 0; i < W; ++i) k.dw[i][j] = 0;
     }
     int n = 0;
     int64_t sa = 0, sb = 0, t = t0;
@@ -213,93 +409,59 @@ __global__ void __launch_bounds__(kThreads) kda_ssm_conv_backward_kernel(const C
         }
         const int64_t s0 = t, s1 = min(sb, t1);          // the tokens of this run in this sequence
         const int64_t last = min(sb, s1 + W - 1);        // dc is needed up to here
-        load_window<IN, V, W>(a, n, sa, t, c0, have, x);
+        load_window<IN, W>(a, n, sa, t, c0, have, k.x);
 #pragma unroll
-        for (int k = 0; k < W; ++k)
+        for (int i = 0; i < W; ++i)
 #pragma unroll
-            for (int i = 0; i < V; ++i) dc[k][i] = 0.f;
-        // step t gives dc_t and completes position t - (W-1); past the end dc = 0
-        for (; t < s1 + W - 1; t += PB) {
-            Raw<IN, V> rx[PB];
-            Raw<DY, V> ry[PB];
-            float sc[PB];
+            for (int j = 0; j < NP; ++j) k.dc[i][j] = 0;
+        // step t gives dc_t and completes position t - (W-1); past the end dc = 0.  The
+        // first W - 1 steps and those from s1 on are the careful ones.
+        while (t < s1 + W - 1) {
+            if (t == s0 + W - 1 && t < s1 && !(a.dcout && s1 > sb - (W - 1))) {
+                if (full) back_run<IN, DY, OUT, W, true>(a, k, t, s1, c0, have);
+                else back_run<IN, DY, OUT, W, false>(a, k, t, s1, c0, have);
+                t = s1;
+                continue;
+            }
+            Raw<IN, V> r;
+            Raw<DY, V> y;
+            r.clear();
+            y.clear();
+            float scale = 0.f;
+            if (t < last) {
+                r.load((const IN *)P.u.p + t * P.u.stride + c0, have, P.u.vec);
+                y.load((const DY *)P.dy.p + t * P.dy.stride + c0, have, P.dy.vec);
+                scale = scale_of<IN>(P.u, t, c0);
+            }
+            if (t < s1) k.template step<IN, DY, true>(r, y, scale, a.swish);
+            else k.template step<IN, DY, false>(r, y, scale, a.swish && t < last);
+            const int64_t p = t - (W - 1);                // the position whose gradient is complete
+            if (p >= s0 || s0 == sa) {                    // p < s0 = sa: the carried state
+                f2 o[NP];
+                k.complete(o);
+                // the carried state out holds the last W - 1 positions
+                const int64_t back = p - (sb - (W - 1));
+                if (a.dcout && back >= 0) {
+                    f2 e[NP];
+                    load4(a.dcout + ((int64_t)n * (W - 1) + back) * P.D + c0, e, have, a.fvec);
 #pragma unroll
-            for (int i = 0; i < PB; ++i) {
-                rx[i].clear();
-                ry[i].clear();
-                sc[i] = 0.f;
-                if (t + i < last) {
-                    rx[i].load((const IN *)P.u.p + (t + i) * P.u.stride + c0, have, P.u.vec);
-                    ry[i].load((const DY *)P.dy.p + (t + i) * P.dy.stride + c0, have, P.dy.vec);
-                    if constexpr (sizeof(IN) == 1) sc[i] = P.u.scales[(t + i) * P.u.ngroups + c0 / kPackGroup];
+                    for (int j = 0; j < NP; ++j) o[j] = add2(o[j], e[j]);
+                }
+                if (p >= sa) {
+                    store_pairs<OUT, false>((OUT *)a.out + p * P.D + c0, o, have, a.ovec);
+                } else if (a.dcin) {
+                    store4(a.dcin + ((int64_t)n * (W - 1) + (p - sa + W - 1)) * P.D + c0, o, have, a.fvec);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < PB; ++i) {
-                const int64_t ti = t + i;
-                if (ti >= s1 + W - 1) break;
-                const bool own = ti < s1;                 // counted by this run; later ones by the next
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    x[W - 1][j] = sizeof(IN) == 1 ? rx[i].get(j) * sc[i] : rx[i].get(j);
-                    float d = ry[i].get(j);               // 0 past the end
-                    if (a.swish) {
-                        float c = b[j];
-#pragma unroll
-                        for (int k = 0; k < W; ++k) c = fmaf(w[k][j], x[k][j], c);
-                        const float s = sigmoid_fast(c);
-                        d *= fmaf(c * s, 1.f - s, s);
-                    }
-                    if (ti >= last) d = 0.f;
-                    dc[W - 1][j] = d;
-                    if (own) {
-                        db[j] += d;
-#pragma unroll
-                        for (int k = 0; k < W; ++k) dw[k][j] = fmaf(d, x[k][j], dw[k][j]);
-                    }
-                }
-                const int64_t p = ti - (W - 1);           // the position whose gradient is complete
-                if (p >= s0 || s0 == sa) {                // p < s0 = sa: the carried state
-                    float o[V];
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        float v = 0.f;
-#pragma unroll
-                        for (int k = 0; k < W; ++k) v = fmaf(w[W - 1 - k][j], dc[k][j], v);
-                        o[j] = v;
-                    }
-                    // the carried state out holds the last W - 1 positions
-                    const int64_t back = p - (sb - (W - 1));
-                    if (a.dcout && back >= 0) {
-                        float e[V];
-                        load_cols<V>(a.dcout + ((int64_t)n * (W - 1) + back) * P.D + c0, e, have);
-#pragma unroll
-                        for (int j = 0; j < V; ++j) o[j] += e[j];
-                    }
-                    if (p >= sa) {
-                        store_row<OUT, V>((OUT *)a.out + p * P.D + c0, o, have, a.ovec);
-                    } else if (a.dcin) {
-                        float *q = a.dcin + ((int64_t)n * (W - 1) + (p - sa + W - 1)) * P.D + c0;
-#pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            if (j < have) q[j] = o[j];
-                    }
-                }
-                shift<V, W>(x);
-                shift<V, W>(dc);
-            }
+            k.move();
+            ++t;
         }
         t = s1;
     }
     float *part = a.part + tile * (W + 1) * P.D + c0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        if (j < have) {
-#pragma unroll
-            for (int k = 0; k < W; ++k) part[(int64_t)k * P.D + j] = dw[k][j];
-            part[(int64_t)W * P.D + j] = db[j];
-        }
-    }
+    for (int i = 0; i < W; ++i) store4(part + (int64_t)i * P.D, k.dw[i], have, a.fvec);
+    store4(part + (int64_t)W * P.D, k.db, have, a.fvec);
 }
 
 // dw and dbias: the runs' shares, added in their order.  A warp takes 32
@@ -339,10 +501,9 @@ __global__ void __launch_bounds__(kThreads) kda_ssm_conv_empty_kernel(const Conv
     if (sa == sb) a.dcin[i] = a.dcout ? a.dcout[i] : 0.f;
 }
 
-// Tokens of a run: 64 (32 without gradients), fewer where that would leave the
-// GPU without work: at least a warp a scheduler is wanted, and 16 tokens keep the
-// rows that two runs read within a fifth.
-int run_length(int64_t T, int32_t D, int V, int most) {
+// Tokens of a run: `most`, fewer where that would leave the GPU without work (16
+// warps an SM are wanted); 16 tokens keep the rows that two runs read within a fifth.
+int run_length(int64_t T, int32_t D, int most) {
     const int64_t columns = (D + (int64_t)V * 32 - 1) / (V * 32);   // warps across
     int tile = most;
     while (tile > 16 && (T + tile - 1) / tile * columns < 152 * 16) tile /= 2;
@@ -351,17 +512,16 @@ int run_length(int64_t T, int32_t D, int V, int most) {
 
 template <typename IN, typename OUT, int W>
 cudaError_t forward(ConvArgs &a, cudaStream_t stream) {
-    constexpr int V = sizeof(IN) == 2 ? 8 : 4;
     const SsmProblem &P = a.P;
+    const int64_t across = (P.D + V * kThreads - 1) / (V * kThreads);
     if (!P.cu && P.seq_len == 1) {
-        const int64_t n = (int64_t)P.N * ((P.D + V - 1) / V);
-        kda_ssm_conv_token_kernel<IN, OUT, V, W><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
+        kda_ssm_conv_token_kernel<IN, OUT, W><<<(unsigned)(P.N * across), kThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
     if (P.T > 0) {
-        a.tile = run_length(P.T, P.D, V, 32);
-        const int64_t blocks = (P.T + a.tile - 1) / a.tile * ((P.D + V * kThreads - 1) / (V * kThreads));
-        kda_ssm_conv_kernel<IN, OUT, V, W><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+        a.tile = run_length(P.T, P.D, 64);
+        const int64_t blocks = (P.T + a.tile - 1) / a.tile * across;
+        kda_ssm_conv_kernel<IN, OUT, W><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -380,16 +540,13 @@ cudaError_t forward_taps(ConvArgs &a, cudaStream_t s) {
     return forward<IN, OUT, 4>(a, s);
 }
 
-constexpr int kBackV = 4;
-
 template <typename IN, typename DY, typename OUT, int W>
 cudaError_t backward(ConvArgs &a, float *dw, float *dbias, cudaStream_t stream) {
-    constexpr int V = kBackV;
     const SsmProblem &P = a.P;
     const int64_t tiles = kda_ssm_conv_backward_tiles(P, &a.tile);
     if (tiles > 0) {
         const int64_t blocks = tiles * ((P.D + V * kThreads - 1) / (V * kThreads));
-        kda_ssm_conv_backward_kernel<IN, DY, OUT, V, W><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+        kda_ssm_conv_backward_kernel<IN, DY, OUT, W><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -422,7 +579,12 @@ cudaError_t backward_input(ConvArgs &a, float *dw, float *dbias, cudaStream_t s)
 
 bool out_vec(const void *p, const SsmProblem &P) {
     const int es = P.out_dtype == KDA_DTYPE_BF16 ? 2 : 4;
-    return ((uintptr_t)p & 15u) == 0 && (int64_t)P.D * es % 16 == 0;
+    return ((uintptr_t)p & 15u) == 0 && (int64_t)P.D * es % (V * es) == 0;
+}
+bool all_aligned(const SsmProblem &P, std::initializer_list<const void *> ps) {
+    for (const void *p : ps)
+        if ((uintptr_t)p & 15u) return false;
+    return P.D % V == 0;
 }
 
 }  // namespace
@@ -438,6 +600,7 @@ cudaError_t kda_launch_ssm_conv(const SsmProblem &P, const float *w, const float
     a.out = out;
     a.cout = cout;
     a.ovec = out_vec(out, P);
+    a.fvec = all_aligned(P, {w, bias, cin, cout});
     const bool ib = P.in_dtype == KDA_DTYPE_BF16, ob = P.out_dtype == KDA_DTYPE_BF16;
     if (ib && ob) return forward_taps<__nv_bfloat16, __nv_bfloat16>(a, stream);
     if (ib) return forward_taps<__nv_bfloat16, float>(a, stream);
@@ -446,7 +609,7 @@ cudaError_t kda_launch_ssm_conv(const SsmProblem &P, const float *w, const float
 }
 
 int64_t kda_ssm_conv_backward_tiles(const SsmProblem &P, int *tile) {
-    *tile = run_length(P.T, P.D, kBackV, 64);
+    *tile = run_length(P.T, P.D, 64);
     return ((int64_t)P.T + *tile - 1) / *tile;
 }
 
@@ -464,6 +627,7 @@ cudaError_t kda_launch_ssm_conv_backward(const SsmProblem &P, const float *w, co
     a.dcin = dcin;
     a.part = workspace;
     a.ovec = out_vec(dx, P);
+    a.fvec = all_aligned(P, {w, bias, cin, dcout, dcin, workspace});
     const bool ib = P.in_dtype == KDA_DTYPE_BF16, ob = P.out_dtype == KDA_DTYPE_BF16;
     if (ib && ob) return backward_input<__nv_bfloat16, __nv_bfloat16>(a, dw, dbias, stream);
     if (ib) return backward_input<__nv_bfloat16, float>(a, dw, dbias, stream);

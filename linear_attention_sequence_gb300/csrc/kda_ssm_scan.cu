@@ -19,8 +19,10 @@ namespace {
 
 using namespace kda;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kWarps = 4;                 // warps that scan
+constexpr int kScanners = 32 * kWarps;
+constexpr int kStagers = 256;             // threads that stage
+constexpr int kThreads = kScanners + kStagers;
 constexpr int TT = kSsmTile;
 
 struct ScanArgs {
@@ -37,21 +39,135 @@ template <int LN>
 struct Layout {
     static constexpr int CW = 32 / LN;         // channels of a warp
     static constexpr int CB = kWarps * CW;     // channels of a block
-    static constexpr int E = CB / 4;           // elements of a row that one thread stages (4 threads a row)
-    static constexpr int YS = CB + 8;          // row of the output tile: the 4 tokens a warp writes at once take different banks
-    static constexpr int BI = (TT * LN + kThreads - 1) / kThreads;   // 4-element pieces of B (and C) that a thread stages
+    static constexpr int TR = CB >= 16 ? 8 : 4;   // threads that stage a row
+    static constexpr int E = CB / TR;          // its elements that each of them stages
+    static constexpr int BI = (TT * LN + kStagers - 1) / kStagers;   // 4-element pieces of B (and C) that a thread stages
     struct Smem {
-        float2 d[2][TT][CB];                   // Delta, Delta u
+        float2 d[2][TT][CB];                   // Delta, Delta u; channel pairs permuted (column())
         float4 b[2][TT][LN], c[2][TT][LN];
-        float y[TT][YS];
+        float y[2][TT][CB][LN];                // the lanes' shares of C_t h_t
     };
+    // Where channel c lies in a row of d: the 16-byte pieces that eight staging threads
+    // write at once take different banks, and the channels of a warp stay together.
+    static __device__ __forceinline__ int column(int c) { return c ^ (((c >> 4) & 3) << 1); }
+};
+
+// The staging warps: load a tile, form Delta and Delta u, and finish the outputs of
+// an earlier tile.
+template <typename IN, typename OUT, int LN>
+struct Stager {
+    using L = Layout<LN>;
+    static constexpr int E = L::E;
+    const ScanArgs &a;
+    typename L::Smem &sm;
+    int64_t sb;
+    int tid, srow, sc, ch0, have;
+    float bias[E], skip[E];
+    Raw<IN, E> ru, rd, rz;                     // the tile being fetched
+    Raw<IN, E> u0, z0, u1, z1;                 // of the tile staged last, and of the one before
+    Raw<IN, 4> rb[L::BI], rc[L::BI];
+
+    __device__ __forceinline__ Stager(const ScanArgs &a_, typename L::Smem &sm_, int64_t sb_, int ch0_)
+        : a(a_), sm(sm_), sb(sb_), ch0(ch0_) {
+        tid = threadIdx.x - kScanners;
+        srow = tid / L::TR;
+        sc = tid % L::TR * E;
+        have = srow < TT ? a.P.D - (ch0 + sc) : 0;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            bias[i] = (a.P.dt_bias && i < have) ? a.P.dt_bias[ch0 + sc + i] : 0.f;
+            skip[i] = (a.P.skip && i < have) ? a.P.skip[ch0 + sc + i] : 0.f;
+        }
+        u0.clear();
+        z0.clear();
+    }
+    __device__ __forceinline__ void fetch(int64_t t0) {
+        const SsmProblem &P = a.P;
+        const int64_t t = t0 + srow;
+        ru.clear();
+        rd.clear();
+        rz.clear();
+        if (t < sb && have > 0) {
+            ru.load((const IN *)P.u.p + t * P.u.stride + ch0 + sc, have, P.u.vec);
+            rd.load((const IN *)P.dt.p + t * P.dt.stride + ch0 + sc, have, P.dt.vec);
+            if (P.z.p) rz.load((const IN *)P.z.p + t * P.z.stride + ch0 + sc, have, P.z.vec);
+        }
+#pragma unroll
+        for (int k = 0; k < L::BI; ++k) {
+            const int i = tid + k * kStagers;
+            const int64_t tb = t0 + i / LN;
+            const int nb = 4 * (i % LN);
+            rb[k].clear();
+            rc[k].clear();
+            if (i < TT * LN && tb < sb && nb < P.S) {
+                rb[k].load((const IN *)P.B.p + tb * P.B.stride + nb, P.S - nb, P.B.vec);
+                rc[k].load((const IN *)P.C.p + tb * P.C.stride + nb, P.S - nb, P.C.vec);
+            }
+        }
+    }
+    // The fetched tile, which starts at t0, into buffer `buf`; tokens past the end
+    // have Delta = 0.
+    __device__ __forceinline__ void stage(int64_t t0, int buf) {
+        const bool in = t0 + srow < sb;
+        if (srow < TT) {
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            float4 v;
+            const float x = rd.get(i) + bias[i], y = rd.get(i + 1) + bias[i + 1];
+            v.x = in ? (a.P.softplus ? softplus_fast(x) : x) : 0.f;
+            v.z = in ? (a.P.softplus ? softplus_fast(y) : y) : 0.f;
+            v.y = v.x * ru.get(i);
+            v.w = v.z * ru.get(i + 1);
+            *reinterpret_cast<float4 *>(&sm.d[buf][srow][L::column(sc + i)]) = v;
+        }
+        }
+#pragma unroll
+        for (int k = 0; k < L::BI; ++k) {
+            const int i = tid + k * kStagers;
+            if (i < TT * LN) {
+                sm.b[buf][i / LN][i % LN] = make_float4(rb[k].get(0), rb[k].get(1), rb[k].get(2), rb[k].get(3));
+                sm.c[buf][i / LN][i % LN] = make_float4(rc[k].get(0), rc[k].get(1), rc[k].get(2), rc[k].get(3));
+            }
+        }
+        u1 = u0;
+        z1 = z0;
+        u0 = ru;
+        z0 = rz;
+    }
+    // The outputs of the tile that starts at t0.
+    __device__ __forceinline__ void finish(int64_t t0, int buf, const Raw<IN, E> &u, const Raw<IN, E> &z) {
+        if (t0 + srow >= sb || have <= 0) return;
+        float o[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float *p = sm.y[buf][srow][sc + i];
+            float v = 0.f;
+            if constexpr (LN == 2) {
+                const float2 y = *reinterpret_cast<const float2 *>(p);
+                v = y.x + y.y;
+            } else {
+#pragma unroll
+                for (int k = 0; k < LN; k += 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(p + k);
+                    v += (y.x + y.y) + (y.z + y.w);
+                }
+            }
+            v = fmaf(skip[i], u.get(i), v);
+            if (a.P.z.p) {
+                const float g = z.get(i);
+                v *= g * sigmoid_fast(g);
+            }
+            o[i] = v;
+        }
+        store_row<OUT, E>((OUT *)a.out + (t0 + srow) * a.P.D + ch0 + sc, o, have, a.ovec);
+    }
 };
 
 template <typename IN, typename OUT, int LN>
 __global__ void __launch_bounds__(kThreads)
 kda_ssm_scan_kernel(const ScanArgs a) {
     using L = Layout<LN>;
-    constexpr int CW = L::CW, CB = L::CB, E = L::E;
+    constexpr int CW = L::CW, CB = L::CB;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     typename L::Smem &sm = *reinterpret_cast<typename L::Smem *>(smem_raw);
     __shared__ int s_seq;
@@ -62,9 +178,34 @@ kda_ssm_scan_kernel(const ScanArgs a) {
     const int ch0 = (blockIdx.x % ncb) * CB;
     int64_t sa, sb;
     seq_bounds(P.cu, n, P.T, P.seq_len, sa, sb);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t tiles = (sb - sa + TT - 1) / TT;
 
-    // this lane's states
+    if (threadIdx.x >= kScanners) {
+        // Between barriers k and k + 1 the scanning warps run over tile k; these
+        // warps stage tile k + 1 and finish tile k - 1.
+        Stager<IN, OUT, LN> st(a, sm, sb, ch0);
+        if (tiles > 0) {
+            st.fetch(sa);
+            st.stage(sa, 0);
+        }
+        if (tiles > 1) st.fetch(sa + TT);
+        __syncthreads();
+        for (int64_t k = 0; k < tiles; ++k) {
+            const int64_t t0 = sa + k * TT;
+            if (k + 1 < tiles) {
+                st.stage(t0 + TT, (int)(k + 1) & 1);
+                if (k + 2 < tiles) st.fetch(t0 + 2 * TT);
+            } else {
+                st.u1 = st.u0;
+                st.z1 = st.z0;
+            }
+            __syncthreads();
+            st.finish(t0, (int)k & 1, st.u1, st.z1);
+        }
+        return;
+    }
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int wc = warp * CW + lane / LN;      // channel within the block
     const int ch = ch0 + wc;
     const int q = lane % LN, n0 = 4 * q;
@@ -80,88 +221,53 @@ kda_ssm_scan_kernel(const ScanArgs a) {
             h23 = pack2(h.z, h.w);
         }
     }
-
-    // this thread's part of the staging: row tid / 4, E channels
-    const int srow = tid >> 2, sc = (tid & 3) * E;
-    const int have = P.D - (ch0 + sc);         // channels that exist (may be <= 0)
-    float bias[E], skip[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        bias[i] = (P.dt_bias && i < have) ? P.dt_bias[ch0 + sc + i] : 0.f;
-        skip[i] = (P.skip && i < have) ? P.skip[ch0 + sc + i] : 0.f;
-    }
-    Raw<IN, E> ru, rd, rz;
-    Raw<IN, 4> rb[L::BI], rc[L::BI];
-    auto fetch = [&](int64_t t0) {
-        const int64_t t = t0 + srow;
-        ru.clear();
-        rd.clear();
-        rz.clear();
-        if (t < sb && have > 0) {
-            ru.load((const IN *)P.u.p + t * P.u.stride + ch0 + sc, have, P.u.vec);
-            rd.load((const IN *)P.dt.p + t * P.dt.stride + ch0 + sc, have, P.dt.vec);
-            if (P.z.p) rz.load((const IN *)P.z.p + t * P.z.stride + ch0 + sc, have, P.z.vec);
-        }
-#pragma unroll
-        for (int k = 0; k < L::BI; ++k) {
-            const int i = tid + k * kThreads;
-            const int64_t tb = t0 + i / LN;
-            const int nb = 4 * (i % LN);
-            rb[k].clear();
-            rc[k].clear();
-            if (i < TT * LN && tb < sb && nb < P.S) {
-                rb[k].load((const IN *)P.B.p + tb * P.B.stride + nb, P.S - nb, P.B.vec);
-                rc[k].load((const IN *)P.C.p + tb * P.C.stride + nb, P.S - nb, P.C.vec);
-            }
-        }
-    };
-    fetch(sa);
     const int64_t row0 = a.chunks ? ckpt_first_row(P.cu, n, P.T, P.seq_len, TT) : 0;
-
-    for (int64_t t0 = sa, tile = 0; t0 < sb; t0 += TT, ++tile) {
-        const int buf = (int)(tile & 1);
-        // stage: tokens past the end have Delta = 0
-        {
-            const bool in = t0 + srow < sb;
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float x = rd.get(i) + bias[i];
-                const float dl = in ? (P.softplus ? softplus_fast(x) : x) : 0.f;
-                sm.d[buf][srow][sc + i] = make_float2(dl, dl * ru.get(i));
-            }
-#pragma unroll
-            for (int k = 0; k < L::BI; ++k) {
-                const int i = tid + k * kThreads;
-                if (i < TT * LN) {
-                    sm.b[buf][i / LN][i % LN] = make_float4(rb[k].get(0), rb[k].get(1), rb[k].get(2), rb[k].get(3));
-                    sm.c[buf][i / LN][i % LN] = make_float4(rc[k].get(0), rc[k].get(1), rc[k].get(2), rc[k].get(3));
-                }
-            }
-        }
-        const Raw<IN, E> cu_u = ru, cu_z = rz;
-        if (t0 + TT < sb) fetch(t0 + TT);
-        __syncthreads();
-
-        constexpr int G = LN < 4 ? 4 : LN;     // tokens between two reductions
-#pragma unroll 1
-        for (int g = 0; g < TT; g += G) {
-            float y[G];
+    const int col = L::column(wc);
+    __syncthreads();
+    for (int64_t k = 0; k < tiles; ++k) {
+        const int buf = (int)k & 1;
+        // Groups of G tokens.  While one group's recurrence (a chain of fused
+        // multiply-adds) runs, the next group's decays and inputs are formed and the
+        // operands of the one behind it are read.
+        constexpr int G = 4;
+        float *ys = sm.y[buf][0][wc] + q;
+        float2 d[G];
+        ulonglong2 b[G], c[2][G];
+        f2 a01[2][G], a23[2][G], x01[2][G], x23[2][G];
+        auto read = [&](int g) {
 #pragma unroll
             for (int i = 0; i < G; ++i) {
-                const float2 d = sm.d[buf][g + i][wc];
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&sm.b[buf][g + i][q]);
-                const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(&sm.c[buf][g + i][q]);
-                const f2 dd = pack2(d.x, d.x), du = pack2(d.y, d.y);
-                h01 = fma2(exp2_pair(mul2(dd, A01)), h01, mul2(du, b.x));
-                h23 = fma2(exp2_pair(mul2(dd, A23)), h23, mul2(du, b.y));
-                y[i] = sum2(fma2(c.x, h01, mul2(c.y, h23)));
+                d[i] = sm.d[buf][g * G + i][col];
+                b[i] = *reinterpret_cast<const ulonglong2 *>(&sm.b[buf][g * G + i][q]);
             }
-            reduce_scatter<LN, 1, G>(y);
+        };
+        auto form = [&](int g) {
 #pragma unroll
-            for (int i = 0; i < G / LN; ++i) sm.y[g + q * (G / LN) + i][wc] = y[i];
+            for (int i = 0; i < G; ++i) {
+                const f2 dd = pack2(d[i].x, d[i].x), du = pack2(d[i].y, d[i].y);
+                a01[g & 1][i] = exp2_pair(mul2(dd, A01));
+                a23[g & 1][i] = exp2_pair(mul2(dd, A23));
+                x01[g & 1][i] = mul2(du, b[i].x);
+                x23[g & 1][i] = mul2(du, b[i].y);
+                c[g & 1][i] = *reinterpret_cast<const ulonglong2 *>(&sm.c[buf][g * G + i][q]);
+            }
+        };
+        read(0);
+        form(0);
+        read(1);
+#pragma unroll
+        for (int g = 0; g < TT / G; ++g) {
+            if (g + 1 < TT / G) form(g + 1);
+            if (g + 2 < TT / G) read(g + 2);
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                h01 = fma2(a01[g & 1][i], h01, x01[g & 1][i]);
+                h23 = fma2(a23[g & 1][i], h23, x23[g & 1][i]);
+                ys[(g * G + i) * CB * LN] = sum2(fma2(c[g & 1][i].x, h01, mul2(c[g & 1][i].y, h23)));
+            }
         }
-        if (a.chunks && t0 + TT <= sb && live) {
-            const int64_t row = row0 + tile;
+        if (a.chunks && sa + (k + 1) * TT <= sb && live) {
+            const int64_t row = row0 + k;
             if (row < a.chunk_capacity) {
                 float4 h;
                 unpack2(h01, h.x, h.y);
@@ -170,19 +276,6 @@ kda_ssm_scan_kernel(const ScanArgs a) {
             }
         }
         __syncthreads();
-        if (t0 + srow < sb && have > 0) {
-            float o[E];
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                float v = fmaf(skip[i], cu_u.get(i), sm.y[srow][sc + i]);
-                if (P.z.p) {
-                    const float z = cu_z.get(i);
-                    v *= z * sigmoid_fast(z);
-                }
-                o[i] = v;
-            }
-            store_row<OUT, E>((OUT *)a.out + (t0 + srow) * P.D + ch0 + sc, o, have, a.ovec);
-        }
     }
     if (a.fin && live) {
         float4 h;

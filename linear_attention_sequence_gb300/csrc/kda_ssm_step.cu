@@ -3,10 +3,11 @@
 //
 // HBM-bound: a state entry is read once and written once, 8 bytes for about 7
 // operations.  One lane holds four states of a channel (a 16-byte access),
-// LN = ceil(S / 4) lanes (a power of two) a channel; the lanes of a warp cover
+// LN >= S / 4 lanes (2, 4, 8 or 16) a channel; the lanes of a warp cover
 // neighbouring channels, so a warp moves whole lines.  NB sequences a lane keep
 // NB state loads in flight and use the decay rates A (read once from DRAM, then
-// from L2) NB times.
+// from L2) NB times; a channel's lanes share out the step sizes and gates of
+// the NB sequences between them.
 
 #include "kda_ssm_common.cuh"
 
@@ -22,93 +23,121 @@ struct StepArgs {
     void *out;
 };
 
-template <typename IN, typename OUT, int LN, int NB>
+// NB sequences a lane; lane q of a channel prepares and finishes OWN of them: numbers
+// q OWN .. (where LN > NB, lanes from NB on none).  FULL: four states at a time.
+template <typename IN, typename OUT, int LN, int NB, bool FULL>
 __global__ void __launch_bounds__(kThreads) kda_ssm_step_kernel(const StepArgs a) {
     constexpr int CB = kThreads / LN;
+    constexpr int OWN = NB >= LN ? NB / LN : 1;
     const SsmProblem &P = a.P;
     const int ncb = (P.D + CB - 1) / CB;
-    const int seq0 = (int)(blockIdx.x / ncb) * NB;
-    const int ch = (int)(blockIdx.x % ncb) * CB + threadIdx.x / LN;
+    const int64_t seq0 = (int64_t)(blockIdx.x / ncb) * NB;
+    const int count = (int)min((int64_t)NB, P.N - seq0);
+    const int chx = (int)(blockIdx.x % ncb) * CB + threadIdx.x / LN;
+    const bool live = chx < P.D;
+    const int ch = live ? chx : P.D - 1;        // lanes past the last channel run along on it
     const int q = threadIdx.x % LN, n0 = 4 * q;
-    const bool live = ch < P.D;
     float4 h[NB];
     Raw<IN, 4> rb[NB], rc[NB];
-    float dt[NB], u[NB], z[NB];
+    float *st = a.state + (seq0 * P.D + ch) * P.S + n0;
+    const int64_t sstep = (int64_t)P.D * P.S;
+    const IN *pb = (const IN *)P.B.p + seq0 * P.B.stride + n0, *pc = (const IN *)P.C.p + seq0 * P.C.stride + n0;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-        const int64_t n = seq0 + i;
         h[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         rb[i].clear();
         rc[i].clear();
-        dt[i] = u[i] = z[i] = 0.f;
-        if (n < P.N && live) {
-            const float *s = a.state + (n * P.D + ch) * P.S;
-            if (P.svec) {
-                if (n0 < P.S) h[i] = __ldcs(reinterpret_cast<const float4 *>(s + n0));
+        if (i < count && n0 < P.S) {
+            if (FULL) {
+                h[i] = __ldcs(reinterpret_cast<const float4 *>(st + i * sstep));
             } else {
-                h[i] = load_states(s, n0, P.S, false);
+                h[i] = load_states(st + i * sstep, 0, P.S - n0, P.svec);
             }
-            if (n0 < P.S) {
-                rb[i].load((const IN *)P.B.p + n * P.B.stride + n0, P.S - n0, P.B.vec);
-                rc[i].load((const IN *)P.C.p + n * P.C.stride + n0, P.S - n0, P.C.vec);
-            }
-            dt[i] = ld_elem((const IN *)P.dt.p + n * P.dt.stride + ch);
-            u[i] = ld_elem((const IN *)P.u.p + n * P.u.stride + ch);
-            if (P.z.p) z[i] = ld_elem((const IN *)P.z.p + n * P.z.stride + ch);
+            rb[i].template load<FULL>(pb + i * P.B.stride, P.S - n0, P.B.vec);
+            rc[i].template load<FULL>(pc + i * P.C.stride, P.S - n0, P.C.vec);
         }
+    }
+    const int first = OWN * (LN > NB && q >= NB ? 0 : q);
+    float dt[OWN], u[OWN], z[OWN];
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const int64_t n = seq0 + min(first + i, count - 1);
+        dt[i] = ld_elem((const IN *)P.dt.p + n * P.dt.stride + ch);
+        u[i] = ld_elem((const IN *)P.u.p + n * P.u.stride + ch);
+        z[i] = P.z.p ? ld_elem((const IN *)P.z.p + n * P.z.stride + ch) : 0.f;
     }
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-    float bias = 0.f, skip = 0.f;
-    if (live) {
-        A = load_states(P.A + (int64_t)ch * P.S, n0, P.S, P.svec);
-        if (P.dt_bias) bias = P.dt_bias[ch];
-        if (P.skip) skip = P.skip[ch];
+    if (n0 < P.S) {
+        const float *p = P.A + (int64_t)ch * P.S + n0;
+        A = FULL ? *reinterpret_cast<const float4 *>(p) : load_states(p, 0, P.S - n0, P.svec);
     }
     A.x *= kLog2e; A.y *= kLog2e; A.z *= kLog2e; A.w *= kLog2e;
+    const float bias = P.dt_bias ? P.dt_bias[ch] : 0.f, skip = P.skip ? P.skip[ch] : 0.f;
+    float dl[OWN], du[OWN];
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const float x = dt[i] + bias;
+        dl[i] = P.softplus ? softplus_fast(x) : x;
+        du[i] = dl[i] * u[i];
+    }
+    float y[NB];
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-        const int64_t n = seq0 + i;
-        const float x = dt[i] + bias;
-        const float dl = P.softplus ? softplus_fast(x) : x;
-        const float du = dl * u[i];
-        h[i].x = fmaf(exp2_fast(dl * A.x), h[i].x, du * rb[i].get(0));
-        h[i].y = fmaf(exp2_fast(dl * A.y), h[i].y, du * rb[i].get(1));
-        h[i].z = fmaf(exp2_fast(dl * A.z), h[i].z, du * rb[i].get(2));
-        h[i].w = fmaf(exp2_fast(dl * A.w), h[i].w, du * rb[i].get(3));
-        float y = fmaf(rc[i].get(0), h[i].x, rc[i].get(1) * h[i].y) + fmaf(rc[i].get(2), h[i].z, rc[i].get(3) * h[i].w);
-#pragma unroll
-        for (int off = LN / 2; off; off /= 2) y += __shfl_xor_sync(0xffffffffu, y, off);
-        if (n < P.N && live) {
-            float *s = a.state + (n * P.D + ch) * P.S;
-            if (P.svec) {
-                if (n0 < P.S) __stcs(reinterpret_cast<float4 *>(s + n0), h[i]);
+        const float d = __shfl_sync(0xffffffffu, dl[i % OWN], i / OWN, LN), x = __shfl_sync(0xffffffffu, du[i % OWN], i / OWN, LN);
+        h[i].x = fmaf(exp2_fast(d * A.x), h[i].x, x * rb[i].get(0));
+        h[i].y = fmaf(exp2_fast(d * A.y), h[i].y, x * rb[i].get(1));
+        h[i].z = fmaf(exp2_fast(d * A.z), h[i].z, x * rb[i].get(2));
+        h[i].w = fmaf(exp2_fast(d * A.w), h[i].w, x * rb[i].get(3));
+        y[i] = fmaf(rc[i].get(0), h[i].x, rc[i].get(1) * h[i].y) + fmaf(rc[i].get(2), h[i].z, rc[i].get(3) * h[i].w);
+        if (i < count && live && n0 < P.S) {
+            if (FULL) {
+                __stcs(reinterpret_cast<float4 *>(st + i * sstep), h[i]);
             } else {
-                store_states(s, h[i], n0, P.S, false);
-            }
-            if (q == 0) {
-                y = fmaf(skip, u[i], y);
-                if (P.z.p) y *= z[i] * sigmoid_fast(z[i]);
-                st_elem((OUT *)a.out + n * P.D + ch, y);
+                store_states(st + i * sstep, h[i], 0, P.S - n0, P.svec);
             }
         }
     }
+    if constexpr (LN > NB) {
+        // lanes NB apart first, then as below
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int off = LN / 2; off >= NB; off /= 2) y[i] += __shfl_xor_sync(0xffffffffu, y[i], off);
+        reduce_scatter<NB, 1, NB>(y);
+    } else {
+        reduce_scatter<LN, 1, NB>(y);
+    }
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        if (live && q * OWN + i < count) {
+            float v = fmaf(skip, u[i], y[i]);
+            if (P.z.p) v *= z[i] * sigmoid_fast(z[i]);
+            st_elem((OUT *)a.out + (seq0 + q * OWN + i) * P.D + ch, v);
+        }
+    }
+}
+
+template <typename IN, typename OUT, int LN, int NB>
+cudaError_t launch_nb(const StepArgs &a, cudaStream_t stream) {
+    const SsmProblem &P = a.P;
+    const int64_t blocks = (P.D + kThreads / LN - 1) / (kThreads / LN) * (((int64_t)P.N + NB - 1) / NB);
+    if (P.svec && P.B.vec && P.C.vec)
+        kda_ssm_step_kernel<IN, OUT, LN, NB, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    else
+        kda_ssm_step_kernel<IN, OUT, LN, NB, false><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename IN, typename OUT, int LN>
 cudaError_t launch(const StepArgs &a, cudaStream_t stream) {
     const int64_t ncb = (a.P.D + kThreads / LN - 1) / (kThreads / LN);
     // four sequences a lane once that still leaves every SM several blocks
-    if (ncb * a.P.N >= 4 * 152 * 8) {
-        kda_ssm_step_kernel<IN, OUT, LN, 4><<<(unsigned)(ncb * ((a.P.N + 3) / 4)), kThreads, 0, stream>>>(a);
-    } else {
-        kda_ssm_step_kernel<IN, OUT, LN, 1><<<(unsigned)(ncb * a.P.N), kThreads, 0, stream>>>(a);
-    }
-    return cudaGetLastError();
+    if (ncb * a.P.N >= 4 * 152 * 8) return launch_nb<IN, OUT, LN, 4>(a, stream);
+    return launch_nb<IN, OUT, LN, 1>(a, stream);
 }
 
 template <typename IN, typename OUT>
 cudaError_t by_states(const StepArgs &a, cudaStream_t s) {
-    if (a.P.S <= 4) return launch<IN, OUT, 1>(a, s);
     if (a.P.S <= 8) return launch<IN, OUT, 2>(a, s);
     if (a.P.S <= 16) return launch<IN, OUT, 4>(a, s);
     if (a.P.S <= 32) return launch<IN, OUT, 8>(a, s);

@@ -8,7 +8,26 @@ import torch
 
 import linear_attention_sequence_gb300 as kda
 from linear_attention_sequence_gb300 import _build
-from linear_attention_sequence_gb300._ssm import _Grads, _Inputs, _Rows, _SsmDims
+
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("scales", ctypes.c_void_p)]
+
+
+class _SsmDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_seqs", "total_tokens", "channels", "state_size",
+                                              "in_dtype", "out_dtype")]
+
+
+class _Inputs(ctypes.Structure):
+    _fields_ = [(n, _Rows) for n in ("u", "dt", "B", "C", "z")] + [
+        (n, ctypes.c_void_p) for n in ("A", "D", "dt_bias", "cu_seqlens")] + [("delta_softplus", ctypes.c_int32)]
+
+
+class _Grads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("du", "ddt", "dB", "dC", "dz", "dA", "dD", "ddt_bias", "d_init_state")]
+
 
 INVALID, UNSUPPORTED = 1, 2
 BF16 = 1
@@ -196,6 +215,16 @@ def test_nothing_to_do_launches_nothing(L):
     assert scan(L, d, inputs(), out=None, fin=None) == 0
     d.state_size = 4
     assert conv(L, d, out=None, cout=None) == 0
+
+
+def test_binding_packs_the_structures():
+    """The binding's byte layouts are those of the C structures."""
+    from linear_attention_sequence_gb300 import _ssm
+    for packer, struct in ((_ssm._ROWS, _Rows), (_ssm._DIMS, _SsmDims), (_ssm._INPUTS, _Inputs), (_ssm._GRADS, _Grads)):
+        assert packer.size == ctypes.sizeof(struct)
+    i = inputs(cu_seqlens=at(9))
+    v = [x for n in ("u", "dt", "B", "C", "z") for x in (getattr(i, n).data, getattr(i, n).stride, 0)]
+    assert _ssm._INPUTS.pack(*v, i.A, i.D, i.dt_bias, i.cu_seqlens, 1) == bytes(i)
 
 
 def test_binding_refuses():
