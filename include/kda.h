@@ -549,10 +549,12 @@ kda_status kda_ssm_conv_backward(const kda_ssm_dims *dims, const kda_rows *x, co
  *   chunk_states device fp32 [chunk_capacity, D, S] or NULL (with chunk_capacity 0): the
  *                state after every KDA_CHUNK tokens of each sequence, rows as in
  *                kda_prefill_checkpointed with interval KDA_CHUNK; what the gradients need.
+ *   workspace    kda_ssm_scan_workspace(dims) bytes (0 for batches that need none), 16-byte aligned.
  */
+int64_t kda_ssm_scan_workspace(const kda_ssm_dims *dims);
 kda_status kda_ssm_scan(const kda_ssm_dims *dims, const kda_ssm_inputs *in, const float *init_state,
                         void *out, float *final_state, float *chunk_states, int64_t chunk_capacity,
-                        kda_stream_t stream);
+                        void *workspace, int64_t workspace_bytes, kda_stream_t stream);
 
 /*
  * kda_ssm_step -- one token for each of N sequences: state (device fp32 [N, D, S],

@@ -29,12 +29,13 @@ def declare(L):
     for name, args in (("kda_act_pack8", [_i32, _i32, _i32] + [_vp] * 4),
                        ("kda_ssm_conv", [_vp] * 6 + [_i32] + [_vp] * 3),
                        ("kda_ssm_conv_backward", [_vp] * 6 + [_i32] + [_vp] * 7 + [_i64, _vp]),
-                       ("kda_ssm_scan", [_vp] * 6 + [_i64, _vp]),
+                       ("kda_ssm_scan", [_vp] * 6 + [_i64, _vp, _i64, _vp]),
                        ("kda_ssm_step", [_vp] * 5),
                        ("kda_ssm_scan_backward", [_vp] * 4 + [_i64] + [_vp] * 4 + [_i64, _vp])):
         getattr(L, name).argtypes = args
         getattr(L, name).restype = ctypes.c_int
-    for name in ("kda_ssm_conv_backward_workspace", "kda_ssm_scan_backward_workspace"):
+    for name in ("kda_ssm_conv_backward_workspace", "kda_ssm_scan_workspace",
+                 "kda_ssm_scan_backward_workspace"):
         getattr(L, name).argtypes = [_vp]
         getattr(L, name).restype = _i64
 
@@ -284,8 +285,10 @@ def kda_ssm_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, init_state=None, 
             chunk_states = torch.empty((rows, ch, S), dtype=_F32, device=dt.device)
         cap = 0 if chunk_states is None else chunk_states.shape[0]
         chunks = _is(chunk_states, "chunk_states", dev, _F32, (cap, ch, S))
+        ws = _workspace("kda_ssm_scan_workspace", dims, dt.device)
         _run("kda_ssm_scan", dev, dims, ins, init, _is(out, "out", dev, odt, (T, ch)),
-             _is(final_state, "final_state", dev, _F32, (N, ch, S)), chunks, cap)
+             _is(final_state, "final_state", dev, _F32, (N, ch, S)), chunks, cap, ws.data_ptr(),
+             ws.shape[0])
     return (out, final_state) if chunk_states is None else (out, final_state, chunk_states)
 
 

@@ -82,7 +82,7 @@ Checked check_rows(const kda_rows *x, int64_t T, int64_t width, size_t es, bool 
 size_t cu_bytes(const SsmProblem &P) { return P.cu ? (size_t)(P.N + 1) * 4 : 0; }
 
 // Pieces that the scan kernels read of a row: a thread's share of a block's
-// channels (at least four threads a row), at most 16 bytes.
+// channels, at most 16 bytes.
 size_t scan_piece(int S, size_t es) {
     const int ln = S <= 8 ? 2 : S <= 16 ? 4 : S <= 32 ? 8 : 16;
     const size_t b = 32 / ln * es;
@@ -223,8 +223,15 @@ kda_status kda_ssm_conv_backward(const kda_ssm_dims *dims, const kda_rows *x, co
     return e == cudaSuccess ? KDA_OK : kda_cuda_fail(e, "kda_ssm_conv_backward");
 }
 
+int64_t kda_ssm_scan_workspace(const kda_ssm_dims *dims) {
+    SsmProblem P;
+    if (check_dims(dims, false, P) != KDA_OK) return -1;
+    return kda_ssm_scan_ws(P);
+}
+
 kda_status kda_ssm_scan(const kda_ssm_dims *dims, const kda_ssm_inputs *in, const float *init_state, void *out,
-                        float *final_state, float *chunk_states, int64_t chunk_capacity, kda_stream_t stream) {
+                        float *final_state, float *chunk_states, int64_t chunk_capacity, void *workspace,
+                        int64_t workspace_bytes, kda_stream_t stream) {
     SsmProblem P;
     Span reads[13];
     kda_status st = check_dims(dims, false, P);
@@ -234,17 +241,19 @@ kda_status kda_ssm_scan(const kda_ssm_dims *dims, const kda_ssm_inputs *in, cons
         misaligned(out, esize(P.out_dtype)) || misaligned(init_state, 4) || misaligned(final_state, 4) ||
         misaligned(chunk_states, 4))
         return KDA_ERR_INVALID_ARGUMENT;
+    const int64_t need = kda_ssm_scan_ws(P);
+    if (workspace_bytes < need || (need > 0 && !workspace) || misaligned(workspace, 16)) return KDA_ERR_INVALID_ARGUMENT;
     if (P.N == 0) return KDA_OK;
     const size_t row = (size_t)P.D * P.S * 4, sb = P.N * row;
     if (any_conflict({{out, (size_t)P.T * P.D * esize(P.out_dtype)}, {final_state, sb},
-                      {chunk_states, (size_t)chunk_capacity * row}},
+                      {chunk_states, (size_t)chunk_capacity * row}, {workspace, (size_t)need}},
                      reads, {{init_state == final_state ? nullptr : init_state, sb}}))
         return KDA_ERR_INVALID_ARGUMENT;
     P.svec = P.S % 4 == 0;
     for (const void *p : {(const void *)P.A, (const void *)init_state, (const void *)final_state, (const void *)chunk_states})
         if (misaligned(p, 16)) P.svec = false;
     cudaError_t e = kda_launch_ssm_scan(P, init_state, out, final_state, chunk_capacity > 0 ? chunk_states : nullptr,
-                                        chunk_capacity, (cudaStream_t)stream);
+                                        chunk_capacity, (float *)workspace, (cudaStream_t)stream);
     return e == cudaSuccess ? KDA_OK : kda_cuda_fail(e, "kda_ssm_scan");
 }
 

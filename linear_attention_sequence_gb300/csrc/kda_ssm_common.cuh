@@ -81,6 +81,28 @@ __device__ __forceinline__ float softplus_fast(float x) {
     return fmaf(p, r, fmaxf(x, 0.f));
 }
 
+// The same of many values at once, step by step, so that their chains of
+// dependent operations overlap.
+template <int N>
+__device__ __forceinline__ void softplus_all(float (&x)[N]) {
+    float w[N], r[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = exp2_fast(-kLog2e * fabsf(x[i]));
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = rcp_fast(2.f + w[i]);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const f2 q = mul2(pack2(w[i], w[i + 1]), pack2(r[i], r[i + 1])), s = mul2(q, q);
+        f2 p = pack2(0.28174657f, 0.28174657f);
+        p = fma2(p, s, pack2(0.27961419f, 0.27961419f));
+        p = fma2(p, s, pack2(0.40024854f, 0.40024854f));
+        p = fma2(p, s, pack2(0.66666316f, 0.66666316f));
+        p = fma2(p, s, pack2(2.00000001f, 2.00000001f));
+        p = fma2(p, q, pack2(fmaxf(x[i], 0.f), fmaxf(x[i + 1], 0.f)));
+        unpack2(p, x[i], x[i + 1]);
+    }
+}
+
 // ---- rows of activations as the kernels get them
 struct Rows {
     const void *p;         // first element; nullptr: absent
@@ -275,7 +297,8 @@ struct SsmProblem {
 cudaError_t kda_launch_act_pack8(int64_t rows, int32_t D, int32_t in_dtype, const kda::Rows &x, int8_t *codes,
                                  float *scales, cudaStream_t stream);
 cudaError_t kda_launch_ssm_scan(const kda::SsmProblem &P, const float *init, void *out, float *final_state,
-                                float *chunk_states, int64_t chunk_capacity, cudaStream_t stream);
+                                float *chunk_states, int64_t chunk_capacity, float *workspace, cudaStream_t stream);
+int64_t kda_ssm_scan_ws(const kda::SsmProblem &P);
 cudaError_t kda_launch_ssm_conv(const kda::SsmProblem &P, const float *w, const float *bias, const float *cin,
                                 bool swish, void *out, float *cout, cudaStream_t stream);
 int64_t kda_ssm_conv_backward_tiles(const kda::SsmProblem &P, int *tile);

@@ -4,14 +4,26 @@
 //   h_t[d,n] = exp(Delta_t[d] A[d,n]) h_{t-1}[d,n] + Delta_t[d] u_t[d] B_t[n]
 //   y_t[d]   = (sum_n C_t[n] h_t[d,n] + D[d] u_t[d]) z_t[d] Sigmoid(z_t[d])
 //
-// Every state entry is a recurrence of its own.  One lane holds four states of
-// one channel, LN >= S / 4 lanes (2, 4, 8 or 16) hold a channel, a block of four
-// warps 128 / LN channels of one sequence, and walks the sequence in
-// tiles of 32 tokens: the block stages Delta, Delta u, B and C of a tile in
-// shared memory as fp32 while the next tile's loads are in flight, each warp
-// runs its recurrences over the tile, and the block writes the tile's outputs.
-// Tokens past the sequence's end are staged as Delta = 0, which leaves a state as
-// it is.
+// Every state entry is a recurrence of its own.  A lane holds four states of each
+// of two neighbouring channels, LN >= S / 4 lanes (2, 4, 8 or 16) hold a channel pair, a
+// block of four scanning warps 256 / LN channels.  It walks its part of a sequence
+// in tiles of 32 tokens.  Four more warps stage the tiles: they form Delta and Delta u
+// in shared memory one tile ahead, and finish the outputs of the tile before
+// (the lanes' shares of C_t h_t added up, the skip, the gate), so that the
+// scanning warps hold nothing but recurrences.
+//
+// What bounds it.  A state entry costs one exponential and about six operations,
+// its share of B and C read from shared memory, and of Delta.  Shared memory gives
+// 128 bytes a cycle an SM whatever lanes share, and a lane that held one
+// channel needed 11 bytes an entry (44 cycles for 128 entries a scheduler,
+// against 16 of exponentials); two channels a lane and, for bf16, B and C kept as
+// bf16 bring that to 5.
+//
+// Few channels.  A sequence is cut into K parts where its channels alone would
+// not fill the GPU: a first kernel runs all parts but the last from a zero state
+// (no outputs), a second one carries the states from part to part, h_in' =
+// h_part + exp(A sum Delta) h_in, and the scan proper runs every part from its own
+// h_in.  That costs the exponentials again, so K = 1 where the channels suffice.
 
 #include "kda_ssm_common.cuh"
 
@@ -19,9 +31,7 @@ namespace {
 
 using namespace kda;
 
-constexpr int kWarps = 4;                 // warps that scan
-constexpr int kScanners = 32 * kWarps;
-constexpr int kStagers = 256;             // threads that stage
+constexpr int kScanners = 128, kStagers = 128;
 constexpr int kThreads = kScanners + kStagers;
 constexpr int TT = kSsmTile;
 
@@ -33,270 +43,441 @@ struct ScanArgs {
     float *chunks;
     int64_t chunk_capacity;
     bool ovec;
+    int parts;         // K
+    float *carry;      // [N][K-1][D][S]: what a part ends with, then what the next one starts with
+    float *sums;       // [N][K-1][D]: sum of Delta over a part
 };
 
-template <int LN>
+template <typename IN, int LN>
 struct Layout {
-    static constexpr int CW = 32 / LN;         // channels of a warp
-    static constexpr int CB = kWarps * CW;     // channels of a block
-    static constexpr int TR = CB >= 16 ? 8 : 4;   // threads that stage a row
-    static constexpr int E = CB / TR;          // its elements that each of them stages
-    static constexpr int BI = (TT * LN + kStagers - 1) / kStagers;   // 4-element pieces of B (and C) that a thread stages
+    static constexpr int CW = 64 / LN;         // channels of a warp
+    static constexpr int CB = 4 * CW;          // channels of a block
+    static constexpr int TR = 8;               // threads that stage a row
+    static constexpr int RP = kStagers / TR;   // rows staged at once
+    static constexpr int NR = TT / RP;         // times a thread does that in a tile
+    static constexpr int E = CB / TR;          // channels of a thread
+    static constexpr bool kBf = sizeof(IN) == 2;
+    static constexpr int BI = (TT * LN + kStagers - 1) / kStagers;   // four-state pieces of B (and C) a thread stages
+    // Row of the lanes' shares.  Its length spreads a half-warp's stores over all
+    // banks, and the gap after 32 channels the reads of eight staging threads.
+    static constexpr int YS = CB == 128 ? 144 : CB == 64 ? 72 : CB == 32 ? 36 : 18;
     struct Smem {
-        float2 d[2][TT][CB];                   // Delta, Delta u; channel pairs permuted (column())
-        float4 b[2][TT][LN], c[2][TT][LN];
-        float y[2][TT][CB][LN];                // the lanes' shares of C_t h_t
+        float2 d[2][TT][CB];                   // Delta, Delta u (column())
+        uint4 bc[2][TT][LN][kBf ? 1 : 2];      // four states of B and C: bf16 both in one piece
+        float y[2][TT][LN][YS];                // the lanes' shares of C_t h_t (ycol())
     };
     // Where channel c lies in a row of d: the 16-byte pieces that eight staging threads
-    // write at once take different banks, and the channels of a warp stay together.
-    static __device__ __forceinline__ int column(int c) { return c ^ (((c >> 4) & 3) << 1); }
+    // write at once take different banks; a warp's channels stay together.
+    static __device__ __forceinline__ int column(int c) { return c ^ (((c >> 4) & 7) << 1); }
+    static __device__ __forceinline__ int ycol(int c) { return c + 4 * (c >> 5); }
 };
 
-// The staging warps: load a tile, form Delta and Delta u, and finish the outputs of
-// an earlier tile.
-template <typename IN, typename OUT, int LN>
+// The tokens of part k of K of the sequence [sa, sb): whole tiles, the last part
+// what is left.
+__device__ __forceinline__ void part_bounds(int64_t sa, int64_t sb, int k, int K, int64_t &pa, int64_t &pb) {
+    const int64_t tiles = (sb - sa + TT - 1) / TT, per = (tiles + K - 1) / K;
+    pa = min(sb, sa + k * per * TT);
+    pb = min(sb, sa + (k + 1) * per * TT);
+}
+
+// The staging warps.  STATES: only what the states need.
+template <typename IN, typename OUT, int LN, bool STATES>
 struct Stager {
-    using L = Layout<LN>;
-    static constexpr int E = L::E;
+    using L = Layout<IN, LN>;
+    static constexpr int E = L::E, NR = L::NR, RP = L::RP, BI = L::BI;
     const ScanArgs &a;
     typename L::Smem &sm;
-    int64_t sb;
-    int tid, srow, sc, ch0, have;
+    const int64_t pb;
+    int tid, srow, sc, have;
+    bool full, bcfull;                         // unchecked accesses to a whole tile
+    const IN *pu, *pd, *pz, *pB, *pC;          // this thread's place in the tile to fetch
+    const IN *fu, *fz;                         // and in the tile to finish
+    OUT *po;
     float bias[E], skip[E];
-    Raw<IN, E> ru, rd, rz;                     // the tile being fetched
-    Raw<IN, E> u0, z0, u1, z1;                 // of the tile staged last, and of the one before
-    Raw<IN, 4> rb[L::BI], rc[L::BI];
+    Raw<IN, E> ru[NR], rd[NR];
+    Raw<IN, 4> rb[BI], rc[BI];
+    Raw<IN, E> gu[NR], gz[NR];
 
-    __device__ __forceinline__ Stager(const ScanArgs &a_, typename L::Smem &sm_, int64_t sb_, int ch0_)
-        : a(a_), sm(sm_), sb(sb_), ch0(ch0_) {
+    __device__ __forceinline__ Stager(const ScanArgs &a_, typename L::Smem &sm_, int64_t pa, int64_t pb_, int ch0)
+        : a(a_), sm(sm_), pb(pb_) {
+        const SsmProblem &P = a.P;
         tid = threadIdx.x - kScanners;
         srow = tid / L::TR;
         sc = tid % L::TR * E;
-        have = srow < TT ? a.P.D - (ch0 + sc) : 0;
+        have = P.D - (ch0 + sc);
+        full = P.D - ch0 >= L::CB && P.u.vec && P.dt.vec && (STATES || !P.z.p || P.z.vec) && (STATES || a.ovec);
+        bcfull = P.B.vec && P.C.vec && P.S == 4 * LN;
+        const int64_t t = pa + srow;
+        pu = fu = (const IN *)P.u.p + t * P.u.stride + ch0 + sc;
+        pd = (const IN *)P.dt.p + t * P.dt.stride + ch0 + sc;
+        pz = fz = (const IN *)P.z.p + t * P.z.stride + ch0 + sc;
+        po = (OUT *)a.out + t * P.D + ch0 + sc;
+        pB = (const IN *)P.B.p + (pa + tid / LN) * P.B.stride + 4 * (tid % LN);
+        pC = (const IN *)P.C.p + (pa + tid / LN) * P.C.stride + 4 * (tid % LN);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            bias[i] = (a.P.dt_bias && i < have) ? a.P.dt_bias[ch0 + sc + i] : 0.f;
-            skip[i] = (a.P.skip && i < have) ? a.P.skip[ch0 + sc + i] : 0.f;
+            bias[i] = (P.dt_bias && i < have) ? P.dt_bias[ch0 + sc + i] : 0.f;
+            skip[i] = (P.skip && i < have) ? P.skip[ch0 + sc + i] : 0.f;
         }
-        u0.clear();
-        z0.clear();
     }
+    // Loads the next tile, which starts at t0.
     __device__ __forceinline__ void fetch(int64_t t0) {
         const SsmProblem &P = a.P;
-        const int64_t t = t0 + srow;
-        ru.clear();
-        rd.clear();
-        rz.clear();
-        if (t < sb && have > 0) {
-            ru.load((const IN *)P.u.p + t * P.u.stride + ch0 + sc, have, P.u.vec);
-            rd.load((const IN *)P.dt.p + t * P.dt.stride + ch0 + sc, have, P.dt.vec);
-            if (P.z.p) rz.load((const IN *)P.z.p + t * P.z.stride + ch0 + sc, have, P.z.vec);
-        }
+        const bool whole = t0 + TT <= pb;
+        if (full && whole) {
 #pragma unroll
-        for (int k = 0; k < L::BI; ++k) {
-            const int i = tid + k * kStagers;
-            const int64_t tb = t0 + i / LN;
-            const int nb = 4 * (i % LN);
-            rb[k].clear();
-            rc[k].clear();
-            if (i < TT * LN && tb < sb && nb < P.S) {
-                rb[k].load((const IN *)P.B.p + tb * P.B.stride + nb, P.S - nb, P.B.vec);
-                rc[k].load((const IN *)P.C.p + tb * P.C.stride + nb, P.S - nb, P.C.vec);
+            for (int r = 0; r < NR; ++r) {
+                ru[r].load_all(pu + r * RP * P.u.stride);
+                rd[r].load_all(pd + r * RP * P.dt.stride);
             }
-        }
-    }
-    // The fetched tile, which starts at t0, into buffer `buf`; tokens past the end
-    // have Delta = 0.
-    __device__ __forceinline__ void stage(int64_t t0, int buf) {
-        const bool in = t0 + srow < sb;
-        if (srow < TT) {
+        } else {
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {
-            float4 v;
-            const float x = rd.get(i) + bias[i], y = rd.get(i + 1) + bias[i + 1];
-            v.x = in ? (a.P.softplus ? softplus_fast(x) : x) : 0.f;
-            v.z = in ? (a.P.softplus ? softplus_fast(y) : y) : 0.f;
-            v.y = v.x * ru.get(i);
-            v.w = v.z * ru.get(i + 1);
-            *reinterpret_cast<float4 *>(&sm.d[buf][srow][L::column(sc + i)]) = v;
-        }
-        }
-#pragma unroll
-        for (int k = 0; k < L::BI; ++k) {
-            const int i = tid + k * kStagers;
-            if (i < TT * LN) {
-                sm.b[buf][i / LN][i % LN] = make_float4(rb[k].get(0), rb[k].get(1), rb[k].get(2), rb[k].get(3));
-                sm.c[buf][i / LN][i % LN] = make_float4(rc[k].get(0), rc[k].get(1), rc[k].get(2), rc[k].get(3));
-            }
-        }
-        u1 = u0;
-        z1 = z0;
-        u0 = ru;
-        z0 = rz;
-    }
-    // The outputs of the tile that starts at t0.
-    __device__ __forceinline__ void finish(int64_t t0, int buf, const Raw<IN, E> &u, const Raw<IN, E> &z) {
-        if (t0 + srow >= sb || have <= 0) return;
-        float o[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float *p = sm.y[buf][srow][sc + i];
-            float v = 0.f;
-            if constexpr (LN == 2) {
-                const float2 y = *reinterpret_cast<const float2 *>(p);
-                v = y.x + y.y;
-            } else {
-#pragma unroll
-                for (int k = 0; k < LN; k += 4) {
-                    const float4 y = *reinterpret_cast<const float4 *>(p + k);
-                    v += (y.x + y.y) + (y.z + y.w);
+            for (int r = 0; r < NR; ++r) {
+                ru[r].clear();
+                rd[r].clear();
+                if (t0 + srow + r * RP < pb && have > 0) {
+                    ru[r].load(pu + r * RP * P.u.stride, have, P.u.vec);
+                    rd[r].load(pd + r * RP * P.dt.stride, have, P.dt.vec);
                 }
             }
-            v = fmaf(skip[i], u.get(i), v);
-            if (a.P.z.p) {
-                const float g = z.get(i);
-                v *= g * sigmoid_fast(g);
-            }
-            o[i] = v;
         }
-        store_row<OUT, E>((OUT *)a.out + (t0 + srow) * a.P.D + ch0 + sc, o, have, a.ovec);
+        pu += TT * P.u.stride;
+        pd += TT * P.dt.stride;
+#pragma unroll
+        for (int k = 0; k < BI; ++k) {
+            const int i = tid + k * kStagers;
+            const IN *qB = pB + k * (kStagers / LN) * P.B.stride, *qC = pC + k * (kStagers / LN) * P.C.stride;
+            if (bcfull && whole) {
+                if (i < TT * LN) {
+                    rb[k].load_all(qB);
+                    if (!STATES) rc[k].load_all(qC);
+                }
+            } else {
+                const int nb = 4 * (i % LN);
+                rb[k].clear();
+                rc[k].clear();
+                if (i < TT * LN && t0 + i / LN < pb && nb < P.S) {
+                    rb[k].load(qB, P.S - nb, P.B.vec);
+                    if (!STATES) rc[k].load(qC, P.S - nb, P.C.vec);
+                }
+            }
+        }
+        pB += TT * P.B.stride;
+        pC += TT * P.C.stride;
+    }
+    // The fetched tile, which starts at t0, into buffer `buf`; tokens past the end
+    // have Delta = 0, which leaves a state as it is.
+    __device__ __forceinline__ void stage(int64_t t0, int buf) {
+        // all of a thread's step sizes together: their chains of dependent operations overlap
+        float dl[NR * E];
+#pragma unroll
+        for (int k = 0; k < NR * E; ++k) dl[k] = rd[k / E].get(k % E) + bias[k % E];
+        if (a.P.softplus) softplus_all(dl);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int row = srow + r * RP;
+            const bool in = t0 + row < pb;
+#pragma unroll
+            for (int i = 0; i < E; i += 2) {
+                float4 v;
+                v.x = in ? dl[r * E + i] : 0.f;
+                v.z = in ? dl[r * E + i + 1] : 0.f;
+                v.y = v.x * ru[r].get(i);
+                v.w = v.z * ru[r].get(i + 1);
+                *reinterpret_cast<float4 *>(&sm.d[buf][row][L::column(sc + i)]) = v;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < BI; ++k) {
+            const int i = tid + k * kStagers;
+            if (i < TT * LN) {
+                uint4 *p = sm.bc[buf][i / LN][i % LN];
+                if constexpr (L::kBf) {
+                    p[0] = make_uint4(rb[k].w[0], rb[k].w[1], STATES ? 0u : rc[k].w[0], STATES ? 0u : rc[k].w[1]);
+                } else {
+                    p[0] = make_uint4(rb[k].w[0], rb[k].w[1], rb[k].w[2], rb[k].w[3]);
+                    if (!STATES) p[1] = make_uint4(rc[k].w[0], rc[k].w[1], rc[k].w[2], rc[k].w[3]);
+                }
+            }
+        }
+    }
+    // u and z again, of the tile to finish next, which starts at t0.
+    __device__ __forceinline__ void fetch_again(int64_t t0) {
+        const SsmProblem &P = a.P;
+        if (full && t0 + TT <= pb) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                gu[r].load_all(fu + r * RP * P.u.stride);
+                if (P.z.p) gz[r].load_all(fz + r * RP * P.z.stride);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                if (t0 + srow + r * RP < pb && have > 0) {
+                    gu[r].load(fu + r * RP * P.u.stride, have, P.u.vec);
+                    if (P.z.p) gz[r].load(fz + r * RP * P.z.stride, have, P.z.vec);
+                }
+            }
+        }
+        fu += TT * P.u.stride;
+        fz += TT * P.z.stride;
+    }
+    // The outputs of the tile that starts at t0.
+    __device__ __forceinline__ void finish(int64_t t0, int buf) {
+        const SsmProblem &P = a.P;
+        const bool unchecked = full && t0 + TT <= pb;
+        constexpr int VE = E < 4 ? E : 4;
+        float o[NR * E];
+#pragma unroll
+        for (int k = 0; k < NR * E; k += VE) {
+            float s[VE] = {};
+#pragma unroll
+            for (int q = 0; q < LN; ++q) {
+                const float *p = &sm.y[buf][srow + k / E * RP][q][L::ycol(sc + k % E)];
+                if constexpr (VE == 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(p);
+                    s[0] += y.x; s[1] += y.y; s[2] += y.z; s[3] += y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2 *>(p);
+                    s[0] += y.x; s[1] += y.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VE; ++i) o[k + i] = fmaf(skip[(k + i) % E], gu[k / E].get((k + i) % E), s[i]);
+        }
+        if (P.z.p) {
+#pragma unroll
+            for (int k = 0; k < NR * E; ++k) {
+                const float z = gz[k / E].get(k % E);
+                o[k] *= z * sigmoid_fast(z);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            OUT *p = po + r * RP * (int64_t)P.D;
+            float v[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[i] = o[r * E + i];
+            if (unchecked) store_row<OUT, E, true>(p, v, have, true);
+            else if (t0 + srow + r * RP < pb && have > 0) store_row<OUT, E>(p, v, have, a.ovec);
+        }
+        po += TT * (int64_t)P.D;
     }
 };
 
-template <typename IN, typename OUT, int LN>
-__global__ void __launch_bounds__(kThreads)
+template <typename IN, typename OUT, int LN, bool STATES>
+__global__ void __launch_bounds__(kThreads, LN == 2 ? 1 : 2)
 kda_ssm_scan_kernel(const ScanArgs a) {
-    using L = Layout<LN>;
+    using L = Layout<IN, LN>;
     constexpr int CW = L::CW, CB = L::CB;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     typename L::Smem &sm = *reinterpret_cast<typename L::Smem *>(smem_raw);
     __shared__ int s_seq;
 
     const SsmProblem &P = a.P;
-    const int ncb = (P.D + CB - 1) / CB;
-    const int n = longest_first(P.cu, P.N, P.T, P.seq_len, blockIdx.x / ncb, &s_seq);
-    const int ch0 = (blockIdx.x % ncb) * CB;
-    int64_t sa, sb;
+    const int ncb = (P.D + CB - 1) / CB, K = STATES ? a.parts - 1 : a.parts;
+    const int ch0 = (int)(blockIdx.x % ncb) * CB, part = (int)(blockIdx.x / ncb % K);
+    const int n = longest_first(P.cu, P.N, P.T, P.seq_len, (int)(blockIdx.x / ncb / K), &s_seq);
+    int64_t sa, sb, pa, pb;
     seq_bounds(P.cu, n, P.T, P.seq_len, sa, sb);
-    const int64_t tiles = (sb - sa + TT - 1) / TT;
+    part_bounds(sa, sb, part, a.parts, pa, pb);
+    const int tiles = (int)((pb - pa + TT - 1) / TT);
 
     if (threadIdx.x >= kScanners) {
         // Between barriers k and k + 1 the scanning warps run over tile k; these
         // warps stage tile k + 1 and finish tile k - 1.
-        Stager<IN, OUT, LN> st(a, sm, sb, ch0);
-        if (tiles > 0) {
-            st.fetch(sa);
-            st.stage(sa, 0);
-        }
-        if (tiles > 1) st.fetch(sa + TT);
+        if (tiles == 0) return;
+        Stager<IN, OUT, LN, STATES> st(a, sm, pa, pb, ch0);
+        st.fetch(pa);
+        st.stage(pa, 0);
+        if (tiles > 1) st.fetch(pa + TT);
         __syncthreads();
-        for (int64_t k = 0; k < tiles; ++k) {
-            const int64_t t0 = sa + k * TT;
+        for (int k = 0; k <= tiles; ++k) {
+            const int64_t t0 = pa + (int64_t)k * TT;
             if (k + 1 < tiles) {
-                st.stage(t0 + TT, (int)(k + 1) & 1);
+                st.stage(t0 + TT, (k + 1) & 1);
                 if (k + 2 < tiles) st.fetch(t0 + 2 * TT);
-            } else {
-                st.u1 = st.u0;
-                st.z1 = st.z0;
             }
-            __syncthreads();
-            st.finish(t0, (int)k & 1, st.u1, st.z1);
+            if (!STATES) {
+                if (k > 0) st.finish(t0 - TT, (k - 1) & 1);
+                if (k < tiles) st.fetch_again(t0);
+            }
+            if (k < tiles) __syncthreads();
         }
         return;
     }
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int wc = warp * CW + lane / LN;      // channel within the block
+    const int wc = warp * CW + lane / LN * 2;  // the first of this lane's channels within the block
     const int ch = ch0 + wc;
     const int q = lane % LN, n0 = 4 * q;
-    const bool live = ch < P.D;
-    f2 A01 = 0, A23 = 0, h01 = 0, h23 = 0;
-    if (live) {
-        const float4 A = load_states(P.A + (int64_t)ch * P.S, n0, P.S, P.svec);
-        A01 = pack2(A.x * kLog2e, A.y * kLog2e);
-        A23 = pack2(A.z * kLog2e, A.w * kLog2e);
-        if (a.init) {
-            const float4 h = load_states(a.init + ((int64_t)n * P.D + ch) * P.S, n0, P.S, P.svec);
-            h01 = pack2(h.x, h.y);
-            h23 = pack2(h.z, h.w);
+    f2 A[2][2], h[2][2];                       // channel, pair of states
+    float dsum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (ch + c < P.D) {
+            x = load_states(P.A + (int64_t)(ch + c) * P.S, n0, P.S, P.svec);
+            const float *from = STATES ? nullptr : part == 0 ? (a.init ? a.init + (int64_t)n * P.D * P.S : nullptr)
+                                : a.carry + ((int64_t)n * (a.parts - 1) + part - 1) * P.D * P.S;
+            if (from) y = load_states(from + (int64_t)(ch + c) * P.S, n0, P.S, P.svec);
         }
+        A[c][0] = pack2(x.x * kLog2e, x.y * kLog2e);
+        A[c][1] = pack2(x.z * kLog2e, x.w * kLog2e);
+        h[c][0] = pack2(y.x, y.y);
+        h[c][1] = pack2(y.z, y.w);
     }
-    const int64_t row0 = a.chunks ? ckpt_first_row(P.cu, n, P.T, P.seq_len, TT) : 0;
-    const int col = L::column(wc);
-    __syncthreads();
-    for (int64_t k = 0; k < tiles; ++k) {
-        const int buf = (int)k & 1;
-        // Groups of G tokens.  While one group's recurrence (a chain of fused
-        // multiply-adds) runs, the next group's decays and inputs are formed and the
-        // operands of the one behind it are read.
-        constexpr int G = 4;
-        float *ys = sm.y[buf][0][wc] + q;
-        float2 d[G];
-        ulonglong2 b[G], c[2][G];
-        f2 a01[2][G], a23[2][G], x01[2][G], x23[2][G];
-        auto read = [&](int g) {
+    auto put = [&](float *p) {                 // the states, of [D, S] at p
 #pragma unroll
-            for (int i = 0; i < G; ++i) {
-                d[i] = sm.d[buf][g * G + i][col];
-                b[i] = *reinterpret_cast<const ulonglong2 *>(&sm.b[buf][g * G + i][q]);
-            }
-        };
-        auto form = [&](int g) {
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-                const f2 dd = pack2(d[i].x, d[i].x), du = pack2(d[i].y, d[i].y);
-                a01[g & 1][i] = exp2_pair(mul2(dd, A01));
-                a23[g & 1][i] = exp2_pair(mul2(dd, A23));
-                x01[g & 1][i] = mul2(du, b[i].x);
-                x23[g & 1][i] = mul2(du, b[i].y);
-                c[g & 1][i] = *reinterpret_cast<const ulonglong2 *>(&sm.c[buf][g * G + i][q]);
-            }
-        };
-        read(0);
-        form(0);
-        read(1);
-#pragma unroll
-        for (int g = 0; g < TT / G; ++g) {
-            if (g + 1 < TT / G) form(g + 1);
-            if (g + 2 < TT / G) read(g + 2);
-#pragma unroll
-            for (int i = 0; i < G; ++i) {
-                h01 = fma2(a01[g & 1][i], h01, x01[g & 1][i]);
-                h23 = fma2(a23[g & 1][i], h23, x23[g & 1][i]);
-                ys[(g * G + i) * CB * LN] = sum2(fma2(c[g & 1][i].x, h01, mul2(c[g & 1][i].y, h23)));
-            }
+        for (int c = 0; c < 2; ++c) {
+            float4 v;
+            unpack2(h[c][0], v.x, v.y);
+            unpack2(h[c][1], v.z, v.w);
+            if (ch + c < P.D) store_states(p + (int64_t)(ch + c) * P.S, v, n0, P.S, P.svec);
         }
-        if (a.chunks && sa + (k + 1) * TT <= sb && live) {
-            const int64_t row = row0 + k;
-            if (row < a.chunk_capacity) {
-                float4 h;
-                unpack2(h01, h.x, h.y);
-                unpack2(h23, h.z, h.w);
-                store_states(a.chunks + (row * P.D + ch) * P.S, h, n0, P.S, P.svec);
+    };
+    const int64_t row0 = !STATES && a.chunks ? ckpt_first_row(P.cu, n, P.T, P.seq_len, TT) + (pa - sa) / TT : 0;
+    const int col = L::column(wc), yc = L::ycol(wc);
+    if (tiles > 0) __syncthreads();
+    for (int k = 0; k < tiles; ++k) {
+        const int buf = k & 1;
+        // The operands of one group of tokens are read while the group before is
+        // computed.
+        constexpr int G = 4;
+        float4 d[2][G];
+        uint4 bc[2][G][L::kBf ? 1 : 2];
+        float ds[2] = {0.f, 0.f};
+        auto read = [&](int g, int to) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                d[to][i] = *reinterpret_cast<const float4 *>(&sm.d[buf][g * G + i][col]);
+                bc[to][i][0] = sm.bc[buf][g * G + i][q][0];
+                if constexpr (!L::kBf && !STATES) bc[to][i][1] = sm.bc[buf][g * G + i][q][1];
             }
+        };
+        auto group = [&](int g, int from) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                f2 b01, b23, c01 = 0, c23 = 0;
+                const uint4 w = bc[from][i][0];
+                if constexpr (L::kBf) {
+                    b01 = pack2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
+                    b23 = pack2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+                    if constexpr (!STATES) {
+                        c01 = pack2(__uint_as_float(w.z << 16), __uint_as_float(w.z & 0xffff0000u));
+                        c23 = pack2(__uint_as_float(w.w << 16), __uint_as_float(w.w & 0xffff0000u));
+                    }
+                } else {
+                    b01 = pack2(__uint_as_float(w.x), __uint_as_float(w.y));
+                    b23 = pack2(__uint_as_float(w.z), __uint_as_float(w.w));
+                    if constexpr (!STATES) {
+                        const uint4 v = bc[from][i][1];
+                        c01 = pack2(__uint_as_float(v.x), __uint_as_float(v.y));
+                        c23 = pack2(__uint_as_float(v.z), __uint_as_float(v.w));
+                    }
+                }
+                float2 y;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float dl = c ? d[from][i].z : d[from][i].x, xu = c ? d[from][i].w : d[from][i].y;
+                    const f2 dd = pack2(dl, dl), du = pack2(xu, xu);
+                    h[c][0] = fma2(exp2_pair(mul2(dd, A[c][0])), h[c][0], mul2(du, b01));
+                    h[c][1] = fma2(exp2_pair(mul2(dd, A[c][1])), h[c][1], mul2(du, b23));
+                    if constexpr (STATES) ds[c] += dl;
+                    else (c ? y.y : y.x) = sum2(fma2(c01, h[c][0], mul2(c23, h[c][1])));
+                }
+                if constexpr (!STATES) *reinterpret_cast<float2 *>(&sm.y[buf][g * G + i][q][yc]) = y;
+            }
+        };
+        read(0, 0);
+#pragma unroll 1
+        for (int g = 0; g < TT / G; g += 2) {
+            read(g + 1, 1);
+            group(g, 0);
+            if (g + 2 < TT / G) read(g + 2, 0);
+            group(g + 1, 1);
+        }
+        if (STATES) {
+            dsum[0] += ds[0];
+            dsum[1] += ds[1];
+        } else if (a.chunks && pa + (int64_t)(k + 1) * TT <= sb) {
+            const int64_t row = row0 + k;
+            if (row < a.chunk_capacity) put(a.chunks + row * P.D * P.S);
         }
         __syncthreads();
     }
-    if (a.fin && live) {
-        float4 h;
-        unpack2(h01, h.x, h.y);
-        unpack2(h23, h.z, h.w);
-        store_states(a.fin + ((int64_t)n * P.D + ch) * P.S, h, n0, P.S, P.svec);
+    if (STATES) {
+        const int64_t at = (int64_t)n * (a.parts - 1) + part;
+        put(a.carry + at * P.D * P.S);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            if (q == 0 && ch + c < P.D) a.sums[at * P.D + ch + c] = dsum[c];
+    } else if (a.fin && pb == sb && (tiles > 0 || (part == 0 && sa == sb))) {
+        put(a.fin + (int64_t)n * P.D * P.S);
     }
+}
+
+// From what the parts end with to what the next ones start with, in place.
+__global__ void __launch_bounds__(256) kda_ssm_carry_kernel(const ScanArgs a) {
+    const SsmProblem &P = a.P;
+    const int64_t M = (int64_t)P.D * P.S, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= M * P.N) return;
+    const int64_t n = i / M, m = i - n * M, d = m / P.S;
+    const float A = P.A[m] * kLog2e;
+    float c = a.init ? a.init[i] : 0.f;
+    const int K = a.parts - 1;
+    float *p = a.carry + n * K * M + m;
+    const float *s = a.sums + n * K * P.D + d;
+#pragma unroll 4
+    for (int k = 0; k < K; ++k) {
+        const float local = p[k * M];
+        c = c != 0.f ? fmaf(exp2_fast(A * s[(int64_t)k * P.D]), c, local) : local;
+        p[k * M] = c;
+    }
+}
+
+// Parts of a sequence.  Cutting costs a second pass over the states (about half the
+// scan's time), so a sequence stays whole unless whole ones would leave half of the
+// 152 SMs without a block.  Then as many parts as make the blocks come close under two
+// an SM, or under three where two would leave places empty; no part under four tiles.
+// 8192 tokens, S = 16, bf16, one part against the best of 2 .. 57: 4096 channels 423 and
+// 279 us (7 parts), 2048: 422 and 152 (9), 1024: 414 and 86 (19), 512: 414 and 59.5 (19;
+// the rule's 38: 59.6); 8192: 426 and 508.
+int parts_of(const SsmProblem &P) {
+    const int LN = P.S <= 8 ? 2 : P.S <= 16 ? 4 : P.S <= 32 ? 8 : 16;
+    const int64_t blocks = (int64_t)P.N * ((P.D + 256 / LN - 1) / (256 / LN));
+    if (P.N == 0 || 2 * blocks > 152) return 1;
+    const int64_t tiles = ((int64_t)P.T / P.N + TT - 1) / TT;
+    int64_t K = 304 / blocks;
+    if (K * blocks < 288) K = 456 / blocks;
+    if (K > tiles / 4) K = tiles / 4;
+    return K < 1 ? 1 : (int)K;
+}
+
+template <typename IN, typename OUT, int LN, bool STATES>
+cudaError_t launch_one(const ScanArgs &a, int parts, cudaStream_t stream) {
+    using L = Layout<IN, LN>;
+    const int smem = (int)sizeof(typename L::Smem);
+    cudaError_t e = cudaFuncSetAttribute(kda_ssm_scan_kernel<IN, OUT, LN, STATES>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = (int64_t)a.P.N * parts * ((a.P.D + L::CB - 1) / L::CB);
+    kda_ssm_scan_kernel<IN, OUT, LN, STATES><<<(unsigned)blocks, kThreads, smem, stream>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename IN, typename OUT, int LN>
 cudaError_t launch(const ScanArgs &a, cudaStream_t stream) {
-    using L = Layout<LN>;
-    const int64_t blocks = (int64_t)a.P.N * ((a.P.D + L::CB - 1) / L::CB);
-    const int smem = (int)sizeof(typename L::Smem);
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kda_ssm_scan_kernel<IN, OUT, LN>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (a.parts > 1) {
+        // the output type plays no part in the states
+        cudaError_t e = launch_one<IN, float, LN, true>(a, a.parts - 1, stream);
+        if (e != cudaSuccess) return e;
+        const int64_t n = (int64_t)a.P.N * a.P.D * a.P.S;
+        kda_ssm_carry_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a);
+        e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    kda_ssm_scan_kernel<IN, OUT, LN><<<(unsigned)blocks, kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_one<IN, OUT, LN, false>(a, a.parts, stream);
 }
 
 template <typename IN, typename OUT>
@@ -307,11 +488,19 @@ cudaError_t by_states(const ScanArgs &a, cudaStream_t s) {
     return launch<IN, OUT, 16>(a, s);
 }
 
+int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
+
 }  // namespace
 
+int64_t kda_ssm_scan_ws(const SsmProblem &P) {
+    const int64_t slots = (int64_t)P.N * (parts_of(P) - 1);
+    return (up4(slots * P.D * P.S) + slots * P.D) * (int64_t)sizeof(float);
+}
+
 cudaError_t kda_launch_ssm_scan(const SsmProblem &P, const float *init, void *out, float *final_state,
-                                float *chunk_states, int64_t chunk_capacity, cudaStream_t stream) {
-    ScanArgs a{P, init, out, final_state, chunk_states, chunk_capacity, false};
+                                float *chunk_states, int64_t chunk_capacity, float *workspace, cudaStream_t stream) {
+    ScanArgs a{P, init, out, final_state, chunk_states, chunk_capacity, false, parts_of(P), workspace, nullptr};
+    a.sums = workspace + up4((int64_t)P.N * (a.parts - 1) * P.D * P.S);
     const int es = P.out_dtype == KDA_DTYPE_BF16 ? 2 : 4;
     a.ovec = ((uintptr_t)out & 15u) == 0 && (int64_t)P.D * es % 16 == 0;
     const bool ib = P.in_dtype == KDA_DTYPE_BF16, ob = P.out_dtype == KDA_DTYPE_BF16;

@@ -76,8 +76,8 @@ BAD_INPUTS = [dict(u=rows(1, 40, data=None)), dict(dt=rows(2, 40, data=None)), d
               dict(dt=rows(2, 40, scales=at(20))), dict(B=rows(3, 16, scales=at(20)))]
 
 
-def scan(L, d, i, init=None, out=at(30), fin=at(31), chunks=None, cap=0):
-    return L.kda_ssm_scan(R(d) if d else None, R(i) if i else None, init, out, fin, chunks, cap, None)
+def scan(L, d, i, init=None, out=at(30), fin=at(31), chunks=None, cap=0, ws=at(60), size=1 << 24):
+    return L.kda_ssm_scan(R(d) if d else None, R(i) if i else None, init, out, fin, chunks, cap, ws, size, None)
 
 
 @pytest.mark.parametrize("over,want", BAD_DIMS)
@@ -108,6 +108,20 @@ def test_scan_inputs_are_refused(L, over):
 def test_scan_is_refused(L, over):
     assert scan(L, dims(), inputs(), **over) == INVALID
     assert scan(L, None, inputs()) == INVALID and scan(L, dims(), None) == INVALID
+
+
+def test_scan_workspace(L):
+    """A long sequence of few channels needs one; the call refuses a smaller or a
+    misplaced one."""
+    d = dims(num_seqs=1, total_tokens=4096)
+    need = L.kda_ssm_scan_workspace(R(d))
+    assert need > 0
+    assert scan(L, d, inputs(), size=need - 1) == INVALID
+    assert scan(L, d, inputs(), ws=None) == INVALID
+    assert scan(L, d, inputs(), ws=at(60) + 8) == INVALID
+    assert scan(L, d, inputs(), ws=at(31)) == INVALID
+    assert scan(L, d, inputs(), ws=at(2)) == INVALID
+    assert L.kda_ssm_scan_workspace(R(dims(state_size=65))) == -1
 
 
 def test_scan_refuses_codes(L):
