@@ -446,6 +446,8 @@ kda_status kda_decode(const kda_dims *dims, const void *q, const void *k, const 
  * other sequence or channel (the gradients of B, C and the parameters are sums
  * over channels or tokens).  Rows of an output that belong to no sequence (tokens
  * before cu_seqlens[0] or from cu_seqlens[N] on) are left as they were.
+ * A malformed cu_seqlens never causes an access out of bounds; what a call then
+ * writes to the outputs is unspecified.
  * The calls allocate nothing: a call that needs scratch takes a workspace, whose
  * size another function gives.  Results do not depend on timing: repeated calls
  * give the same bits.  Calls on different streams may overlap as long as they

@@ -279,6 +279,73 @@ __device__ __forceinline__ bool find_seq(const int32_t *cu, int N, int64_t total
     return false;
 }
 
+// How sequences are cut into parts that run side by side: one of more than
+// `whole` tokens into parts of `len` (the last may be shorter), any other stays one
+// part (an empty one too).
+struct Parts {
+    int64_t len, whole;
+    int32_t most;            // parts of the batch at most
+    int64_t rows;            // parts that have one behind them, at most: rows of a carry
+
+    __host__ __device__ int64_t of(int64_t n) const { return n > whole ? (n + len - 1) / len : 1; }
+};
+
+// Part number p of a batch: its sequence n, its place k in it and the sequence's
+// number of parts; n = -1 if there are not so many.  Every warp finds it by
+// itself (all 32 lanes must call).
+__device__ __forceinline__ void find_part(const Parts &parts, const int32_t *cu, int N, int64_t total, int64_t seq_len,
+                                          int p, int &n, int &k, int &count) {
+    if (!cu) {
+        count = (int)parts.of(seq_len);
+        n = p / count;
+        k = p - n * count;
+        if (n >= N) n = -1;
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (int m0 = 0; m0 < N; m0 += 32) {
+        int c = 0;
+        if (m0 + lane < N) {
+            int64_t a, b;
+            seq_bounds(cu, m0 + lane, total, seq_len, a, b);
+            c = (int)parts.of(b - a);
+        }
+        int upto = c;
+#pragma unroll
+        for (int off = 1; off < 32; off *= 2) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += x;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + upto > p);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            n = m0 + l;
+            count = __shfl_sync(0xffffffffu, c, l);
+            k = p - (before + __shfl_sync(0xffffffffu, upto, l) - count);
+            return;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    n = -1;
+}
+
+// The parts of the sequences before n.
+__device__ __forceinline__ int parts_before(const Parts &parts, const int32_t *cu, int N, int64_t total, int64_t seq_len,
+                                            int n) {
+    if (!cu) return n * (int)parts.of(seq_len);
+    const int lane = threadIdx.x & 31;
+    int sum = 0;
+    for (int m = lane; m < n; m += 32) {
+        int64_t a, b;
+        seq_bounds(cu, m, total, seq_len, a, b);
+        sum += (int)parts.of(b - a);
+    }
+#pragma unroll
+    for (int off = 16; off; off /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    return sum;
+}
+
 // Launch parameters of the state space kernels after validation.
 struct SsmProblem {
     int32_t N, T, D, S;          // sequences, tokens, channels, states per channel (or taps)

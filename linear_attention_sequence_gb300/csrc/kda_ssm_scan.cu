@@ -19,11 +19,11 @@
 // against 16 of exponentials); two channels a lane and, for bf16, B and C kept as
 // bf16 bring that to 5.
 //
-// Few channels.  A sequence is cut into K parts where its channels alone would
+// Few channels.  A sequence is cut into parts where its channels alone would
 // not fill the GPU: a first kernel runs all parts but the last from a zero state
 // (no outputs), a second one carries the states from part to part, h_in' =
 // h_part + exp(A sum Delta) h_in, and the scan proper runs every part from its own
-// h_in.  That costs the exponentials again, so K = 1 where the channels suffice.
+// h_in.
 
 #include "kda_ssm_common.cuh"
 
@@ -43,9 +43,11 @@ struct ScanArgs {
     float *chunks;
     int64_t chunk_capacity;
     bool ovec;
-    int parts;         // K
-    float *carry;      // [N][K-1][D][S]: what a part ends with, then what the next one starts with
-    float *sums;       // [N][K-1][D]: sum of Delta over a part
+    Parts parts;
+    // One row for every part but the last of its sequence; row (number of the part)
+    // - (number of its sequence).
+    float *carry;      // [D, S]: what the part ends with, then what the next one starts with
+    float *sums;       // [D]: sum of Delta over the part
 };
 
 template <typename IN, int LN>
@@ -71,14 +73,6 @@ struct Layout {
     static __device__ __forceinline__ int column(int c) { return c ^ (((c >> 4) & 7) << 1); }
     static __device__ __forceinline__ int ycol(int c) { return c + 4 * (c >> 5); }
 };
-
-// The tokens of part k of K of the sequence [sa, sb): whole tiles, the last part
-// what is left.
-__device__ __forceinline__ void part_bounds(int64_t sa, int64_t sb, int k, int K, int64_t &pa, int64_t &pb) {
-    const int64_t tiles = (sb - sa + TT - 1) / TT, per = (tiles + K - 1) / K;
-    pa = min(sb, sa + k * per * TT);
-    pb = min(sb, sa + (k + 1) * per * TT);
-}
 
 // The staging warps.  STATES: only what the states need.
 template <typename IN, typename OUT, int LN, bool STATES>
@@ -275,12 +269,19 @@ kda_ssm_scan_kernel(const ScanArgs a) {
     __shared__ int s_seq;
 
     const SsmProblem &P = a.P;
-    const int ncb = (P.D + CB - 1) / CB, K = STATES ? a.parts - 1 : a.parts;
-    const int ch0 = (int)(blockIdx.x % ncb) * CB, part = (int)(blockIdx.x / ncb % K);
-    const int n = longest_first(P.cu, P.N, P.T, P.seq_len, (int)(blockIdx.x / ncb / K), &s_seq);
-    int64_t sa, sb, pa, pb;
+    const int ncb = (P.D + CB - 1) / CB;
+    const int ch0 = (int)(blockIdx.x % ncb) * CB, slot = (int)(blockIdx.x / ncb);
+    int n, part = 0, count = 1;
+    if (a.parts.most == P.N) n = longest_first(P.cu, P.N, P.T, P.seq_len, slot, &s_seq);
+    else find_part(a.parts, P.cu, P.N, P.T, P.seq_len, slot, n, part, count);
+    if (n < 0 || (STATES && part == count - 1)) return;
+    int64_t sa, sb;
     seq_bounds(P.cu, n, P.T, P.seq_len, sa, sb);
-    part_bounds(sa, sb, part, a.parts, pa, pb);
+    const int64_t pa = sa + part * a.parts.len, pb = part == count - 1 ? sb : pa + a.parts.len;
+    const int64_t row = slot - n;              // of the carry
+    // Sequences that overlap (a malformed cu_seqlens) could need more rows than
+    // there are; their results are unspecified.
+    if (count > 1 && row + (part < count - 1) > a.parts.rows) return;
     const int tiles = (int)((pb - pa + TT - 1) / TT);
 
     if (threadIdx.x >= kScanners) {
@@ -319,7 +320,7 @@ kda_ssm_scan_kernel(const ScanArgs a) {
         if (ch + c < P.D) {
             x = load_states(P.A + (int64_t)(ch + c) * P.S, n0, P.S, P.svec);
             const float *from = STATES ? nullptr : part == 0 ? (a.init ? a.init + (int64_t)n * P.D * P.S : nullptr)
-                                : a.carry + ((int64_t)n * (a.parts - 1) + part - 1) * P.D * P.S;
+                                : a.carry + (row - 1) * P.D * P.S;
             if (from) y = load_states(from + (int64_t)(ch + c) * P.S, n0, P.S, P.svec);
         }
         A[c][0] = pack2(x.x * kLog2e, x.y * kLog2e);
@@ -343,7 +344,7 @@ kda_ssm_scan_kernel(const ScanArgs a) {
         const int buf = k & 1;
         // The operands of one group of tokens are read while the group before is
         // computed.
-        constexpr int G = 4;
+        constexpr int G = L::kBf ? 4 : 2;      // (fp32 operands take twice the registers)
         float4 d[2][G];
         uint4 bc[2][G][L::kBf ? 1 : 2];
         float ds[2] = {0.f, 0.f};
@@ -401,18 +402,16 @@ kda_ssm_scan_kernel(const ScanArgs a) {
             dsum[0] += ds[0];
             dsum[1] += ds[1];
         } else if (a.chunks && pa + (int64_t)(k + 1) * TT <= sb) {
-            const int64_t row = row0 + k;
-            if (row < a.chunk_capacity) put(a.chunks + row * P.D * P.S);
+            if (row0 + k < a.chunk_capacity) put(a.chunks + (row0 + k) * P.D * P.S);
         }
         __syncthreads();
     }
     if (STATES) {
-        const int64_t at = (int64_t)n * (a.parts - 1) + part;
-        put(a.carry + at * P.D * P.S);
+        put(a.carry + row * P.D * P.S);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-            if (q == 0 && ch + c < P.D) a.sums[at * P.D + ch + c] = dsum[c];
-    } else if (a.fin && pb == sb && (tiles > 0 || (part == 0 && sa == sb))) {
+            if (q == 0 && ch + c < P.D) a.sums[row * P.D + ch + c] = dsum[c];
+    } else if (a.fin && part == count - 1) {
         put(a.fin + (int64_t)n * P.D * P.S);
     }
 }
@@ -420,14 +419,21 @@ kda_ssm_scan_kernel(const ScanArgs a) {
 // From what the parts end with to what the next ones start with, in place.
 __global__ void __launch_bounds__(256) kda_ssm_carry_kernel(const ScanArgs a) {
     const SsmProblem &P = a.P;
-    const int64_t M = (int64_t)P.D * P.S, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= M * P.N) return;
-    const int64_t n = i / M, m = i - n * M, d = m / P.S;
+    const int64_t M = (int64_t)P.D * P.S;
+    const int per = (int)((M + 255) / 256), n = blockIdx.x / per;
+    int64_t sa, sb;
+    seq_bounds(P.cu, n, P.T, P.seq_len, sa, sb);
+    const int K = (int)a.parts.of(sb - sa) - 1;
+    if (K == 0) return;
+    const int64_t row = parts_before(a.parts, P.cu, P.N, P.T, P.seq_len, n) - n;
+    if (row + K > a.parts.rows) return;
+    const int64_t m = (int64_t)(blockIdx.x - n * per) * 256 + threadIdx.x;
+    if (m >= M) return;
+    const int64_t d = m / P.S;
     const float A = P.A[m] * kLog2e;
-    float c = a.init ? a.init[i] : 0.f;
-    const int K = a.parts - 1;
-    float *p = a.carry + n * K * M + m;
-    const float *s = a.sums + n * K * P.D + d;
+    float c = a.init ? a.init[n * M + m] : 0.f;
+    float *p = a.carry + row * M + m;
+    const float *s = a.sums + row * P.D + d;
 #pragma unroll 4
     for (int k = 0; k < K; ++k) {
         const float local = p[k * M];
@@ -436,48 +442,57 @@ __global__ void __launch_bounds__(256) kda_ssm_carry_kernel(const ScanArgs a) {
     }
 }
 
-// Parts of a sequence.  Cutting costs a second pass over the states (about half the
-// scan's time), so a sequence stays whole unless whole ones would leave half of the
-// 152 SMs without a block.  Then as many parts as make the blocks come close under two
-// an SM, or under three where two would leave places empty; no part under four tiles.
-// 8192 tokens, S = 16, bf16, one part against the best of 2 .. 57: 4096 channels 423 and
-// 279 us (7 parts), 2048: 422 and 152 (9), 1024: 414 and 86 (19), 512: 414 and 59.5 (19;
-// the rule's 38: 59.6); 8192: 426 and 508.
-int parts_of(const SsmProblem &P) {
+// How a batch is cut.  Cutting costs a second pass over the states (about half the
+// scan's time), so it is for sequences that would outlast the rest: a part is as long
+// as the share of one of 304 places for blocks (two an SM), or of 456 where 304 is far
+// from a multiple of the blocks across, and a sequence of less than 3.5 such parts
+// (2.5 in a ragged batch, whose other sequences are mostly shorter) stays whole.  8192 tokens, S = 16, bf16, whole against the best of 2 .. 57 parts: 4096
+// channels 423 and 279 us (7 parts), 2048: 422 and 152 (9), 1024: 414 and 86 (19), 512:
+// 414 and 59.5 (19; the rule's 38: 59.6); 8192 channels: 426 and 508.
+Parts parts_of(const SsmProblem &P) {
     const int LN = P.S <= 8 ? 2 : P.S <= 16 ? 4 : P.S <= 32 ? 8 : 16;
-    const int64_t blocks = (int64_t)P.N * ((P.D + 256 / LN - 1) / (256 / LN));
-    if (P.N == 0 || 2 * blocks > 152) return 1;
-    const int64_t tiles = ((int64_t)P.T / P.N + TT - 1) / TT;
-    int64_t K = 304 / blocks;
-    if (K * blocks < 288) K = 456 / blocks;
-    if (K > tiles / 4) K = tiles / 4;
-    return K < 1 ? 1 : (int)K;
+    const int64_t across = (P.D + 256 / LN - 1) / (256 / LN);
+    int64_t K = 304 / across;
+    if (K * across < 288) K = 456 / across;
+    if (K < 1) K = 1;
+    Parts parts;
+    parts.len = ((int64_t)P.T / K + TT - 1) / TT * TT;
+    if (parts.len < 4 * TT) parts.len = 4 * TT;
+    parts.whole = P.cu ? parts.len * 5 / 2 : parts.len * 7 / 2;
+    parts.rows = P.T > parts.len * 5 / 2 ? P.T / parts.len : 0;   // the same with and without cu_seqlens
+    parts.most = P.N;
+    if (P.cu) {
+        parts.most = (int32_t)(P.N + parts.rows);
+    } else if (P.N > 0) {
+        parts.most = (int32_t)(P.N * parts.of(P.seq_len));
+    }
+    return parts;
 }
 
 template <typename IN, typename OUT, int LN, bool STATES>
-cudaError_t launch_one(const ScanArgs &a, int parts, cudaStream_t stream) {
+cudaError_t launch_one(const ScanArgs &a, cudaStream_t stream) {
     using L = Layout<IN, LN>;
     const int smem = (int)sizeof(typename L::Smem);
     cudaError_t e = cudaFuncSetAttribute(kda_ssm_scan_kernel<IN, OUT, LN, STATES>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t blocks = (int64_t)a.P.N * parts * ((a.P.D + L::CB - 1) / L::CB);
+    const int64_t blocks = (int64_t)a.parts.most * ((a.P.D + L::CB - 1) / L::CB);
     kda_ssm_scan_kernel<IN, OUT, LN, STATES><<<(unsigned)blocks, kThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
 template <typename IN, typename OUT, int LN>
 cudaError_t launch(const ScanArgs &a, cudaStream_t stream) {
-    if (a.parts > 1) {
+    if (a.parts.most > a.P.N) {
         // the output type plays no part in the states
-        cudaError_t e = launch_one<IN, float, LN, true>(a, a.parts - 1, stream);
+        cudaError_t e = launch_one<IN, float, LN, true>(a, stream);
         if (e != cudaSuccess) return e;
-        const int64_t n = (int64_t)a.P.N * a.P.D * a.P.S;
-        kda_ssm_carry_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a);
+        const int64_t blocks = (int64_t)a.P.N * (((int64_t)a.P.D * a.P.S + 255) / 256);
+        kda_ssm_carry_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    return launch_one<IN, OUT, LN, false>(a, a.parts, stream);
+    return launch_one<IN, OUT, LN, false>(a, stream);
 }
 
 template <typename IN, typename OUT>
@@ -493,14 +508,14 @@ int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 }  // namespace
 
 int64_t kda_ssm_scan_ws(const SsmProblem &P) {
-    const int64_t slots = (int64_t)P.N * (parts_of(P) - 1);
-    return (up4(slots * P.D * P.S) + slots * P.D) * (int64_t)sizeof(float);
+    const int64_t rows = parts_of(P).rows;
+    return (up4(rows * P.D * P.S) + rows * P.D) * (int64_t)sizeof(float);
 }
 
 cudaError_t kda_launch_ssm_scan(const SsmProblem &P, const float *init, void *out, float *final_state,
                                 float *chunk_states, int64_t chunk_capacity, float *workspace, cudaStream_t stream) {
     ScanArgs a{P, init, out, final_state, chunk_states, chunk_capacity, false, parts_of(P), workspace, nullptr};
-    a.sums = workspace + up4((int64_t)P.N * (a.parts - 1) * P.D * P.S);
+    a.sums = workspace + up4(a.parts.rows * P.D * P.S);
     const int es = P.out_dtype == KDA_DTYPE_BF16 ? 2 : 4;
     a.ovec = ((uintptr_t)out & 15u) == 0 && (int64_t)P.D * es % 16 == 0;
     const bool ib = P.in_dtype == KDA_DTYPE_BF16, ob = P.out_dtype == KDA_DTYPE_BF16;

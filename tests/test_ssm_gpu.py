@@ -254,6 +254,48 @@ def test_scan_long(T, D, S, N):
     check("chunks", chunks, w["chunks"])
 
 
+@pytest.mark.parametrize("D", [24, 520])
+@pytest.mark.parametrize("lens", [[3, 2500, 0, 40, 700], [1300, 1, 0, 0, 1999], [0, 0, 3000, 128, 129], [400], [321], [320, 0]])
+def test_scan_long_sequences_in_a_ragged_batch(lens, D):
+    x = scan_inputs(sum(lens), D, 16, len(lens), F32, 15)
+    out, fin, chunks = fwd(x, cu_seqlens=cu_of(lens), return_chunk_states=True)
+    w = ref.scan(h(x), lens)
+    check("out", out, w["out"])
+    check("final", fin, w["final"])
+    check("chunks", chunks, w["chunks"])
+
+
+def test_scan_many_sequences():
+    """More sequences than a warp has lanes, one of them long."""
+    lens = [5] * 40 + [1500] + [7] * 30
+    x = scan_inputs(sum(lens), 24, 16, len(lens), F32, 16)
+    out, fin = fwd(x, cu_seqlens=cu_of(lens))
+    w = ref.scan(h(x), lens)
+    check("out", out, w["out"])
+    check("final", fin, w["final"])
+
+
+def test_malformed_lengths_stay_in_bounds():
+    """Decreasing and out-of-range entries are clamped: the calls end and a
+    guard around the outputs keeps its value (what the outputs hold is unspecified)."""
+    T, D, S = 2000, 24, 16
+    x = scan_inputs(T, D, S, 6, F32, 17)
+    cu = torch.tensor([0, 1990, 0, 1990, -5, 1990, 99999], dtype=torch.int32, device=DEV)
+    guard = 4096
+    out = torch.full((T * D + 2 * guard,), 7.0, device=DEV)
+    fin = torch.full((6 * D * S + 2 * guard,), 7.0, device=DEV)
+    fwd(x, cu_seqlens=cu, out=out[guard:guard + T * D].view(T, D), final_state=fin[guard:guard + 6 * D * S].view(6, D, S))
+    torch.cuda.synchronize()
+    for t in (out, fin):
+        assert bool((t[:guard] == 7).all()) and bool((t[-guard:] == 7).all())
+    bwd(x, cu_seqlens=cu, chunk_states=torch.zeros(400, D, S, device=DEV))
+    c = conv_inputs(T, D, 4, 6, F32, 18)
+    kda.kda_ssm_conv(c["x"], c["weight"], c["bias"], cu, c["state"])
+    kda.kda_ssm_conv_backward(c["x"], c["weight"], c["d_out"], c["bias"], cu, c["state"])
+    torch.cuda.synchronize()
+    kda.kda_get_last_device_error()
+
+
 def test_scan_extreme_steps():
     """Steps so large that the state is forgotten (decay 0) and so small that they
     vanish: no NaN, and the definition's values."""
