@@ -13,13 +13,25 @@
 //   d_init = a_1 g_1
 //
 // The states come again from the forward's states at the chunk starts (every 32
-// tokens).  Lanes hold states as in the scan (four of one channel).  A tile is
-// one chunk, taken in two halves of 16 tokens whose states stay in registers:
-// the second half's start is run up to first, so a decay is formed 2.5 times, and no
-// state goes through memory.  Sums over a channel's states are exchanges between
-// its LN lanes; sums over channels (dB, dC) are exchanges between the lanes of
-// a warp, then shared memory between the warps, then a workspace row per block
-// that a second kernel adds up in order.
+// tokens).  A lane holds four states of two neighbouring channels, as in the scan.
+// Chunks are taken from the last to the first, each in two halves of 16 tokens and
+// four quarters of 8: the states at the quarters' starts are run up to first, then a
+// quarter's states are formed again, kept in registers, and its gradients follow
+// back through it.  A decay is formed 2.75 times; no state goes through memory.
+// Sums over a channel's states are exchanges between its LN lanes.  Sums over
+// channels (dB, dC) are exchanges between the lanes of a warp, then shared
+// memory between the warps, then a workspace row per block that a second kernel
+// adds up in order.
+//
+// Four warps do that; four more stage the activations (step size, gate, values of the
+// codes) a chunk ahead and finish the gradients of the half before, as in the
+// scan.  The two kinds need very different numbers of registers: 160 and 96 of the
+// 128 a thread that two blocks an SM allow.
+//
+// Sequences are cut into parts as in the scan: a first kernel runs the adjoint
+// alone back through every part but the first from zero, g_in' = g_part +
+// exp(A sum Delta) g_in carries it on, and the gradients proper run every part from its
+// own g_in.
 
 #include "kda_ssm_common.cuh"
 
@@ -27,10 +39,11 @@ namespace {
 
 using namespace kda;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kScanners = 128, kStagers = 128;
+constexpr int kThreads = kScanners + kStagers;
 constexpr int TT = kSsmTile;
-constexpr int HT = TT / 2;
+constexpr int HT = TT / 2;       // tokens of a half
+constexpr int QT = 8;            // tokens of a quarter
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ unsigned g_ssm_status = 0;
@@ -40,22 +53,32 @@ struct BackArgs {
     const float *init, *chunks, *d_final;
     int64_t chunk_capacity;
     void *du, *ddt, *dz;
-    float *dA, *dskip, *dbias, *d_init;   // per sequence: [N, D, S], [N, D], [N, D] (the results themselves for N = 1)
-    float *part;                          // [blocks across D][T][2 SP]
+    float *dA, *dskip, *dbias;   // per part: [D, S], [D], [D] (the results themselves where there is one part)
+    float *d_init;
+    float *share;                // [blocks across D][T][2 SP]
     bool ovec, obf;
+    Parts parts;
+    float *carry, *sums;         // as in the scan, from part to the one before it
 };
 
-template <int LN>
+template <typename IN, int LN>
 struct Layout {
-    static constexpr int CW = 32 / LN, CB = kWarps * CW, SP = 4 * LN, E = CB / 4;
-    static constexpr int YS = CB + 8;
-    static constexpr int BI = (TT * LN + kThreads - 1) / kThreads;
+    static constexpr int CW = 64 / LN, CB = 4 * CW, SP = 4 * LN;
+    static constexpr int TR = 8, E = CB / TR;            // threads that stage a row, channels of each
+    static constexpr bool kBf = sizeof(IN) == 2;
+    static constexpr int YS = CB == 128 ? 144 : CB == 64 ? 72 : CB == 32 ? 36 : 20;
     struct Smem {
-        float4 d[TT][CB];                  // Delta, Delta u, dyp, u
-        float4 b[TT][LN], c[TT][LN];
-        float p[TT][YS], r[TT][YS], y[TT][YS];
-        float part[kWarps][TT][2 * SP];    // dC, dB
+        float2 d[2][TT][CB];                 // Delta, Delta u (column())
+        float dyp[2][TT][CB];
+        uint4 bc[2][TT][LN][kBf ? 1 : 2];
+        float h[2][CB][SP];                  // state at the chunk's start
+        float out[2][3][HT][YS];             // p, r, y of a half
+        float share[2][4][HT][2 * SP];       // the warps' shares of dC, dB
+        float bias[CB], skip[CB];
     };
+    static constexpr int kBlocks = sizeof(Smem) <= 113 * 1024 ? 2 : 1;   // an SM
+    static __device__ __forceinline__ int column(int c) { return c ^ (((c >> 4) & 7) << 1); }
+    static __device__ __forceinline__ int ycol(int c) { return c + 4 * (c >> 5); }
 };
 
 template <int E>
@@ -64,279 +87,644 @@ __device__ __forceinline__ void store_grad(void *p, int64_t at, const float (&v)
     else store_row<float, E>((float *)p + at, v, have, vec);
 }
 
+// E values of a row of codes or plain values.
+template <typename X, int E>
+struct Vals {
+    Raw<X, E> r;
+    float s[E > kPackGroup ? E / kPackGroup : 1];
+    __device__ __forceinline__ void load(const Rows &x, int64_t t, int c, int have, bool full) {
+        const X *p = (const X *)x.p + t * x.stride + c;
+        if (full) r.load_all(p);
+        else r.load(p, have, x.vec);
+        if constexpr (sizeof(X) == 1) s[0] = __ldg(x.scales + t * x.ngroups + c / kPackGroup);
+    }
+    __device__ __forceinline__ void clear() {
+        r.clear();
+        s[0] = 0.f;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(X) == 1) return r.get(i) * s[0];
+        return r.get(i);
+    }
+};
+
+// Four states of B and C of a token into shared memory; a token past the end, and states past S, are 0.
+template <typename IN, int LN>
+__device__ __forceinline__ void stage_bc(const SsmProblem &P, uint4 *to, int64_t t, int q, bool in, bool both) {
+    Raw<IN, 4> b, c;
+    b.clear();
+    c.clear();
+    const int n0 = 4 * q;
+    if (in && n0 < P.S) {
+        if (both) b.load((const IN *)P.B.p + t * P.B.stride + n0, P.S - n0, P.B.vec);
+        c.load((const IN *)P.C.p + t * P.C.stride + n0, P.S - n0, P.C.vec);
+    }
+    if constexpr (sizeof(IN) == 2) {
+        to[0] = make_uint4(b.w[0], b.w[1], c.w[0], c.w[1]);
+    } else {
+        to[0] = make_uint4(b.w[0], b.w[1], b.w[2], b.w[3]);
+        to[1] = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+    }
+}
+template <typename IN>
+__device__ __forceinline__ void read_b(const uint4 *p, f2 &b01, f2 &b23) {
+    if constexpr (sizeof(IN) == 2) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        b01 = pack2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
+        b23 = pack2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+    } else {
+        b01 = pack2(__uint_as_float(p[0].x), __uint_as_float(p[0].y));
+        b23 = pack2(__uint_as_float(p[0].z), __uint_as_float(p[0].w));
+    }
+}
+template <typename IN>
+__device__ __forceinline__ void read_c(const uint4 *p, f2 &c01, f2 &c23) {
+    if constexpr (sizeof(IN) == 2) {
+        read_b<IN>(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint2 *>(p) + 1), c01, c23);
+    } else {
+        read_b<IN>(p + 1, c01, c23);
+    }
+}
+
+// What a part of a sequence is to a block.
+struct Place {
+    int n, part, count;
+    int64_t sa, pa, pb, row;
+};
+__device__ __forceinline__ bool find_place(const BackArgs &a, int slot, int *s_seq, Place &w) {
+    const SsmProblem &P = a.P;
+    w.part = 0;
+    w.count = 1;
+    if (a.parts.most == P.N) w.n = longest_first(P.cu, P.N, P.T, P.seq_len, slot, s_seq);
+    else find_part(a.parts, P.cu, P.N, P.T, P.seq_len, slot, w.n, w.part, w.count);
+    if (w.n < 0) return false;
+    int64_t sb;
+    seq_bounds(P.cu, w.n, P.T, P.seq_len, w.sa, sb);
+    w.pa = w.sa + w.part * a.parts.len;
+    w.pb = w.part == w.count - 1 ? sb : w.pa + a.parts.len;
+    w.row = slot - w.n;                      // of the carry: between this part and the next
+    // as in the scan: overlapping sequences could need more rows than there are
+    return w.count == 1 || w.row + (w.part < w.count - 1) <= a.parts.rows;
+}
+
+// The staging warps.
+template <typename X, typename IN, int LN>
+struct Stager {
+    using L = Layout<IN, LN>;
+    static constexpr int E = L::E, CB = L::CB, SP = L::SP;
+    const BackArgs &a;
+    typename L::Smem &sm;
+    const Place &w;
+    int tid, srow, sc, ch0, cb, have;
+    bool fullx, fulld;                        // unchecked accesses: u and z, dt and d_out
+    int64_t row0;
+    Vals<X, E> u, z;                          // of the half to stage next
+    Vals<IN, E> dt, dy;
+    Vals<X, E> fu, fz;                        // of the half to finish next
+    Vals<IN, E> fdt, fdy;
+    float sum_skip[E], sum_bias[E];
+
+    __device__ __forceinline__ Stager(const BackArgs &a_, typename L::Smem &sm_, const Place &w_, int ch0_, int cb_)
+        : a(a_), sm(sm_), w(w_), ch0(ch0_), cb(cb_) {
+        const SsmProblem &P = a.P;
+        tid = threadIdx.x - kScanners;
+        srow = tid / L::TR;
+        sc = tid % L::TR * E;
+        have = P.D - (ch0 + sc);
+        fullx = P.D - ch0 >= CB && P.u.vec && (!P.z.p || P.z.vec);
+        fulld = P.D - ch0 >= CB && P.dt.vec && P.dy.vec;
+        row0 = ckpt_first_row(P.cu, w.n, P.T, P.seq_len, TT);
+#pragma unroll
+        for (int i = 0; i < E; ++i) sum_skip[i] = sum_bias[i] = 0.f;
+        for (int c = tid; c < CB; c += kStagers) {
+            sm.bias[c] = P.dt_bias && ch0 + c < P.D ? P.dt_bias[ch0 + c] : 0.f;
+            sm.skip[c] = P.skip && ch0 + c < P.D ? P.skip[ch0 + c] : 0.f;
+        }
+        asm volatile("bar.sync 1, %0;" ::"r"(kStagers) : "memory");
+    }
+    __device__ __forceinline__ void fetch(int j, Vals<X, E> &vu, Vals<X, E> &vz, Vals<IN, E> &vdt, Vals<IN, E> &vdy) {
+        const SsmProblem &P = a.P;
+        const int64_t t = w.pa + (int64_t)j * HT + srow;
+        const int c = ch0 + sc;
+        if (t < w.pb && have > 0) {
+            vu.load(P.u, t, c, have, fullx);
+            if (P.z.p) vz.load(P.z, t, c, have, fullx);
+            vdt.load(P.dt, t, c, have, fulld);
+            vdy.load(P.dy, t, c, have, fulld);
+        } else {
+            vu.clear();
+            vz.clear();
+            vdt.clear();
+            vdy.clear();
+        }
+    }
+    // Half j into shared memory; with the second half of a chunk, its start state.
+    __device__ __forceinline__ void stage(int j) {
+        const SsmProblem &P = a.P;
+        const int buf = (j >> 1) & 1, row = (j & 1) * HT + srow;
+        const int64_t t0 = w.pa + (int64_t)j * HT;
+        if (j & 1) {
+            const int64_t chunk = (w.pa - w.sa) / TT + (j >> 1);     // within the sequence
+            const float *from = nullptr;
+            if (chunk == 0) {
+                if (a.init) from = a.init + (int64_t)w.n * P.D * P.S;
+            } else if (row0 + chunk - 1 < a.chunk_capacity) {
+                from = a.chunks + (row0 + chunk - 1) * P.D * P.S;
+            } else if (tid == 0) {
+                atomicOr(&g_ssm_status, kBwdMissingState);
+            }
+            for (int i = tid; i < CB * LN; i += kStagers) {
+                const int c = i / LN, n0 = 4 * (i % LN);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (from && ch0 + c < P.D) v = load_states(from + (int64_t)(ch0 + c) * P.S, n0, P.S, P.svec);
+                *reinterpret_cast<float4 *>(&sm.h[buf][c][n0]) = v;
+            }
+        }
+        for (int i = tid; i < HT * LN; i += kStagers) {
+            const int r = i / LN;
+            stage_bc<IN, LN>(P, sm.bc[buf][(j & 1) * HT + r][i % LN], t0 + r, i % LN, t0 + r < w.pb, true);
+        }
+        const bool in = t0 + srow < w.pb && have > 0;
+        float dl[E], dyp[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            dl[i] = dt.get(i) + sm.bias[sc + i];
+            dyp[i] = dy.get(i);
+        }
+        if (P.softplus) softplus_all(dl);
+        if (P.z.p) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float g = z.get(i);
+                dyp[i] *= g * sigmoid_fast(g);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            float4 v;
+            v.x = in ? dl[i] : 0.f;
+            v.z = in ? dl[i + 1] : 0.f;
+            v.y = v.x * u.get(i);
+            v.w = v.z * u.get(i + 1);
+            *reinterpret_cast<float4 *>(&sm.d[buf][row][L::column(sc + i)]) = v;
+            *reinterpret_cast<float2 *>(&sm.dyp[buf][row][sc + i]) = make_float2(dyp[i], dyp[i + 1]);
+        }
+    }
+    // The gradients of half j.
+    __device__ __forceinline__ void finish(int j) {
+        const SsmProblem &P = a.P;
+        const int buf = (j >> 1) & 1, row = (j & 1) * HT + srow, ob = j & 1;
+        const int64_t t0 = w.pa + (int64_t)j * HT;
+        for (int i = tid; i < HT * 2 * SP / 4; i += kStagers) {
+            const int t = i / (2 * SP / 4), k = i % (2 * SP / 4);
+            if (t0 + t < w.pb) {
+                float4 s = *reinterpret_cast<const float4 *>(&sm.share[ob][0][t][4 * k]);
+#pragma unroll
+                for (int v = 1; v < 4; ++v) {
+                    const float4 x = *reinterpret_cast<const float4 *>(&sm.share[ob][v][t][4 * k]);
+                    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+                }
+                *reinterpret_cast<float4 *>(a.share + ((int64_t)cb * P.T + t0 + t) * (2 * SP) + 4 * k) = s;
+            }
+        }
+        if (t0 + srow >= w.pb || have <= 0) return;
+        float o1[E], o2[E], o3[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int c = L::ycol(sc + i);
+            const float p = sm.out[ob][0][srow][c], r = sm.out[ob][1][srow][c] * kLn2, y = sm.out[ob][2][srow][c];
+            const float delta = sm.d[buf][row][L::column(sc + i)].x, dyp = sm.dyp[buf][row][sc + i];   // written by this thread
+            const float skip = sm.skip[sc + i], uv = fu.get(i);
+            o1[i] = fmaf(delta, p, skip * dyp);
+            float x = fmaf(uv, p, r);
+            if (P.softplus) x *= sigmoid_fast(fdt.get(i) + sm.bias[sc + i]);
+            o2[i] = x;
+            sum_bias[i] += x;
+            sum_skip[i] = fmaf(dyp, uv, sum_skip[i]);
+            if (P.z.p) {
+                const float zv = fz.get(i), s = sigmoid_fast(zv);
+                o3[i] = fdy.get(i) * fmaf(skip, uv, y) * fmaf(zv * s, 1.f - s, s);
+            }
+        }
+        const int64_t at = (t0 + srow) * P.D + ch0 + sc;
+        store_grad<E>(a.du, at, o1, have, a.ovec, a.obf);
+        store_grad<E>(a.ddt, at, o2, have, a.ovec, a.obf);
+        if (P.z.p) store_grad<E>(a.dz, at, o3, have, a.ovec, a.obf);
+    }
+};
+
 // X: type of u and z (int8 codes or IN); IN: type of dt, B, C and d_out.
 template <typename X, typename IN, int LN>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, (Layout<IN, LN>::kBlocks))
 kda_ssm_scan_backward_kernel(const BackArgs a) {
-    using L = Layout<LN>;
-    constexpr int CW = L::CW, CB = L::CB, E = L::E, SP = L::SP;
-    constexpr bool kCodes = sizeof(X) == 1;
+    using L = Layout<IN, LN>;
+    constexpr int CW = L::CW, CB = L::CB, SP = L::SP;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     typename L::Smem &sm = *reinterpret_cast<typename L::Smem *>(smem_raw);
     __shared__ int s_seq;
 
     const SsmProblem &P = a.P;
-    const int ncb = (P.D + CB - 1) / CB, cb = blockIdx.x % ncb;
-    const int n = longest_first(P.cu, P.N, P.T, P.seq_len, blockIdx.x / ncb, &s_seq);
+    const int ncb = (P.D + CB - 1) / CB, cb = (int)(blockIdx.x % ncb), slot = (int)(blockIdx.x / ncb);
     const int ch0 = cb * CB;
-    int64_t sa, sb;
-    seq_bounds(P.cu, n, P.T, P.seq_len, sa, sb);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wc = warp * CW + lane / LN, ch = ch0 + wc;
-    const int q = lane % LN, n0 = 4 * q;
-    const bool live = ch < P.D;
-
-    f2 A01 = 0, A23 = 0, g01 = 0, g23 = 0, dA01 = 0, dA23 = 0;
-    if (live) {
-        const float4 A = load_states(P.A + (int64_t)ch * P.S, n0, P.S, P.svec);
-        A01 = pack2(A.x * kLog2e, A.y * kLog2e);
-        A23 = pack2(A.z * kLog2e, A.w * kLog2e);
-        if (a.d_final) {
-            const float4 g = load_states(a.d_final + ((int64_t)n * P.D + ch) * P.S, n0, P.S, P.svec);
-            g01 = pack2(g.x, g.y);
-            g23 = pack2(g.z, g.w);
+    Place w;
+    const bool some = find_place(a, slot, &s_seq, w);
+    // the shares of dA, dD and ddt_bias: by part, or by sequence where those are the same
+    const int64_t at = a.parts.most == P.N && some ? w.n : slot;
+    if (!some) {
+        // a part that the batch does not have: its shares are 0
+        for (int64_t i = threadIdx.x; i < (int64_t)min(CB, P.D - ch0) * P.S; i += kThreads)
+            a.dA[(at * P.D + ch0) * P.S + i] = 0.f;
+        for (int i = threadIdx.x; i < min(CB, P.D - ch0); i += kThreads) {
+            if (a.dskip) a.dskip[at * P.D + ch0 + i] = 0.f;
+            if (a.dbias) a.dbias[at * P.D + ch0 + i] = 0.f;
         }
+        return;
     }
+    const int tiles = (int)((w.pb - w.pa + TT - 1) / TT);
 
-    const int srow = tid >> 2, sc = (tid & 3) * E;
-    const int have = P.D - (ch0 + sc);
-    float bias[E], skip[E], sum_skip[E], sum_bias[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        bias[i] = (P.dt_bias && i < have) ? P.dt_bias[ch0 + sc + i] : 0.f;
-        skip[i] = (P.skip && i < have) ? P.skip[ch0 + sc + i] : 0.f;
-        sum_skip[i] = sum_bias[i] = 0.f;
-    }
-    constexpr int kScales = E <= kPackGroup ? 1 : E / kPackGroup;
-    Raw<X, E> ru, rz;
-    Raw<IN, E> rd, ry;
-    Raw<IN, 4> rb[L::BI], rc[L::BI];
-    float su[kScales], sz[kScales];
-    float4 rh;                                   // the tile's start state
-    const int64_t row0 = ckpt_first_row(P.cu, n, P.T, P.seq_len, TT);
-    auto fetch = [&](int64_t tile) {
-        const int64_t t0 = sa + tile * TT, t = t0 + srow;
-        ru.clear();
-        rz.clear();
-        rd.clear();
-        ry.clear();
-#pragma unroll
-        for (int i = 0; i < kScales; ++i) su[i] = sz[i] = 0.f;
-        if (t < sb && have > 0) {
-            ru.load((const X *)P.u.p + t * P.u.stride + ch0 + sc, have, P.u.vec);
-            if (P.z.p) rz.load((const X *)P.z.p + t * P.z.stride + ch0 + sc, have, P.z.vec);
-            rd.load((const IN *)P.dt.p + t * P.dt.stride + ch0 + sc, have, P.dt.vec);
-            ry.load((const IN *)P.dy.p + t * P.dy.stride + ch0 + sc, have, P.dy.vec);
-            if constexpr (kCodes) {
-#pragma unroll
-                for (int i = 0; i < kScales; ++i) {
-                    const int64_t g = t * P.u.ngroups + (ch0 + sc) / kPackGroup + i;
-                    su[i] = P.u.scales[g];
-                    if (P.z.p) sz[i] = P.z.scales[g];
-                }
-            }
+    if (threadIdx.x >= kScanners) {
+        // While the other warps work through half j, these stage half j - 2 (the
+        // whole chunk before j's is in place when j is its second half) and finish half
+        // j + 1.
+        if constexpr (L::kBlocks == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        Stager<X, IN, LN> st(a, sm, w, ch0, cb);
+        const int last = 2 * tiles - 1;
+        if (tiles > 0) {
+            st.fetch(last, st.u, st.z, st.dt, st.dy);
+            st.stage(last);
+            st.fetch(last - 1, st.u, st.z, st.dt, st.dy);
+            st.stage(last - 1);
+            if (last >= 2) st.fetch(last - 2, st.u, st.z, st.dt, st.dy);
         }
-#pragma unroll
-        for (int k = 0; k < L::BI; ++k) {
-            const int i = tid + k * kThreads;
-            const int64_t tb = t0 + i / LN;
-            const int nb = 4 * (i % LN);
-            rb[k].clear();
-            rc[k].clear();
-            if (i < TT * LN && tb < sb && nb < P.S) {
-                rb[k].load((const IN *)P.B.p + tb * P.B.stride + nb, P.S - nb, P.B.vec);
-                rc[k].load((const IN *)P.C.p + tb * P.C.stride + nb, P.S - nb, P.C.vec);
+        __syncthreads();
+        for (int j = last; j >= 0; --j) {
+            if (j >= 2) {
+                st.stage(j - 2);
+                if (j >= 3) st.fetch(j - 3, st.u, st.z, st.dt, st.dy);
             }
+            if (j < last) st.finish(j + 1);
+            st.fetch(j, st.fu, st.fz, st.fdt, st.fdy);
+            __syncthreads();
         }
-        rh = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live) {
-            if (tile == 0) {
-                if (a.init) rh = load_states(a.init + ((int64_t)n * P.D + ch) * P.S, n0, P.S, P.svec);
-            } else {
-                const int64_t row = row0 + tile - 1;
-                if (row < a.chunk_capacity)
-                    rh = load_states(a.chunks + (row * P.D + ch) * P.S, n0, P.S, P.svec);
-                else
-                    atomicOr(&g_ssm_status, kBwdMissingState);
-            }
-        }
-    };
-    const int64_t tiles = (sb - sa + TT - 1) / TT;
-    if (tiles > 0) fetch(tiles - 1);
-
-#pragma unroll 1
-    for (int64_t tile = tiles - 1; tile >= 0; --tile) {
-        const int64_t t0 = sa + tile * TT;
-        const bool mine = t0 + srow < sb && have > 0;
-        const f2 h0_01 = pack2(rh.x, rh.y), h0_23 = pack2(rh.z, rh.w);
-        float zz[E], dyv[E], raw[E];
+        if (tiles > 0) st.finish(0);
+        // dD and ddt_bias: over the rows of threads
+        asm volatile("bar.sync 1, %0;" ::"r"(kStagers) : "memory");
+        constexpr int E = L::E;
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            float u = ru.get(i), z = rz.get(i);
-            if constexpr (kCodes) {
-                u *= su[i / kPackGroup];
-                z *= sz[i / kPackGroup];
-            }
-            zz[i] = z;
-            dyv[i] = ry.get(i);
-            raw[i] = rd.get(i) + bias[i];
-            const float dl = mine ? (P.softplus ? softplus_fast(raw[i]) : raw[i]) : 0.f;
-            const float dyp = P.z.p ? dyv[i] * (z * sigmoid_fast(z)) : dyv[i];
-            sm.d[srow][sc + i] = make_float4(dl, dl * u, dyp, u);
+            sm.out[0][0][st.srow][st.sc + i] = st.sum_skip[i];
+            sm.out[0][1][st.srow][st.sc + i] = st.sum_bias[i];
         }
-#pragma unroll
-        for (int k = 0; k < L::BI; ++k) {
-            const int i = tid + k * kThreads;
-            if (i < TT * LN) {
-                sm.b[i / LN][i % LN] = make_float4(rb[k].get(0), rb[k].get(1), rb[k].get(2), rb[k].get(3));
-                sm.c[i / LN][i % LN] = make_float4(rc[k].get(0), rc[k].get(1), rc[k].get(2), rc[k].get(3));
-            }
-        }
-        if (tile > 0) fetch(tile - 1);
-        __syncthreads();
-
-#pragma unroll 1
-        for (int half = 1; half >= 0; --half) {
-            f2 s01 = h0_01, s23 = h0_23;
-            if (half) {
-#pragma unroll 4
+        asm volatile("bar.sync 1, %0;" ::"r"(kStagers) : "memory");
+        for (int c = st.tid; c < CB; c += kStagers) {
+            if (ch0 + c < P.D) {
+                float x = 0.f, y = 0.f;
                 for (int t = 0; t < HT; ++t) {
-                    const float4 d = sm.d[t][wc];
-                    const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&sm.b[t][q]);
-                    const f2 dd = pack2(d.x, d.x), du = pack2(d.y, d.y);
-                    s01 = fma2(exp2_pair(mul2(dd, A01)), s01, mul2(du, b.x));
-                    s23 = fma2(exp2_pair(mul2(dd, A23)), s23, mul2(du, b.y));
+                    x += sm.out[0][0][t][c];
+                    y += sm.out[0][1][t][c];
                 }
+                if (a.dskip) a.dskip[at * P.D + ch0 + c] = x;
+                if (a.dbias) a.dbias[at * P.D + ch0 + c] = y;
             }
-            const int tb = half * HT;
-            f2 H01[HT + 1], H23[HT + 1];
-            H01[0] = s01;
-            H23[0] = s23;
+        }
+        return;
+    }
+
+    if constexpr (L::kBlocks == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int wc = warp * CW + lane / LN * 2, ch = ch0 + wc;
+    const int q = lane % LN, n0 = 4 * q;
+    f2 A[2][2], g[2][2], dA[2][2];
 #pragma unroll
-            for (int i = 0; i < HT; ++i) {
-                const float4 d = sm.d[tb + i][wc];
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&sm.b[tb + i][q]);
-                const f2 dd = pack2(d.x, d.x), du = pack2(d.y, d.y);
-                H01[i + 1] = fma2(exp2_pair(mul2(dd, A01)), H01[i], mul2(du, b.x));
-                H23[i + 1] = fma2(exp2_pair(mul2(dd, A23)), H23[i], mul2(du, b.y));
+    for (int c = 0; c < 2; ++c) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (ch + c < P.D) {
+            x = load_states(P.A + (int64_t)(ch + c) * P.S, n0, P.S, P.svec);
+            const float *from = w.part < w.count - 1 ? a.carry + w.row * P.D * P.S
+                                : a.d_final ? a.d_final + (int64_t)w.n * P.D * P.S : nullptr;
+            if (from) y = load_states(from + (int64_t)(ch + c) * P.S, n0, P.S, P.svec);
+        }
+        A[c][0] = pack2(x.x * kLog2e, x.y * kLog2e);
+        A[c][1] = pack2(x.z * kLog2e, x.w * kLog2e);
+        g[c][0] = pack2(y.x, y.y);
+        g[c][1] = pack2(y.z, y.w);
+        dA[c][0] = dA[c][1] = 0;
+    }
+    const int col = L::column(wc), yc = L::ycol(wc);
+    f2 start[2][2], eighth[2][2];            // the states at the chunk's start and at its second quarter
+    __syncthreads();
+#pragma unroll 1
+    for (int j = 2 * tiles - 1; j >= 0; --j) {
+        const int buf = (j >> 1) & 1, ob = j & 1;
+        auto forward = [&](int t, f2 (&h)[2][2]) {
+            const float4 d = *reinterpret_cast<const float4 *>(&sm.d[buf][t][col]);
+            f2 b01, b23;
+            read_b<IN>(sm.bc[buf][t][q], b01, b23);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float dl = c ? d.z : d.x, x = c ? d.w : d.y;
+                const f2 dd = pack2(dl, dl), du = pack2(x, x);
+                h[c][0] = fma2(exp2_pair(mul2(dd, A[c][0])), h[c][0], mul2(du, b01));
+                h[c][1] = fma2(exp2_pair(mul2(dd, A[c][1])), h[c][1], mul2(du, b23));
             }
-            constexpr int G = LN < 4 ? 4 : LN;
+        };
+        f2 third[2][2], s[2][2];             // the state at the half's second quarter; the quarter's start
+        if (j & 1) {
 #pragma unroll
-            for (int j = HT - G; j >= 0; j -= G) {
-                float vp[G], vr[G], vy[G];
+            for (int c = 0; c < 2; ++c) {
+                const float4 v = *reinterpret_cast<const float4 *>(&sm.h[buf][wc + c][n0]);
+                start[c][0] = s[c][0] = pack2(v.x, v.y);
+                start[c][1] = s[c][1] = pack2(v.z, v.w);
+            }
+#pragma unroll 1
+            for (int k = 0; k < 3; ++k) {
 #pragma unroll
-                for (int i = G - 1; i >= 0; --i) {
-                    const int t = tb + j + i;
-                    const float4 d = sm.d[t][wc];
-                    const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&sm.b[t][q]);
-                    const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(&sm.c[t][q]);
-                    const f2 dd = pack2(d.x, d.x), du = pack2(d.y, d.y), dyp = pack2(d.z, d.z);
-                    g01 = fma2(dyp, c.x, g01);
-                    g23 = fma2(dyp, c.y, g23);
-                    vy[i] = sum2(fma2(c.x, H01[j + i + 1], mul2(c.y, H23[j + i + 1])));
-                    vp[i] = sum2(fma2(b.x, g01, mul2(b.y, g23)));
-                    float v[8];
-                    unpack2(mul2(dyp, H01[j + i + 1]), v[0], v[1]);
-                    unpack2(mul2(dyp, H23[j + i + 1]), v[2], v[3]);
-                    unpack2(mul2(du, g01), v[4], v[5]);
-                    unpack2(mul2(du, g23), v[6], v[7]);
-                    g01 = mul2(g01, exp2_pair(mul2(dd, A01)));
-                    g23 = mul2(g23, exp2_pair(mul2(dd, A23)));
-                    const f2 x01 = mul2(g01, H01[j + i]), x23 = mul2(g23, H23[j + i]);
-                    vr[i] = sum2(fma2(x01, A01, mul2(x23, A23)));
-                    dA01 = fma2(x01, dd, dA01);
-                    dA23 = fma2(x23, dd, dA23);
+                for (int t = 0; t < QT; ++t) forward(k * QT + t, s);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (k == 0) eighth[c][i] = s[c][i];
+                        if (k == 1) third[c][i] = s[c][i];
+                    }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    s[c][i] = eighth[c][i];
+                    third[c][i] = start[c][i];
+                }
+        }
+#pragma unroll 1
+        for (int k = 1; k >= 0; --k) {       // the half's quarters, from the states s and third
+            const int tb = (j & 1) * HT + k * QT;
+            f2 H[QT + 1][2][2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) H[0][c][i] = k ? s[c][i] : third[c][i];
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) H[t + 1][c][i] = H[t][c][i];
+                forward(tb + t, H[t + 1]);
+            }
+#pragma unroll
+            for (int t4 = QT - 4; t4 >= 0; t4 -= 4) {
+                float vp[2][4], vr[2][4], vy[2][4];
+#pragma unroll
+                for (int i = 3; i >= 0; --i) {
+                    const int t = t4 + i;
+                    const float4 d = *reinterpret_cast<const float4 *>(&sm.d[buf][tb + t][col]);
+                    const float2 e = *reinterpret_cast<const float2 *>(&sm.dyp[buf][tb + t][wc]);
+                    f2 b01, b23, c01, c23, sC01 = 0, sC23 = 0, sB01 = 0, sB23 = 0;
+                    read_b<IN>(sm.bc[buf][tb + t][q], b01, b23);
+                    read_c<IN>(sm.bc[buf][tb + t][q], c01, c23);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float dl = c ? d.z : d.x, xu = c ? d.w : d.y, ey = c ? e.y : e.x;
+                        const f2 dd = pack2(dl, dl), du = pack2(xu, xu), dyp = pack2(ey, ey);
+                        const f2 h0 = H[t + 1][c][0], h1 = H[t + 1][c][1];
+                        g[c][0] = fma2(dyp, c01, g[c][0]);
+                        g[c][1] = fma2(dyp, c23, g[c][1]);
+                        vy[c][i] = sum2(fma2(c01, h0, mul2(c23, h1)));
+                        vp[c][i] = sum2(fma2(b01, g[c][0], mul2(b23, g[c][1])));
+                        if (c == 0) {
+                            sC01 = mul2(dyp, h0);
+                            sC23 = mul2(dyp, h1);
+                            sB01 = mul2(du, g[c][0]);
+                            sB23 = mul2(du, g[c][1]);
+                        } else {
+                            sC01 = fma2(dyp, h0, sC01);
+                            sC23 = fma2(dyp, h1, sC23);
+                            sB01 = fma2(du, g[c][0], sB01);
+                            sB23 = fma2(du, g[c][1], sB23);
+                        }
+                        g[c][0] = mul2(g[c][0], exp2_pair(mul2(dd, A[c][0])));
+                        g[c][1] = mul2(g[c][1], exp2_pair(mul2(dd, A[c][1])));
+                        const f2 x0 = mul2(g[c][0], H[t][c][0]), x1 = mul2(g[c][1], H[t][c][1]);
+                        vr[c][i] = sum2(fma2(x0, A[c][0], mul2(x1, A[c][1])));
+                        dA[c][0] = fma2(x0, dd, dA[c][0]);
+                        dA[c][1] = fma2(x1, dd, dA[c][1]);
+                    }
                     // over the channels of the warp
-                    constexpr int CL = CW < 8 ? CW : 8;
+                    float v[8];
+                    unpack2(sC01, v[0], v[1]);
+                    unpack2(sC23, v[2], v[3]);
+                    unpack2(sB01, v[4], v[5]);
+                    unpack2(sB23, v[6], v[7]);
+                    constexpr int G = 32 / LN, CL = G < 8 ? G : 8;   // groups of lanes; values are spread over CL of them
                     reduce_scatter<CL, LN, 8>(v);
 #pragma unroll
-                    for (int off = CL; off < CW; off *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off * LN);
+                    for (int off = CL; off < G; off *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off * LN);
                     if (lane / LN < CL) {
 #pragma unroll
-                        for (int k = 0; k < 8 / CL; ++k) {
-                            const int vi = (lane / LN) * (8 / CL) + k;
-                            sm.part[warp][t][(vi >> 2) * SP + n0 + (vi & 3)] = v[k];
+                        for (int m = 0; m < 8 / CL; ++m) {
+                            const int vi = (lane / LN) * (8 / CL) + m;
+                            sm.share[ob][warp][k * QT + t][(vi >> 2) * SP + n0 + (vi & 3)] = v[m];
                         }
                     }
                 }
-                // over the states of a channel
-                reduce_scatter<LN, 1, G>(vp);
-                reduce_scatter<LN, 1, G>(vr);
-                reduce_scatter<LN, 1, G>(vy);
+                // over the states of a channel; lane q ends with the sums of token q (LN = 2: of two)
+                constexpr int QL = LN < 4 ? LN : 4;
 #pragma unroll
-                for (int i = 0; i < G / LN; ++i) {
-                    const int t = tb + j + q * (G / LN) + i;
-                    sm.p[t][wc] = vp[i];
-                    sm.r[t][wc] = vr[i];
-                    sm.y[t][wc] = vy[i];
+                for (int c = 0; c < 2; ++c) {
+                    reduce_scatter<QL, 1, 4>(vp[c]);
+                    reduce_scatter<QL, 1, 4>(vr[c]);
+                    reduce_scatter<QL, 1, 4>(vy[c]);
+#pragma unroll
+                    for (int off = 4; off < LN; off *= 2) {
+                        vp[c][0] += __shfl_xor_sync(0xffffffffu, vp[c][0], off);
+                        vr[c][0] += __shfl_xor_sync(0xffffffffu, vr[c][0], off);
+                        vy[c][0] += __shfl_xor_sync(0xffffffffu, vy[c][0], off);
+                    }
+                }
+                if (q < QL) {
+#pragma unroll
+                    for (int i = 0; i < 4 / QL; ++i) {
+                        const int t = k * QT + t4 + q * (4 / QL) + i;
+                        *reinterpret_cast<float2 *>(&sm.out[ob][0][t][yc]) = make_float2(vp[0][i], vp[1][i]);
+                        *reinterpret_cast<float2 *>(&sm.out[ob][1][t][yc]) = make_float2(vr[0][i], vr[1][i]);
+                        *reinterpret_cast<float2 *>(&sm.out[ob][2][t][yc]) = make_float2(vy[0][i], vy[1][i]);
+                    }
                 }
             }
         }
         __syncthreads();
-        // dB and dC of this block's channels
-        for (int i = tid; i < TT * 2 * SP / 4; i += kThreads) {
-            const int t = i / (2 * SP / 4), k = i % (2 * SP / 4);
-            if (t0 + t < sb) {
-                float4 s = *reinterpret_cast<const float4 *>(&sm.part[0][t][4 * k]);
-#pragma unroll
-                for (int w = 1; w < kWarps; ++w) {
-                    const float4 x = *reinterpret_cast<const float4 *>(&sm.part[w][t][4 * k]);
-                    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
-                }
-                *reinterpret_cast<float4 *>(a.part + ((int64_t)cb * P.T + t0 + t) * (2 * SP) + 4 * k) = s;
-            }
-        }
-        if (mine) {
-            float o1[E], o2[E], o3[E];
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float4 d = sm.d[srow][sc + i];       // written by this thread
-                const float p = sm.p[srow][sc + i], r = sm.r[srow][sc + i] * kLn2;
-                o1[i] = fmaf(d.x, p, skip[i] * d.z);
-                float x = fmaf(d.w, p, r);
-                if (P.softplus) x *= sigmoid_fast(raw[i]);
-                o2[i] = x;
-                sum_bias[i] += x;
-                sum_skip[i] = fmaf(d.z, d.w, sum_skip[i]);
-                const float y = fmaf(skip[i], d.w, sm.y[srow][sc + i]), s = sigmoid_fast(zz[i]);
-                o3[i] = dyv[i] * y * fmaf(zz[i] * s, 1.f - s, s);
-            }
-            const int64_t at = (t0 + srow) * P.D + ch0 + sc;
-            store_grad<E>(a.du, at, o1, have, a.ovec, a.obf);
-            store_grad<E>(a.ddt, at, o2, have, a.ovec, a.obf);
-            if (P.z.p) store_grad<E>(a.dz, at, o3, have, a.ovec, a.obf);
-        }
     }
-    const int64_t at = ((int64_t)n * P.D + ch) * P.S;
-    if (live) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        if (ch + c >= P.D) break;
         float4 v;
-        unpack2(dA01, v.x, v.y);
-        unpack2(dA23, v.z, v.w);
-        store_states(a.dA + at, v, n0, P.S, P.svec);
-        if (a.d_init) {
-            unpack2(g01, v.x, v.y);
-            unpack2(g23, v.z, v.w);
-            store_states(a.d_init + at, v, n0, P.S, P.svec);
+        unpack2(dA[c][0], v.x, v.y);
+        unpack2(dA[c][1], v.z, v.w);
+        store_states(a.dA + (at * P.D + ch + c) * P.S, v, n0, P.S, P.svec);
+        if (a.d_init && w.part == 0) {
+            unpack2(g[c][0], v.x, v.y);
+            unpack2(g[c][1], v.z, v.w);
+            store_states(a.d_init + ((int64_t)w.n * P.D + ch + c) * P.S, v, n0, P.S, P.svec);
         }
     }
-    // dD and ddt_bias: over the 32 rows of threads
-    __syncthreads();
+}
+
+// The adjoint alone, back through every part but a sequence's first, from 0: what it
+// gives the part before, and the sum of Delta.
+template <typename X, typename IN, int LN>
+__global__ void __launch_bounds__(kThreads, 2)
+kda_ssm_adjoint_kernel(const BackArgs a) {
+    using L = Layout<IN, LN>;
+    constexpr int CW = L::CW, CB = L::CB, E = L::E, HTB = kStagers / L::TR;
+    static_assert(HTB == HT, "a thread stages one row of a half");
+    struct Smem {
+        float2 d[2][TT][CB];                 // Delta, dyp
+        uint4 bc[2][TT][LN][L::kBf ? 1 : 2];
+    };
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    __shared__ int s_seq;
+    const SsmProblem &P = a.P;
+    const int ncb = (P.D + CB - 1) / CB, slot = (int)(blockIdx.x / ncb), ch0 = (int)(blockIdx.x % ncb) * CB;
+    Place w;
+    if (!find_place(a, slot, &s_seq, w) || w.part == 0) return;
+    const int tiles = (int)((w.pb - w.pa + TT - 1) / TT);
+
+    if (threadIdx.x >= kScanners) {
+        const int tid = threadIdx.x - kScanners, srow = tid / L::TR, sc = tid % L::TR * E, have = P.D - (ch0 + sc);
+        const bool full = P.D - ch0 >= CB && (!P.z.p || P.z.vec) && P.dt.vec && P.dy.vec;
+        float bias[E];
+        Vals<X, E> z[2];
+        Vals<IN, E> dt[2], dy[2];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        sm.p[srow][sc + i] = sum_skip[i];
-        sm.r[srow][sc + i] = sum_bias[i];
-    }
-    __syncthreads();
-    for (int c = tid; c < CB; c += kThreads) {
-        if (ch0 + c < P.D) {
-            float x = 0.f, y = 0.f;
-            for (int t = 0; t < TT; ++t) {
-                x += sm.p[t][c];
-                y += sm.r[t][c];
+        for (int i = 0; i < E; ++i) bias[i] = P.dt_bias && i < have ? P.dt_bias[ch0 + sc + i] : 0.f;
+        auto fetch = [&](int k) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int64_t t = w.pa + (int64_t)k * TT + r * HT + srow;
+                if (t < w.pb && have > 0) {
+                    if (P.z.p) z[r].load(P.z, t, ch0 + sc, have, full);
+                    dt[r].load(P.dt, t, ch0 + sc, have, full);
+                    dy[r].load(P.dy, t, ch0 + sc, have, full);
+                } else {
+                    z[r].clear();
+                    dt[r].clear();
+                    dy[r].clear();
+                }
             }
-            if (a.dskip) a.dskip[(int64_t)n * P.D + ch0 + c] = x;
-            if (a.dbias) a.dbias[(int64_t)n * P.D + ch0 + c] = y;
+        };
+        auto stage = [&](int k) {
+            const int buf = k & 1;
+            const int64_t t0 = w.pa + (int64_t)k * TT;
+            for (int i = tid; i < TT * LN; i += kStagers)
+                stage_bc<IN, LN>(P, sm.bc[buf][i / LN][i % LN], t0 + i / LN, i % LN, t0 + i / LN < w.pb, false);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = r * HT + srow;
+                const bool in = t0 + row < w.pb;
+                float dl[E], e[E];
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    dl[i] = dt[r].get(i) + bias[i];
+                    e[i] = dy[r].get(i);
+                }
+                if (P.softplus) softplus_all(dl);
+                if (P.z.p) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        const float x = z[r].get(i);
+                        e[i] *= x * sigmoid_fast(x);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < E; i += 2)
+                    *reinterpret_cast<float4 *>(&sm.d[buf][row][L::column(sc + i)]) =
+                        make_float4(in ? dl[i] : 0.f, e[i], in ? dl[i + 1] : 0.f, e[i + 1]);
+            }
+        };
+        fetch(tiles - 1);
+        stage(tiles - 1);
+        if (tiles > 1) fetch(tiles - 2);
+        __syncthreads();
+        for (int k = tiles - 1; k >= 0; --k) {
+            if (k > 0) {
+                stage(k - 1);
+                if (k > 1) fetch(k - 2);
+            }
+            __syncthreads();
         }
+        return;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int wc = warp * CW + lane / LN * 2, ch = ch0 + wc, q = lane % LN, n0 = 4 * q;
+    f2 A[2][2], g[2][2];
+    float dsum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ch + c < P.D) x = load_states(P.A + (int64_t)(ch + c) * P.S, n0, P.S, P.svec);
+        A[c][0] = pack2(x.x * kLog2e, x.y * kLog2e);
+        A[c][1] = pack2(x.z * kLog2e, x.w * kLog2e);
+        g[c][0] = g[c][1] = 0;
+    }
+    const int col = L::column(wc);
+    __syncthreads();
+    for (int k = tiles - 1; k >= 0; --k) {
+        const int buf = k & 1;
+        float ds[2] = {0.f, 0.f};
+#pragma unroll 8
+        for (int t = TT - 1; t >= 0; --t) {
+            const float4 d = *reinterpret_cast<const float4 *>(&sm.d[buf][t][col]);
+            f2 c01, c23;
+            read_c<IN>(sm.bc[buf][t][q], c01, c23);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float dl = c ? d.z : d.x, e = c ? d.w : d.y;
+                const f2 dd = pack2(dl, dl), dyp = pack2(e, e);
+                g[c][0] = mul2(fma2(dyp, c01, g[c][0]), exp2_pair(mul2(dd, A[c][0])));
+                g[c][1] = mul2(fma2(dyp, c23, g[c][1]), exp2_pair(mul2(dd, A[c][1])));
+                ds[c] += dl;
+            }
+        }
+        dsum[0] += ds[0];
+        dsum[1] += ds[1];
+        __syncthreads();
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        if (ch + c >= P.D) break;
+        float4 v;
+        unpack2(g[c][0], v.x, v.y);
+        unpack2(g[c][1], v.z, v.w);
+        store_states(a.carry + ((w.row - 1) * P.D + ch + c) * P.S, v, n0, P.S, P.svec);
+        if (q == 0) a.sums[(w.row - 1) * P.D + ch + c] = dsum[c];
+    }
+}
+
+// From what the parts give back to what the ones before them start with, in place.
+__global__ void __launch_bounds__(256) kda_ssm_carry_back_kernel(const BackArgs a) {
+    const SsmProblem &P = a.P;
+    const int64_t M = (int64_t)P.D * P.S;
+    const int per = (int)((M + 255) / 256), n = blockIdx.x / per;
+    int64_t sa, sb;
+    seq_bounds(P.cu, n, P.T, P.seq_len, sa, sb);
+    const int K = (int)a.parts.of(sb - sa) - 1;
+    if (K == 0) return;
+    const int64_t row = parts_before(a.parts, P.cu, P.N, P.T, P.seq_len, n) - n;
+    if (row + K > a.parts.rows) return;
+    const int64_t m = (int64_t)(blockIdx.x - n * per) * 256 + threadIdx.x;
+    if (m >= M) return;
+    const float A = P.A[m] * kLog2e;
+    float c = a.d_final ? a.d_final[n * M + m] : 0.f;
+    float *p = a.carry + row * M + m;
+    const float *s = a.sums + row * P.D + m / P.S;
+#pragma unroll 4
+    for (int k = K - 1; k >= 0; --k) {
+        const float local = p[k * M];
+        c = c != 0.f ? fmaf(exp2_fast(A * s[(int64_t)k * P.D]), c, local) : local;
+        p[k * M] = c;
     }
 }
 
@@ -363,7 +751,7 @@ kda_ssm_reduce_bc_kernel(const SsmProblem P, const float *__restrict__ part, int
     st_elem((k < SP ? dC : dB) + t * P.S + n, v);
 }
 
-// Sums over the sequences of [N, M] into [M].
+// Sums over the parts of [N, M] into [M], in their order.
 __global__ void __launch_bounds__(256) kda_ssm_reduce_seq_kernel(const float *__restrict__ part, int N, int64_t M, float *out) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= M) return;
@@ -375,20 +763,32 @@ __global__ void __launch_bounds__(256) kda_ssm_reduce_seq_kernel(const float *__
 
 int lanes_of(int S) { return S <= 8 ? 2 : S <= 16 ? 4 : S <= 32 ? 8 : 16; }
 int blocks_across(const SsmProblem &P) {
-    const int CB = kWarps * 32 / lanes_of(P.S);
+    const int CB = 256 / lanes_of(P.S);
     return (P.D + CB - 1) / CB;
 }
 int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 
 template <typename X, typename IN, int LN>
 cudaError_t launch(const BackArgs &a, cudaStream_t stream) {
-    using L = Layout<LN>;
+    using L = Layout<IN, LN>;
+    const unsigned blocks = (unsigned)((int64_t)a.parts.most * blocks_across(a.P));
+    cudaError_t e;
+    if (a.parts.most > a.P.N) {
+        const int smem = (int)(sizeof(float2) * 2 * TT * L::CB + sizeof(uint4) * 2 * TT * LN * (L::kBf ? 1 : 2));
+        e = cudaFuncSetAttribute(kda_ssm_adjoint_kernel<X, IN, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        kda_ssm_adjoint_kernel<X, IN, LN><<<blocks, kThreads, smem, stream>>>(a);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        const int64_t n = (int64_t)a.P.N * (((int64_t)a.P.D * a.P.S + 255) / 256);
+        kda_ssm_carry_back_kernel<<<(unsigned)n, 256, 0, stream>>>(a);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     const int smem = (int)sizeof(typename L::Smem);
-    cudaError_t e = cudaFuncSetAttribute(kda_ssm_scan_backward_kernel<X, IN, LN>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(kda_ssm_scan_backward_kernel<X, IN, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t blocks = (int64_t)a.P.N * blocks_across(a.P);
-    kda_ssm_scan_backward_kernel<X, IN, LN><<<(unsigned)blocks, kThreads, smem, stream>>>(a);
+    kda_ssm_scan_backward_kernel<X, IN, LN><<<blocks, kThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -400,6 +800,22 @@ cudaError_t by_states(const BackArgs &a, cudaStream_t s) {
         case 8: return launch<X, IN, 8>(a, s);
         default: return launch<X, IN, 16>(a, s);
     }
+}
+
+// Places in the workspace, in floats.
+struct Space {
+    int64_t dA, dskip, dbias, carry, sums, all;
+};
+Space space_of(const SsmProblem &P, const Parts &parts) {
+    const int64_t most = P.N + parts.rows, row = (int64_t)P.D * P.S;   // with cu_seqlens; without, no more
+    Space s;
+    s.dA = up4((int64_t)blocks_across(P) * P.T * 8 * lanes_of(P.S));
+    s.dskip = s.dA + up4(most * row);
+    s.dbias = s.dskip + up4(most * P.D);
+    s.carry = s.dbias + up4(most * P.D);
+    s.sums = s.carry + up4(parts.rows * row);
+    s.all = s.sums + up4(parts.rows * P.D);
+    return s;
 }
 
 }  // namespace
@@ -416,10 +832,7 @@ cudaError_t kda_ssm_read_status(unsigned *status) {
 }
 
 int64_t kda_ssm_scan_backward_ws(const SsmProblem &P) {
-    const int SP = 4 * lanes_of(P.S);
-    int64_t n = (int64_t)blocks_across(P) * P.T * 2 * SP;
-    if (P.N != 1) n += up4((int64_t)P.N * P.D * P.S) + 2 * up4((int64_t)P.N * P.D);
-    return n * (int64_t)sizeof(float);
+    return space_of(P, kda_ssm_parts(P)).all * (int64_t)sizeof(float);
 }
 
 cudaError_t kda_launch_ssm_scan_backward(const SsmProblem &P, const float *init, const float *chunk_states,
@@ -440,14 +853,17 @@ cudaError_t kda_launch_ssm_scan_backward(const SsmProblem &P, const float *init,
     a.ovec = (int64_t)P.D * (a.obf ? 2 : 4) % 16 == 0;
     for (const void *p : {(const void *)du, (const void *)ddt, (const void *)dz})
         if ((uintptr_t)p & 15u) a.ovec = false;
+    a.parts = kda_ssm_parts(P);
+    const Space sp = space_of(P, a.parts);
     const int SP = 4 * lanes_of(P.S), ncb = blocks_across(P);
-    a.part = workspace;
-    float *more = workspace + (int64_t)ncb * P.T * 2 * SP;
     const int64_t nA = (int64_t)P.D * P.S;
-    const bool direct = P.N == 1;
-    a.dA = direct ? dA : more;
-    a.dskip = !dskip ? nullptr : direct ? dskip : more + up4(P.N * nA);
-    a.dbias = !dbias ? nullptr : direct ? dbias : more + up4(P.N * nA) + up4((int64_t)P.N * P.D);
+    const bool direct = a.parts.most == 1;
+    a.share = workspace;
+    a.dA = direct ? dA : workspace + sp.dA;
+    a.dskip = !dskip ? nullptr : direct ? dskip : workspace + sp.dskip;
+    a.dbias = !dbias ? nullptr : direct ? dbias : workspace + sp.dbias;
+    a.carry = workspace + sp.carry;
+    a.sums = workspace + sp.sums;
     cudaError_t e = cudaSuccess;
     if (P.N > 0) {
         const bool bf = P.in_dtype == KDA_DTYPE_BF16;
@@ -459,16 +875,16 @@ cudaError_t kda_launch_ssm_scan_backward(const SsmProblem &P, const float *init,
         const int64_t n = (int64_t)P.T * 2 * SP;
         const unsigned blocks = (unsigned)((n + 255) / 256);
         if (a.obf)
-            kda_ssm_reduce_bc_kernel<__nv_bfloat16><<<blocks, 256, 0, stream>>>(P, a.part, ncb, SP, (__nv_bfloat16 *)dB, (__nv_bfloat16 *)dC);
+            kda_ssm_reduce_bc_kernel<__nv_bfloat16><<<blocks, 256, 0, stream>>>(P, a.share, ncb, SP, (__nv_bfloat16 *)dB, (__nv_bfloat16 *)dC);
         else
-            kda_ssm_reduce_bc_kernel<float><<<blocks, 256, 0, stream>>>(P, a.part, ncb, SP, (float *)dB, (float *)dC);
+            kda_ssm_reduce_bc_kernel<float><<<blocks, 256, 0, stream>>>(P, a.share, ncb, SP, (float *)dB, (float *)dC);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     if (!direct) {
-        kda_ssm_reduce_seq_kernel<<<(unsigned)((nA + 255) / 256), 256, 0, stream>>>(a.dA, P.N, nA, dA);
-        if (dskip) kda_ssm_reduce_seq_kernel<<<(unsigned)((P.D + 255) / 256), 256, 0, stream>>>(a.dskip, P.N, P.D, dskip);
-        if (dbias) kda_ssm_reduce_seq_kernel<<<(unsigned)((P.D + 255) / 256), 256, 0, stream>>>(a.dbias, P.N, P.D, dbias);
+        kda_ssm_reduce_seq_kernel<<<(unsigned)((nA + 255) / 256), 256, 0, stream>>>(a.dA, a.parts.most, nA, dA);
+        if (dskip) kda_ssm_reduce_seq_kernel<<<(unsigned)((P.D + 255) / 256), 256, 0, stream>>>(a.dskip, a.parts.most, P.D, dskip);
+        if (dbias) kda_ssm_reduce_seq_kernel<<<(unsigned)((P.D + 255) / 256), 256, 0, stream>>>(a.dbias, a.parts.most, P.D, dbias);
         e = cudaGetLastError();
     }
     return e;

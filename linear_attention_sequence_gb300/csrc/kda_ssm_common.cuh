@@ -365,6 +365,7 @@ cudaError_t kda_launch_act_pack8(int64_t rows, int32_t D, int32_t in_dtype, cons
                                  float *scales, cudaStream_t stream);
 cudaError_t kda_launch_ssm_scan(const kda::SsmProblem &P, const float *init, void *out, float *final_state,
                                 float *chunk_states, int64_t chunk_capacity, float *workspace, cudaStream_t stream);
+kda::Parts kda_ssm_parts(const kda::SsmProblem &P);
 int64_t kda_ssm_scan_ws(const kda::SsmProblem &P);
 cudaError_t kda_launch_ssm_conv(const kda::SsmProblem &P, const float *w, const float *bias, const float *cin,
                                 bool swish, void *out, float *cout, cudaStream_t stream);

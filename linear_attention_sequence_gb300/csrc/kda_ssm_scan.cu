@@ -442,33 +442,6 @@ __global__ void __launch_bounds__(256) kda_ssm_carry_kernel(const ScanArgs a) {
     }
 }
 
-// How a batch is cut.  Cutting costs a second pass over the states (about half the
-// scan's time), so it is for sequences that would outlast the rest: a part is as long
-// as the share of one of 304 places for blocks (two an SM), or of 456 where 304 is far
-// from a multiple of the blocks across, and a sequence of less than 3.5 such parts
-// (2.5 in a ragged batch, whose other sequences are mostly shorter) stays whole.  8192 tokens, S = 16, bf16, whole against the best of 2 .. 57 parts: 4096
-// channels 423 and 279 us (7 parts), 2048: 422 and 152 (9), 1024: 414 and 86 (19), 512:
-// 414 and 59.5 (19; the rule's 38: 59.6); 8192 channels: 426 and 508.
-Parts parts_of(const SsmProblem &P) {
-    const int LN = P.S <= 8 ? 2 : P.S <= 16 ? 4 : P.S <= 32 ? 8 : 16;
-    const int64_t across = (P.D + 256 / LN - 1) / (256 / LN);
-    int64_t K = 304 / across;
-    if (K * across < 288) K = 456 / across;
-    if (K < 1) K = 1;
-    Parts parts;
-    parts.len = ((int64_t)P.T / K + TT - 1) / TT * TT;
-    if (parts.len < 4 * TT) parts.len = 4 * TT;
-    parts.whole = P.cu ? parts.len * 5 / 2 : parts.len * 7 / 2;
-    parts.rows = P.T > parts.len * 5 / 2 ? P.T / parts.len : 0;   // the same with and without cu_seqlens
-    parts.most = P.N;
-    if (P.cu) {
-        parts.most = (int32_t)(P.N + parts.rows);
-    } else if (P.N > 0) {
-        parts.most = (int32_t)(P.N * parts.of(P.seq_len));
-    }
-    return parts;
-}
-
 template <typename IN, typename OUT, int LN, bool STATES>
 cudaError_t launch_one(const ScanArgs &a, cudaStream_t stream) {
     using L = Layout<IN, LN>;
@@ -507,14 +480,41 @@ int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 
 }  // namespace
 
+// How a batch is cut.  Cutting costs a second pass over the states (about half the
+// scan's time), so it is for sequences that would outlast the rest: a part is as long
+// as the share of one of 304 places for blocks (two an SM), or of 456 where 304 is far
+// from a multiple of the blocks across, and a sequence of less than 3.5 such parts
+// (2.5 in a ragged batch, whose other sequences are mostly shorter) stays whole.  8192 tokens, S = 16, bf16, whole against the best of 2 .. 57 parts: 4096
+// channels 423 and 279 us (7 parts), 2048: 422 and 152 (9), 1024: 414 and 86 (19), 512:
+// 414 and 59.5 (19; the rule's 38: 59.6); 8192 channels: 426 and 508.
+Parts kda_ssm_parts(const SsmProblem &P) {
+    const int LN = P.S <= 8 ? 2 : P.S <= 16 ? 4 : P.S <= 32 ? 8 : 16;
+    const int64_t across = (P.D + 256 / LN - 1) / (256 / LN);
+    int64_t K = 304 / across;
+    if (K * across < 288) K = 456 / across;
+    if (K < 1) K = 1;
+    Parts parts;
+    parts.len = ((int64_t)P.T / K + TT - 1) / TT * TT;
+    if (parts.len < 4 * TT) parts.len = 4 * TT;
+    parts.whole = P.cu ? parts.len * 5 / 2 : parts.len * 7 / 2;
+    parts.rows = P.T > parts.len * 5 / 2 ? P.T / parts.len : 0;   // the same with and without cu_seqlens
+    parts.most = P.N;
+    if (P.cu) {
+        parts.most = (int32_t)(P.N + parts.rows);
+    } else if (P.N > 0) {
+        parts.most = (int32_t)(P.N * parts.of(P.seq_len));
+    }
+    return parts;
+}
+
 int64_t kda_ssm_scan_ws(const SsmProblem &P) {
-    const int64_t rows = parts_of(P).rows;
+    const int64_t rows = kda_ssm_parts(P).rows;
     return (up4(rows * P.D * P.S) + rows * P.D) * (int64_t)sizeof(float);
 }
 
 cudaError_t kda_launch_ssm_scan(const SsmProblem &P, const float *init, void *out, float *final_state,
                                 float *chunk_states, int64_t chunk_capacity, float *workspace, cudaStream_t stream) {
-    ScanArgs a{P, init, out, final_state, chunk_states, chunk_capacity, false, parts_of(P), workspace, nullptr};
+    ScanArgs a{P, init, out, final_state, chunk_states, chunk_capacity, false, kda_ssm_parts(P), workspace, nullptr};
     a.sums = workspace + up4(a.parts.rows * P.D * P.S);
     const int es = P.out_dtype == KDA_DTYPE_BF16 ? 2 : 4;
     a.ovec = ((uintptr_t)out & 15u) == 0 && (int64_t)P.D * es % 16 == 0;

@@ -388,6 +388,17 @@ def test_scan_backward_long(T, D, N):
         check(n, g[n], w[n])
 
 
+@pytest.mark.parametrize("D", [24, 520])
+@pytest.mark.parametrize("lens", [[3, 1500, 0, 40, 700], [0, 0, 1000, 128, 129], [321]])
+def test_scan_backward_long_sequences_in_a_ragged_batch(lens, D):
+    x = scan_inputs(sum(lens), D, 16, len(lens), F32, 35)
+    chunks = fwd(x, cu_seqlens=cu_of(lens), return_chunk_states=True)[2]
+    g = bwd(x, cu_seqlens=cu_of(lens), chunk_states=chunks)
+    w = ref.scan_backward(h(x), lens, chunks.double().cpu())
+    for n in w:
+        check(n, g[n], w[n])
+
+
 def test_scan_backward_without_options():
     x = scan_inputs(66, 40, 16, 2, F32, 5)
     dt = x["dt"].abs() * 0.1
