@@ -46,7 +46,7 @@ __device__ __forceinline__ uint32_t abs_max(const Raw<__nv_bfloat16, kE> &r) {
 }
 
 template <typename IN, bool FULL>
-__global__ void __launch_bounds__(kThreads) kda_act_pack8_kernel(const PackArgs a) {
+__global__ void __launch_bounds__(kThreads) kda_act_pack8_kernel(const __grid_constant__ PackArgs a) {
     // four lanes to a group of channels, of kRowsOf rows
     const int64_t id = (int64_t)blockIdx.x * (kThreads / 4) + threadIdx.x / 4;
     const int64_t block = a.total >> 32 ? id / a.ng : (int64_t)((uint32_t)id / (uint32_t)a.ng);

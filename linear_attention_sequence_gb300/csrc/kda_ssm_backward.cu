@@ -33,6 +33,8 @@
 // exp(A sum Delta) g_in carries it on, and the gradients proper run every part from its
 // own g_in.
 
+#include <type_traits>
+
 #include "kda_ssm_common.cuh"
 
 namespace {
@@ -69,17 +71,45 @@ struct Layout {
     static constexpr int YS = CB == 128 ? 144 : CB == 64 ? 72 : CB == 32 ? 36 : 20;
     struct Smem {
         float2 d[2][TT][CB];                 // Delta, Delta u (column())
-        float dyp[2][TT][CB];
+        float dyp[2][TT][CB];                // (swz())
         uint4 bc[2][TT][LN][kBf ? 1 : 2];
         float h[2][CB][SP];                  // state at the chunk's start
         float out[2][3][HT][YS];             // p, r, y of a half
         float share[2][4][HT][2 * SP];       // the warps' shares of dC, dB
-        float bias[CB], skip[CB];
+        float bias[CB], skip[CB];            // (swz())
+        float sums[2][HT][CB];               // of dyp u and of ddt, by row of staging threads (swz())
     };
     static constexpr int kBlocks = sizeof(Smem) <= 113 * 1024 ? 2 : 1;   // an SM
     static __device__ __forceinline__ int column(int c) { return c ^ (((c >> 4) & 7) << 1); }
     static __device__ __forceinline__ int ycol(int c) { return c + 4 * (c >> 5); }
+    // The same for rows of floats that staging threads read and write four at a time.
+    static __device__ __forceinline__ int swz(int c) { return c ^ (((c >> 5) & 3) << 2); }
 };
+
+// E consecutive floats, from channel c on, of a row laid out by swz().
+template <typename L, int E>
+__device__ __forceinline__ void read_swz(const float *row, int c, float (&v)[E]) {
+    if constexpr (E == 2) {
+        const float2 x = *reinterpret_cast<const float2 *>(row + L::swz(c));
+        v[0] = x.x; v[1] = x.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(row + L::swz(c + i));
+            v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+        }
+    }
+}
+template <typename L, int E>
+__device__ __forceinline__ void write_swz(float *row, int c, const float (&v)[E]) {
+    if constexpr (E == 2) {
+        *reinterpret_cast<float2 *>(row + L::swz(c)) = make_float2(v[0], v[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; i += 4)
+            *reinterpret_cast<float4 *>(row + L::swz(c + i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+}
 
 template <int E>
 __device__ __forceinline__ void store_grad(void *p, int64_t at, const float (&v)[E], int have, bool vec, bool bf) {
@@ -92,15 +122,22 @@ template <typename X, int E>
 struct Vals {
     Raw<X, E> r;
     float s[E > kPackGroup ? E / kPackGroup : 1];
-    __device__ __forceinline__ void load(const Rows &x, int64_t t, int c, int have, bool full) {
-        const X *p = (const X *)x.p + t * x.stride + c;
-        if (full) r.load_all(p);
-        else r.load(p, have, x.vec);
-        if constexpr (sizeof(X) == 1) s[0] = __ldg(x.scales + t * x.ngroups + c / kPackGroup);
-    }
-    __device__ __forceinline__ void clear() {
-        r.clear();
-        s[0] = 0.f;
+    // The row of token t from channel c on, or zeros if !ok.  FAST: all channels or
+    // none exist, at an address that allows wide accesses.
+    template <bool FAST>
+    __device__ __forceinline__ void load(const Rows &x, int t, int c, int have, bool ok) {
+        const X *p = (const X *)x.p + (int64_t)t * x.stride + c;
+        if constexpr (FAST) {
+            r.load_if(p, ok);
+        } else {
+            if (ok) r.load(p, have, x.vec);
+            else r.clear();
+        }
+        if constexpr (sizeof(X) == 1) {
+            uint32_t w = 0;
+            ahead4(w, x.scales + (int64_t)t * x.ngroups + c / kPackGroup, ok);
+            s[0] = __uint_as_float(w);
+        }
     }
     __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(X) == 1) return r.get(i) * s[0];
@@ -108,24 +145,78 @@ struct Vals {
     }
 };
 
-// Four states of B and C of a token into shared memory; a token past the end, and states past S, are 0.
-template <typename IN, int LN>
-__device__ __forceinline__ void stage_bc(const SsmProblem &P, uint4 *to, int64_t t, int q, bool in, bool both) {
-    Raw<IN, 4> b, c;
-    b.clear();
-    c.clear();
-    const int n0 = 4 * q;
-    if (in && n0 < P.S) {
-        if (both) b.load((const IN *)P.B.p + t * P.B.stride + n0, P.S - n0, P.B.vec);
-        c.load((const IN *)P.C.p + t * P.C.stride + n0, P.S - n0, P.C.vec);
+// Four states of B and C of each of N tokens that a thread stages (one of ROWS in
+// all); tokens past the end, and states past S, are 0.
+template <typename IN, int LN, int ROWS>
+struct RawBC {
+    static constexpr int N = (ROWS * LN + kStagers - 1) / kStagers;
+    Raw<IN, 4> b[N], c[N];
+    template <bool BOTH, bool FAST>
+    __device__ __forceinline__ void load(const SsmProblem &P, int t0, int end, int tid, bool live) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = tid + k * kStagers, n0 = 4 * (i % LN);
+            const int t = t0 + i / LN;
+            const IN *pb = (const IN *)P.B.p + (int64_t)t * P.B.stride + n0, *pc = (const IN *)P.C.p + (int64_t)t * P.C.stride + n0;
+            const bool ok = i < ROWS * LN && live && t < end && n0 < P.S;
+            if constexpr (FAST) {
+                if (BOTH) b[k].load_if(pb, ok);
+                c[k].load_if(pc, ok);
+            } else {
+                if (BOTH) b[k].clear();
+                c[k].clear();
+                if (ok) {
+                    if (BOTH) b[k].load(pb, P.S - n0, P.B.vec);
+                    c[k].load(pc, P.S - n0, P.C.vec);
+                }
+            }
+        }
     }
-    if constexpr (sizeof(IN) == 2) {
-        to[0] = make_uint4(b.w[0], b.w[1], c.w[0], c.w[1]);
+    // `to`: [ROWS][LN][1 or 2] pieces
+    template <bool BOTH>
+    __device__ __forceinline__ void put(uint4 *to, int tid) const {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = tid + k * kStagers;
+            if (i < ROWS * LN) {
+                if constexpr (sizeof(IN) == 2) {
+                    to[i] = make_uint4(BOTH ? b[k].w[0] : 0u, BOTH ? b[k].w[1] : 0u, c[k].w[0], c[k].w[1]);
+                } else {
+                    if (BOTH) to[2 * i] = make_uint4(b[k].w[0], b[k].w[1], b[k].w[2], b[k].w[3]);
+                    to[2 * i + 1] = make_uint4(c[k].w[0], c[k].w[1], c[k].w[2], c[k].w[3]);
+                }
+            }
+        }
+    }
+};
+
+// Whether a thread's E channels, and four states, all exist or none do, and may be
+// read at once.
+template <int E>
+__device__ __forceinline__ bool all_wide(const SsmProblem &P, bool u) {
+    return P.D % E == 0 && P.S % 4 == 0 && P.dt.vec && P.dy.vec && P.B.vec && P.C.vec && (!u || P.u.vec) && (!P.z.p || P.z.vec);
+}
+
+// Sixteen bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+
+// E consecutive floats of shared memory (aligned to 16 bytes, or 8 for E = 2).
+template <int E>
+__device__ __forceinline__ void read_row(const float *p, float (&v)[E]) {
+    if constexpr (E == 2) {
+        const float2 x = *reinterpret_cast<const float2 *>(p);
+        v[0] = x.x; v[1] = x.y;
     } else {
-        to[0] = make_uint4(b.w[0], b.w[1], b.w[2], b.w[3]);
-        to[1] = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(p + i);
+            v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+        }
     }
 }
+
 template <typename IN>
 __device__ __forceinline__ void read_b(const uint4 *p, f2 &b01, f2 &b23) {
     if constexpr (sizeof(IN) == 2) {
@@ -149,7 +240,8 @@ __device__ __forceinline__ void read_c(const uint4 *p, f2 &c01, f2 &c23) {
 // What a part of a sequence is to a block.
 struct Place {
     int n, part, count;
-    int64_t sa, pa, pb, row;
+    int sa, pa, pb;                          // (token numbers are below 2^31)
+    int row;
 };
 __device__ __forceinline__ bool find_place(const BackArgs &a, int slot, int *s_seq, Place &w) {
     const SsmProblem &P = a.P;
@@ -158,126 +250,131 @@ __device__ __forceinline__ bool find_place(const BackArgs &a, int slot, int *s_s
     if (a.parts.most == P.N) w.n = longest_first(P.cu, P.N, P.T, P.seq_len, slot, s_seq);
     else find_part(a.parts, P.cu, P.N, P.T, P.seq_len, slot, w.n, w.part, w.count);
     if (w.n < 0) return false;
-    int64_t sb;
-    seq_bounds(P.cu, w.n, P.T, P.seq_len, w.sa, sb);
-    w.pa = w.sa + w.part * a.parts.len;
-    w.pb = w.part == w.count - 1 ? sb : w.pa + a.parts.len;
+    int64_t sa, sb;
+    seq_bounds(P.cu, w.n, P.T, P.seq_len, sa, sb);
+    const int64_t pa = sa + w.part * a.parts.len;
+    w.sa = (int)sa;
+    w.pa = (int)pa;
+    w.pb = (int)(w.part == w.count - 1 ? sb : pa + a.parts.len);
     w.row = slot - w.n;                      // of the carry: between this part and the next
     // as in the scan: overlapping sequences could need more rows than there are
     return w.count == 1 || w.row + (w.part < w.count - 1) <= a.parts.rows;
 }
 
 // The staging warps.
-template <typename X, typename IN, int LN>
+template <typename X, typename IN, int LN, bool FAST>
 struct Stager {
     using L = Layout<IN, LN>;
     static constexpr int E = L::E, CB = L::CB, SP = L::SP;
     const BackArgs &a;
     typename L::Smem &sm;
-    const Place &w;
+    const int pa, pb;
     int tid, srow, sc, ch0, cb, have;
-    bool fullx, fulld;                        // unchecked accesses: u and z, dt and d_out
-    int64_t row0;
+    int64_t row0;                             // of the chunk states: the part's first chunk's start, in sequences' numbering
     Vals<X, E> u, z;                          // of the half to stage next
     Vals<IN, E> dt, dy;
     Vals<X, E> fu, fz;                        // of the half to finish next
     Vals<IN, E> fdt, fdy;
-    float sum_skip[E], sum_bias[E];
+    RawBC<IN, LN, HT> bc;
+    int first;                                // the sequence, where the part is its first; else -1
 
-    __device__ __forceinline__ Stager(const BackArgs &a_, typename L::Smem &sm_, const Place &w_, int ch0_, int cb_)
-        : a(a_), sm(sm_), w(w_), ch0(ch0_), cb(cb_) {
+    __device__ __forceinline__ Stager(const BackArgs &a_, typename L::Smem &sm_, const Place &w, int ch0_, int cb_)
+        : a(a_), sm(sm_), pa(w.pa), pb(w.pb), ch0(ch0_), cb(cb_) {
         const SsmProblem &P = a.P;
         tid = threadIdx.x - kScanners;
         srow = tid / L::TR;
         sc = tid % L::TR * E;
         have = P.D - (ch0 + sc);
-        fullx = P.D - ch0 >= CB && P.u.vec && (!P.z.p || P.z.vec);
-        fulld = P.D - ch0 >= CB && P.dt.vec && P.dy.vec;
-        row0 = ckpt_first_row(P.cu, w.n, P.T, P.seq_len, TT);
+        // chunk k of the part starts with row row0 + k; the sequence's first chunk with its initial state
+        row0 = ckpt_first_row(P.cu, w.n, P.T, P.seq_len, TT) + (w.pa - w.sa) / TT - 1;
+        first = w.pa == w.sa ? w.n : -1;
 #pragma unroll
-        for (int i = 0; i < E; ++i) sum_skip[i] = sum_bias[i] = 0.f;
+        for (int i = 0; i < E; ++i) sm.sums[0][srow][L::swz(sc + i)] = sm.sums[1][srow][L::swz(sc + i)] = 0.f;
         for (int c = tid; c < CB; c += kStagers) {
-            sm.bias[c] = P.dt_bias && ch0 + c < P.D ? P.dt_bias[ch0 + c] : 0.f;
-            sm.skip[c] = P.skip && ch0 + c < P.D ? P.skip[ch0 + c] : 0.f;
+            sm.bias[L::swz(c)] = P.dt_bias && ch0 + c < P.D ? P.dt_bias[ch0 + c] : 0.f;
+            sm.skip[L::swz(c)] = P.skip && ch0 + c < P.D ? P.skip[ch0 + c] : 0.f;
         }
         asm volatile("bar.sync 1, %0;" ::"r"(kStagers) : "memory");
     }
     __device__ __forceinline__ void fetch(int j, Vals<X, E> &vu, Vals<X, E> &vz, Vals<IN, E> &vdt, Vals<IN, E> &vdy) {
         const SsmProblem &P = a.P;
-        const int64_t t = w.pa + (int64_t)j * HT + srow;
-        const int c = ch0 + sc;
-        if (t < w.pb && have > 0) {
-            vu.load(P.u, t, c, have, fullx);
-            if (P.z.p) vz.load(P.z, t, c, have, fullx);
-            vdt.load(P.dt, t, c, have, fulld);
-            vdy.load(P.dy, t, c, have, fulld);
-        } else {
-            vu.clear();
-            vz.clear();
-            vdt.clear();
-            vdy.clear();
-        }
+        const int t = pa + j * HT + srow, c = ch0 + sc;
+        const bool ok = j >= 0 && t < pb && have > 0;
+        vu.template load<FAST>(P.u, t, c, have, ok);
+        if (P.z.p) vz.template load<FAST>(P.z, t, c, have, ok);
+        vdt.template load<FAST>(P.dt, t, c, have, ok);
+        vdy.template load<FAST>(P.dy, t, c, have, ok);
+    }
+    __device__ __forceinline__ void fetch_next(int j) {
+        fetch(j, u, z, dt, dy);
+        bc.template load<true, FAST>(a.P, pa + j * HT, pb, tid, j >= 0);
     }
     // Half j into shared memory; with the second half of a chunk, its start state.
     __device__ __forceinline__ void stage(int j) {
         const SsmProblem &P = a.P;
         const int buf = (j >> 1) & 1, row = (j & 1) * HT + srow;
-        const int64_t t0 = w.pa + (int64_t)j * HT;
+        const int t0 = pa + j * HT;
         if (j & 1) {
-            const int64_t chunk = (w.pa - w.sa) / TT + (j >> 1);     // within the sequence
+            const int64_t row = row0 + (j >> 1);
             const float *from = nullptr;
-            if (chunk == 0) {
-                if (a.init) from = a.init + (int64_t)w.n * P.D * P.S;
-            } else if (row0 + chunk - 1 < a.chunk_capacity) {
-                from = a.chunks + (row0 + chunk - 1) * P.D * P.S;
+            if (j == 1 && first >= 0) {
+                if (a.init) from = a.init + (int64_t)first * P.D * P.S;
+            } else if (row < a.chunk_capacity) {
+                from = a.chunks + row * P.D * P.S;
             } else if (tid == 0) {
                 atomicOr(&g_ssm_status, kBwdMissingState);
             }
             for (int i = tid; i < CB * LN; i += kStagers) {
                 const int c = i / LN, n0 = 4 * (i % LN);
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (from && ch0 + c < P.D) v = load_states(from + (int64_t)(ch0 + c) * P.S, n0, P.S, P.svec);
-                *reinterpret_cast<float4 *>(&sm.h[buf][c][n0]) = v;
+                float4 *to = reinterpret_cast<float4 *>(&sm.h[buf][c][n0]);
+                if (from && ch0 + c < P.D && P.svec && n0 < P.S)
+                    copy16(to, from + (int64_t)(ch0 + c) * P.S + n0);   // waited for before the barrier
+                else if (from && ch0 + c < P.D)
+                    *to = load_states(from + (int64_t)(ch0 + c) * P.S, n0, P.S, P.svec);
+                else
+                    *to = make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
-        for (int i = tid; i < HT * LN; i += kStagers) {
-            const int r = i / LN;
-            stage_bc<IN, LN>(P, sm.bc[buf][(j & 1) * HT + r][i % LN], t0 + r, i % LN, t0 + r < w.pb, true);
-        }
-        const bool in = t0 + srow < w.pb && have > 0;
-        float dl[E], dyp[E];
+        bc.template put<true>(sm.bc[buf][(j & 1) * HT][0], tid);
+        const bool in = t0 + srow < pb && have > 0;
+        constexpr int VE = E < 4 ? E : 4;      // at a time
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            dl[i] = dt.get(i) + sm.bias[sc + i];
-            dyp[i] = dy.get(i);
-        }
-        if (P.softplus) softplus_all(dl);
-        if (P.z.p) {
+        for (int i0 = 0; i0 < E; i0 += VE) {
+            float dl[VE], dyp[VE];
+            read_swz<L, VE>(sm.bias, sc + i0, dl);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float g = z.get(i);
-                dyp[i] *= g * sigmoid_fast(g);
+            for (int i = 0; i < VE; ++i) {
+                dl[i] += dt.get(i0 + i);
+                dyp[i] = dy.get(i0 + i);
             }
-        }
+            if (P.softplus) softplus_all(dl);
+            if (P.z.p) {
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {
-            float4 v;
-            v.x = in ? dl[i] : 0.f;
-            v.z = in ? dl[i + 1] : 0.f;
-            v.y = v.x * u.get(i);
-            v.w = v.z * u.get(i + 1);
-            *reinterpret_cast<float4 *>(&sm.d[buf][row][L::column(sc + i)]) = v;
-            *reinterpret_cast<float2 *>(&sm.dyp[buf][row][sc + i]) = make_float2(dyp[i], dyp[i + 1]);
+                for (int i = 0; i < VE; ++i) {
+                    const float g = z.get(i0 + i);
+                    dyp[i] *= g * sigmoid_fast(g);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VE; i += 2) {
+                float4 v;
+                v.x = in ? dl[i] : 0.f;
+                v.z = in ? dl[i + 1] : 0.f;
+                v.y = v.x * u.get(i0 + i);
+                v.w = v.z * u.get(i0 + i + 1);
+                *reinterpret_cast<float4 *>(&sm.d[buf][row][L::column(sc + i0 + i)]) = v;
+            }
+            write_swz<L, VE>(sm.dyp[buf][row], sc + i0, dyp);
         }
     }
     // The gradients of half j.
     __device__ __forceinline__ void finish(int j) {
         const SsmProblem &P = a.P;
         const int buf = (j >> 1) & 1, row = (j & 1) * HT + srow, ob = j & 1;
-        const int64_t t0 = w.pa + (int64_t)j * HT;
+        const int t0 = pa + j * HT;
         for (int i = tid; i < HT * 2 * SP / 4; i += kStagers) {
             const int t = i / (2 * SP / 4), k = i % (2 * SP / 4);
-            if (t0 + t < w.pb) {
+            if (t0 + t < pb) {
                 float4 s = *reinterpret_cast<const float4 *>(&sm.share[ob][0][t][4 * k]);
 #pragma unroll
                 for (int v = 1; v < 4; ++v) {
@@ -287,36 +384,92 @@ struct Stager {
                 *reinterpret_cast<float4 *>(a.share + ((int64_t)cb * P.T + t0 + t) * (2 * SP) + 4 * k) = s;
             }
         }
-        if (t0 + srow >= w.pb || have <= 0) return;
-        float o1[E], o2[E], o3[E];
+        if (t0 + srow >= pb || have <= 0) return;
+        // a few channels at a time, to keep few values alive; Delta and dyp were written by this thread
+        constexpr int VE = E < 4 ? E : 4;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = L::ycol(sc + i);
-            const float p = sm.out[ob][0][srow][c], r = sm.out[ob][1][srow][c] * kLn2, y = sm.out[ob][2][srow][c];
-            const float delta = sm.d[buf][row][L::column(sc + i)].x, dyp = sm.dyp[buf][row][sc + i];   // written by this thread
-            const float skip = sm.skip[sc + i], uv = fu.get(i);
-            o1[i] = fmaf(delta, p, skip * dyp);
-            float x = fmaf(uv, p, r);
-            if (P.softplus) x *= sigmoid_fast(fdt.get(i) + sm.bias[sc + i]);
-            o2[i] = x;
-            sum_bias[i] += x;
-            sum_skip[i] = fmaf(dyp, uv, sum_skip[i]);
+        for (int k = 0; k < E; k += VE) {
+            const int c = sc + k, yc = L::ycol(c);
+            const int64_t at = (int64_t)(t0 + srow) * P.D + ch0 + c;
+            float o[VE], x[VE], dyp[VE], v[VE];
+            read_swz<L, VE>(sm.skip, c, v);
             if (P.z.p) {
-                const float zv = fz.get(i), s = sigmoid_fast(zv);
-                o3[i] = fdy.get(i) * fmaf(skip, uv, y) * fmaf(zv * s, 1.f - s, s);
+                read_row<VE>(&sm.out[ob][2][srow][yc], o);
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const float g = fz.get(k + i), s = sigmoid_fast(g);
+                    o[i] = fdy.get(k + i) * fmaf(v[i], fu.get(k + i), o[i]) * fmaf(g * s, 1.f - s, s);
+                }
+                store_grad<VE>(a.dz, at, o, have - k, a.ovec, a.obf);
             }
+            read_row<VE>(&sm.out[ob][0][srow][yc], o);
+            read_row<VE>(&sm.out[ob][1][srow][yc], x);
+            read_swz<L, VE>(sm.dyp[buf][row], c, dyp);
+#pragma unroll
+            for (int i = 0; i < VE; i += 2) {
+                const float4 d = *reinterpret_cast<const float4 *>(&sm.d[buf][row][L::column(c + i)]);
+                x[i] = fmaf(fu.get(k + i), o[i], x[i] * kLn2);
+                x[i + 1] = fmaf(fu.get(k + i + 1), o[i + 1], x[i + 1] * kLn2);
+                o[i] = fmaf(d.x, o[i], v[i] * dyp[i]);
+                o[i + 1] = fmaf(d.z, o[i + 1], v[i + 1] * dyp[i + 1]);
+            }
+            store_grad<VE>(a.du, at, o, have - k, a.ovec, a.obf);
+            read_swz<L, VE>(sm.sums[0][srow], c, v);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) v[i] = fmaf(dyp[i], fu.get(k + i), v[i]);
+            write_swz<L, VE>(sm.sums[0][srow], c, v);
+            if (P.softplus) {
+                read_swz<L, VE>(sm.bias, c, v);
+#pragma unroll
+                for (int i = 0; i < VE; ++i) x[i] *= sigmoid_fast(fdt.get(k + i) + v[i]);
+            }
+            store_grad<VE>(a.ddt, at, x, have - k, a.ovec, a.obf);
+            read_swz<L, VE>(sm.sums[1][srow], c, v);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) v[i] += x[i];
+            write_swz<L, VE>(sm.sums[1][srow], c, v);
         }
-        const int64_t at = (t0 + srow) * P.D + ch0 + sc;
-        store_grad<E>(a.du, at, o1, have, a.ovec, a.obf);
-        store_grad<E>(a.ddt, at, o2, have, a.ovec, a.obf);
-        if (P.z.p) store_grad<E>(a.dz, at, o3, have, a.ovec, a.obf);
     }
 };
+
+// What the staging warps do for a part.
+template <typename X, typename IN, int LN, bool FAST>
+__device__ __forceinline__ void stage_part(const BackArgs &a, typename Layout<IN, LN>::Smem &sm, const Place &w, int ch0,
+                                           int cb, int tiles) {
+    // While the other warps work through half j, these stage half j - 2 (the
+    // whole chunk before j's is in place when j is its second half) and finish half
+    // j + 1.
+    Stager<X, IN, LN, FAST> st(a, sm, w, ch0, cb);
+    const int last = 2 * tiles - 1;
+    if (tiles > 0) {
+        st.fetch_next(last);
+        st.stage(last);
+        st.fetch_next(last - 1);
+        st.stage(last - 1);
+        st.fetch_next(last - 2);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    __syncthreads();
+    
+    for (int j = last; j >= 0; --j) {
+        if (j < last) st.finish(j + 1);
+        if (j >= 2) {
+            st.stage(j - 2);
+            st.fetch_next(j - 3);
+        }
+        st.fetch(j, st.fu, st.fz, st.fdt, st.fdy);
+        // a chunk's start state is needed two steps after it was asked for
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+    }
+    if (tiles > 0) st.finish(0);
+}
 
 // X: type of u and z (int8 codes or IN); IN: type of dt, B, C and d_out.
 template <typename X, typename IN, int LN>
 __global__ void __launch_bounds__(kThreads, (Layout<IN, LN>::kBlocks))
-kda_ssm_scan_backward_kernel(const BackArgs a) {
+kda_ssm_scan_backward_kernel(const __grid_constant__ BackArgs a) {
     using L = Layout<IN, LN>;
     constexpr int CW = L::CW, CB = L::CB, SP = L::SP;
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -343,45 +496,17 @@ kda_ssm_scan_backward_kernel(const BackArgs a) {
     const int tiles = (int)((w.pb - w.pa + TT - 1) / TT);
 
     if (threadIdx.x >= kScanners) {
-        // While the other warps work through half j, these stage half j - 2 (the
-        // whole chunk before j's is in place when j is its second half) and finish half
-        // j + 1.
         if constexpr (L::kBlocks == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        Stager<X, IN, LN> st(a, sm, w, ch0, cb);
-        const int last = 2 * tiles - 1;
-        if (tiles > 0) {
-            st.fetch(last, st.u, st.z, st.dt, st.dy);
-            st.stage(last);
-            st.fetch(last - 1, st.u, st.z, st.dt, st.dy);
-            st.stage(last - 1);
-            if (last >= 2) st.fetch(last - 2, st.u, st.z, st.dt, st.dy);
-        }
-        __syncthreads();
-        for (int j = last; j >= 0; --j) {
-            if (j >= 2) {
-                st.stage(j - 2);
-                if (j >= 3) st.fetch(j - 3, st.u, st.z, st.dt, st.dy);
-            }
-            if (j < last) st.finish(j + 1);
-            st.fetch(j, st.fu, st.fz, st.fdt, st.fdy);
-            __syncthreads();
-        }
-        if (tiles > 0) st.finish(0);
+        if (all_wide<L::E>(P, true)) stage_part<X, IN, LN, true>(a, sm, w, ch0, cb, tiles);
+        else stage_part<X, IN, LN, false>(a, sm, w, ch0, cb, tiles);
         // dD and ddt_bias: over the rows of threads
         asm volatile("bar.sync 1, %0;" ::"r"(kStagers) : "memory");
-        constexpr int E = L::E;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            sm.out[0][0][st.srow][st.sc + i] = st.sum_skip[i];
-            sm.out[0][1][st.srow][st.sc + i] = st.sum_bias[i];
-        }
-        asm volatile("bar.sync 1, %0;" ::"r"(kStagers) : "memory");
-        for (int c = st.tid; c < CB; c += kStagers) {
+        for (int c = threadIdx.x - kScanners; c < CB; c += kStagers) {
             if (ch0 + c < P.D) {
                 float x = 0.f, y = 0.f;
                 for (int t = 0; t < HT; ++t) {
-                    x += sm.out[0][0][t][c];
-                    y += sm.out[0][1][t][c];
+                    x += sm.sums[0][t][L::swz(c)];
+                    y += sm.sums[1][t][L::swz(c)];
                 }
                 if (a.dskip) a.dskip[at * P.D + ch0 + c] = x;
                 if (a.dbias) a.dbias[at * P.D + ch0 + c] = y;
@@ -400,7 +525,7 @@ kda_ssm_scan_backward_kernel(const BackArgs a) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
         if (ch + c < P.D) {
             x = load_states(P.A + (int64_t)(ch + c) * P.S, n0, P.S, P.svec);
-            const float *from = w.part < w.count - 1 ? a.carry + w.row * P.D * P.S
+            const float *from = w.part < w.count - 1 ? a.carry + (int64_t)w.row * P.D * P.S
                                 : a.d_final ? a.d_final + (int64_t)w.n * P.D * P.S : nullptr;
             if (from) y = load_states(from + (int64_t)(ch + c) * P.S, n0, P.S, P.svec);
         }
@@ -411,7 +536,7 @@ kda_ssm_scan_backward_kernel(const BackArgs a) {
         dA[c][0] = dA[c][1] = 0;
     }
     const int col = L::column(wc), yc = L::ycol(wc);
-    f2 start[2][2], eighth[2][2];            // the states at the chunk's start and at its second quarter
+    f2 eighth[2][2];                         // the states at the chunk's second quarter
     __syncthreads();
 #pragma unroll 1
     for (int j = 2 * tiles - 1; j >= 0; --j) {
@@ -433,8 +558,8 @@ kda_ssm_scan_backward_kernel(const BackArgs a) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const float4 v = *reinterpret_cast<const float4 *>(&sm.h[buf][wc + c][n0]);
-                start[c][0] = s[c][0] = pack2(v.x, v.y);
-                start[c][1] = s[c][1] = pack2(v.z, v.w);
+                s[c][0] = pack2(v.x, v.y);
+                s[c][1] = pack2(v.z, v.w);
             }
 #pragma unroll 1
             for (int k = 0; k < 3; ++k) {
@@ -450,12 +575,13 @@ kda_ssm_scan_backward_kernel(const BackArgs a) {
             }
         } else {
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    s[c][i] = eighth[c][i];
-                    third[c][i] = start[c][i];
-                }
+            for (int c = 0; c < 2; ++c) {
+                s[c][0] = eighth[c][0];
+                s[c][1] = eighth[c][1];
+                const float4 v = *reinterpret_cast<const float4 *>(&sm.h[buf][wc + c][n0]);
+                third[c][0] = pack2(v.x, v.y);
+                third[c][1] = pack2(v.z, v.w);
+            }
         }
 #pragma unroll 1
         for (int k = 1; k >= 0; --k) {       // the half's quarters, from the states s and third
@@ -480,7 +606,7 @@ kda_ssm_scan_backward_kernel(const BackArgs a) {
                 for (int i = 3; i >= 0; --i) {
                     const int t = t4 + i;
                     const float4 d = *reinterpret_cast<const float4 *>(&sm.d[buf][tb + t][col]);
-                    const float2 e = *reinterpret_cast<const float2 *>(&sm.dyp[buf][tb + t][wc]);
+                    const float2 e = *reinterpret_cast<const float2 *>(&sm.dyp[buf][tb + t][L::swz(wc)]);
                     f2 b01, b23, c01, c23, sC01 = 0, sC23 = 0, sB01 = 0, sB23 = 0;
                     read_b<IN>(sm.bc[buf][tb + t][q], b01, b23);
                     read_c<IN>(sm.bc[buf][tb + t][q], c01, c23);
@@ -575,7 +701,7 @@ kda_ssm_scan_backward_kernel(const BackArgs a) {
 // gives the part before, and the sum of Delta.
 template <typename X, typename IN, int LN>
 __global__ void __launch_bounds__(kThreads, 2)
-kda_ssm_adjoint_kernel(const BackArgs a) {
+kda_ssm_adjoint_kernel(const __grid_constant__ BackArgs a) {
     using L = Layout<IN, LN>;
     constexpr int CW = L::CW, CB = L::CB, E = L::E, HTB = kStagers / L::TR;
     static_assert(HTB == HT, "a thread stages one row of a half");
@@ -594,32 +720,28 @@ kda_ssm_adjoint_kernel(const BackArgs a) {
 
     if (threadIdx.x >= kScanners) {
         const int tid = threadIdx.x - kScanners, srow = tid / L::TR, sc = tid % L::TR * E, have = P.D - (ch0 + sc);
-        const bool full = P.D - ch0 >= CB && (!P.z.p || P.z.vec) && P.dt.vec && P.dy.vec;
         float bias[E];
         Vals<X, E> z[2];
         Vals<IN, E> dt[2], dy[2];
+        RawBC<IN, LN, TT> bc;
 #pragma unroll
         for (int i = 0; i < E; ++i) bias[i] = P.dt_bias && i < have ? P.dt_bias[ch0 + sc + i] : 0.f;
-        auto fetch = [&](int k) {
+        auto fetch = [&](int k, auto fast) {
+            constexpr bool FAST = decltype(fast)::value;
+            bc.template load<false, FAST>(P, w.pa + k * TT, w.pb, tid, k >= 0);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int64_t t = w.pa + (int64_t)k * TT + r * HT + srow;
-                if (t < w.pb && have > 0) {
-                    if (P.z.p) z[r].load(P.z, t, ch0 + sc, have, full);
-                    dt[r].load(P.dt, t, ch0 + sc, have, full);
-                    dy[r].load(P.dy, t, ch0 + sc, have, full);
-                } else {
-                    z[r].clear();
-                    dt[r].clear();
-                    dy[r].clear();
-                }
+                const int t = w.pa + k * TT + r * HT + srow;
+                const bool ok = k >= 0 && t < w.pb && have > 0;
+                if (P.z.p) z[r].template load<FAST>(P.z, t, ch0 + sc, have, ok);
+                dt[r].template load<FAST>(P.dt, t, ch0 + sc, have, ok);
+                dy[r].template load<FAST>(P.dy, t, ch0 + sc, have, ok);
             }
         };
         auto stage = [&](int k) {
             const int buf = k & 1;
-            const int64_t t0 = w.pa + (int64_t)k * TT;
-            for (int i = tid; i < TT * LN; i += kStagers)
-                stage_bc<IN, LN>(P, sm.bc[buf][i / LN][i % LN], t0 + i / LN, i % LN, t0 + i / LN < w.pb, false);
+            const int t0 = w.pa + k * TT;
+            bc.template put<false>(sm.bc[buf][0][0], tid);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int row = r * HT + srow;
@@ -644,17 +766,21 @@ kda_ssm_adjoint_kernel(const BackArgs a) {
                         make_float4(in ? dl[i] : 0.f, e[i], in ? dl[i + 1] : 0.f, e[i + 1]);
             }
         };
-        fetch(tiles - 1);
-        stage(tiles - 1);
-        if (tiles > 1) fetch(tiles - 2);
-        __syncthreads();
-        for (int k = tiles - 1; k >= 0; --k) {
-            if (k > 0) {
-                stage(k - 1);
-                if (k > 1) fetch(k - 2);
-            }
+        auto run = [&](auto fast) {
+            fetch(tiles - 1, fast);
+            stage(tiles - 1);
+            fetch(tiles - 2, fast);               // (nothing where there is no such tile)
             __syncthreads();
-        }
+            for (int k = tiles - 1; k >= 0; --k) {
+                if (k > 0) {
+                    stage(k - 1);
+                    fetch(k - 2, fast);
+                }
+                __syncthreads();
+            }
+        };
+        if (all_wide<E>(P, false)) run(std::true_type());
+        else run(std::false_type());
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -698,13 +824,13 @@ kda_ssm_adjoint_kernel(const BackArgs a) {
         float4 v;
         unpack2(g[c][0], v.x, v.y);
         unpack2(g[c][1], v.z, v.w);
-        store_states(a.carry + ((w.row - 1) * P.D + ch + c) * P.S, v, n0, P.S, P.svec);
-        if (q == 0) a.sums[(w.row - 1) * P.D + ch + c] = dsum[c];
+        store_states(a.carry + ((int64_t)(w.row - 1) * P.D + ch + c) * P.S, v, n0, P.S, P.svec);
+        if (q == 0) a.sums[(int64_t)(w.row - 1) * P.D + ch + c] = dsum[c];
     }
 }
 
 // From what the parts give back to what the ones before them start with, in place.
-__global__ void __launch_bounds__(256) kda_ssm_carry_back_kernel(const BackArgs a) {
+__global__ void __launch_bounds__(256) kda_ssm_carry_back_kernel(const __grid_constant__ BackArgs a) {
     const SsmProblem &P = a.P;
     const int64_t M = (int64_t)P.D * P.S;
     const int per = (int)((M + 255) / 256), n = blockIdx.x / per;
@@ -766,6 +892,37 @@ int blocks_across(const SsmProblem &P) {
     const int CB = 256 / lanes_of(P.S);
     return (P.D + CB - 1) / CB;
 }
+// How a batch is cut: b blocks of sequences side by side, each in K parts.  Two
+// blocks share an SM; a round of 304 blocks takes 2.9 where one of up to 152, alone on
+// their SMs, takes 2, and the adjoint's own pass adds 0.19 of that where K > 1.  The K of
+// least cost is taken; no part is under four tiles.  8192 tokens, S = 16, bf16, u and z
+// in 8 bits, K = 1 / 4 / 7 / 9 / 14 / 19: 4096 channels 2019 / 957 / 881 / 832 / 833 / 828 us,
+// 8192 channels 2049 / 1785 / 1596 / 1547 / 1513 / 1562.
+int best_parts(int64_t b, int64_t tokens) {
+    const auto cost = [&](int64_t K) {
+        const int64_t n = b * K, rest = n % 304;
+        const double rounds = 2.9 * (double)(n / 304) + (rest > 152 ? 2.9 : rest > 0 ? 2.0 : 0.0);
+        return rounds / (double)K * (K > 1 ? 1.19 : 1.0) + 0.004 * (double)K;
+    };
+    int best = 1;
+    for (int K = 2; K <= 64 && K <= tokens / (4 * TT); ++K)
+        if (cost(K) < cost(best)) best = K;
+    return best;
+}
+// Where the lengths are known only on the device (`ragged`), the batch is cut as if it
+// were one sequence, and a sequence of up to one and a half parts' length stays whole.
+Parts back_parts(const SsmProblem &P, bool ragged) {
+    const int64_t b = blocks_across(P), tokens = ragged || P.N == 0 ? P.T : P.T / P.N;
+    const int K = best_parts(ragged ? b : b * P.N, tokens);
+    Parts parts;
+    parts.len = ((tokens + K - 1) / K + TT - 1) / TT * TT;
+    if (parts.len < TT) parts.len = TT;
+    parts.whole = K == 1 ? INT32_MAX : ragged ? parts.len * 3 / 2 : parts.len;
+    parts.rows = P.T > parts.whole || (!ragged && tokens > parts.whole) ? P.T / parts.len : 0;
+    parts.most = ragged ? P.N + (int32_t)parts.rows : (int32_t)(P.N * parts.of(tokens));
+    return parts;
+}
+
 int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 
 template <typename X, typename IN, int LN>
@@ -806,15 +963,17 @@ cudaError_t by_states(const BackArgs &a, cudaStream_t s) {
 struct Space {
     int64_t dA, dskip, dbias, carry, sums, all;
 };
-Space space_of(const SsmProblem &P, const Parts &parts) {
-    const int64_t most = P.N + parts.rows, row = (int64_t)P.D * P.S;   // with cu_seqlens; without, no more
+// (for a batch with cu_seqlens and one without, whichever takes more)
+Space space_of(const SsmProblem &P) {
+    const Parts x = back_parts(P, true), y = back_parts(P, false);
+    const int64_t rows = x.rows > y.rows ? x.rows : y.rows, most = P.N + rows, row = (int64_t)P.D * P.S;
     Space s;
     s.dA = up4((int64_t)blocks_across(P) * P.T * 8 * lanes_of(P.S));
     s.dskip = s.dA + up4(most * row);
     s.dbias = s.dskip + up4(most * P.D);
     s.carry = s.dbias + up4(most * P.D);
-    s.sums = s.carry + up4(parts.rows * row);
-    s.all = s.sums + up4(parts.rows * P.D);
+    s.sums = s.carry + up4(rows * row);
+    s.all = s.sums + up4(rows * P.D);
     return s;
 }
 
@@ -832,7 +991,7 @@ cudaError_t kda_ssm_read_status(unsigned *status) {
 }
 
 int64_t kda_ssm_scan_backward_ws(const SsmProblem &P) {
-    return space_of(P, kda_ssm_parts(P)).all * (int64_t)sizeof(float);
+    return space_of(P).all * (int64_t)sizeof(float);
 }
 
 cudaError_t kda_launch_ssm_scan_backward(const SsmProblem &P, const float *init, const float *chunk_states,
@@ -853,8 +1012,8 @@ cudaError_t kda_launch_ssm_scan_backward(const SsmProblem &P, const float *init,
     a.ovec = (int64_t)P.D * (a.obf ? 2 : 4) % 16 == 0;
     for (const void *p : {(const void *)du, (const void *)ddt, (const void *)dz})
         if ((uintptr_t)p & 15u) a.ovec = false;
-    a.parts = kda_ssm_parts(P);
-    const Space sp = space_of(P, a.parts);
+    a.parts = back_parts(P, P.cu != nullptr);
+    const Space sp = space_of(P);
     const int SP = 4 * lanes_of(P.S), ncb = blocks_across(P);
     const int64_t nA = (int64_t)P.D * P.S;
     const bool direct = a.parts.most == 1;

@@ -112,6 +112,28 @@ struct Rows {
     int32_t vec;           // rows may be read with 16-byte accesses
 };
 
+// Loads of inputs ahead of their use.  They stay where they are written (a plain
+// read-only load may be moved by the compiler down to its first use, across
+// barriers too), leave L1 to what is read again, and are predicated instead of
+// branched around: a register that a load writes in one branch only is copied where
+// the branches meet, and that copy waits for the load.  With !ok the value stays.
+__device__ __forceinline__ void ahead16(uint32_t &x, uint32_t &y, uint32_t &z, uint32_t &w, const void *p, bool ok) {
+    asm volatile("{ .reg .pred q; setp.ne.u32 q, %5, 0; @q ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4]; }"
+                 : "+r"(x), "+r"(y), "+r"(z), "+r"(w) : "l"(p), "r"((uint32_t)ok));
+}
+__device__ __forceinline__ void ahead8(uint32_t &x, uint32_t &y, const void *p, bool ok) {
+    asm volatile("{ .reg .pred q; setp.ne.u32 q, %3, 0; @q ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2]; }"
+                 : "+r"(x), "+r"(y) : "l"(p), "r"((uint32_t)ok));
+}
+__device__ __forceinline__ void ahead4(uint32_t &x, const void *p, bool ok) {
+    asm volatile("{ .reg .pred q; setp.ne.u32 q, %2, 0; @q ld.global.nc.L1::no_allocate.u32 %0, [%1]; }"
+                 : "+r"(x) : "l"(p), "r"((uint32_t)ok));
+}
+__device__ __forceinline__ void ahead2(uint32_t &x, const void *p, bool ok) {
+    asm volatile("{ .reg .pred q; .reg .u16 h; setp.ne.u32 q, %2, 0; mov.u16 h, 0; @q ld.global.nc.L1::no_allocate.u16 h, [%1]; "
+                 "cvt.u32.u16 %0, h; }" : "+r"(x) : "l"(p), "r"((uint32_t)ok));
+}
+
 // E consecutive elements of a row, raw (as loaded) and as fp32.  Elements at or
 // past `have` read as 0.
 template <typename T, int E>
@@ -124,27 +146,25 @@ struct Raw {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = 0;
     }
-    // All E elements, from an address aligned to min(16, kBytes) bytes.
-    __device__ __forceinline__ void load_all(const T *p) {
+    // All E elements, from an address aligned to min(16, kBytes) bytes; with !ok, zeros.
+    __device__ __forceinline__ void load_if(const T *p, bool ok) {
+        clear();
         if constexpr (kBytes % 16 == 0) {
 #pragma unroll
-            for (int i = 0; i < kBytes / 16; ++i) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-            }
+            for (int i = 0; i < kBytes / 16; ++i)
+                ahead16(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3], reinterpret_cast<const uint4 *>(p) + i, ok);
         } else if constexpr (kBytes % 8 == 0) {
 #pragma unroll
-            for (int i = 0; i < kBytes / 8; ++i) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
-                w[2 * i] = v.x; w[2 * i + 1] = v.y;
-            }
+            for (int i = 0; i < kBytes / 8; ++i) ahead8(w[2 * i], w[2 * i + 1], reinterpret_cast<const uint2 *>(p) + i, ok);
         } else if constexpr (kBytes % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < kBytes / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+            for (int i = 0; i < kBytes / 4; ++i) ahead4(w[i], reinterpret_cast<const uint32_t *>(p) + i, ok);
         } else {
-            slow(p, E);
+            static_assert(kBytes == 2, "two, or a multiple of four bytes");
+            ahead2(w[0], p, ok);
         }
     }
+    __device__ __forceinline__ void load_all(const T *p) { load_if(p, true); }
     // `vec`: p is aligned to min(16, kBytes) bytes; FULL: that, and all E elements exist
     template <bool FULL = false>
     __device__ __forceinline__ void load(const T *p, int have, bool vec) {

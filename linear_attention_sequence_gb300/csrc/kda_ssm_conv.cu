@@ -202,7 +202,7 @@ __device__ __forceinline__ void conv_run(const ConvArgs &a, const f2 (&w)[W][NP]
 }
 
 template <typename IN, typename OUT, int W>
-__global__ void __launch_bounds__(kThreads) kda_ssm_conv_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kThreads) kda_ssm_conv_kernel(const __grid_constant__ ConvArgs a) {
     const SsmProblem &P = a.P;
     const int nvb = (P.D + V * kThreads - 1) / (V * kThreads);
     const int c0 = ((int)(blockIdx.x % nvb) * kThreads + threadIdx.x) * V;
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads) kda_ssm_conv_kernel(const ConvArgs a
 // The last W - 1 inputs of every sequence.  A thread owns one channel of one
 // sequence and reads before it writes: cout may be cin.
 template <typename IN, int W>
-__global__ void __launch_bounds__(kThreads) kda_ssm_conv_state_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kThreads) kda_ssm_conv_state_kernel(const __grid_constant__ ConvArgs a) {
     const SsmProblem &P = a.P;
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (i >= (int64_t)P.N * P.D) return;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads) kda_ssm_conv_state_kernel(const Conv
 // One token a sequence: output and new state in one pass (cout may be cin: a thread
 // reads what it writes).
 template <typename IN, typename OUT, int W>
-__global__ void __launch_bounds__(kThreads) kda_ssm_conv_token_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kThreads) kda_ssm_conv_token_kernel(const __grid_constant__ ConvArgs a) {
     const SsmProblem &P = a.P;
     const int nv = (P.D + V * kThreads - 1) / (V * kThreads);
     const int64_t n = blockIdx.x / nv;
@@ -383,7 +383,7 @@ __device__ __forceinline__ void back_run(const ConvArgs &a, Back<W> &k, int64_t 
 }
 
 template <typename IN, typename DY, typename OUT, int W>
-__global__ void __launch_bounds__(kThreads) kda_ssm_conv_backward_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kThreads) kda_ssm_conv_backward_kernel(const __grid_constant__ ConvArgs a) {
     const SsmProblem &P = a.P;
     const int nvb = (P.D + V * kThreads - 1) / (V * kThreads);
     const int c0 = ((int)(blockIdx.x % nvb) * kThreads + threadIdx.x) * V;
@@ -491,7 +491,7 @@ kda_ssm_conv_reduce_kernel(const float *__restrict__ part, int64_t tiles, int D,
 }
 
 // A sequence without tokens hands its state on: so does its gradient.
-__global__ void __launch_bounds__(kThreads) kda_ssm_conv_empty_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(kThreads) kda_ssm_conv_empty_kernel(const __grid_constant__ ConvArgs a) {
     const SsmProblem &P = a.P;
     const int W = P.S;
     const int64_t per = (int64_t)(W - 1) * P.D, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;

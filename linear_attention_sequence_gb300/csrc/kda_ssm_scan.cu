@@ -25,6 +25,8 @@
 // h_part + exp(A sum Delta) h_in, and the scan proper runs every part from its own
 // h_in.
 
+#include <type_traits>
+
 #include "kda_ssm_common.cuh"
 
 namespace {
@@ -74,8 +76,9 @@ struct Layout {
     static __device__ __forceinline__ int ycol(int c) { return c + 4 * (c >> 5); }
 };
 
-// The staging warps.  STATES: only what the states need.
-template <typename IN, typename OUT, int LN, bool STATES>
+// The staging warps.  STATES: only what the states need.  FAST: a thread's channels,
+// and four states, all exist or none do, and may be read and written at once.
+template <typename IN, typename OUT, int LN, bool STATES, bool FAST>
 struct Stager {
     using L = Layout<IN, LN>;
     static constexpr int E = L::E, NR = L::NR, RP = L::RP, BI = L::BI;
@@ -83,7 +86,6 @@ struct Stager {
     typename L::Smem &sm;
     const int64_t pb;
     int tid, srow, sc, have;
-    bool full, bcfull;                         // unchecked accesses to a whole tile
     const IN *pu, *pd, *pz, *pB, *pC;          // this thread's place in the tile to fetch
     const IN *fu, *fz;                         // and in the tile to finish
     OUT *po;
@@ -99,8 +101,6 @@ struct Stager {
         srow = tid / L::TR;
         sc = tid % L::TR * E;
         have = P.D - (ch0 + sc);
-        full = P.D - ch0 >= L::CB && P.u.vec && P.dt.vec && (STATES || !P.z.p || P.z.vec) && (STATES || a.ovec);
-        bcfull = P.B.vec && P.C.vec && P.S == 4 * LN;
         const int64_t t = pa + srow;
         pu = fu = (const IN *)P.u.p + t * P.u.stride + ch0 + sc;
         pd = (const IN *)P.dt.p + t * P.dt.stride + ch0 + sc;
@@ -114,43 +114,37 @@ struct Stager {
             skip[i] = (P.skip && i < have) ? P.skip[ch0 + sc + i] : 0.f;
         }
     }
-    // Loads the next tile, which starts at t0.
-    __device__ __forceinline__ void fetch(int64_t t0) {
-        const SsmProblem &P = a.P;
-        const bool whole = t0 + TT <= pb;
-        if (full && whole) {
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                ru[r].load_all(pu + r * RP * P.u.stride);
-                rd[r].load_all(pd + r * RP * P.dt.stride);
-            }
+    static __device__ __forceinline__ void load(Raw<IN, E> &r, const IN *p, int have, bool vec, bool ok) {
+        if constexpr (FAST) {
+            r.load_if(p, ok);
         } else {
+            if (ok) r.load(p, have, vec);
+            else r.clear();
+        }
+    }
+    // Loads the next tile, which starts at t0 (nothing if !live).
+    __device__ __forceinline__ void fetch(int64_t t0, bool live) {
+        const SsmProblem &P = a.P;
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                ru[r].clear();
-                rd[r].clear();
-                if (t0 + srow + r * RP < pb && have > 0) {
-                    ru[r].load(pu + r * RP * P.u.stride, have, P.u.vec);
-                    rd[r].load(pd + r * RP * P.dt.stride, have, P.dt.vec);
-                }
-            }
+        for (int r = 0; r < NR; ++r) {
+            const bool ok = live && t0 + srow + r * RP < pb && have > 0;
+            load(ru[r], pu + r * RP * P.u.stride, have, P.u.vec, ok);
+            load(rd[r], pd + r * RP * P.dt.stride, have, P.dt.vec, ok);
         }
         pu += TT * P.u.stride;
         pd += TT * P.dt.stride;
 #pragma unroll
         for (int k = 0; k < BI; ++k) {
-            const int i = tid + k * kStagers;
+            const int i = tid + k * kStagers, nb = 4 * (i % LN);
             const IN *qB = pB + k * (kStagers / LN) * P.B.stride, *qC = pC + k * (kStagers / LN) * P.C.stride;
-            if (bcfull && whole) {
-                if (i < TT * LN) {
-                    rb[k].load_all(qB);
-                    if (!STATES) rc[k].load_all(qC);
-                }
+            const bool ok = live && i < TT * LN && t0 + i / LN < pb && nb < P.S;
+            if constexpr (FAST) {
+                rb[k].load_if(qB, ok);
+                if (!STATES) rc[k].load_if(qC, ok);
             } else {
-                const int nb = 4 * (i % LN);
                 rb[k].clear();
                 rc[k].clear();
-                if (i < TT * LN && t0 + i / LN < pb && nb < P.S) {
+                if (ok) {
                     rb[k].load(qB, P.S - nb, P.B.vec);
                     if (!STATES) rc[k].load(qC, P.S - nb, P.C.vec);
                 }
@@ -196,22 +190,13 @@ struct Stager {
         }
     }
     // u and z again, of the tile to finish next, which starts at t0.
-    __device__ __forceinline__ void fetch_again(int64_t t0) {
+    __device__ __forceinline__ void fetch_again(int64_t t0, bool live) {
         const SsmProblem &P = a.P;
-        if (full && t0 + TT <= pb) {
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                gu[r].load_all(fu + r * RP * P.u.stride);
-                if (P.z.p) gz[r].load_all(fz + r * RP * P.z.stride);
-            }
-        } else {
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                if (t0 + srow + r * RP < pb && have > 0) {
-                    gu[r].load(fu + r * RP * P.u.stride, have, P.u.vec);
-                    if (P.z.p) gz[r].load(fz + r * RP * P.z.stride, have, P.z.vec);
-                }
-            }
+        for (int r = 0; r < NR; ++r) {
+            const bool ok = live && t0 + srow + r * RP < pb && have > 0;
+            load(gu[r], fu + r * RP * P.u.stride, have, P.u.vec, ok);
+            if (P.z.p) load(gz[r], fz + r * RP * P.z.stride, have, P.z.vec, ok);
         }
         fu += TT * P.u.stride;
         fz += TT * P.z.stride;
@@ -219,7 +204,6 @@ struct Stager {
     // The outputs of the tile that starts at t0.
     __device__ __forceinline__ void finish(int64_t t0, int buf) {
         const SsmProblem &P = a.P;
-        const bool unchecked = full && t0 + TT <= pb;
         constexpr int VE = E < 4 ? E : 4;
         float o[NR * E];
 #pragma unroll
@@ -252,8 +236,7 @@ struct Stager {
             float v[E];
 #pragma unroll
             for (int i = 0; i < E; ++i) v[i] = o[r * E + i];
-            if (unchecked) store_row<OUT, E, true>(p, v, have, true);
-            else if (t0 + srow + r * RP < pb && have > 0) store_row<OUT, E>(p, v, have, a.ovec);
+            if (t0 + srow + r * RP < pb && have > 0) store_row<OUT, E, FAST>(p, v, have, a.ovec);
         }
         po += TT * (int64_t)P.D;
     }
@@ -261,7 +244,7 @@ struct Stager {
 
 template <typename IN, typename OUT, int LN, bool STATES>
 __global__ void __launch_bounds__(kThreads, LN == 2 ? 1 : 2)
-kda_ssm_scan_kernel(const ScanArgs a) {
+kda_ssm_scan_kernel(const __grid_constant__ ScanArgs a) {
     using L = Layout<IN, LN>;
     constexpr int CW = L::CW, CB = L::CB;
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -288,23 +271,32 @@ kda_ssm_scan_kernel(const ScanArgs a) {
         // Between barriers k and k + 1 the scanning warps run over tile k; these
         // warps stage tile k + 1 and finish tile k - 1.
         if (tiles == 0) return;
-        Stager<IN, OUT, LN, STATES> st(a, sm, pa, pb, ch0);
-        st.fetch(pa);
-        st.stage(pa, 0);
-        if (tiles > 1) st.fetch(pa + TT);
-        __syncthreads();
-        for (int k = 0; k <= tiles; ++k) {
-            const int64_t t0 = pa + (int64_t)k * TT;
-            if (k + 1 < tiles) {
-                st.stage(t0 + TT, (k + 1) & 1);
-                if (k + 2 < tiles) st.fetch(t0 + 2 * TT);
+        auto run = [&](auto fast) {
+            Stager<IN, OUT, LN, STATES, decltype(fast)::value> st(a, sm, pa, pb, ch0);
+            if (tiles > 0) {
+                st.fetch(pa, true);
+                st.stage(pa, 0);
+                if (tiles > 1) st.fetch(pa + TT, true);
+                __syncthreads();
+                for (int k = 0; k <= tiles; ++k) {
+                    const int64_t t0 = pa + (int64_t)k * TT;
+                    if (k + 1 < tiles) {
+                        st.stage(t0 + TT, (k + 1) & 1);
+                        if (k + 2 < tiles) st.fetch(t0 + 2 * TT, true);
+                    }
+                    if (!STATES) {
+                        if (k > 0) st.finish(t0 - TT, (k - 1) & 1);
+                        if (k < tiles) st.fetch_again(t0, true);
+                    }
+                    if (k < tiles) __syncthreads();
+                }
             }
-            if (!STATES) {
-                if (k > 0) st.finish(t0 - TT, (k - 1) & 1);
-                if (k < tiles) st.fetch_again(t0);
-            }
-            if (k < tiles) __syncthreads();
-        }
+        };
+        if (P.D % L::E == 0 && P.S % 4 == 0 && P.u.vec && P.dt.vec && P.B.vec && P.C.vec && (STATES || !P.z.p || P.z.vec) &&
+            (STATES || a.ovec))
+            run(std::true_type());
+        else
+            run(std::false_type());
         return;
     }
 
@@ -417,7 +409,7 @@ kda_ssm_scan_kernel(const ScanArgs a) {
 }
 
 // From what the parts end with to what the next ones start with, in place.
-__global__ void __launch_bounds__(256) kda_ssm_carry_kernel(const ScanArgs a) {
+__global__ void __launch_bounds__(256) kda_ssm_carry_kernel(const __grid_constant__ ScanArgs a) {
     const SsmProblem &P = a.P;
     const int64_t M = (int64_t)P.D * P.S;
     const int per = (int)((M + 255) / 256), n = blockIdx.x / per;

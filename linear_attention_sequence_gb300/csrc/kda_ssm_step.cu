@@ -26,7 +26,7 @@ struct StepArgs {
 // NB sequences a lane; lane q of a channel prepares and finishes OWN of them: numbers
 // q OWN .. (where LN > NB, lanes from NB on none).  FULL: four states at a time.
 template <typename IN, typename OUT, int LN, int NB, bool FULL>
-__global__ void __launch_bounds__(kThreads) kda_ssm_step_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(kThreads) kda_ssm_step_kernel(const __grid_constant__ StepArgs a) {
     constexpr int CB = kThreads / LN;
     constexpr int OWN = NB >= LN ? NB / LN : 1;
     const SsmProblem &P = a.P;
