@@ -164,7 +164,27 @@ struct Raw {
             ahead2(w[0], p, ok);
         }
     }
-    __device__ __forceinline__ void load_all(const T *p) { load_if(p, true); }
+    // All E elements at once, for use soon.
+    __device__ __forceinline__ void load_all(const T *p) {
+        if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+            }
+        } else if constexpr (kBytes % 8 == 0) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 8; ++i) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+                w[2 * i] = v.x; w[2 * i + 1] = v.y;
+            }
+        } else if constexpr (kBytes % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+        } else {
+            slow(p, E);
+        }
+    }
     // `vec`: p is aligned to min(16, kBytes) bytes; FULL: that, and all E elements exist
     template <bool FULL = false>
     __device__ __forceinline__ void load(const T *p, int have, bool vec) {
