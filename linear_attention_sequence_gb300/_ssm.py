@@ -133,9 +133,14 @@ class _on:
             self.inner.__exit__(*exc)
 
 
+# The handle of a device's current stream; the first form makes no stream object.
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _run(call, dev, *args):
     """The C call on the current stream of device ``dev``, which is the current device."""
-    st = getattr(_kda._lib or _kda.lib(), call)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    st = getattr(_kda._lib or _kda.lib(), call)(*args, _stream_of(dev))
     if st:
         _kda._check(st, call)
 

@@ -854,37 +854,56 @@ __global__ void __launch_bounds__(256) kda_ssm_carry_back_kernel(const __grid_co
     }
 }
 
-// dB and dC: the blocks' shares, added in their order.  Tokens outside every
-// sequence are left as they are.
+// The sums that cross blocks, each in a fixed order: dB and dC over the blocks
+// across the channels (`first` blocks; tokens outside every sequence are left as they
+// are), then dA, dD and ddt_bias over the parts.
+struct ReduceArgs {
+    SsmProblem P;
+    const float *share;          // [ncb][T][2 SP]: dC, dB
+    int ncb, SP;
+    unsigned first;
+    int parts;
+    const float *from[3];        // [parts][n[k]]
+    float *to[3];                // [n[k]], or nullptr
+    int64_t n[3];
+    void *dB, *dC;
+};
 template <typename OUT>
-__global__ void __launch_bounds__(256)
-kda_ssm_reduce_bc_kernel(const SsmProblem P, const float *__restrict__ part, int ncb, int SP, OUT *dB, OUT *dC) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t t = i / (2 * SP);
-    if (t >= P.T) return;
-    const int k = (int)(i - t * (2 * SP)), n = k % SP;
-    if (n >= P.S) return;
-    if (P.cu) {
-        int m;
-        int64_t sa, sb;
-        if (!find_seq(P.cu, P.N, P.T, P.seq_len, t, m, sa, sb)) return;
-    }
-    float v = 0.f;
-    const float *p = part + i;
-    const int64_t step = (int64_t)P.T * 2 * SP;
+__global__ void __launch_bounds__(256) kda_ssm_reduce_kernel(const __grid_constant__ ReduceArgs a) {
+    const SsmProblem &P = a.P;
+    if (blockIdx.x < a.first) {
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        const int64_t t = i / (2 * a.SP);
+        if (t >= P.T) return;
+        const int k = (int)(i - t * (2 * a.SP)), n = k % a.SP;
+        if (n >= P.S) return;
+        if (P.cu) {
+            int m;
+            int64_t sa, sb;
+            if (!find_seq(P.cu, P.N, P.T, P.seq_len, t, m, sa, sb)) return;
+        }
+        float v = 0.f;
+        const float *p = a.share + i;
+        const int64_t step = (int64_t)P.T * 2 * a.SP;
 #pragma unroll 8
-    for (int c = 0; c < ncb; ++c) v += p[c * step];
-    st_elem((k < SP ? dC : dB) + t * P.S + n, v);
-}
-
-// Sums over the parts of [N, M] into [M], in their order.
-__global__ void __launch_bounds__(256) kda_ssm_reduce_seq_kernel(const float *__restrict__ part, int N, int64_t M, float *out) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= M) return;
-    float v = 0.f;
-#pragma unroll 4
-    for (int n = 0; n < N; ++n) v += part[n * M + i];
-    out[i] = v;
+        for (int c = 0; c < a.ncb; ++c) v += __ldg(p + c * step);
+        st_elem((OUT *)(k < a.SP ? a.dC : a.dB) + t * P.S + n, v);
+        return;
+    }
+    int64_t i = (int64_t)(blockIdx.x - a.first) * 256 + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        if (a.to[k]) {
+            if (i < a.n[k]) {
+                float v = 0.f;
+#pragma unroll 8
+                for (int p = 0; p < a.parts; ++p) v += __ldg(a.from[k] + p * a.n[k] + i);
+                a.to[k][i] = v;
+                return;
+            }
+            i -= a.n[k];
+        }
+    }
 }
 
 int lanes_of(int S) { return S <= 8 ? 2 : S <= 16 ? 4 : S <= 32 ? 8 : 16; }
@@ -1030,21 +1049,29 @@ cudaError_t kda_launch_ssm_scan_backward(const SsmProblem &P, const float *init,
         else e = bf ? by_states<__nv_bfloat16, __nv_bfloat16>(a, stream) : by_states<float, float>(a, stream);
         if (e != cudaSuccess) return e;
     }
-    if (P.T > 0 && P.N > 0) {
-        const int64_t n = (int64_t)P.T * 2 * SP;
-        const unsigned blocks = (unsigned)((n + 255) / 256);
-        if (a.obf)
-            kda_ssm_reduce_bc_kernel<__nv_bfloat16><<<blocks, 256, 0, stream>>>(P, a.share, ncb, SP, (__nv_bfloat16 *)dB, (__nv_bfloat16 *)dC);
-        else
-            kda_ssm_reduce_bc_kernel<float><<<blocks, 256, 0, stream>>>(P, a.share, ncb, SP, (float *)dB, (float *)dC);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
+    ReduceArgs r{};
+    r.P = P;
+    r.share = a.share;
+    r.ncb = ncb;
+    r.SP = SP;
+    r.first = P.N > 0 ? (unsigned)(((int64_t)P.T * 2 * SP + 255) / 256) : 0;
+    r.parts = a.parts.most;
+    r.dB = dB;
+    r.dC = dC;
+    int64_t n = 0;
     if (!direct) {
-        kda_ssm_reduce_seq_kernel<<<(unsigned)((nA + 255) / 256), 256, 0, stream>>>(a.dA, a.parts.most, nA, dA);
-        if (dskip) kda_ssm_reduce_seq_kernel<<<(unsigned)((P.D + 255) / 256), 256, 0, stream>>>(a.dskip, a.parts.most, P.D, dskip);
-        if (dbias) kda_ssm_reduce_seq_kernel<<<(unsigned)((P.D + 255) / 256), 256, 0, stream>>>(a.dbias, a.parts.most, P.D, dbias);
-        e = cudaGetLastError();
+        const float *from[3] = {a.dA, a.dskip, a.dbias};
+        float *to[3] = {dA, dskip, dbias};
+        for (int k = 0; k < 3; ++k) {
+            r.from[k] = from[k];
+            r.to[k] = to[k];
+            r.n[k] = k ? P.D : nA;
+            if (to[k]) n += r.n[k];
+        }
     }
-    return e;
+    const unsigned blocks = r.first + (unsigned)((n + 255) / 256);
+    if (blocks == 0) return cudaSuccess;
+    if (a.obf) kda_ssm_reduce_kernel<__nv_bfloat16><<<blocks, 256, 0, stream>>>(r);
+    else kda_ssm_reduce_kernel<float><<<blocks, 256, 0, stream>>>(r);
+    return cudaGetLastError();
 }

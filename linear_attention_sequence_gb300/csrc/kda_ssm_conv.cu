@@ -39,6 +39,7 @@ struct ConvArgs {
     const float *dcout;
     float *dcin, *part;
     int tile;
+    unsigned state_block;     // first block that moves states instead
 };
 
 // Four neighbouring fp32 values; those at or past `have`, and all of a NULL array, are 0.
@@ -201,9 +202,38 @@ __device__ __forceinline__ void conv_run(const ConvArgs &a, const f2 (&w)[W][NP]
     }
 }
 
+// The last W - 1 inputs of every sequence.  A thread owns one channel of one
+// sequence and reads before it writes: cout may be cin.
+template <typename IN, int W>
+__device__ __forceinline__ void conv_state(const ConvArgs &a, int64_t i) {
+    const SsmProblem &P = a.P;
+    if (i >= (int64_t)P.N * P.D) return;
+    const int n = (int)(i / P.D);
+    const int64_t c = i - (int64_t)n * P.D;
+    int64_t sa, sb;
+    seq_bounds(P.cu, n, P.T, P.seq_len, sa, sb);
+    float v[W - 1];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+        const int64_t u = sb - (W - 1) + k;
+        if (u >= sa) v[k] = ld_elem((const IN *)P.u.p + u * P.u.stride + c);
+        else v[k] = a.cin ? a.cin[((int64_t)n * (W - 1) + (u - sa + W - 1)) * P.D + c] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) a.cout[((int64_t)n * (W - 1) + k) * P.D + c] = v[k];
+}
+template <typename IN, int W>
+__global__ void __launch_bounds__(kThreads) kda_ssm_conv_state_kernel(const __grid_constant__ ConvArgs a) {
+    conv_state<IN, W>(a, (int64_t)blockIdx.x * kThreads + threadIdx.x);
+}
+
 template <typename IN, typename OUT, int W>
 __global__ void __launch_bounds__(kThreads) kda_ssm_conv_kernel(const __grid_constant__ ConvArgs a) {
     const SsmProblem &P = a.P;
+    if (blockIdx.x >= a.state_block) {         // the blocks behind: the state
+        conv_state<IN, W>(a, (int64_t)(blockIdx.x - a.state_block) * kThreads + threadIdx.x);
+        return;
+    }
     const int nvb = (P.D + V * kThreads - 1) / (V * kThreads);
     const int c0 = ((int)(blockIdx.x % nvb) * kThreads + threadIdx.x) * V;
     const int64_t t0 = (int64_t)(blockIdx.x / nvb) * a.tile, t1 = min(t0 + a.tile, (int64_t)P.T);
@@ -225,28 +255,6 @@ __global__ void __launch_bounds__(kThreads) kda_ssm_conv_kernel(const __grid_con
         else conv_run<IN, OUT, W, false>(a, w, b, x, t, end, c0, have);
         t = end;
     }
-}
-
-// The last W - 1 inputs of every sequence.  A thread owns one channel of one
-// sequence and reads before it writes: cout may be cin.
-template <typename IN, int W>
-__global__ void __launch_bounds__(kThreads) kda_ssm_conv_state_kernel(const __grid_constant__ ConvArgs a) {
-    const SsmProblem &P = a.P;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= (int64_t)P.N * P.D) return;
-    const int n = (int)(i / P.D);
-    const int64_t c = i - (int64_t)n * P.D;
-    int64_t sa, sb;
-    seq_bounds(P.cu, n, P.T, P.seq_len, sa, sb);
-    float v[W - 1];
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-        const int64_t u = sb - (W - 1) + k;
-        if (u >= sa) v[k] = ld_elem((const IN *)P.u.p + u * P.u.stride + c);
-        else v[k] = a.cin ? a.cin[((int64_t)n * (W - 1) + (u - sa + W - 1)) * P.D + c] : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) a.cout[((int64_t)n * (W - 1) + k) * P.D + c] = v[k];
 }
 
 // One token a sequence: output and new state in one pass (cout may be cin: a thread
@@ -383,7 +391,7 @@ __device__ __forceinline__ void back_run(const ConvArgs &a, Back<W> &k, int64_t 
 }
 
 template <typename IN, typename DY, typename OUT, int W>
-__global__ void __launch_bounds__(kThreads) kda_ssm_conv_backward_kernel(const __grid_constant__ ConvArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kda_ssm_conv_backward_kernel(const __grid_constant__ ConvArgs a) {
     const SsmProblem &P = a.P;
     const int nvb = (P.D + V * kThreads - 1) / (V * kThreads);
     const int c0 = ((int)(blockIdx.x % nvb) * kThreads + threadIdx.x) * V;
@@ -466,17 +474,32 @@ __global__ void __launch_bounds__(kThreads) kda_ssm_conv_backward_kernel(const _
 
 // dw and dbias: the runs' shares, added in their order.  A warp takes 32
 // channels of one row of the shares; its kRuns warps add every kRuns-th run and
-// join through shared memory.
+// join through shared memory.  The blocks behind hand the gradient of the state
+// of sequences without tokens on, as those hand on their state.
 constexpr int kRuns = 8;
 __global__ void __launch_bounds__(32 * kRuns)
-kda_ssm_conv_reduce_kernel(const float *__restrict__ part, int64_t tiles, int D, int W, float *dw, float *dbias) {
+kda_ssm_conv_reduce_kernel(const __grid_constant__ ConvArgs a, int64_t tiles, unsigned blocks, float *dw, float *dbias) {
+    const SsmProblem &P = a.P;
+    const int D = P.D, W = P.S;
+    if (blockIdx.x >= blocks) {
+        const int64_t per = (int64_t)(W - 1) * D, i = (int64_t)(blockIdx.x - blocks) * (32 * kRuns) + threadIdx.x;
+        if (i >= per * P.N) return;
+        int64_t sa, sb;
+        seq_bounds(P.cu, (int)(i / per), P.T, P.seq_len, sa, sb);
+        if (sa == sb) a.dcin[i] = a.dcout ? a.dcout[i] : 0.f;
+        return;
+    }
     __shared__ float s[kRuns][32];
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int nb = (D + 31) / 32;
     const int k = blockIdx.x / nb, c = (blockIdx.x % nb) * 32 + lane;
     float v = 0.f;
-    if (c < D)
-        for (int64_t i = y; i < tiles; i += kRuns) v += part[(i * (W + 1) + k) * D + c];
+    if (c < D) {
+        const float *p = a.part + (int64_t)k * D + c;
+        const int64_t step = (int64_t)(W + 1) * D;
+#pragma unroll 8
+        for (int64_t i = y; i < tiles; i += kRuns) v += __ldg(p + i * step);
+    }
     s[y][lane] = v;
     __syncthreads();
     if (y == 0 && c < D) {
@@ -488,17 +511,6 @@ kda_ssm_conv_reduce_kernel(const float *__restrict__ part, int64_t tiles, int D,
             dbias[c] = v;
         }
     }
-}
-
-// A sequence without tokens hands its state on: so does its gradient.
-__global__ void __launch_bounds__(kThreads) kda_ssm_conv_empty_kernel(const __grid_constant__ ConvArgs a) {
-    const SsmProblem &P = a.P;
-    const int W = P.S;
-    const int64_t per = (int64_t)(W - 1) * P.D, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= per * P.N) return;
-    int64_t sa, sb;
-    seq_bounds(P.cu, (int)(i / per), P.T, P.seq_len, sa, sb);
-    if (sa == sb) a.dcin[i] = a.dcout ? a.dcout[i] : 0.f;
 }
 
 // Tokens of a run: `most`, fewer where that would leave the GPU without work (16
@@ -518,16 +530,18 @@ cudaError_t forward(ConvArgs &a, cudaStream_t stream) {
         kda_ssm_conv_token_kernel<IN, OUT, W><<<(unsigned)(P.N * across), kThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
+    const unsigned state_blocks = a.cout ? (unsigned)(((int64_t)P.N * P.D + kThreads - 1) / kThreads) : 0;
+    // a state in place is written only behind the kernel that reads it
+    const bool apart = a.cout == a.cin || P.T == 0;
     if (P.T > 0) {
         a.tile = run_length(P.T, P.D, 64);
-        const int64_t blocks = (P.T + a.tile - 1) / a.tile * across;
-        kda_ssm_conv_kernel<IN, OUT, W><<<(unsigned)blocks, kThreads, 0, stream>>>(a);
+        a.state_block = (unsigned)((P.T + a.tile - 1) / a.tile * across);
+        kda_ssm_conv_kernel<IN, OUT, W><<<a.state_block + (apart ? 0 : state_blocks), kThreads, 0, stream>>>(a);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    if (a.cout) {
-        const int64_t n = (int64_t)P.N * P.D;
-        kda_ssm_conv_state_kernel<IN, W><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
+    if (state_blocks && apart) {
+        kda_ssm_conv_state_kernel<IN, W><<<state_blocks, kThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
     return cudaSuccess;
@@ -550,18 +564,12 @@ cudaError_t backward(ConvArgs &a, float *dw, float *dbias, cudaStream_t stream) 
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    if (dw || dbias) {
-        const unsigned blocks = (unsigned)((W + 1) * ((P.D + 31) / 32));
-        kda_ssm_conv_reduce_kernel<<<blocks, 32 * kRuns, 0, stream>>>(a.part, tiles, P.D, W, dw, dbias);
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
-    if (a.dcin && (P.cu || P.seq_len == 0)) {
-        const int64_t n = (int64_t)P.N * (W - 1) * P.D;
-        kda_ssm_conv_empty_kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
-        return cudaGetLastError();
-    }
-    return cudaSuccess;
+    const unsigned blocks = dw || dbias ? (unsigned)((W + 1) * ((P.D + 31) / 32)) : 0;
+    const int64_t n = a.dcin && (P.cu || P.seq_len == 0) ? (int64_t)P.N * (W - 1) * P.D : 0;
+    const unsigned more = (unsigned)((n + 32 * kRuns - 1) / (32 * kRuns));
+    if (blocks + more == 0) return cudaSuccess;
+    kda_ssm_conv_reduce_kernel<<<blocks + more, 32 * kRuns, 0, stream>>>(a, tiles, blocks, dw, dbias);
+    return cudaGetLastError();
 }
 
 template <typename IN, typename DY, typename OUT>
@@ -609,7 +617,7 @@ cudaError_t kda_launch_ssm_conv(const SsmProblem &P, const float *w, const float
 }
 
 int64_t kda_ssm_conv_backward_tiles(const SsmProblem &P, int *tile) {
-    *tile = run_length(P.T, P.D, 64);
+    *tile = run_length(P.T, P.D, 128);
     return ((int64_t)P.T + *tile - 1) / *tile;
 }
 
