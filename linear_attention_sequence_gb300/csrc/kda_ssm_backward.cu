@@ -914,14 +914,15 @@ int blocks_across(const SsmProblem &P) {
 // How a batch is cut: b blocks of sequences side by side, each in K parts.  Two
 // blocks share an SM; a round of 304 blocks takes 2.9 where one of up to 152, alone on
 // their SMs, takes 2, and the adjoint's own pass adds 0.19 of that where K > 1.  The K of
-// least cost is taken; no part is under four tiles.  8192 tokens, S = 16, bf16, u and z
+// least cost is taken (among equals about the larger: the sums over a part's tokens
+// are then shorter, and round less); no part is under four tiles.  8192 tokens, S = 16, bf16, u and z
 // in 8 bits, K = 1 / 4 / 7 / 9 / 14 / 19: 4096 channels 2019 / 957 / 881 / 832 / 833 / 828 us,
 // 8192 channels 2049 / 1785 / 1596 / 1547 / 1513 / 1562.
 int best_parts(int64_t b, int64_t tokens) {
     const auto cost = [&](int64_t K) {
         const int64_t n = b * K, rest = n % 304;
         const double rounds = 2.9 * (double)(n / 304) + (rest > 152 ? 2.9 : rest > 0 ? 2.0 : 0.0);
-        return rounds / (double)K * (K > 1 ? 1.19 : 1.0) + 0.004 * (double)K;
+        return rounds / (double)K * (K > 1 ? 1.19 : 1.0) + 0.001 * (double)K;
     };
     int best = 1;
     for (int K = 2; K <= 64 && K <= tokens / (4 * TT); ++K)
