@@ -476,6 +476,7 @@ kda_ssm_scan_backward_kernel(const __grid_constant__ BackArgs a) {
     typename L::Smem &sm = *reinterpret_cast<typename L::Smem *>(smem_raw);
     __shared__ int s_seq;
 
+    let_next();
     const SsmProblem &P = a.P;
     const int ncb = (P.D + CB - 1) / CB, cb = (int)(blockIdx.x % ncb), slot = (int)(blockIdx.x / ncb);
     const int ch0 = cb * CB;
@@ -516,6 +517,7 @@ kda_ssm_scan_backward_kernel(const __grid_constant__ BackArgs a) {
     }
 
     if constexpr (L::kBlocks == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    wait_before();                           // the carry; the staging warps need nothing of it
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int wc = warp * CW + lane / LN * 2, ch = ch0 + wc;
     const int q = lane % LN, n0 = 4 * q;
@@ -712,6 +714,7 @@ kda_ssm_adjoint_kernel(const __grid_constant__ BackArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     __shared__ int s_seq;
+    let_next();
     const SsmProblem &P = a.P;
     const int ncb = (P.D + CB - 1) / CB, slot = (int)(blockIdx.x / ncb), ch0 = (int)(blockIdx.x % ncb) * CB;
     Place w;
@@ -831,6 +834,7 @@ kda_ssm_adjoint_kernel(const __grid_constant__ BackArgs a) {
 
 // From what the parts give back to what the ones before them start with, in place.
 __global__ void __launch_bounds__(256) kda_ssm_carry_back_kernel(const __grid_constant__ BackArgs a) {
+    let_next();
     const SsmProblem &P = a.P;
     const int64_t M = (int64_t)P.D * P.S;
     const int per = (int)((M + 255) / 256), n = blockIdx.x / per;
@@ -840,6 +844,7 @@ __global__ void __launch_bounds__(256) kda_ssm_carry_back_kernel(const __grid_co
     if (K == 0) return;
     const int64_t row = parts_before(a.parts, P.cu, P.N, P.T, P.seq_len, n) - n;
     if (row + K > a.parts.rows) return;
+    wait_before();
     const int64_t m = (int64_t)(blockIdx.x - n * per) * 256 + threadIdx.x;
     if (m >= M) return;
     const float A = P.A[m] * kLog2e;
@@ -871,6 +876,7 @@ struct ReduceArgs {
 template <typename OUT>
 __global__ void __launch_bounds__(256) kda_ssm_reduce_kernel(const __grid_constant__ ReduceArgs a) {
     const SsmProblem &P = a.P;
+    wait_before();
     if (blockIdx.x < a.first) {
         const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
         const int64_t t = i / (2 * a.SP);
@@ -958,15 +964,13 @@ cudaError_t launch(const BackArgs &a, cudaStream_t stream) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         const int64_t n = (int64_t)a.P.N * (((int64_t)a.P.D * a.P.S + 255) / 256);
-        kda_ssm_carry_back_kernel<<<(unsigned)n, 256, 0, stream>>>(a);
-        e = cudaGetLastError();
+        e = launch_behind(true, kda_ssm_carry_back_kernel, (unsigned)n, 256, 0, stream, a);
         if (e != cudaSuccess) return e;
     }
     const int smem = (int)sizeof(typename L::Smem);
     e = cudaFuncSetAttribute(kda_ssm_scan_backward_kernel<X, IN, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kda_ssm_scan_backward_kernel<X, IN, LN><<<blocks, kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_behind(a.parts.most > a.P.N, kda_ssm_scan_backward_kernel<X, IN, LN>, blocks, kThreads, smem, stream, a);
 }
 
 template <typename X, typename IN>
@@ -1072,7 +1076,6 @@ cudaError_t kda_launch_ssm_scan_backward(const SsmProblem &P, const float *init,
     }
     const unsigned blocks = r.first + (unsigned)((n + 255) / 256);
     if (blocks == 0) return cudaSuccess;
-    if (a.obf) kda_ssm_reduce_kernel<__nv_bfloat16><<<blocks, 256, 0, stream>>>(r);
-    else kda_ssm_reduce_kernel<float><<<blocks, 256, 0, stream>>>(r);
-    return cudaGetLastError();
+    return launch_behind(P.N > 0, a.obf ? kda_ssm_reduce_kernel<__nv_bfloat16> : kda_ssm_reduce_kernel<float>, blocks, 256, 0,
+                         stream, r);
 }

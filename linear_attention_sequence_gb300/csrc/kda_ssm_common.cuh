@@ -12,6 +12,29 @@ constexpr int kSsmTile = KDA_CHUNK;
 // Channels that share one scale in the 8-bit packing.
 constexpr int kPackGroup = KDA_PACK_GROUP;
 
+// ---- kernels that follow one another
+// A kernel launched by launch_behind() may start once every block of the one before
+// it has started and called let_next(); it calls wait_before() ahead of its first read
+// of what that one (and those before it) wrote.  The kernel in front of the first of
+// such a chain is complete when the chain starts.
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(bool behind, void (*kernel)(Params...), unsigned blocks, int threads, int smem, cudaStream_t stream,
+                          const Args &...args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cfg.attrs = behind ? &attr : nullptr;
+    cfg.numAttrs = behind ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- packed pairs of fp32 (one issue slot for two operations)
 typedef unsigned long long f2;
 __device__ __forceinline__ f2 pack2(float x, float y) {

@@ -392,6 +392,7 @@ __device__ __forceinline__ void back_run(const ConvArgs &a, Back<W> &k, int64_t 
 
 template <typename IN, typename DY, typename OUT, int W>
 __global__ void __launch_bounds__(kThreads, 4) kda_ssm_conv_backward_kernel(const __grid_constant__ ConvArgs a) {
+    let_next();
     const SsmProblem &P = a.P;
     const int nvb = (P.D + V * kThreads - 1) / (V * kThreads);
     const int c0 = ((int)(blockIdx.x % nvb) * kThreads + threadIdx.x) * V;
@@ -479,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_ssm_conv_backward_kernel(cons
 constexpr int kRuns = 8;
 __global__ void __launch_bounds__(32 * kRuns)
 kda_ssm_conv_reduce_kernel(const __grid_constant__ ConvArgs a, int64_t tiles, unsigned blocks, float *dw, float *dbias) {
+    wait_before();
     const SsmProblem &P = a.P;
     const int D = P.D, W = P.S;
     if (blockIdx.x >= blocks) {
@@ -568,8 +570,7 @@ cudaError_t backward(ConvArgs &a, float *dw, float *dbias, cudaStream_t stream) 
     const int64_t n = a.dcin && (P.cu || P.seq_len == 0) ? (int64_t)P.N * (W - 1) * P.D : 0;
     const unsigned more = (unsigned)((n + 32 * kRuns - 1) / (32 * kRuns));
     if (blocks + more == 0) return cudaSuccess;
-    kda_ssm_conv_reduce_kernel<<<blocks + more, 32 * kRuns, 0, stream>>>(a, tiles, blocks, dw, dbias);
-    return cudaGetLastError();
+    return launch_behind(tiles > 0, kda_ssm_conv_reduce_kernel, blocks + more, 32 * kRuns, 0, stream, a, tiles, blocks, dw, dbias);
 }
 
 template <typename IN, typename DY, typename OUT>

@@ -257,6 +257,7 @@ kda_ssm_scan_kernel(const __grid_constant__ ScanArgs a) {
     typename L::Smem &sm = *reinterpret_cast<typename L::Smem *>(smem_raw);
     __shared__ int s_seq;
 
+    if (STATES) let_next();
     const SsmProblem &P = a.P;
     const int ncb = (P.D + CB - 1) / CB;
     const int ch0 = (int)(blockIdx.x % ncb) * CB, slot = (int)(blockIdx.x / ncb);
@@ -306,6 +307,7 @@ kda_ssm_scan_kernel(const __grid_constant__ ScanArgs a) {
         return;
     }
 
+    if (!STATES) wait_before();                // the carry; the staging warps need nothing of it
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int wc = warp * CW + lane / LN * 2;  // the first of this lane's channels within the block
     const int ch = ch0 + wc;
@@ -416,6 +418,7 @@ kda_ssm_scan_kernel(const __grid_constant__ ScanArgs a) {
 
 // From what the parts end with to what the next ones start with, in place.
 __global__ void __launch_bounds__(256) kda_ssm_carry_kernel(const __grid_constant__ ScanArgs a) {
+    let_next();
     const SsmProblem &P = a.P;
     const int64_t M = (int64_t)P.D * P.S;
     const int per = (int)((M + 255) / 256), n = blockIdx.x / per;
@@ -425,6 +428,7 @@ __global__ void __launch_bounds__(256) kda_ssm_carry_kernel(const __grid_constan
     if (K == 0) return;
     const int64_t row = parts_before(a.parts, P.cu, P.N, P.T, P.seq_len, n) - n;
     if (row + K > a.parts.rows) return;
+    wait_before();
     const int64_t m = (int64_t)(blockIdx.x - n * per) * 256 + threadIdx.x;
     if (m >= M) return;
     const int64_t d = m / P.S;
@@ -448,8 +452,8 @@ cudaError_t launch_one(const ScanArgs &a, cudaStream_t stream) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t blocks = (int64_t)a.parts.most * ((a.P.D + L::CB - 1) / L::CB);
-    kda_ssm_scan_kernel<IN, OUT, LN, STATES><<<(unsigned)blocks, kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_behind(!STATES && a.parts.most > a.P.N, kda_ssm_scan_kernel<IN, OUT, LN, STATES>, (unsigned)blocks, kThreads,
+                         smem, stream, a);
 }
 
 template <typename IN, typename OUT, int LN>
@@ -459,8 +463,7 @@ cudaError_t launch(const ScanArgs &a, cudaStream_t stream) {
         cudaError_t e = launch_one<IN, float, LN, true>(a, stream);
         if (e != cudaSuccess) return e;
         const int64_t blocks = (int64_t)a.P.N * (((int64_t)a.P.D * a.P.S + 255) / 256);
-        kda_ssm_carry_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a);
-        e = cudaGetLastError();
+        e = launch_behind(true, kda_ssm_carry_kernel, (unsigned)blocks, 256, 0, stream, a);
         if (e != cudaSuccess) return e;
     }
     return launch_one<IN, OUT, LN, false>(a, stream);
