@@ -515,13 +515,16 @@ kda_ssm_conv_reduce_kernel(const __grid_constant__ ConvArgs a, int64_t tiles, un
     }
 }
 
-// Tokens of a run: `most`, fewer where that would leave the GPU without work (16
-// warps an SM are wanted); 16 tokens keep the rows that two runs read within a fifth.
-int run_length(int64_t T, int32_t D, int most) {
-    const int64_t columns = (D + (int64_t)V * 32 - 1) / (V * 32);   // warps across
-    int tile = most;
-    while (tile > 16 && (T + tile - 1) / tile * columns < 152 * 16) tile /= 2;
-    return tile;
+// Tokens of a run: as many as make the blocks fill the GPU's places (`per_sm` an SM)
+// a whole number of times, with at most `most` tokens a run; at least 16, which keeps the
+// rows that two runs read within a fifth.  (8192 x 8192, gradient: runs of 128, which
+// fill 1.7 times the places, 93 us, of 216, once, 79.)
+int run_length(int64_t T, int32_t D, int per_sm, int most) {
+    const int64_t work = T * ((D + V * kThreads - 1) / (V * kThreads)), places = 152 * (int64_t)per_sm;
+    int64_t rounds = (work + places * most - 1) / (places * most);
+    if (rounds < 1) rounds = 1;
+    const int64_t tile = (work + places * rounds - 1) / (places * rounds);
+    return tile < 16 ? 16 : (int)tile;
 }
 
 template <typename IN, typename OUT, int W>
@@ -536,7 +539,7 @@ cudaError_t forward(ConvArgs &a, cudaStream_t stream) {
     // a state in place is written only behind the kernel that reads it
     const bool apart = a.cout == a.cin || P.T == 0;
     if (P.T > 0) {
-        a.tile = run_length(P.T, P.D, 64);
+        a.tile = run_length(P.T, P.D, sizeof(IN) == 2 ? 5 : 4, 200);
         a.state_block = (unsigned)((P.T + a.tile - 1) / a.tile * across);
         kda_ssm_conv_kernel<IN, OUT, W><<<a.state_block + (apart ? 0 : state_blocks), kThreads, 0, stream>>>(a);
         cudaError_t e = cudaGetLastError();
@@ -618,7 +621,7 @@ cudaError_t kda_launch_ssm_conv(const SsmProblem &P, const float *w, const float
 }
 
 int64_t kda_ssm_conv_backward_tiles(const SsmProblem &P, int *tile) {
-    *tile = run_length(P.T, P.D, 128);
+    *tile = run_length(P.T, P.D, 4, 256);
     return ((int64_t)P.T + *tile - 1) / *tile;
 }
 
