@@ -1,6 +1,10 @@
 """Binding of the state space layer calls and the 8-bit packing (see
 ``include/kda.h``).  As in the rest of the package: pointers, sizes and checks,
-no arithmetic of the method and no fallback."""
+no arithmetic of the method and no fallback.
+
+In a packed batch with ``cu_seqlens``, rows that belong to no sequence (before its
+first entry, from its last one on) are not written: outputs allocated here hold
+whatever the memory held there."""
 from __future__ import annotations
 
 import ctypes

@@ -32,6 +32,10 @@
 // alone back through every part but the first from zero, g_in' = g_part +
 // exp(A sum Delta) g_in carries it on, and the gradients proper run every part from its
 // own g_in.
+//
+// 8192 tokens of 4096 channels with 16 states, bf16, u and z in 8 bits: 802 us, of which
+// 140 for the adjoint alone and 13 for the sums across blocks.  Bound by instruction
+// issue: about 120 instructions per 128 state entries, 0.58 a cycle.
 
 #include <type_traits>
 

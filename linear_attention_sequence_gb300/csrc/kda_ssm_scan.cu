@@ -17,7 +17,8 @@
 // 128 bytes a cycle an SM whatever lanes share, and a lane that held one
 // channel needed 11 bytes an entry (44 cycles for 128 entries a scheduler,
 // against 16 of exponentials); two channels a lane and, for bf16, B and C kept as
-// bf16 bring that to 5.
+// bf16 bring that to 5.  8192 tokens of 4096 channels with 16 states, bf16: 274 us (110 of
+// them the first of the passes below, 164 the second), 0.6 instructions issued a cycle.
 //
 // Few channels.  A sequence is cut into parts where its channels alone would
 // not fill the GPU: a first kernel runs all parts but the last from a zero state
