@@ -486,7 +486,7 @@ int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 // scan's time), so it is for sequences that would outlast the rest: a part is as long
 // as the share of one of 304 places for blocks (two an SM), or of 456 where 304 is far
 // from a multiple of the blocks across, and a sequence of less than 3.5 such parts
-// (2.5 in a ragged batch, whose other sequences are mostly shorter) stays whole.  8192 tokens, S = 16, bf16, whole against the best of 2 .. 57 parts: 4096
+// (1.5 in a ragged batch, whose other sequences are mostly shorter) stays whole.  8192 tokens, S = 16, bf16, whole against the best of 2 .. 57 parts: 4096
 // channels 423 and 279 us (7 parts), 2048: 422 and 152 (9), 1024: 414 and 86 (19), 512:
 // 414 and 59.5 (19; the rule's 38: 59.6); 8192 channels: 426 and 508.
 Parts kda_ssm_parts(const SsmProblem &P) {
@@ -498,8 +498,8 @@ Parts kda_ssm_parts(const SsmProblem &P) {
     Parts parts;
     parts.len = ((int64_t)P.T / K + TT - 1) / TT * TT;
     if (parts.len < 4 * TT) parts.len = 4 * TT;
-    parts.whole = P.cu ? parts.len * 5 / 2 : parts.len * 7 / 2;
-    parts.rows = P.T > parts.len * 5 / 2 ? P.T / parts.len : 0;   // the same with and without cu_seqlens
+    parts.whole = P.cu ? parts.len * 3 / 2 : parts.len * 7 / 2;
+    parts.rows = P.T > parts.len * 3 / 2 ? P.T / parts.len : 0;   // the same with and without cu_seqlens
     parts.most = P.N;
     if (P.cu) {
         parts.most = (int32_t)(P.N + parts.rows);
