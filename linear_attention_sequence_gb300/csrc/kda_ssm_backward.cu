@@ -115,10 +115,17 @@ __device__ __forceinline__ void write_swz(float *row, int c, const float (&v)[E]
     }
 }
 
-template <int E>
+// E gradients.  WIDE: their type is known (BF) and they may be written at once; a
+// branch around each store would keep the steps of several channels from overlapping.
+template <bool WIDE, bool BF, int E>
 __device__ __forceinline__ void store_grad(void *p, int64_t at, const float (&v)[E], int have, bool vec, bool bf) {
-    if (bf) store_row<__nv_bfloat16, E>((__nv_bfloat16 *)p + at, v, have, vec);
-    else store_row<float, E>((float *)p + at, v, have, vec);
+    if constexpr (WIDE) {
+        if constexpr (BF) store_row<__nv_bfloat16, E, true>((__nv_bfloat16 *)p + at, v, have, true);
+        else store_row<float, E, true>((float *)p + at, v, have, true);
+    } else {
+        if (bf) store_row<__nv_bfloat16, E>((__nv_bfloat16 *)p + at, v, have, vec);
+        else store_row<float, E>((float *)p + at, v, have, vec);
+    }
 }
 
 // E values of a row of codes or plain values.
@@ -142,6 +149,10 @@ struct Vals {
             ahead4(w, x.scales + (int64_t)t * x.ngroups + c / kPackGroup, ok);
             s[0] = __uint_as_float(w);
         }
+    }
+    __device__ __forceinline__ void clear() {
+        r.clear();
+        s[0] = 0.f;
     }
     __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(X) == 1) return r.get(i) * s[0];
@@ -266,7 +277,7 @@ __device__ __forceinline__ bool find_place(const BackArgs &a, int slot, int *s_s
 }
 
 // The staging warps.
-template <typename X, typename IN, int LN, bool FAST>
+template <typename X, typename IN, int LN, bool FAST, bool BF>
 struct Stager {
     using L = Layout<IN, LN>;
     static constexpr int E = L::E, CB = L::CB, SP = L::SP;
@@ -289,6 +300,8 @@ struct Stager {
         srow = tid / L::TR;
         sc = tid % L::TR * E;
         have = P.D - (ch0 + sc);
+        z.clear();                            // (where there is no gate, its values are formed and left out)
+        fz.clear();
         // chunk k of the part starts with row row0 + k; the sequence's first chunk with its initial state
         row0 = ckpt_first_row(P.cu, w.n, P.T, P.seq_len, TT) + (w.pa - w.sa) / TT - 1;
         first = w.pa == w.sa ? w.n : -1;
@@ -351,14 +364,16 @@ struct Stager {
                 dl[i] += dt.get(i0 + i);
                 dyp[i] = dy.get(i0 + i);
             }
-            if (P.softplus) softplus_all(dl);
-            if (P.z.p) {
+            float sp[VE];
 #pragma unroll
-                for (int i = 0; i < VE; ++i) {
-                    const float g = z.get(i0 + i);
-                    dyp[i] *= g * sigmoid_fast(g);
-                }
+            for (int i = 0; i < VE; ++i) {
+                sp[i] = dl[i];
+                const float g = z.get(i0 + i), f = g * sigmoid_fast(g);
+                dyp[i] *= P.z.p ? f : 1.f;
             }
+            softplus_all(sp);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) dl[i] = P.softplus ? sp[i] : dl[i];
 #pragma unroll
             for (int i = 0; i < VE; i += 2) {
                 float4 v;
@@ -391,21 +406,26 @@ struct Stager {
         if (t0 + srow >= pb || have <= 0) return;
         // a few channels at a time, to keep few values alive; Delta and dyp were written by this thread
         constexpr int VE = E < 4 ? E : 4;
+        const int64_t row_at = (int64_t)(t0 + srow) * P.D + ch0 + sc;
+        if (P.z.p) {
 #pragma unroll
-        for (int k = 0; k < E; k += VE) {
-            const int c = sc + k, yc = L::ycol(c);
-            const int64_t at = (int64_t)(t0 + srow) * P.D + ch0 + c;
-            float o[VE], x[VE], dyp[VE], v[VE];
-            read_swz<L, VE>(sm.skip, c, v);
-            if (P.z.p) {
-                read_row<VE>(&sm.out[ob][2][srow][yc], o);
+            for (int k = 0; k < E; k += VE) {
+                float o[VE], v[VE];
+                read_swz<L, VE>(sm.skip, sc + k, v);
+                read_row<VE>(&sm.out[ob][2][srow][L::ycol(sc + k)], o);
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
                     const float g = fz.get(k + i), s = sigmoid_fast(g);
                     o[i] = fdy.get(k + i) * fmaf(v[i], fu.get(k + i), o[i]) * fmaf(g * s, 1.f - s, s);
                 }
-                store_grad<VE>(a.dz, at, o, have - k, a.ovec, a.obf);
+                store_grad<FAST, BF, VE>(a.dz, row_at + k, o, have - k, a.ovec, a.obf);
             }
+        }
+#pragma unroll
+        for (int k = 0; k < E; k += VE) {
+            const int c = sc + k, yc = L::ycol(c);
+            float o[VE], x[VE], dyp[VE], v[VE];
+            read_swz<L, VE>(sm.skip, c, v);
             read_row<VE>(&sm.out[ob][0][srow][yc], o);
             read_row<VE>(&sm.out[ob][1][srow][yc], x);
             read_swz<L, VE>(sm.dyp[buf][row], c, dyp);
@@ -417,33 +437,35 @@ struct Stager {
                 o[i] = fmaf(d.x, o[i], v[i] * dyp[i]);
                 o[i + 1] = fmaf(d.z, o[i + 1], v[i + 1] * dyp[i + 1]);
             }
-            store_grad<VE>(a.du, at, o, have - k, a.ovec, a.obf);
-            read_swz<L, VE>(sm.sums[0][srow], c, v);
+            store_grad<FAST, BF, VE>(a.du, row_at + k, o, have - k, a.ovec, a.obf);
+            read_swz<L, VE>(sm.bias, c, v);
 #pragma unroll
-            for (int i = 0; i < VE; ++i) v[i] = fmaf(dyp[i], fu.get(k + i), v[i]);
-            write_swz<L, VE>(sm.sums[0][srow], c, v);
-            if (P.softplus) {
-                read_swz<L, VE>(sm.bias, c, v);
-#pragma unroll
-                for (int i = 0; i < VE; ++i) x[i] *= sigmoid_fast(fdt.get(k + i) + v[i]);
+            for (int i = 0; i < VE; ++i) {
+                const float s = sigmoid_fast(fdt.get(k + i) + v[i]);
+                x[i] *= P.softplus ? s : 1.f;
             }
-            store_grad<VE>(a.ddt, at, x, have - k, a.ovec, a.obf);
-            read_swz<L, VE>(sm.sums[1][srow], c, v);
+            store_grad<FAST, BF, VE>(a.ddt, row_at + k, x, have - k, a.ovec, a.obf);
+            read_swz<L, VE>(sm.sums[0][srow], c, v);
+            read_swz<L, VE>(sm.sums[1][srow], c, o);
 #pragma unroll
-            for (int i = 0; i < VE; ++i) v[i] += x[i];
-            write_swz<L, VE>(sm.sums[1][srow], c, v);
+            for (int i = 0; i < VE; ++i) {
+                v[i] = fmaf(dyp[i], fu.get(k + i), v[i]);
+                o[i] += x[i];
+            }
+            write_swz<L, VE>(sm.sums[0][srow], c, v);
+            write_swz<L, VE>(sm.sums[1][srow], c, o);
         }
     }
 };
 
 // What the staging warps do for a part.
-template <typename X, typename IN, int LN, bool FAST>
+template <typename X, typename IN, int LN, bool FAST, bool BF>
 __device__ __forceinline__ void stage_part(const BackArgs &a, typename Layout<IN, LN>::Smem &sm, const Place &w, int ch0,
                                            int cb, int tiles) {
     // While the other warps work through half j, these stage half j - 2 (the
     // whole chunk before j's is in place when j is its second half) and finish half
     // j + 1.
-    Stager<X, IN, LN, FAST> st(a, sm, w, ch0, cb);
+    Stager<X, IN, LN, FAST, BF> st(a, sm, w, ch0, cb);
     const int last = 2 * tiles - 1;
     if (tiles > 0) {
         st.fetch_next(last);
@@ -502,8 +524,9 @@ kda_ssm_scan_backward_kernel(const __grid_constant__ BackArgs a) {
 
     if (threadIdx.x >= kScanners) {
         if constexpr (L::kBlocks == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        if (all_wide<L::E>(P, true)) stage_part<X, IN, LN, true>(a, sm, w, ch0, cb, tiles);
-        else stage_part<X, IN, LN, false>(a, sm, w, ch0, cb, tiles);
+        if (!all_wide<L::E>(P, true) || !a.ovec) stage_part<X, IN, LN, false, false>(a, sm, w, ch0, cb, tiles);
+        else if (a.obf) stage_part<X, IN, LN, true, true>(a, sm, w, ch0, cb, tiles);
+        else stage_part<X, IN, LN, true, false>(a, sm, w, ch0, cb, tiles);
         // dD and ddt_bias: over the rows of threads
         asm volatile("bar.sync 1, %0;" ::"r"(kStagers) : "memory");
         for (int c = threadIdx.x - kScanners; c < CB; c += kStagers) {
