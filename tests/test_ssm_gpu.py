@@ -675,3 +675,169 @@ def test_decode_step_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(o, w)
+
+
+# ------------------------------------------------------------------ addresses
+
+def off_by_one(t):
+    """The same values one fp32 element past an allocation's start: contiguous, not 16-byte aligned."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    v = flat[1:].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+def test_misaligned_parameters_and_states():
+    x = scan_inputs(sum(LENS), 72, 16, len(LENS), F32, 301)
+    cu = cu_of(LENS)
+    for n in ("A", "D", "dt_bias", "state", "d_final"):
+        x[n] = off_by_one(x[n])
+    rows = kda.checkpoint_count(sum(LENS), kda.CHUNK, cu)
+    fin, chunks = off_by_one(torch.empty_like(x["state"])), off_by_one(torch.empty(rows, 72, 16, device=DEV))
+    out = off_by_one(torch.empty(sum(LENS), 72, device=DEV))
+    fwd(x, cu_seqlens=cu, out=out, final_state=fin, chunk_states=chunks)
+    w = ref.scan(h(x), LENS)
+    for n, t in (("out", out), ("final", fin), ("chunks", chunks)):
+        check(n, t, w[n])
+    g, wg = bwd(x, cu_seqlens=cu, chunk_states=chunks), ref.scan_backward(h(x), LENS, chunks.double().cpu())
+    for n in wg:
+        check(n, g[n], wg[n])
+    one = {k: (v[:8] if k in ("u", "dt", "B", "C", "z") else v) for k, v in x.items()}
+    st = off_by_one(x["state"])
+    o = kda.kda_ssm_step(one["u"], one["dt"], x["A"], one["B"], one["C"], st, D=x["D"], z=one["z"], dt_bias=x["dt_bias"])
+    w = ref.scan(h(dict(one, d_out=None)), [1] * 8)
+    check("step", o, w["out"])
+    check("state", st, w["final"])
+    c = conv_inputs(sum(LENS), 72, 4, len(LENS), F32, 302)
+    for n in ("weight", "bias", "state", "d_state"):
+        c[n] = off_by_one(c[n])
+    last = off_by_one(torch.empty_like(c["state"]))
+    y, _ = kda.kda_ssm_conv(c["x"], c["weight"], c["bias"], cu, c["state"], conv_state_out=last)
+    d = h(c)
+    wy, wl = ref.conv(d["x"], d["weight"], d["bias"], d["state"], LENS)
+    check("conv", y, wy)
+    assert torch.equal(last.double().cpu(), wl)
+    g = kda.kda_ssm_conv_backward(c["x"], c["weight"], c["d_out"], c["bias"], cu, c["state"], d_conv_state_out=c["d_state"])
+    w = ref.conv_backward(d["x"], d["weight"], d["bias"], d["state"], LENS, d["d_out"], d["d_state"])
+    for n in w:
+        check(n, g[n], w[n])
+    codes, scales = kda.kda_act_pack8(off_by_one(c["x"]))
+    want = ref.pack8(c["x"].cpu())
+    assert torch.equal(codes.cpu(), want[0]) and torch.equal(scales.cpu(), want[1])
+
+
+def test_offsets_past_32_bits():
+    """Rows a stride of 2^30 elements apart: the third starts past 2^31."""
+    T, D, S, stride = 3, 40, 16, (1 << 30) + 8
+    x = scan_inputs(T, D, S, 1, BF16, 311)
+    c = conv_inputs(T, D, 4, 1, BF16, 312)
+    big = torch.empty(2 * stride + 4096, dtype=BF16, device=DEV)
+    at = 0
+
+    def far(t):
+        nonlocal at
+        v = big.as_strided((T, t.shape[1]), (stride, 1), at)
+        v.copy_(t)
+        at += 64
+        return v
+
+    for n in ("u", "dt", "B", "C", "z", "d_out"):
+        x[n] = far(x[n])
+    c["x"], c["d_out"] = far(c["x"]), far(c["d_out"])
+    out, fin = fwd(x, out_dtype=F32)
+    w = ref.scan(h(x), [T])
+    check("out", out, w["out"])
+    check("final", fin, w["final"])
+    g, wg = bwd(x, grad_dtype=F32), ref.scan_backward(h(x), [T], None)
+    for n in wg:
+        check(n, g[n], wg[n])
+    d = h(c)
+    y, last = kda.kda_ssm_conv(c["x"], c["weight"], c["bias"], conv_state=c["state"], out_dtype=F32)
+    wy, wl = ref.conv(d["x"], d["weight"], d["bias"], d["state"], [T])
+    check("conv", y, wy)
+    assert torch.equal(last.double().cpu(), wl)
+    g = kda.kda_ssm_conv_backward(c["x"], c["weight"], c["d_out"], c["bias"], conv_state=c["state"], grad_dtype=F32)
+    w = ref.conv_backward(d["x"], d["weight"], d["bias"], d["state"], [T], d["d_out"], torch.zeros_like(d["d_state"]))
+    for n in w:
+        check(n, g[n], w[n])
+    codes, scales = kda.kda_act_pack8(c["x"])
+    want = ref.pack8(c["x"].float().cpu())
+    assert torch.equal(codes.cpu(), want[0]) and torch.equal(scales.cpu(), want[1])
+    st = torch.stack([x["state"][0]] * 3)
+    o = kda.kda_ssm_step(x["u"], x["dt"], x["A"], x["B"], x["C"], st, D=x["D"], z=x["z"], dt_bias=x["dt_bias"], out_dtype=F32)
+    w = ref.scan(h(dict(x, state=torch.stack([x["state"][0]] * 3))), [1] * 3)
+    check("step", o, w["out"])
+    del big
+    torch.cuda.empty_cache()
+
+
+def test_states_past_32_bits():
+    """More than 2^31 state entries: the last sequence's last channels."""
+    N, D, S = 260, 524288 + 16, 16
+    A = torch.full((D, S), -0.5, device=DEV)
+    st = torch.ones((N, D, S), device=DEV)
+    u = torch.full((N, D), 0.25, dtype=BF16, device=DEV)
+    dt = torch.zeros((N, D), dtype=BF16, device=DEV)
+    bc = torch.ones((N, S), dtype=BF16, device=DEV)
+    out = kda.kda_ssm_step(u, dt, A, bc, bc, st, out_dtype=F32)
+    delta = np.log(2.0)                     # softplus(0)
+    want = np.exp(-0.5 * delta) + delta * 0.25
+    for t, v in ((st[-1, -40:], want), (st[0, :40], want), (out[-1, -40:], 16 * want)):
+        assert float((t.double() - v).abs().max()) <= 1e-5 * v
+    assert float((st.double().sum(-1)[[0, 100, 259]] / 16 - want).abs().max()) <= 1e-5
+    del A, st, u, dt, out
+    torch.cuda.empty_cache()
+
+
+def test_two_graphs_of_a_call_replayed_side_by_side():
+    """Two captures of the same calls have workspaces of their own: replayed at once on two
+    streams they give what the calls give."""
+    x = scan_inputs(3000, 72, 16, 1, BF16, 321)
+    chunks = fwd(x, return_chunk_states=True)[2]
+
+    def calls():
+        out, fin = fwd(x)
+        return [out, fin, *(v for v in bwd(x, chunk_states=chunks).values() if v is not None)]
+
+    want = calls()
+    torch.cuda.synchronize()
+    graphs, held = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held.append(calls())
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for r in held:
+        for a, b in zip(r, want):
+            assert torch.equal(a, b)
+
+
+def test_binding_refuses_on_the_gpu():
+    x = scan_inputs(64, 40, 16, 2, F32, 331)
+    with pytest.raises(ValueError, match="dt_bias"):
+        fwd(dict(x, dt_bias=x["dt_bias"][:39]), num_seqs=2)
+    with pytest.raises(ValueError, match="init_state"):
+        fwd(x, num_seqs=1)
+    with pytest.raises(ValueError, match="rows must be contiguous"):
+        fwd(dict(x, u=x["u"].t().contiguous().t()), num_seqs=2)
+    with pytest.raises(ValueError, match="overlap"):
+        fwd(dict(x, B=x["B"][:1].expand(64, 16)), num_seqs=2)
+    with pytest.raises(ValueError, match="z must be"):
+        fwd(dict(x, z=x["z"].to(BF16)), num_seqs=2)
+    with pytest.raises(ValueError, match="both be packed"):
+        codes, scales = kda.kda_act_pack8(x["u"])
+        bwd(dict(x, u=codes), u_scales=scales, num_seqs=2)
+    with pytest.raises(ValueError, match="chunk_states"):
+        kda.kda_ssm_scan_backward(codes, x["dt"], x["A"], x["B"], x["C"], x["d_out"], u_scales=scales, num_seqs=2)
+    with pytest.raises(kda.KdaError):
+        fwd(x, num_seqs=2, out=x["u"])
+    with pytest.raises(kda.KdaError):
+        kda.kda_ssm_conv(x["u"], torch.zeros(40, 5, device=DEV))
+    with pytest.raises(ValueError, match="fp32 or bf16"):
+        kda.kda_act_pack8(x["u"].half())
