@@ -256,24 +256,22 @@ __device__ __forceinline__ void read_c(const uint4 *p, f2 &c01, f2 &c23) {
 struct Place {
     int n, part, count;
     int sa, pa, pb;                          // (token numbers are below 2^31)
-    int row;
+    int row;                                 // of the carry: between this part and the next
 };
-__device__ __forceinline__ bool find_place(const BackArgs &a, int slot, int *s_seq, Place &w) {
-    const SsmProblem &P = a.P;
-    w.part = 0;
-    w.count = 1;
-    if (a.parts.most == P.N) w.n = longest_first(P.cu, P.N, P.T, P.seq_len, slot, s_seq);
-    else find_part(a.parts, P.cu, P.N, P.T, P.seq_len, slot, w.n, w.part, w.count);
-    if (w.n < 0) return false;
+__device__ __forceinline__ bool place_of(const BackArgs &a, const Part &p, Place &w) {
+    w.n = p.n;
+    w.part = p.k;
+    w.count = p.count;
+    w.row = p.row;
+    if (p.n < 0) return false;
     int64_t sa, sb;
-    seq_bounds(P.cu, w.n, P.T, P.seq_len, sa, sb);
-    const int64_t pa = sa + w.part * a.parts.len;
+    seq_bounds(a.P.cu, p.n, a.P.T, a.P.seq_len, sa, sb);
+    const int64_t pa = sa + p.k * a.parts.len;
     w.sa = (int)sa;
     w.pa = (int)pa;
-    w.pb = (int)(w.part == w.count - 1 ? sb : pa + a.parts.len);
-    w.row = slot - w.n;                      // of the carry: between this part and the next
+    w.pb = (int)(p.k == p.count - 1 ? sb : pa + a.parts.len);
     // as in the scan: overlapping sequences could need more rows than there are
-    return w.count == 1 || w.row + (w.part < w.count - 1) <= a.parts.rows;
+    return p.count == 1 || p.row + (p.k < p.count - 1) <= a.parts.rows;
 }
 
 // The staging warps.
@@ -500,16 +498,16 @@ kda_ssm_scan_backward_kernel(const __grid_constant__ BackArgs a) {
     constexpr int CW = L::CW, CB = L::CB, SP = L::SP;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     typename L::Smem &sm = *reinterpret_cast<typename L::Smem *>(smem_raw);
-    __shared__ int s_seq;
+    __shared__ Part s_part;
 
     let_next();
     const SsmProblem &P = a.P;
     const int ncb = (P.D + CB - 1) / CB, cb = (int)(blockIdx.x % ncb), slot = (int)(blockIdx.x / ncb);
     const int ch0 = cb * CB;
     Place w;
-    const bool some = find_place(a, slot, &s_seq, w);
-    // the shares of dA, dD and ddt_bias: by part, or by sequence where those are the same
-    const int64_t at = a.parts.most == P.N && some ? w.n : slot;
+    const bool some = place_of(a, longest_part(a.parts, P.cu, P.N, P.T, P.seq_len, slot, &s_part), w);
+    // the shares of dA, dD and ddt_bias: by part, in the sequences' order where it keeps them
+    const int64_t at = some && w.row + w.n < a.parts.most ? w.row + w.n : slot;
     if (!some) {
         // a part that the batch does not have: its shares are 0
         for (int64_t i = threadIdx.x; i < (int64_t)min(CB, P.D - ch0) * P.S; i += kThreads)
@@ -740,12 +738,14 @@ kda_ssm_adjoint_kernel(const __grid_constant__ BackArgs a) {
     };
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
-    __shared__ int s_seq;
     let_next();
     const SsmProblem &P = a.P;
-    const int ncb = (P.D + CB - 1) / CB, slot = (int)(blockIdx.x / ncb), ch0 = (int)(blockIdx.x % ncb) * CB;
+    const int ncb = (P.D + CB - 1) / CB, ch0 = (int)(blockIdx.x % ncb) * CB;
+    Part p = part_of_row<false>(a.parts, P.cu, P.N, P.T, P.seq_len, (int)(blockIdx.x / ncb));
+    ++p.k;                                   // the part behind the row
+    ++p.row;
     Place w;
-    if (!find_place(a, slot, &s_seq, w) || w.part == 0) return;
+    if (!place_of(a, p, w)) return;
     const int tiles = (int)((w.pb - w.pa + TT - 1) / TT);
 
     if (threadIdx.x >= kScanners) {
@@ -864,15 +864,13 @@ __global__ void __launch_bounds__(256) kda_ssm_carry_back_kernel(const __grid_co
     let_next();
     const SsmProblem &P = a.P;
     const int64_t M = (int64_t)P.D * P.S;
-    const int per = (int)((M + 255) / 256), n = blockIdx.x / per;
-    int64_t sa, sb;
-    seq_bounds(P.cu, n, P.T, P.seq_len, sa, sb);
-    const int K = (int)a.parts.of(sb - sa) - 1;
-    if (K == 0) return;
-    const int64_t row = parts_before(a.parts, P.cu, P.N, P.T, P.seq_len, n) - n;
-    if (row + K > a.parts.rows) return;
+    const int per = (int)((M + 255) / 256), i = blockIdx.x / per;
+    const Part w = part_of_row<true>(a.parts, P.cu, P.N, P.T, P.seq_len, i);
+    const int64_t n = w.n, row = w.row;
+    const int K = w.count - 1;
+    if (n < 0 || row + K > a.parts.rows) return;
     wait_before();
-    const int64_t m = (int64_t)(blockIdx.x - n * per) * 256 + threadIdx.x;
+    const int64_t m = (int64_t)(blockIdx.x - i * per) * 256 + threadIdx.x;
     if (m >= M) return;
     const float A = P.A[m] * kLog2e;
     float c = a.d_final ? a.d_final[n * M + m] : 0.f;
@@ -944,36 +942,27 @@ int blocks_across(const SsmProblem &P) {
     const int CB = 256 / lanes_of(P.S);
     return (P.D + CB - 1) / CB;
 }
-// How a batch is cut: b blocks of sequences side by side, each in K parts.  Two
-// blocks share an SM; a round of 304 blocks takes 2.9 where one of up to 152, alone on
-// their SMs, takes 2, and the adjoint's own pass adds 0.19 of that where K > 1.  The K of
-// least cost is taken (among equals about the larger: the sums over a part's tokens
-// are then shorter, and round less); no part is under four tiles.  8192 tokens, S = 16, bf16, u and z
-// in 8 bits, K = 1 / 4 / 7 / 9 / 14 / 19: 4096 channels 2019 / 957 / 881 / 832 / 833 / 828 us,
-// 8192 channels 2049 / 1785 / 1596 / 1547 / 1513 / 1562.
-int best_parts(int64_t b, int64_t tokens) {
-    const auto cost = [&](int64_t K) {
-        const int64_t n = b * K, rest = n % 304;
-        const double rounds = 2.9 * (double)(n / 304) + (rest > 152 ? 2.9 : rest > 0 ? 2.0 : 0.0);
-        return rounds / (double)K * (K > 1 ? 1.19 : 1.0) + 0.001 * (double)K;
-    };
-    int best = 1;
-    for (int K = 2; K <= 64 && K <= tokens / (4 * TT); ++K)
-        if (cost(K) < cost(best)) best = K;
-    return best;
+template <int LN>
+int blocks_an_sm(bool bf) {
+    return bf ? Layout<__nv_bfloat16, LN>::kBlocks : Layout<float, LN>::kBlocks;
 }
-// Where the lengths are known only on the device (`ragged`), the batch is cut as if it
-// were one sequence, and a sequence of up to one and a half parts' length stays whole.
+// Cutting adds the adjoint's pass only, 0.19 of the kernel's own.  8192 tokens, S = 16,
+// bf16, u and z in 8 bits, in 1 / 4 / 7 / 9 / 14 / 19 parts: 4096 channels 2019 / 957 /
+// 881 / 832 / 833 / 828 us, 8192 channels 2049 / 1785 / 1596 / 1547 / 1513 / 1562.  One
+// sequence of 512 tokens and 512 channels, bf16: whole 121 us, parts of four tiles 47, of one
+// 29.  A ragged batch's parts cost the same whatever they were cut from, so that every
+// sequence longer than a part is cut (3148 tokens in 13 sequences, 1000 channels: 98 us;
+// from 1.5 parts' length on 115; from 2 134).
 Parts back_parts(const SsmProblem &P, bool ragged) {
-    const int64_t b = blocks_across(P), tokens = ragged || P.N == 0 ? P.T : P.T / P.N;
-    const int K = best_parts(ragged ? b : b * P.N, tokens);
-    Parts parts;
-    parts.len = ((tokens + K - 1) / K + TT - 1) / TT * TT;
-    if (parts.len < TT) parts.len = TT;
-    parts.whole = K == 1 ? INT32_MAX : ragged ? parts.len * 3 / 2 : parts.len;
-    parts.rows = P.T > parts.whole || (!ragged && tokens > parts.whole) ? P.T / parts.len : 0;
-    parts.most = ragged ? P.N + (int32_t)parts.rows : (int32_t)(P.N * parts.of(tokens));
-    return parts;
+    const bool bf = P.in_dtype == KDA_DTYPE_BF16;
+    int of = 1;
+    switch (lanes_of(P.S)) {
+        case 2: of = blocks_an_sm<2>(bf); break;
+        case 4: of = blocks_an_sm<4>(bf); break;
+        case 8: of = blocks_an_sm<8>(bf); break;
+        default: of = blocks_an_sm<16>(bf); break;
+    }
+    return cut_parts(P, ragged, blocks_across(P), {of == 2 ? 1.45 : 2.0, 0.19, 0.7, 0.02, 1.0});
 }
 
 int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
@@ -981,23 +970,24 @@ int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 template <typename X, typename IN, int LN>
 cudaError_t launch(const BackArgs &a, cudaStream_t stream) {
     using L = Layout<IN, LN>;
-    const unsigned blocks = (unsigned)((int64_t)a.parts.most * blocks_across(a.P));
+    const int64_t across = blocks_across(a.P);
     cudaError_t e;
-    if (a.parts.most > a.P.N) {
+    if (a.parts.rows > 0) {
         const int smem = (int)(sizeof(float2) * 2 * TT * L::CB + sizeof(uint4) * 2 * TT * LN * (L::kBf ? 1 : 2));
         e = cudaFuncSetAttribute(kda_ssm_adjoint_kernel<X, IN, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        kda_ssm_adjoint_kernel<X, IN, LN><<<blocks, kThreads, smem, stream>>>(a);
+        kda_ssm_adjoint_kernel<X, IN, LN><<<(unsigned)(a.parts.rows * across), kThreads, smem, stream>>>(a);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        const int64_t n = (int64_t)a.P.N * (((int64_t)a.P.D * a.P.S + 255) / 256);
+        const int64_t n = (int64_t)a.parts.cut * (((int64_t)a.P.D * a.P.S + 255) / 256);
         e = launch_behind(true, kda_ssm_carry_back_kernel, (unsigned)n, 256, 0, stream, a);
         if (e != cudaSuccess) return e;
     }
     const int smem = (int)sizeof(typename L::Smem);
     e = cudaFuncSetAttribute(kda_ssm_scan_backward_kernel<X, IN, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_behind(a.parts.most > a.P.N, kda_ssm_scan_backward_kernel<X, IN, LN>, blocks, kThreads, smem, stream, a);
+    return launch_behind(a.parts.rows > 0, kda_ssm_scan_backward_kernel<X, IN, LN>, (unsigned)(a.parts.most * across), kThreads, smem,
+                         stream, a);
 }
 
 template <typename X, typename IN>

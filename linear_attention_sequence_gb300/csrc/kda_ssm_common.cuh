@@ -349,64 +349,145 @@ struct Parts {
     int64_t len, whole;
     int32_t most;            // parts of the batch at most
     int64_t rows;            // parts that have one behind them, at most: rows of a carry
+    int32_t cut;             // sequences that are cut, at most
 
-    __host__ __device__ int64_t of(int64_t n) const { return n > whole ? (n + len - 1) / len : 1; }
+    __host__ __device__ int of(int64_t n) const {
+        return n > whole ? (int)(((unsigned)n + (unsigned)len - 1u) / (unsigned)len) : 1;
+    }
 };
 
-// Part number p of a batch: its sequence n, its place k in it and the sequence's
-// number of parts; n = -1 if there are not so many.  Every warp finds it by
-// itself (all 32 lanes must call).
-__device__ __forceinline__ void find_part(const Parts &parts, const int32_t *cu, int N, int64_t total, int64_t seq_len,
-                                          int p, int &n, int &k, int &count) {
+// A part of a batch: its sequence (-1: there is none), its place in it, the sequence's
+// number of parts, and the row of a carry between it and the part behind it (of a last
+// part, the row past its sequence's).
+struct Part {
+    int n, k, count, row;
+};
+
+// The part of a batch in place p of the launch; places start in order, so the parts of
+// long sequences come first and the short sequences fill in at the end (a third of the
+// time of 16 sequences of up to 1,500 tokens and 2,048 channels).  A thread looks at one
+// sequence, as in longest_first(), and the one that p falls in answers through *answer;
+// batches of more sequences than threads keep
+// their order.  Every thread of the block
+// must call it.
+__device__ __forceinline__ Part longest_part(const Parts &parts, const int32_t *cu, int N, int64_t total, int64_t seq_len,
+                                             int p, Part *answer) {
+    Part w;
+    w.n = -1;
+    w.k = 0;
+    w.count = 1;
+    w.row = 0;
     if (!cu) {
-        count = (int)parts.of(seq_len);
-        n = p / count;
-        k = p - n * count;
-        if (n >= N) n = -1;
-        return;
+        w.count = parts.of(seq_len);
+        w.n = p / w.count;
+        w.k = p - w.n * w.count;
+        w.row = p - w.n;
+        if (w.n >= N) w.n = -1;
+        return w;
+    }
+    if (threadIdx.x == 0) *answer = w;
+    __syncthreads();
+    if (N <= (int)blockDim.x) {
+        const int m = threadIdx.x;
+        if (m < N) {
+            int64_t a, b;
+            seq_bounds(cu, m, total, seq_len, a, b);
+            const int64_t n = b - a;
+            int before = 0, rows = 0;
+            for (int m2 = 0; m2 < N; ++m2) {
+                seq_bounds(cu, m2, total, seq_len, a, b);
+                const int c = parts.of(b - a);
+                if (b - a > n || (b - a == n && m2 < m)) before += c;
+                if (m2 < m) rows += c - 1;
+            }
+            w.count = parts.of(n);
+            w.k = p - before;
+            w.n = m;
+            w.row = rows + w.k;
+            if (w.k >= 0 && w.k < w.count) *answer = w;
+        }
+    } else if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int before = 0;
+        for (int m0 = 0; m0 < N; m0 += 32) {
+            int c = 0;
+            if (m0 + lane < N) {
+                int64_t a, b;
+                seq_bounds(cu, m0 + lane, total, seq_len, a, b);
+                c = parts.of(b - a);
+            }
+            int upto = c;
+#pragma unroll
+            for (int off = 1; off < 32; off *= 2) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, off);
+                if (lane >= off) upto += x;
+            }
+            w.k = p - (before + upto - c);
+            if (w.k >= 0 && w.k < c) {
+                w.n = m0 + lane;
+                w.count = c;
+                w.row = p - w.n;
+                *answer = w;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
+            if (before > p) break;
+        }
+    }
+    __syncthreads();
+    return *answer;
+}
+
+// The part before row r of a carry (CUT: the first of the cut sequence number r).
+// Every warp finds it by itself (all 32 lanes must call).
+template <bool CUT>
+__device__ __forceinline__ Part part_of_row(const Parts &parts, const int32_t *cu, int N, int64_t total, int64_t seq_len,
+                                            int r) {
+    Part w;
+    w.n = -1;
+    w.k = 0;
+    w.count = 1;
+    w.row = 0;
+    if (!cu) {
+        w.count = parts.of(seq_len);
+        const int rows = w.count - 1;
+        if (rows == 0) return w;
+        w.n = CUT ? r : r / rows;
+        w.k = CUT ? 0 : r - w.n * rows;
+        w.row = CUT ? w.n * rows : r;
+        if (w.n >= N) w.n = -1;
+        return w;
     }
     const int lane = threadIdx.x & 31;
-    int before = 0;
+    int rows = 0, seen = 0;                    // of the sequences before: rows, and those that are cut
     for (int m0 = 0; m0 < N; m0 += 32) {
         int c = 0;
         if (m0 + lane < N) {
             int64_t a, b;
             seq_bounds(cu, m0 + lane, total, seq_len, a, b);
-            c = (int)parts.of(b - a);
+            c = parts.of(b - a) - 1;
         }
+        const unsigned cut = __ballot_sync(0xffffffffu, c > 0);
         int upto = c;
 #pragma unroll
         for (int off = 1; off < 32; off *= 2) {
             const int x = __shfl_up_sync(0xffffffffu, upto, off);
             if (lane >= off) upto += x;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + upto > p);
+        const int k = r - (rows + upto - c);
+        const bool mine = CUT ? c > 0 && seen + __popc(cut & ((1u << lane) - 1u)) == r : k >= 0 && k < c;
+        const unsigned hit = __ballot_sync(0xffffffffu, mine);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            n = m0 + l;
-            count = __shfl_sync(0xffffffffu, c, l);
-            k = p - (before + __shfl_sync(0xffffffffu, upto, l) - count);
-            return;
+            w.n = m0 + l;
+            w.count = __shfl_sync(0xffffffffu, c, l) + 1;
+            w.k = CUT ? 0 : __shfl_sync(0xffffffffu, k, l);
+            w.row = CUT ? __shfl_sync(0xffffffffu, rows + upto - c, l) : r;
+            return w;
         }
-        before += __shfl_sync(0xffffffffu, upto, 31);
+        rows += __shfl_sync(0xffffffffu, upto, 31);
+        seen += __popc(cut);
     }
-    n = -1;
-}
-
-// The parts of the sequences before n.
-__device__ __forceinline__ int parts_before(const Parts &parts, const int32_t *cu, int N, int64_t total, int64_t seq_len,
-                                            int n) {
-    if (!cu) return n * (int)parts.of(seq_len);
-    const int lane = threadIdx.x & 31;
-    int sum = 0;
-    for (int m = lane; m < n; m += 32) {
-        int64_t a, b;
-        seq_bounds(cu, m, total, seq_len, a, b);
-        sum += (int)parts.of(b - a);
-    }
-#pragma unroll
-    for (int off = 16; off; off /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    return sum;
+    return w;
 }
 
 // Launch parameters of the state space kernels after validation.
@@ -421,6 +502,57 @@ struct SsmProblem {
     bool svec;                   // state rows may be read with 16-byte accesses
 };
 
+// What a kernel's run takes, in the time that a block alone on its SM takes for a tile.
+struct PartCosts {
+    double pair;             // two blocks that share an SM, each a tile (2: they do not share)
+    double first;            // the pass that cutting adds, of the kernel's own
+    double start;            // a round of blocks, before their first tile
+    double part;             // a part in the carry
+    double whole;            // a ragged batch's longest sequence that stays whole, in parts' lengths
+};
+
+// How a batch is cut, with `across` blocks side by side for a sequence: into the K
+// parts of least cost, if n blocks run in rounds of 304, of which the last may find them
+// alone (a little less than alone after others: the first to end make room early).
+// Against the best of up to 20 K on batches of equal lengths (64 .. 8192 tokens, 64 ..
+// 8192 channels, 8 .. 64 states) what it picks takes 1.00 to 1.08 of the time.  Where
+// the lengths are known only on the device (`ragged`), a part is one 304th of the batch's
+// work, which no sequence that stays whole outlasts by much.
+inline Parts cut_parts(const SsmProblem &P, bool ragged, int64_t across, const PartCosts &c) {
+    const int64_t tokens = ragged || P.N == 0 ? P.T : P.T / P.N, b = ragged || P.N == 0 ? across : across * P.N;
+    const int64_t tiles = (tokens + kSsmTile - 1) / kSsmTile;
+    const auto cost = [&](int64_t n, int64_t t) {
+        const int64_t full = n / 304, rest = n % 304;
+        const double last = rest > 152 ? c.pair : rest == 0 ? 0.0 : full > 0 ? 0.9 : 1.0;
+        return (c.pair * (double)full + last) * (double)t + c.start * (double)(full + (rest > 0));
+    };
+    Parts parts;
+    parts.len = (tiles < 1 ? 1 : tiles) * kSsmTile;
+    parts.whole = INT32_MAX;
+    if (ragged) {
+        const int64_t t = (tiles * across + 303) / 304;
+        if (t < tiles) {
+            parts.len = t * kSsmTile;
+            parts.whole = (int64_t)(c.whole * (double)parts.len);
+        }
+    } else {
+        double least = cost(b, tiles);
+        for (int64_t K = 2; K <= 64 && K <= tiles; ++K) {
+            const int64_t t = (tiles + K - 1) / K, k = (tiles + t - 1) / t;
+            if (k != K) continue;              // (as short as with fewer)
+            const double x = c.first * cost(b * (k - 1), t) + cost(b * k, t) + c.part * (double)k;
+            if (x < least) {
+                least = x;
+                parts.len = parts.whole = t * kSsmTile;
+            }
+        }
+    }
+    parts.rows = parts.whole == INT32_MAX ? 0 : ragged ? P.T / parts.len : (int64_t)P.N * (parts.of(tokens) - 1);
+    parts.cut = ragged && parts.rows < P.N ? (int32_t)parts.rows : parts.rows ? P.N : 0;
+    parts.most = P.N + (int32_t)parts.rows;
+    return parts;
+}
+
 }  // namespace kda
 
 // Launchers.
@@ -428,7 +560,6 @@ cudaError_t kda_launch_act_pack8(int64_t rows, int32_t D, int32_t in_dtype, cons
                                  float *scales, cudaStream_t stream);
 cudaError_t kda_launch_ssm_scan(const kda::SsmProblem &P, const float *init, void *out, float *final_state,
                                 float *chunk_states, int64_t chunk_capacity, float *workspace, cudaStream_t stream);
-kda::Parts kda_ssm_parts(const kda::SsmProblem &P);
 int64_t kda_ssm_scan_ws(const kda::SsmProblem &P);
 cudaError_t kda_launch_ssm_conv(const kda::SsmProblem &P, const float *w, const float *bias, const float *cin,
                                 bool swish, void *out, float *cout, cudaStream_t stream);

@@ -256,20 +256,20 @@ kda_ssm_scan_kernel(const __grid_constant__ ScanArgs a) {
     constexpr int CW = L::CW, CB = L::CB;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     typename L::Smem &sm = *reinterpret_cast<typename L::Smem *>(smem_raw);
-    __shared__ int s_seq;
+    __shared__ Part s_part;
 
     if (STATES) let_next();
     const SsmProblem &P = a.P;
     const int ncb = (P.D + CB - 1) / CB;
     const int ch0 = (int)(blockIdx.x % ncb) * CB, slot = (int)(blockIdx.x / ncb);
-    int n, part = 0, count = 1;
-    if (a.parts.most == P.N) n = longest_first(P.cu, P.N, P.T, P.seq_len, slot, &s_seq);
-    else find_part(a.parts, P.cu, P.N, P.T, P.seq_len, slot, n, part, count);
-    if (n < 0 || (STATES && part == count - 1)) return;
+    const Part w = STATES ? part_of_row<false>(a.parts, P.cu, P.N, P.T, P.seq_len, slot)
+                          : longest_part(a.parts, P.cu, P.N, P.T, P.seq_len, slot, &s_part);
+    const int n = w.n, part = w.k, count = w.count;
+    const int64_t row = w.row;                 // of the carry
+    if (n < 0) return;
     int64_t sa, sb;
     seq_bounds(P.cu, n, P.T, P.seq_len, sa, sb);
     const int64_t pa = sa + part * a.parts.len, pb = part == count - 1 ? sb : pa + a.parts.len;
-    const int64_t row = slot - n;              // of the carry
     // Sequences that overlap (a malformed cu_seqlens) could need more rows than
     // there are; their results are unspecified.
     if (count > 1 && row + (part < count - 1) > a.parts.rows) return;
@@ -422,15 +422,13 @@ __global__ void __launch_bounds__(256) kda_ssm_carry_kernel(const __grid_constan
     let_next();
     const SsmProblem &P = a.P;
     const int64_t M = (int64_t)P.D * P.S;
-    const int per = (int)((M + 255) / 256), n = blockIdx.x / per;
-    int64_t sa, sb;
-    seq_bounds(P.cu, n, P.T, P.seq_len, sa, sb);
-    const int K = (int)a.parts.of(sb - sa) - 1;
-    if (K == 0) return;
-    const int64_t row = parts_before(a.parts, P.cu, P.N, P.T, P.seq_len, n) - n;
-    if (row + K > a.parts.rows) return;
+    const int per = (int)((M + 255) / 256), i = blockIdx.x / per;
+    const Part w = part_of_row<true>(a.parts, P.cu, P.N, P.T, P.seq_len, i);
+    const int64_t n = w.n, row = w.row;
+    const int K = w.count - 1;
+    if (n < 0 || row + K > a.parts.rows) return;
     wait_before();
-    const int64_t m = (int64_t)(blockIdx.x - n * per) * 256 + threadIdx.x;
+    const int64_t m = (int64_t)(blockIdx.x - i * per) * 256 + threadIdx.x;
     if (m >= M) return;
     const int64_t d = m / P.S;
     const float A = P.A[m] * kLog2e;
@@ -452,18 +450,18 @@ cudaError_t launch_one(const ScanArgs &a, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kda_ssm_scan_kernel<IN, OUT, LN, STATES>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t blocks = (int64_t)a.parts.most * ((a.P.D + L::CB - 1) / L::CB);
-    return launch_behind(!STATES && a.parts.most > a.P.N, kda_ssm_scan_kernel<IN, OUT, LN, STATES>, (unsigned)blocks, kThreads,
+    const int64_t blocks = (STATES ? a.parts.rows : a.parts.most) * ((a.P.D + L::CB - 1) / L::CB);
+    return launch_behind(!STATES && a.parts.rows > 0, kda_ssm_scan_kernel<IN, OUT, LN, STATES>, (unsigned)blocks, kThreads,
                          smem, stream, a);
 }
 
 template <typename IN, typename OUT, int LN>
 cudaError_t launch(const ScanArgs &a, cudaStream_t stream) {
-    if (a.parts.most > a.P.N) {
+    if (a.parts.rows > 0) {
         // the output type plays no part in the states
         cudaError_t e = launch_one<IN, float, LN, true>(a, stream);
         if (e != cudaSuccess) return e;
-        const int64_t blocks = (int64_t)a.P.N * (((int64_t)a.P.D * a.P.S + 255) / 256);
+        const int64_t blocks = (int64_t)a.parts.cut * (((int64_t)a.P.D * a.P.S + 255) / 256);
         e = launch_behind(true, kda_ssm_carry_kernel, (unsigned)blocks, 256, 0, stream, a);
         if (e != cudaSuccess) return e;
     }
@@ -480,43 +478,33 @@ cudaError_t by_states(const ScanArgs &a, cudaStream_t s) {
 
 int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 
-}  // namespace
-
-// How a batch is cut.  Cutting costs a second pass over the states (about half the
-// scan's time), so it is for sequences that would outlast the rest: a part is as long
-// as the share of one of 304 places for blocks (two an SM), or of 456 where 304 is far
-// from a multiple of the blocks across, and a sequence of less than 3.5 such parts
-// (1.5 in a ragged batch, whose other sequences are mostly shorter) stays whole.  8192 tokens, S = 16, bf16, whole against the best of 2 .. 57 parts: 4096
-// channels 423 and 279 us (7 parts), 2048: 422 and 152 (9), 1024: 414 and 86 (19), 512:
-// 414 and 59.5 (19; the rule's 38: 59.6); 8192 channels: 426 and 508.
-Parts kda_ssm_parts(const SsmProblem &P) {
+// Cutting adds a pass over the states, 0.67 of the scan's own time.  8192 tokens, S = 16,
+// bf16, whole against the best of 2 .. 64 parts: 4096 channels 423 and 279 us (7 parts),
+// 2048: 422 and 152 (9), 1024: 414 and 84 (19), 512: 414 and 54 (37); 8192 channels: 426 and
+// 508.  One sequence of 256 tokens and 512 channels: whole 18.8 us, 8 parts 12.9.  fp32 rows
+// of up to 16 states keep a block alone on its SM waiting for memory, so that a second one
+// costs less (4096 channels: 418 us in 19 parts, 466 in the 7 of bf16; 8192: 700 in 2
+// parts, 737 whole).  A ragged batch's sequence of up to 1.5 parts stays whole (28,000
+// tokens in 8 sequences, 4096 channels: 655 us; with all longer ones cut 796).
+Parts scan_parts(const SsmProblem &P, bool ragged) {
     const int LN = P.S <= 8 ? 2 : P.S <= 16 ? 4 : P.S <= 32 ? 8 : 16;
-    const int64_t across = (P.D + 256 / LN - 1) / (256 / LN);
-    int64_t K = 304 / across;
-    if (K * across < 288) K = 456 / across;
-    if (K < 1) K = 1;
-    Parts parts;
-    parts.len = ((int64_t)P.T / K + TT - 1) / TT * TT;
-    if (parts.len < 4 * TT) parts.len = 4 * TT;
-    parts.whole = P.cu ? parts.len * 3 / 2 : parts.len * 7 / 2;
-    parts.rows = P.T > parts.len * 3 / 2 ? P.T / parts.len : 0;   // the same with and without cu_seqlens
-    parts.most = P.N;
-    if (P.cu) {
-        parts.most = (int32_t)(P.N + parts.rows);
-    } else if (P.N > 0) {
-        parts.most = (int32_t)(P.N * parts.of(P.seq_len));
-    }
-    return parts;
+    const bool waits = P.in_dtype == KDA_DTYPE_F32 && LN <= 4;
+    const double pair = LN == 2 ? 2.0 : waits ? 1.3 : 1.63, start = waits ? 1.8 : 3.0;
+    return cut_parts(P, ragged, (P.D + 256 / LN - 1) / (256 / LN), {pair, 0.67, start, 0.1, 1.5});
 }
 
+}  // namespace
+
+// (for a batch with cu_seqlens and one without, whichever takes more)
 int64_t kda_ssm_scan_ws(const SsmProblem &P) {
-    const int64_t rows = kda_ssm_parts(P).rows;
+    const Parts x = scan_parts(P, true), y = scan_parts(P, false);
+    const int64_t rows = x.rows > y.rows ? x.rows : y.rows;
     return (up4(rows * P.D * P.S) + rows * P.D) * (int64_t)sizeof(float);
 }
 
 cudaError_t kda_launch_ssm_scan(const SsmProblem &P, const float *init, void *out, float *final_state,
                                 float *chunk_states, int64_t chunk_capacity, float *workspace, cudaStream_t stream) {
-    ScanArgs a{P, init, out, final_state, chunk_states, chunk_capacity, false, kda_ssm_parts(P), workspace, nullptr};
+    ScanArgs a{P, init, out, final_state, chunk_states, chunk_capacity, false, scan_parts(P, P.cu != nullptr), workspace, nullptr};
     a.sums = workspace + up4(a.parts.rows * P.D * P.S);
     const int es = P.out_dtype == KDA_DTYPE_BF16 ? 2 : 4;
     a.ovec = ((uintptr_t)out & 15u) == 0 && (int64_t)P.D * es % 16 == 0;

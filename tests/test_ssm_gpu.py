@@ -841,3 +841,37 @@ def test_binding_refuses_on_the_gpu():
         kda.kda_ssm_conv(x["u"], torch.zeros(40, 5, device=DEV))
     with pytest.raises(ValueError, match="fp32 or bf16"):
         kda.kda_act_pack8(x["u"].half())
+
+
+# ------------------------------------------------------------------ how a batch is cut
+
+@pytest.mark.parametrize("singles", [6, 250, 251, 300])
+@pytest.mark.parametrize("D,S", [(72, 16), (520, 5)])
+def test_ragged_batches_with_long_sequences_among_many(singles, D, S):
+    """Long sequences among many short ones, fewer and more sequences than a block has
+    threads (256): the long ones are cut, wherever they stand."""
+    lens = [700] + [1] * (singles // 2) + [0, 333, 49] + [1] * (singles - singles // 2) + [48, 0]
+    x = scan_inputs(sum(lens), D, S, len(lens), F32, 400 + singles)
+    cu = cu_of(lens)
+    out, fin, chunks = fwd(x, cu_seqlens=cu, return_chunk_states=True)
+    w = ref.scan(h(x), lens)
+    for n, t in (("out", out), ("final", fin), ("chunks", chunks)):
+        check(n, t, w[n])
+    g, wg = bwd(x, cu_seqlens=cu, chunk_states=chunks), ref.scan_backward(h(x), lens, chunks.double().cpu())
+    for n in wg:
+        check(n, g[n], wg[n])
+    # the same bits again
+    again = fwd(x, cu_seqlens=cu)[0]
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("T", [33, 64, 95, 96, 257])
+def test_short_prompts_are_cut_too(T):
+    x = scan_inputs(T, 40, 16, 1, BF16, 450 + T)
+    out, fin, chunks = fwd(x, return_chunk_states=True, out_dtype=F32)
+    w = ref.scan(h(x), [T])
+    for n, t in (("out", out), ("final", fin), ("chunks", chunks)):
+        check(n, t, w[n])
+    g, wg = bwd(x, chunk_states=chunks, grad_dtype=F32), ref.scan_backward(h(x), [T], chunks.double().cpu())
+    for n in wg:
+        check(n, g[n], wg[n])
