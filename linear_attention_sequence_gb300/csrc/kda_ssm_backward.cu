@@ -33,8 +33,8 @@
 // exp(A sum Delta) g_in carries it on, and the gradients proper run every part from its
 // own g_in.
 //
-// 8192 tokens of 4096 channels with 16 states, bf16, u and z in 8 bits: 802 us, of which
-// 140 for the adjoint alone and 13 for the sums across blocks.  Bound by instruction
+// 8192 tokens of 4096 channels with 16 states, bf16, u and z in 8 bits: 770 us, of which
+// 121 for the adjoint alone and 14 for the sums across blocks.  Bound by instruction
 // issue: about 120 instructions per 128 state entries, 0.58 a cycle.
 
 #include <type_traits>
@@ -947,8 +947,8 @@ int blocks_an_sm(bool bf) {
     return bf ? Layout<__nv_bfloat16, LN>::kBlocks : Layout<float, LN>::kBlocks;
 }
 // Cutting adds the adjoint's pass only, 0.19 of the kernel's own.  8192 tokens, S = 16,
-// bf16, u and z in 8 bits, in 1 / 4 / 7 / 9 / 14 / 19 parts: 4096 channels 2019 / 957 /
-// 881 / 832 / 833 / 828 us, 8192 channels 2049 / 1785 / 1596 / 1547 / 1513 / 1562.  One
+// bf16, u and z in 8 bits, in 1 / 4 / 7 / 14 / 19 / 24 parts: 4096 channels 1768 / 864 /
+// 780 / 773 / 768 / 764 us, 8192 channels 1804 / 1627 / 1453 / 1429 / 1473 / 1466.  One
 // sequence of 512 tokens and 512 channels, bf16: whole 121 us, parts of four tiles 47, of one
 // 29.  A ragged batch's parts cost the same whatever they were cut from, so that every
 // sequence longer than a part is cut (3148 tokens in 13 sequences, 1000 channels: 98 us;

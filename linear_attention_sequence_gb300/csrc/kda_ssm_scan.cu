@@ -17,8 +17,8 @@
 // 128 bytes a cycle an SM whatever lanes share, and a lane that held one
 // channel needed 11 bytes an entry (44 cycles for 128 entries a scheduler,
 // against 16 of exponentials); two channels a lane and, for bf16, B and C kept as
-// bf16 bring that to 5.  8192 tokens of 4096 channels with 16 states, bf16: 274 us (110 of
-// them the first of the passes below, 164 the second), 0.6 instructions issued a cycle.
+// bf16 bring that to 5.  8192 tokens of 4096 channels with 16 states, bf16: 277 us (111 of
+// them the first of the passes below, 166 the second), 0.6 instructions issued a cycle.
 //
 // Few channels.  A sequence is cut into parts where its channels alone would
 // not fill the GPU: a first kernel runs all parts but the last from a zero state
@@ -479,12 +479,12 @@ cudaError_t by_states(const ScanArgs &a, cudaStream_t s) {
 int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 
 // Cutting adds a pass over the states, 0.67 of the scan's own time.  8192 tokens, S = 16,
-// bf16, whole against the best of 2 .. 64 parts: 4096 channels 423 and 279 us (7 parts),
-// 2048: 422 and 152 (9), 1024: 414 and 84 (19), 512: 414 and 54 (37); 8192 channels: 426 and
-// 508.  One sequence of 256 tokens and 512 channels: whole 18.8 us, 8 parts 12.9.  fp32 rows
+// bf16, whole against the best of 2 .. 64 parts: 4096 channels 425 and 277 us (7 parts; 4:
+// 314, 19: 279), 2048: 422 and 152 (19), 1024: 414 and 84 (19), 512: 414 and 54 (37);
+// 8192 channels: 432 and 513 (14).  One sequence of 256 tokens and 512 channels: whole 18.8 us, 8 parts 12.9.  fp32 rows
 // of up to 16 states keep a block alone on its SM waiting for memory, so that a second one
-// costs less (4096 channels: 418 us in 19 parts, 466 in the 7 of bf16; 8192: 700 in 2
-// parts, 737 whole).  A ragged batch's sequence of up to 1.5 parts stays whole (28,000
+// costs less (4096 channels: 396 us in 19 parts, 466 in the 7 of bf16; 8192: 700 in 2
+// parts, 739 whole).  A ragged batch's sequence of up to 1.5 parts stays whole (28,000
 // tokens in 8 sequences, 4096 channels: 655 us; with all longer ones cut 796).
 Parts scan_parts(const SsmProblem &P, bool ragged) {
     const int LN = P.S <= 8 ? 2 : P.S <= 16 ? 4 : P.S <= 32 ? 8 : 16;
