@@ -876,12 +876,7 @@ __global__ void __launch_bounds__(256) kda_ssm_carry_back_kernel(const __grid_co
     float c = a.d_final ? a.d_final[n * M + m] : 0.f;
     float *p = a.carry + row * M + m;
     const float *s = a.sums + row * P.D + m / P.S;
-#pragma unroll 4
-    for (int k = K - 1; k >= 0; --k) {
-        const float local = p[k * M];
-        c = c != 0.f ? fmaf(exp2_fast(A * s[(int64_t)k * P.D]), c, local) : local;
-        p[k * M] = c;
-    }
+    carry_on<true>(p, s, K, M, P.D, A, c);
 }
 
 // The sums that cross blocks, each in a fixed order: dB and dC over the blocks

@@ -435,12 +435,7 @@ __global__ void __launch_bounds__(256) kda_ssm_carry_kernel(const __grid_constan
     float c = a.init ? a.init[n * M + m] : 0.f;
     float *p = a.carry + row * M + m;
     const float *s = a.sums + row * P.D + d;
-#pragma unroll 4
-    for (int k = 0; k < K; ++k) {
-        const float local = p[k * M];
-        c = c != 0.f ? fmaf(exp2_fast(A * s[(int64_t)k * P.D]), c, local) : local;
-        p[k * M] = c;
-    }
+    carry_on<false>(p, s, K, M, P.D, A, c);
 }
 
 template <typename IN, typename OUT, int LN, bool STATES>
