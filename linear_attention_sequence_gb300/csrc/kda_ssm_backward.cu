@@ -957,7 +957,7 @@ Parts back_parts(const SsmProblem &P, bool ragged) {
         case 8: of = blocks_an_sm<8>(bf); break;
         default: of = blocks_an_sm<16>(bf); break;
     }
-    return cut_parts(P, ragged, blocks_across(P), {of == 2 ? 1.45 : 2.0, 0.19, 0.7, 0.02, 1.0});
+    return cut_parts(P, ragged, blocks_across(P), {of == 2 ? 1.45 : 2.0, 0.19, 0.7, 0.02, 1.0, 304});
 }
 
 int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }

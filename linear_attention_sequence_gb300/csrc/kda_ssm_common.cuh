@@ -532,6 +532,7 @@ struct PartCosts {
     double start;            // a round of blocks, before their first tile
     double part;             // a part in the carry
     double whole;            // a ragged batch's longest sequence that stays whole, in parts' lengths
+    int places;              // parts that a ragged batch is cut into, at full length
 };
 
 // How a batch is cut, with `across` blocks side by side for a sequence: into the K
@@ -539,8 +540,9 @@ struct PartCosts {
 // alone (a little less than alone after others: the first to end make room early).
 // Against the best of up to 20 K on batches of equal lengths (64 .. 8192 tokens, 64 ..
 // 8192 channels, 8 .. 64 states) what it picks takes 1.00 to 1.09 of the time.  Where
-// the lengths are known only on the device (`ragged`), a part is one 304th of the batch's
-// work, which no sequence that stays whole outlasts by much.
+// the lengths are known only on the device (`ragged`), a part is one place's share of the
+// batch's work, which no sequence that stays whole outlasts by much (30 batches, S = 16: shares
+// of one 380th, 456th and 608th take 1.02 to 1.12 of a 304th's time, one 152nd 1.0 to 1.4).
 inline Parts cut_parts(const SsmProblem &P, bool ragged, int64_t across, const PartCosts &c) {
     const int64_t tokens = ragged || P.N == 0 ? P.T : P.T / P.N, b = ragged || P.N == 0 ? across : across * P.N;
     const int64_t tiles = (tokens + kSsmTile - 1) / kSsmTile;
@@ -553,7 +555,7 @@ inline Parts cut_parts(const SsmProblem &P, bool ragged, int64_t across, const P
     parts.len = (tiles < 1 ? 1 : tiles) * kSsmTile;
     parts.whole = INT32_MAX;
     if (ragged) {
-        const int64_t t = (tiles * across + 303) / 304;
+        const int64_t t = (tiles * across + c.places - 1) / c.places;
         if (t < tiles) {
             parts.len = t * kSsmTile;
             parts.whole = (int64_t)(c.whole * (double)parts.len);

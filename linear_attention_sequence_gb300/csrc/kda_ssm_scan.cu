@@ -480,12 +480,13 @@ int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 // of up to 16 states keep a block alone on its SM waiting for memory, so that a second one
 // costs less (4096 channels: 396 us in 19 parts, 466 in the 7 of bf16; 8192: 700 in 2
 // parts, 739 whole).  A ragged batch's sequence of up to 1.5 parts stays whole (28,000
-// tokens in 8 sequences, 4096 channels: 655 us; with all longer ones cut 796).
+// tokens in 8 sequences, 4096 channels: 655 us; with all longer ones cut 796).  Up to 8 states
+// take a whole SM a block: 152 places are then 0.89 of the time of 304 (18 ragged batches).
 Parts scan_parts(const SsmProblem &P, bool ragged) {
     const int LN = P.S <= 8 ? 2 : P.S <= 16 ? 4 : P.S <= 32 ? 8 : 16;
     const bool waits = P.in_dtype == KDA_DTYPE_F32 && LN <= 4;
     const double pair = LN == 2 ? 2.0 : waits ? 1.3 : 1.63, start = waits ? 1.8 : 3.0;
-    return cut_parts(P, ragged, (P.D + 256 / LN - 1) / (256 / LN), {pair, 0.67, start, 0.1, 1.5});
+    return cut_parts(P, ragged, (P.D + 256 / LN - 1) / (256 / LN), {pair, 0.67, start, 0.1, 1.5, LN == 2 ? 152 : 304});
 }
 
 }  // namespace
