@@ -19,8 +19,8 @@ __device__ __forceinline__ void st_elem(__nv_bfloat16 *p, float x) { *p = __floa
 // Sequence bounds for sequence n.  Entries of cu_seqlens are clamped into
 // [0, total] and a decreasing pair is read as an empty sequence, so a
 // malformed array never leads to an out-of-range access.
-__device__ __forceinline__ void seq_bounds(const int32_t *cu, int n, int64_t total,
-                                           int64_t seq_len, int64_t &a, int64_t &b) {
+__host__ __device__ __forceinline__ void seq_bounds(const int32_t *cu, int n, int64_t total,
+                                                    int64_t seq_len, int64_t &a, int64_t &b) {
     if (cu) {
         int64_t x = cu[n], y = cu[n + 1];
         x = x < 0 ? 0 : (x > total ? total : x);

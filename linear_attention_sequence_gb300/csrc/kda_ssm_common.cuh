@@ -318,9 +318,10 @@ __device__ __forceinline__ void store_states(float *p, float4 v, int n0, int S, 
 
 // The sequence of token t in a packed batch: its number n and its bounds.  False
 // if the token lies outside every sequence; then sa is the first token after t
-// that may lie in one (total if there is none).
-__device__ __forceinline__ bool find_seq(const int32_t *cu, int N, int64_t total, int64_t seq_len, int64_t t, int &n,
-                                         int64_t &sa, int64_t &sb) {
+// that may lie in one (total if there is none: no sequences, or malformed lengths), so
+// that a walk which goes on there comes to an end.  t < total.
+__host__ __device__ __forceinline__ bool find_seq(const int32_t *cu, int N, int64_t total, int64_t seq_len, int64_t t,
+                                                  int &n, int64_t &sa, int64_t &sb) {
     if (!cu) {
         n = (int)(t / seq_len);   // t < total = N seq_len, so seq_len > 0
     } else {
@@ -330,9 +331,9 @@ __device__ __forceinline__ bool find_seq(const int32_t *cu, int N, int64_t total
             if (cu[m] <= t) lo = m; else hi = m;
         }
         n = lo;
-        if (n < 0) {
-            sa = cu[0] < total ? cu[0] : total;
-            sb = sa;
+        if (n < 0) {              // before the first sequence, or there is none
+            const int64_t first = N > 0 ? cu[0] : total;
+            sa = sb = first > t && first < total ? first : total;
             return false;
         }
     }

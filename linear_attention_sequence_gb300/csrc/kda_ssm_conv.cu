@@ -625,7 +625,7 @@ cudaError_t kda_launch_ssm_conv(const SsmProblem &P, const float *w, const float
 
 int64_t kda_ssm_conv_backward_tiles(const SsmProblem &P, int *tile) {
     *tile = run_length(P.T, P.D, 4, 256);
-    return ((int64_t)P.T + *tile - 1) / *tile;
+    return P.N == 0 ? 0 : ((int64_t)P.T + *tile - 1) / *tile;   // (rows without a sequence belong to no run)
 }
 
 cudaError_t kda_launch_ssm_conv_backward(const SsmProblem &P, const float *w, const float *bias, const float *cin,
