@@ -545,7 +545,8 @@ struct PartCosts {
 // batch's work, which no sequence that stays whole outlasts by much (30 batches, S = 16: shares
 // of one 380th, 456th and 608th take 1.02 to 1.12 of a 304th's time, one 152nd 1.0 to 1.4).
 inline Parts cut_parts(const SsmProblem &P, bool ragged, int64_t across, const PartCosts &c) {
-    const int64_t tokens = ragged || P.N == 0 ? P.T : P.T / P.N, b = ragged || P.N == 0 ? across : across * P.N;
+    if (P.N == 0) return {kSsmTile, INT32_MAX, 0, 0, 0};   // no parts, whatever rows there are
+    const int64_t tokens = ragged ? P.T : P.T / P.N, b = ragged ? across : across * P.N;
     const int64_t tiles = (tokens + kSsmTile - 1) / kSsmTile;
     const auto cost = [&](int64_t n, int64_t t) {
         const int64_t full = n / 304, rest = n % 304;

@@ -5,7 +5,7 @@ import torch
 
 import linear_attention_sequence_gb300 as kda
 from linear_attention_sequence_gb300 import _ssm
-from test_ssm_gpu import BF16, DEV, F32, conv_inputs
+from test_ssm_gpu import BF16, DEV, F32, bwd, conv_inputs, fwd, scan_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -35,4 +35,42 @@ def test_conv_of_rows_without_sequences(first, dtype, packed):
     _ssm._run("kda_ssm_conv_backward", torch.cuda.current_device(), dims, rows(x["x"]), x["weight"].data_ptr(), 0, 0,
               cu.data_ptr(), 1, rows(x["d_out"]), 0, dx.data_ptr(), dw.data_ptr(), 0, 0, 0, 0)
     assert bool((dx == 7).all()) and not dw.any()
+    assert kda.kda_get_last_device_error() == 0
+
+
+@pytest.fixture
+def nan_workspaces(monkeypatch):
+    """Every workspace holds NaN before the call."""
+    plain = _ssm._workspace
+    monkeypatch.setattr(_ssm, "_workspace", lambda query, dims, device: plain(query, dims, device).fill_(255))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T,D", [(1, 40), (32, 40), (200, 40), (2000, 40), (64, 5000)])
+def test_scan_of_rows_without_sequences(T, D, packed, nan_workspaces):
+    """The same of the scan: the gradients of A, D and dt_bias are sums over nothing."""
+    S = 16
+    x = scan_inputs(T, D, S, 0, BF16, 502)
+    cu = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = torch.full((T, D), 7.0, device=DEV, dtype=BF16)
+    _, fin, chunks = fwd(x, cu_seqlens=cu, out=out, chunk_states=torch.empty(3, D, S, device=DEV))
+    assert fin.shape == (0, D, S) and bool((out == 7).all())
+    kw = {}
+    if packed:
+        (x["u"], kw["u_scales"]), (x["z"], kw["z_scales"]) = kda.kda_act_pack8(x["u"]), kda.kda_act_pack8(x["z"])
+    g = bwd(x, cu_seqlens=cu, chunk_states=chunks, **kw)
+    for n in ("dA", "dD", "ddt_bias"):
+        assert bool((g[n] == 0).all()), n
+    assert g["d_init_state"].shape == (0, D, S)
+    # the C call, for the rows of the others
+    gr = {n: torch.full((T, S if n in ("dB", "dC") else D), 7.0, device=DEV, dtype=BF16) for n in ("du", "ddt", "dB", "dC", "dz")}
+    dA = torch.full((D, S), 7.0, device=DEV)
+    dims = _ssm._DIMS.pack(0, T, D, S, 1, 1)
+    ins = _ssm._scan_args(x["u"], x["dt"], x["A"], x["B"], x["C"], x["D"], x["z"], x["dt_bias"], cu, None, True,
+                          kw.get("u_scales"), kw.get("z_scales"))[-1]
+    ws = _ssm._workspace("kda_ssm_scan_backward_workspace", dims, DEV)
+    _ssm._run("kda_ssm_scan_backward", torch.cuda.current_device(), dims, ins, 0, 0, 0,
+              _ssm._ROWS.pack(x["d_out"].data_ptr(), D, 0), 0,
+              _ssm._GRADS.pack(*(gr[n].data_ptr() for n in gr), dA.data_ptr(), 0, 0, 0), ws.data_ptr(), ws.shape[0])
+    assert bool((dA == 0).all()) and all(bool((t == 7).all()) for t in gr.values())
     assert kda.kda_get_last_device_error() == 0

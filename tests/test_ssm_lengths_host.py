@@ -15,6 +15,15 @@ SOURCE = """
 extern "C" int find(const int32_t *cu, int N, int64_t total, int64_t seq_len, int64_t t, int *n, int64_t *sa, int64_t *sb) {
     return kda::find_seq(cu, N, total, seq_len, t, *n, *sa, *sb);
 }
+extern "C" void cut(int N, int T, int ragged, int across, int places, int64_t *rows_cut_most) {
+    kda::SsmProblem P{};
+    P.N = N;
+    P.T = T;
+    const kda::Parts p = kda::cut_parts(P, ragged, across, {1.6, 0.5, 2.0, 0.1, 1.0, places});
+    rows_cut_most[0] = p.rows;
+    rows_cut_most[1] = p.cut;
+    rows_cut_most[2] = p.most;
+}
 """
 
 
@@ -81,3 +90,16 @@ def test_no_runs_without_sequences():
     from linear_attention_sequence_gb300 import _ssm, lib
     size = lambda N: lib().kda_ssm_conv_backward_workspace(_ssm._DIMS.pack(N, 200, 40, 4, 0, 0))  # noqa: E731
     assert size(0) == 0 and size(1) > 0
+
+
+def test_no_parts_without_sequences(H):
+    """A batch without sequences has no parts, however many rows: sums over its parts are
+    sums over nothing."""
+    got = (ctypes.c_int64 * 3)()
+    for T in (0, 1, 32, 33, 200, 2000, 100000):
+        for ragged in (0, 1):
+            for across in (1, 2, 64, 500):
+                H.cut(0, T, ragged, across, 304, got)
+                assert list(got) == [0, 0, 0], (T, ragged, across)
+                H.cut(1, T, ragged, across, 304, got)
+                assert got[2] == 1 + got[0]
