@@ -51,6 +51,10 @@ struct ScanArgs {
     // - (number of its sequence).
     float *carry;      // [D, S]: what the part ends with, then what the next one starts with
     float *sums;       // [D]: sum of Delta over the part
+    // Where the final state takes the initial state's place, part 0 of a cut sequence could
+    // read after its last part has written: it reads a copy, [D, S] at its row of the carry,
+    // that the carry kernel takes.  nullptr: it reads init.
+    float *first;
 };
 
 template <typename IN, int LN>
@@ -320,8 +324,9 @@ kda_ssm_scan_kernel(const __grid_constant__ ScanArgs a) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
         if (ch + c < P.D) {
             x = load_states(P.A + (int64_t)(ch + c) * P.S, n0, P.S, P.svec);
-            const float *from = STATES ? nullptr : part == 0 ? (a.init ? a.init + (int64_t)n * P.D * P.S : nullptr)
-                                : a.carry + (row - 1) * P.D * P.S;
+            const float *from = STATES ? nullptr : part > 0 ? a.carry + (row - 1) * P.D * P.S
+                                : a.first && count > 1 ? a.first + row * P.D * P.S
+                                : a.init ? a.init + (int64_t)n * P.D * P.S : nullptr;
             if (from) y = load_states(from + (int64_t)(ch + c) * P.S, n0, P.S, P.svec);
         }
         A[c][0] = pack2(x.x * kLog2e, x.y * kLog2e);
@@ -433,6 +438,7 @@ __global__ void __launch_bounds__(256) kda_ssm_carry_kernel(const __grid_constan
     const int64_t d = m / P.S;
     const float A = P.A[m] * kLog2e;
     float c = a.init ? a.init[n * M + m] : 0.f;
+    if (a.first) a.first[row * M + m] = c;
     float *p = a.carry + row * M + m;
     const float *s = a.sums + row * P.D + d;
     carry_on<false>(p, s, K, M, P.D, A, c);
@@ -495,13 +501,15 @@ Parts scan_parts(const SsmProblem &P, bool ragged) {
 int64_t kda_ssm_scan_ws(const SsmProblem &P) {
     const Parts x = scan_parts(P, true), y = scan_parts(P, false);
     const int64_t rows = x.rows > y.rows ? x.rows : y.rows;
-    return (up4(rows * P.D * P.S) + rows * P.D) * (int64_t)sizeof(float);
+    return (2 * up4(rows * P.D * P.S) + rows * P.D) * (int64_t)sizeof(float);
 }
 
 cudaError_t kda_launch_ssm_scan(const SsmProblem &P, const float *init, void *out, float *final_state,
                                 float *chunk_states, int64_t chunk_capacity, float *workspace, cudaStream_t stream) {
-    ScanArgs a{P, init, out, final_state, chunk_states, chunk_capacity, false, scan_parts(P, P.cu != nullptr), workspace, nullptr};
-    a.sums = workspace + up4(a.parts.rows * P.D * P.S);
+    ScanArgs a{P, init, out, final_state, chunk_states, chunk_capacity, false, scan_parts(P, P.cu != nullptr), workspace, nullptr, nullptr};
+    float *first = workspace + up4(a.parts.rows * P.D * P.S);
+    a.sums = first + up4(a.parts.rows * P.D * P.S);
+    if (init && init == final_state) a.first = first;
     const int es = P.out_dtype == KDA_DTYPE_BF16 ? 2 : 4;
     a.ovec = ((uintptr_t)out & 15u) == 0 && (int64_t)P.D * es % 16 == 0;
     const bool ib = P.in_dtype == KDA_DTYPE_BF16, ob = P.out_dtype == KDA_DTYPE_BF16;

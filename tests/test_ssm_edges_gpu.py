@@ -5,7 +5,8 @@ import torch
 
 import linear_attention_sequence_gb300 as kda
 from linear_attention_sequence_gb300 import _ssm
-from test_ssm_gpu import BF16, DEV, F32, bwd, conv_inputs, fwd, scan_inputs
+import ssm_reference as ref
+from test_ssm_gpu import BF16, DEV, F32, bwd, check, conv_inputs, cu_of, fwd, h, scan_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,45 @@ def test_scan_of_rows_without_sequences(T, D, packed, nan_workspaces):
               _ssm._GRADS.pack(*(gr[n].data_ptr() for n in gr), dA.data_ptr(), 0, 0, 0), ws.data_ptr(), ws.shape[0])
     assert bool((dA == 0).all()) and all(bool((t == 7).all()) for t in gr.values())
     assert kda.kda_get_last_device_error() == 0
+
+
+# ------------------------------------------------------------------ states in place
+
+def misaligned(t):
+    """The same values one fp32 element past an allocation's start."""
+    v = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)[1:].view(t.shape)
+    return v.copy_(t)
+
+
+@pytest.mark.parametrize("place", [torch.clone, misaligned])
+@pytest.mark.parametrize("dtype,D,S", [(F32, 40, 16), (BF16, 72, 5), (F32, 24, 64), (BF16, 520, 16)])
+@pytest.mark.parametrize("N,lens", [(1, [257]), (3, [736] * 3), (1, [1500]), (None, [700]), (None, [257, 0, 900, 5, 1]),
+                                    (None, [1] * 290 + [700, 0, 333])])
+def test_scan_of_cut_sequences_in_place(N, lens, dtype, D, S, place, nan_workspaces):
+    """The final state in the initial state's place, of sequences that are cut into parts
+    (257 tokens: parts of 32, the last of one token): the bits of the call with two buffers,
+    every time."""
+    x = scan_inputs(sum(lens), D, S, len(lens), dtype, 600 + sum(lens) + D)
+    kw = dict(num_seqs=N) if N else dict(cu_seqlens=cu_of(lens))
+    x["state"] = start = place(x["state"])
+    out, fin, chunks = fwd(x, return_chunk_states=True, out_dtype=F32, **kw)
+    w = ref.scan(h(x), lens)
+    for n, t in (("out", out), ("final", fin), ("chunks", chunks)):
+        check(n, t, w[n])
+    states = [place(start) for _ in range(10)]
+    outs = [fwd(dict(x, state=st), out_dtype=F32, final_state=st, **kw)[0] for st in states]
+    for st, o in zip(states, outs):
+        assert torch.equal(st, fin) and torch.equal(o, out)
+
+
+def test_long_prompt_in_pieces_in_place():
+    """A prompt given in pieces that are each cut, with one buffer for its state."""
+    T, D, S = 1800, 40, 16
+    x = scan_inputs(T, D, S, 1, F32, 611)
+    w = ref.scan(h(x), [T])
+    st, outs = x["state"].clone(), []
+    for a, b in ((0, 600), (600, 601), (601, 1225), (1225, T)):
+        part = {k: (v[a:b] if k in ("u", "dt", "B", "C", "z") else v) for k, v in x.items()}
+        outs.append(fwd(dict(part, state=st), final_state=st)[0])
+    check("out", torch.cat(outs), w["out"])
+    check("state", st, w["final"])
