@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(256) kda_ssm_reduce_kernel(const __grid_consta
         const float *p = a.share + i;
         const int64_t step = (int64_t)P.T * 2 * a.SP;
 #pragma unroll 8
-        for (int c = 0; c < a.ncb; ++c) v += __ldg(p + c * step);
+        for (int c = 0; c < a.ncb; ++c) v += p[c * step];
         st_elem((OUT *)(k < a.SP ? a.dC : a.dB) + t * P.S + n, v);
         return;
     }
@@ -923,7 +923,7 @@ __global__ void __launch_bounds__(256) kda_ssm_reduce_kernel(const __grid_consta
             if (i < a.n[k]) {
                 float v = 0.f;
 #pragma unroll 8
-                for (int p = 0; p < a.parts; ++p) v += __ldg(a.from[k] + p * a.n[k] + i);
+                for (int p = 0; p < a.parts; ++p) v += a.from[k][p * a.n[k] + i];
                 a.to[k][i] = v;
                 return;
             }

@@ -16,7 +16,9 @@ constexpr int kPackGroup = KDA_PACK_GROUP;
 // A kernel launched by launch_behind() may start once every block of the one before
 // it has started and called let_next(); it calls wait_before() ahead of its first read
 // of what that one (and those before it) wrote.  The kernel in front of the first of
-// such a chain is complete when the chain starts.
+// such a chain is complete when the chain starts.  What the one before writes changes
+// while the later kernel is on the GPU, so that it is read with ordinary loads; __ldg and
+// ld.global.nc are for what no kernel of the chain writes.
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... Params, typename... Args>

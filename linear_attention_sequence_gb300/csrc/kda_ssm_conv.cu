@@ -503,7 +503,7 @@ kda_ssm_conv_reduce_kernel(const __grid_constant__ ConvArgs a, int64_t tiles, un
         const float *p = a.part + (int64_t)k * D + c;
         const int64_t step = (int64_t)(W + 1) * D;
 #pragma unroll 8
-        for (int64_t i = y; i < tiles; i += kRuns) v += __ldg(p + i * step);
+        for (int64_t i = y; i < tiles; i += kRuns) v += p[i * step];
     }
     s[y][lane] = v;
     __syncthreads();

@@ -117,3 +117,45 @@ def test_long_prompt_in_pieces_in_place():
         outs.append(fwd(dict(part, state=st), final_state=st)[0])
     check("out", torch.cat(outs), w["out"])
     check("state", st, w["final"])
+
+
+# ------------------------------------------------------------------ calls close behind one another
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T,D,S", [(600, 1032, 16), (2048, 264, 24), (333, 40, 8)])
+def test_gradients_behind_one_another_share_a_workspace(T, D, S, packed, monkeypatch):
+    """Calls on a stream with one workspace, of two sets of inputs in turn and nothing
+    between them: each gives the bits of a call alone, whose kernels nobody's were in front
+    of.  What a kernel adds up is what the one before it in its own call wrote."""
+    sets = []
+    for seed in (621, 622):
+        x, c = scan_inputs(T, D, S, 1, BF16, seed), conv_inputs(T, D, 4, 1, BF16, seed)
+        chunks, kw, cx = fwd(x, return_chunk_states=True)[2], {}, {}
+        if packed:
+            (x["u"], kw["u_scales"]), (x["z"], kw["z_scales"]) = kda.kda_act_pack8(x["u"]), kda.kda_act_pack8(x["z"])
+            c["x"], cx["x_scales"] = kda.kda_act_pack8(c["x"])
+        sets.append((x, chunks, kw, c, cx))
+
+    def both(s):
+        x, chunks, kw, c, cx = s
+        return bwd(x, chunk_states=chunks, **kw), kda.kda_ssm_conv_backward(
+            c["x"], c["weight"], c["d_out"], c["bias"], None, c["state"], d_conv_state_out=c["d_state"], **cx)
+
+    want = []
+    for s in sets:
+        torch.cuda.synchronize()
+        want.append(both(s))
+        torch.cuda.synchronize()
+    plain, held = _ssm._workspace, {}
+
+    def shared(query, dims, device):
+        if (query, dims) not in held:
+            held[query, dims] = plain(query, dims, device).fill_(255)
+        return held[query, dims]
+
+    monkeypatch.setattr(_ssm, "_workspace", shared)
+    got = [both(sets[i % 2]) for i in range(16)]
+    for i, pair in enumerate(got):
+        for g, w in zip(pair, want[i % 2]):
+            for n in w:
+                assert torch.equal(g[n], w[n]), (i, n)
