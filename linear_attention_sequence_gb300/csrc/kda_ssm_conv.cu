@@ -46,6 +46,7 @@ struct ConvArgs {
 };
 
 // Four neighbouring fp32 values; those at or past `have`, and all of a NULL array, are 0.
+// Ordinary loads: the one-token kernel may write a state where it has read it.
 __device__ __forceinline__ void load4(const float *p, f2 (&v)[NP], int have, bool vec) {
     float x[V];
     if (!p) {
@@ -53,7 +54,7 @@ __device__ __forceinline__ void load4(const float *p, f2 (&v)[NP], int have, boo
         return;
     }
     if (vec && have >= V) {
-        const float4 q = __ldg(reinterpret_cast<const float4 *>(p));
+        const float4 q = *reinterpret_cast<const float4 *>(p);
         v[0] = pack2(q.x, q.y);
         v[1] = pack2(q.z, q.w);
         return;

@@ -119,6 +119,28 @@ def test_long_prompt_in_pieces_in_place():
     check("state", st, w["final"])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("N,D", [(1, 1), (3, 70), (256, 2048), (5, 12288)])
+def test_conv_tokens_in_place(N, D, W, dtype):
+    """Tokens one at a time with the state moved in its own buffer: the bits of calls with
+    two buffers, over many in a row."""
+    T = 9
+    x = conv_inputs(N * T, D, W, N, dtype, 615)
+    rows = x["x"].view(T, N, D)
+    one, here = x["state"], x["state"].clone()
+    call = lambda t, st, to: kda.kda_ssm_conv(rows[t], x["weight"], x["bias"], conv_state=st, conv_state_out=to, num_seqs=N)  # noqa: E731
+    outs = [call(t, here, here)[0] for t in range(T)]
+    for t in range(T):
+        y, one = call(t, one, torch.empty_like(one))
+        assert torch.equal(y, outs[t])
+    assert torch.equal(one, here)
+    line = torch.cat([x["state"].transpose(0, 1).double(), rows.double()])          # [W - 1 + T, N, D]
+    assert torch.equal(here.double(), line[T:].transpose(0, 1))
+    c = x["bias"].double() + sum(line[k:k + T] * x["weight"][:, k].double() for k in range(W))
+    check("out", torch.stack(outs), (c / (1 + torch.exp(-c))).cpu())
+
+
 # ------------------------------------------------------------------ calls close behind one another
 
 @pytest.mark.parametrize("packed", [False, True])
