@@ -445,7 +445,8 @@ kda_status kda_decode(const kda_dims *dims, const void *q, const void *k, const 
  * infinity or a NaN in an input reaches the outputs that depend on it and no
  * other sequence or channel (the gradients of B, C and the parameters are sums
  * over channels or tokens).  Rows of an output that belong to no sequence (tokens
- * before cu_seqlens[0] or from cu_seqlens[N] on) are left as they were.
+ * before cu_seqlens[0] or from cu_seqlens[N] on) are left as they were, those of
+ * gradients too; with N == 0 that is every row, and the parameters' gradients are 0.
  * A malformed cu_seqlens never causes an access out of bounds; what a call then
  * writes to the outputs is unspecified.
  * The calls allocate nothing: a call that needs scratch takes a workspace, whose
@@ -532,7 +533,8 @@ kda_status kda_ssm_conv(const kda_ssm_dims *dims, const kda_rows *x, const float
  *                  are then those at the values the codes stand for.
  *   dx             device, out_dtype [T, D];  dweight  fp32 [D, W];  dbias  fp32 [D] or NULL;
  *   d_conv_state_in  fp32 [N, W-1, D] or NULL.
- *   workspace      kda_ssm_conv_backward_workspace(dims) bytes, 16-byte aligned.
+ *   workspace      kda_ssm_conv_backward_workspace(dims) bytes, 16-byte aligned: W + 1 rows of
+ *                  D floats a run of tokens (6 MB for 8192 tokens of 8192 channels, W = 4).
  */
 int64_t kda_ssm_conv_backward_workspace(const kda_ssm_dims *dims);
 kda_status kda_ssm_conv_backward(const kda_ssm_dims *dims, const kda_rows *x, const float *weight,
@@ -547,11 +549,13 @@ kda_status kda_ssm_conv_backward(const kda_ssm_dims *dims, const kda_rows *x, co
  *
  *   init_state   device fp32 [N, D, S] or NULL (zeros).
  *   out          device, out_dtype [T, D].
- *   final_state  device fp32 [N, D, S] or NULL.  May be init_state itself.
+ *   final_state  device fp32 [N, D, S] or NULL.  May be init_state itself, with the same results.
  *   chunk_states device fp32 [chunk_capacity, D, S] or NULL (with chunk_capacity 0): the
  *                state after every KDA_CHUNK tokens of each sequence, rows as in
  *                kda_prefill_checkpointed with interval KDA_CHUNK; what the gradients need.
- *   workspace    kda_ssm_scan_workspace(dims) bytes (0 for batches that need none), 16-byte aligned.
+ *   workspace    kda_ssm_scan_workspace(dims) bytes (0 for batches that need none), 16-byte
+ *                aligned: 2 S + 1 floats a channel for each place where a sequence is cut (3 MB
+ *                for 8192 tokens of 4096 channels with 16 states).
  */
 int64_t kda_ssm_scan_workspace(const kda_ssm_dims *dims);
 kda_status kda_ssm_scan(const kda_ssm_dims *dims, const kda_ssm_inputs *in, const float *init_state,
@@ -583,7 +587,10 @@ typedef struct {
  *   chunk_states the forward's, chunk_capacity rows (NULL with 0 rows).  Where a row that is
  *                needed is missing: as in kda_backward (an error where lengths are known on
  *                the host, else the device status word).
- *   workspace    kda_ssm_scan_backward_workspace(dims) bytes, 16-byte aligned.
+ *   workspace    kda_ssm_scan_backward_workspace(dims) bytes, 16-byte aligned.  Most of it are
+ *                shares of dB and dC: 2 s floats a token for every 1024 / s channels, s = 8, 16,
+ *                32 or 64 the first not below S (8192 tokens of 4096 channels: 74 MB with 16
+ *                states, 1.0 GB with 64).
  */
 int64_t kda_ssm_scan_backward_workspace(const kda_ssm_dims *dims);
 kda_status kda_ssm_scan_backward(const kda_ssm_dims *dims, const kda_ssm_inputs *in,

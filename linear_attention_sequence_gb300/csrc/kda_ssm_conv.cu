@@ -15,7 +15,7 @@
 // complete.  A run's share of dw and dbias goes to a workspace, and a second
 // kernel adds the runs up in their order, so the sums do not depend on timing.
 // 8192 x 8192 bf16: the convolution 48 us (5.6 TB/s) alone, 53 a call; the gradient
-// from 8-bit x 91 us a call, bound by instruction issue at 14 warps an SM (two
+// from 8-bit x 92 us a call, bound by instruction issue at 14 warps an SM (two
 // channels a thread at twice the warps took 111).  256 tokens of 12288 channels: 17.5 us.
 
 #include <initializer_list>
@@ -521,8 +521,9 @@ kda_ssm_conv_reduce_kernel(const __grid_constant__ ConvArgs a, int64_t tiles, un
 
 // Tokens of a run: as many as make the blocks fill the GPU's places (`per_sm` an SM)
 // a whole number of times, with at most `most` tokens a run; at least 16, which keeps the
-// rows that two runs read within a fifth.  (8192 x 8192, gradient: runs of 128, which
-// fill 1.7 times the places, 93 us, of 216, once, 79.)
+// rows that two runs read within a fifth.  (8192 x 8192, gradient from 8 bits, the kernel
+// alone under a profiler: runs of 128, which fill 1.7 times the places, 93 us, of 216,
+// once, 88.)
 int run_length(int64_t T, int32_t D, int per_sm, int most) {
     const int64_t work = T * ((D + V * kThreads - 1) / (V * kThreads)), places = 152 * (int64_t)per_sm;
     int64_t rounds = (work + places * most - 1) / (places * most);

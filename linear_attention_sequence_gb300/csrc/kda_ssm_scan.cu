@@ -24,7 +24,9 @@
 // not fill the GPU: a first kernel runs all parts but the last from a zero state
 // (no outputs), a second one carries the states from part to part, h_in' =
 // h_part + exp(A sum Delta) h_in, and the scan proper runs every part from its own
-// h_in.
+// h_in.  Where the final state takes the initial state's place, the second kernel also
+// copies the initial states that the third reads (no time that shows: 277 us with one
+// buffer and with two).
 
 #include <type_traits>
 

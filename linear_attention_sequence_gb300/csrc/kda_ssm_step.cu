@@ -8,7 +8,7 @@
 // NB state loads in flight and use the decay rates A (read once from DRAM, then
 // from L2) NB times; a channel's lanes share out the step sizes and gates of
 // the NB sequences between them.  256 sequences of 12288 channels with 16 states, bf16: 69 us,
-// 6.2 TB/s (92 % of the measured copy rate); every lane computing its own step sizes: 118 us.
+// 6.2 TB/s (91 % of the measured copy rate); every lane computing its own step sizes: 118 us.
 
 #include "kda_ssm_common.cuh"
 
