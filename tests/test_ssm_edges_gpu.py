@@ -119,6 +119,36 @@ def test_long_prompt_in_pieces_in_place():
     check("state", st, w["final"])
 
 
+def test_scan_in_place_in_graphs_and_on_a_stream():
+    """A cut scan in place, captured and replayed, two graphs in turn on one state, and on a
+    stream of its own: each call goes on from the state that the one before left."""
+    lens, D, S = [700, 0, 257], 40, 16
+    cu, N = cu_of(lens), len(lens)
+    sets = [scan_inputs(sum(lens), D, S, N, BF16, seed) for seed in (631, 632)]
+    start, want = sets[0]["state"].clone(), []
+    st = start.clone()
+    for i in range(6):
+        out, st = fwd(dict(sets[i % 2], state=st), cu_seqlens=cu)
+        want.append((out, st))
+    here = start.clone()
+    call = lambda x, **kw: fwd(dict(x, state=here), cu_seqlens=cu, final_state=here, **kw)[0]  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [call(sets[i % 2], stream=side) for i in range(6)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, (w, _) in zip(outs, want)) and torch.equal(here, want[-1][1])
+    graphs, outs = [], []
+    for x in sets:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(call(x))
+    here.copy_(start)
+    for i, (o, f) in enumerate(want):
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i % 2], o) and torch.equal(here, f)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("W", [2, 3, 4])
 @pytest.mark.parametrize("N,D", [(1, 1), (3, 70), (256, 2048), (5, 12288)])
