@@ -57,7 +57,9 @@ typedef enum {
     KDA_ERR_TIMEOUT = 4           /* a bounded device-side wait gave up */
 } kda_status;
 
-typedef enum { KDA_DTYPE_F32 = 0, KDA_DTYPE_BF16 = 1 } kda_dtype;
+/* KDA_DTYPE_F16 is taken by the softmax attention and cache calls (kda_attn_*,
+ * kda_cache_*) only. */
+typedef enum { KDA_DTYPE_F32 = 0, KDA_DTYPE_BF16 = 1, KDA_DTYPE_F16 = 2 } kda_dtype;
 
 /* Prefill kernel selection: a diagnostic and test selector, not a tuning
  * knob.  KDA_PREFILL_DEFAULT (what callers should pass) picks TC where it
@@ -605,6 +607,103 @@ kda_status kda_ssm_scan_backward(const kda_ssm_dims *dims, const kda_ssm_inputs 
  * row excepted), an overlap, or a workspace too small; KDA_ERR_UNSUPPORTED for S
  * outside 1..64, W outside 2..4, or sizes beyond one grid.  The workspace
  * functions return -1 for dims that the call refuses. */
+
+/* ---------------------------------------------------------------------------
+ * Softmax attention and its paged cache
+ * ---------------------------------------------------------------------------
+ * A hybrid stack keeps a softmax attention layer after every few KDA layers ("The
+ * Kimi K3 Architecture", hybrid backbone).  The pages use a compressed form of it; the calls
+ * below are the plain one with grouped heads.  For query head h, key head h / G of
+ * H_kv = H_q / G, token i of a sequence of L tokens whose last n are the call's, and
+ * scores s_ij = scale q_i . k_j over the keys j <= L - n + i:
+ *
+ *   lse_i = log sum_j e^(s_ij),   out_i = sum_j e^(s_ij - lse_i) v_j
+ *
+ * A token that sees no key (L < n) has out 0 and lse -inf.
+ *
+ * Conventions: activations are 16-bit (bf16 or fp16, one type a call), products are
+ * accumulated in fp32 on the tensor cores, maxima, sums and log-sums are fp32, and
+ * the weights e^(s - max) are rounded to the 16-bit type for the product with v.  Heads are
+ * given with strides (kda_heads), so that parts of a projection's rows need no copy.  Keys
+ * and values that a row may not see never reach it, whatever they hold, as long as
+ * they belong to another sequence or lie behind the cache's length; inside a sequence an
+ * infinity or a NaN in k or v reaches the tokens that see it and may reach up to 127
+ * tokens before it.  Rows of an output that belong to no sequence are left as they were.
+ * A malformed cu_seqlens, length or page table never causes an access out of bounds; what
+ * a call then writes to its outputs is unspecified.
+ * The calls allocate nothing and give the same bits every time; calls on different streams
+ * may overlap as long as they share no written buffer (workspace included); every call
+ * may be captured into a CUDA graph, whose replays use the buffers named at the capture.
+ */
+
+/* [T, H, head_dim] activations: head h of token t starts at data + t * token_stride +
+ * h * head_stride elements.  data 16-byte aligned, strides multiples of 8. */
+typedef struct {
+    const void *data;
+    int64_t token_stride, head_stride;
+} kda_heads;
+
+/* The same of a cache [num_pages, page_size, H_kv, head_dim]. */
+typedef struct {
+    const void *data;
+    int64_t page_stride, token_stride, head_stride;
+} kda_pages;
+
+typedef struct {
+    int32_t num_seqs;     /* N >= 0 */
+    int32_t total_tokens; /* T >= 0 */
+    int32_t q_heads;      /* H_q, a multiple of H_kv */
+    int32_t kv_heads;     /* H_kv >= 1 */
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t in_dtype;     /* KDA_DTYPE_BF16 or KDA_DTYPE_F16 */
+    int32_t out_dtype;    /* in_dtype or KDA_DTYPE_F32 */
+    float scale;          /* > 0 */
+} kda_attn_dims;
+
+typedef struct {
+    int32_t num_pages;    /* P >= 1 */
+    int32_t page_size;    /* tokens of a page: 8, 16, 32, ... 1024 */
+    int32_t max_pages;    /* pages of a sequence: the row length of the page table */
+} kda_cache_dims;
+
+/*
+ * kda_attn_prefill -- causal attention over the whole prompts of a packed batch.
+ *
+ *   q         heads [T, H_q, d];  k, v  heads [T, H_kv, d].
+ *   cu_seqlens device int32 [N+1], or NULL (N equal sequences), as in kda_prefill.
+ *   out       device, out_dtype [T, H_q, d], contiguous, 16-byte aligned.
+ *   lse       device fp32 [T, H_q] or NULL: what the gradients need.
+ */
+kda_status kda_attn_prefill(const kda_attn_dims *dims, const kda_heads *q, const kda_heads *k,
+                            const kda_heads *v, const int32_t *cu_seqlens, void *out, float *lse,
+                            kda_stream_t stream);
+
+/*
+ * kda_attn_paged -- attention of each sequence's new tokens over its pages of a cache, in
+ * which the new tokens' keys and values are already (kda_cache_append).  One token a
+ * sequence is the decode step; pieces of prompts and single tokens may be mixed.
+ *
+ *   q          heads [T, H_q, d] of the new tokens.
+ *   k_pages, v_pages  [P, page_size, H_kv, d].
+ *   page_table device int32 [N, max_pages]: page j of sequence n holds its tokens
+ *              j page_size ...; entries behind a sequence's last page are not read.  A
+ *              page number outside [0, P), or a length past the table, is recorded in the
+ *              device status word (kda_get_last_device_error then returns
+ *              KDA_ERR_INVALID_ARGUMENT); such keys and values read as zeros.
+ *   kv_lens    device int32 [N]: tokens in the cache, the new ones among them.
+ *   cu_seqlens device int32 [N+1] of the new tokens, or NULL (T / N each).
+ *   out, lse   as in kda_attn_prefill.
+ *   workspace  kda_attn_paged_workspace(dims, cache, cu_seqlens) bytes, 16-byte aligned
+ *              (of cu_seqlens it matters only whether it is NULL): shares of rows whose
+ *              keys are split over blocks, 21 MB for one token of 8 key heads of 128 channels.
+ */
+int64_t kda_attn_paged_workspace(const kda_attn_dims *dims, const kda_cache_dims *cache,
+                                 const int32_t *cu_seqlens);
+kda_status kda_attn_paged(const kda_attn_dims *dims, const kda_cache_dims *cache,
+                          const kda_heads *q, const kda_pages *k_pages, const kda_pages *v_pages,
+                          const int32_t *page_table, const int32_t *kv_lens,
+                          const int32_t *cu_seqlens, void *out, float *lse, void *workspace,
+                          int64_t workspace_bytes, kda_stream_t stream);
 
 /*
  * kda_get_last_device_error -- report, then clear, the device-side status.

@@ -26,6 +26,11 @@ packing of the activations their gradients read:
     kda_ssm_step(..., state)            one token, states in place
     kda_ssm_scan_backward(...)          gradients of the scan, from u and z or their 8-bit codes
     kda_act_pack8(x)                    an activation as int8 codes and scales
+
+Softmax attention, for the layers of a hybrid stack that keep it, and its paged cache:
+
+    kda_attn_prefill(q, k, v, ...)      causal attention over packed prompts, grouped heads
+    kda_attn_paged(q, k_pages, v_pages, page_table, kv_lens, ...)   new tokens over a paged cache
 """
 from __future__ import annotations
 
@@ -41,6 +46,7 @@ __all__ = ["KdaError", "kda_prefill", "kda_prefill_noalloc", "kda_prefill_checkp
            "kda_get_last_device_error", "kda_selftest_timeout",
            "kda_act_pack8", "kda_ssm_conv", "kda_ssm_conv_backward", "kda_ssm_scan",
            "kda_ssm_step", "kda_ssm_scan_backward", "PACK_GROUP",
+           "kda_attn_prefill", "kda_attn_paged",
            "PREFILL_DEFAULT", "PREFILL_FP32", "PREFILL_TC", "PREFILL_TC_SPLIT", "PREFILL_TC_2PASS", "Dims"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -111,6 +117,7 @@ def lib():
         L.kda_decode.argtypes = [ctypes.POINTER(Dims), vp, vp, vp, fp, fp, fp, vp, vp]
         L.kda_decode.restype = ctypes.c_int
         _declare_ssm(L)
+        _declare_attn(L)
         L.kda_status_string.argtypes = [ctypes.c_int]
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_last_cuda_error.restype = ctypes.c_char_p
@@ -492,3 +499,5 @@ def kda_decode(q, k, v, g, beta, state, *, out=None, out_dtype=None, stream=None
 from ._ssm import (PACK_GROUP, kda_act_pack8, kda_ssm_conv, kda_ssm_conv_backward,  # noqa: E402
                    kda_ssm_scan, kda_ssm_scan_backward, kda_ssm_step)
 from ._ssm import declare as _declare_ssm  # noqa: E402
+from ._attn import kda_attn_paged, kda_attn_prefill  # noqa: E402
+from ._attn import declare as _declare_attn  # noqa: E402

@@ -1,0 +1,159 @@
+"""Binding of the softmax attention calls (see ``include/kda.h``).  As in the rest of the
+package: pointers, sizes and checks, no arithmetic of the method and no fallback.
+
+In a packed batch with ``cu_seqlens``, rows that belong to no sequence (before its first
+entry, from its last one on) are not written: outputs allocated here hold whatever the
+memory held there."""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+import linear_attention_sequence_gb300 as _kda
+
+from ._ssm import _is, _on, _run, _sequences
+
+_vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+_F32, _I32 = torch.float32, torch.int32
+_TYPES = {torch.bfloat16: 1, torch.float16: 2}     # KDA_DTYPE_*
+_OUT_TYPES = {torch.float32: 0, **_TYPES}
+
+# The structures of include/kda.h as bytes (see _ssm.py).
+_HEADS = struct.Struct("Pqq")                      # data, token stride, head stride
+_PAGES = struct.Struct("Pqqq")                     # data, page, token, head stride
+_DIMS = struct.Struct("7if")                       # N, T, H_q, H_kv, d, in, out, scale
+_CACHE = struct.Struct("3i")                       # P, page_size, max_pages
+
+
+def declare(L):
+    """Argument types of the C entry points (structures go in as bytes)."""
+    for name, args in (("kda_attn_prefill", [_vp] * 8),
+                       ("kda_attn_paged", [_vp] * 11 + [_i64, _vp])):
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = ctypes.c_int
+    L.kda_attn_paged_workspace.argtypes = [_vp] * 3
+    L.kda_attn_paged_workspace.restype = _i64
+
+
+def _heads(t, name, dev, dtype, shape):
+    """The bytes of a [T, H, d] activation whose tokens and heads may lie strides apart."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev:
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    a, b, c = t.stride()
+    if c != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    T, H, d = shape
+    if T <= 1:
+        a = H * d
+    if H == 1:
+        b = d
+    if a % 8 or b % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned, in its strides too")
+    return _HEADS.pack(t.data_ptr(), a, b)
+
+
+def _pages(t, name, dev, dtype, shape):
+    """The bytes of a cache [P, page, H, d] with strides."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != dev:
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    s = list(t.stride())
+    if s[3] != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    for i in (2, 1, 0):
+        if shape[i] == 1:
+            s[i] = s[i + 1] * shape[i + 1]
+    if any(x % 8 for x in s[:3]) or t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned, in its strides too")
+    return _PAGES.pack(t.data_ptr(), *s[:3])
+
+
+def _query(q, kv_heads, N, scale, out_dtype):
+    """(device, T, H_q, d, type, dims) of a call with queries q [T, H_q, d]."""
+    if q.dim() != 3 or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor [T, H, d]")
+    code = _TYPES.get(q.dtype)
+    if code is None:
+        raise ValueError("q must be bf16 or fp16")
+    T, H, d = q.shape
+    out_code = _OUT_TYPES.get(out_dtype)
+    if out_code is None:
+        raise ValueError("out_dtype must be q's dtype or fp32")
+    if scale is None:
+        scale = d ** -0.5 if d else 1.0
+    return _DIMS.pack(N, T, H, kv_heads, d, code, out_code, scale)
+
+
+def kda_attn_prefill(q, k, v, cu_seqlens=None, *, num_seqs=None, scale=None, out=None, out_dtype=None,
+                     lse=None, return_lse=False, stream=None):
+    """Causal softmax attention over the whole prompts of a packed batch (C entry point
+    ``kda_attn_prefill``).
+
+    q [T, H, d], k and v [T, H_kv, d] in bf16 or fp16, d 64 or 128, H a multiple of H_kv;
+    tokens and heads may lie strides apart (multiples of 8 elements).  scale defaults
+    to d^-1/2.  Returns ``out`` [T, H, d] (``out_dtype``, default q's), and with
+    ``return_lse`` (or a buffer given) ``(out, lse)``, lse fp32 [T, H], which the gradients need."""
+    if k.dim() != 3:
+        raise ValueError("k must be [T, H, d]")
+    odt = out_dtype or q.dtype
+    dev = q.get_device()
+    N = _sequences(cu_seqlens, num_seqs, dev)
+    dims = _query(q, k.shape[1], N, scale, odt)
+    T, H, d = q.shape
+    kv = (T, k.shape[1], d)
+    rq, rk, rv = (_heads(q, "q", dev, q.dtype, (T, H, d)), _heads(k, "k", dev, q.dtype, kv),
+                  _heads(v, "v", dev, q.dtype, kv))
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, H, d), dtype=odt, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty((T, H), dtype=_F32, device=q.device)
+        _run("kda_attn_prefill", dev, dims, rq, rk, rv, 0 if cu_seqlens is None else cu_seqlens.data_ptr(),
+             _is(out, "out", dev, odt, (T, H, d)), _is(lse, "lse", dev, _F32, (T, H)))
+    return out if lse is None else (out, lse)
+
+
+def kda_attn_paged(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *, scale=None, out=None,
+                   out_dtype=None, lse=None, return_lse=False, stream=None):
+    """Attention of each sequence's new tokens over its pages of a cache, which holds their
+    keys and values already (C entry point ``kda_attn_paged``).
+
+    q [T, H, d] of the new tokens (bf16 or fp16, d 64 or 128); k_pages and v_pages
+    [P, page_size, H_kv, d] with strides (multiples of 8 elements), page_size a power of two
+    from 8 to 1024; page_table int32 [N, max_pages]; kv_lens int32 [N], the tokens in the
+    cache with the new ones; cu_seqlens int32 [N+1] of the new tokens, or None: T / N each
+    (T == N is the decode step).  Returns ``out`` [T, H, d], and with ``return_lse`` (or
+    a buffer given) ``(out, lse)``.  A token that sees no key has out 0 and lse -inf."""
+    if k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("k_pages must be [P, page_size, H, d] and page_table [N, max_pages]")
+    odt = out_dtype or q.dtype
+    dev = q.get_device()
+    N, wide = page_table.shape
+    if cu_seqlens is not None and _sequences(cu_seqlens, None, dev) != N:
+        raise ValueError("cu_seqlens must hold N + 1 entries")
+    P, page, Hkv, _ = k_pages.shape
+    dims, cache = _query(q, Hkv, N, scale, odt), _CACHE.pack(P, page, wide)
+    T, H, d = q.shape
+    kv = (P, page, Hkv, d)
+    rq, rk, rv = (_heads(q, "q", dev, q.dtype, (T, H, d)), _pages(k_pages, "k_pages", dev, q.dtype, kv),
+                  _pages(v_pages, "v_pages", dev, q.dtype, kv))
+    table = _is(page_table, "page_table", dev, _I32, (N, wide))
+    lens = _is(kv_lens, "kv_lens", dev, _I32, (N,))
+    cu = 0 if cu_seqlens is None else cu_seqlens.data_ptr()
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, H, d), dtype=odt, device=q.device)
+        if lse is None and return_lse:
+            lse = torch.empty((T, H), dtype=_F32, device=q.device)
+        n = _kda.lib().kda_attn_paged_workspace(dims, cache, cu)
+        if n < 0:
+            raise _kda.KdaError(2 if T else 1, "kda_attn_paged_workspace")
+        ws = torch.empty((n,), dtype=torch.uint8, device=q.device)
+        _run("kda_attn_paged", dev, dims, cache, rq, rk, rv, table, lens, cu,
+             _is(out, "out", dev, odt, (T, H, d)), _is(lse, "lse", dev, _F32, (T, H)), ws.data_ptr(), n)
+    return out if lse is None else (out, lse)

@@ -79,7 +79,7 @@ kda_status kda_get_last_device_error(kda_stream_t stream) {
     unsigned status = 0;
     cudaError_t e = kda_read_device_status((cudaStream_t)stream, &status);
     if (e != cudaSuccess) return cuda_fail(e, "kda_get_last_device_error");
-    if (status & kda::kBwdMissingState) return KDA_ERR_INVALID_ARGUMENT;
+    if (status & (kda::kBwdMissingState | kda::kCacheBadPage)) return KDA_ERR_INVALID_ARGUMENT;
     return status ? KDA_ERR_TIMEOUT : KDA_OK;
 }
 

@@ -1,0 +1,146 @@
+// kda_attn_plan.cuh -- which part of a packed batch a block works on.  The lengths are
+// known on the device only, so every block finds its own part: each thread counts the
+// parts of a run of sequences, and one scan over the block says whose run holds the
+// block's number.  A batch of 256 sequences costs a block about a microsecond.
+#pragma once
+
+#include "kda_attn_common.cuh"
+
+namespace kda {
+
+// One block's part of the work: query rows [tile * rows of a tile, ...) of sequence n
+// against key tiles [j0, j1); `slot`: where a share of a split row tile goes (-1: the part
+// is all of it).
+struct AttnPart {
+    int32_t n, tile, head, j0, j1, split, splits, slot;
+};
+
+// Exclusive sums over the block's threads; `total` of all.  Every thread calls it.
+template <int THREADS>
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t &total, int64_t *sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh[warp] = s;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += sh[w];
+        all += sh[w];
+    }
+    total = all;
+    return before + s - x;
+}
+
+// What a sequence needs: its row tiles and the key tiles of each (0 row tiles: none here).
+struct AttnNeed {
+    int32_t tiles, keys;
+};
+
+// Longest key run of a part, by the number of row tiles (times heads) and their key tiles.
+// Few row tiles: as many parts as `slots` blocks run at once, so that all run side by
+// side.  More: runs short enough that the last ones to finish do not matter.  Enough:
+// row tiles are not cut.
+__host__ __device__ inline int32_t attn_run(int64_t tiles, int64_t keys, int slots, int waves, int least) {
+    if (tiles >= (int64_t)slots * waves) return INT32_MAX;
+    const int64_t parts = tiles * 2 <= slots ? slots - tiles : (int64_t)slots * waves;
+    int64_t run = (keys + parts - 1) / parts;
+    if (run < least) run = least;
+    return run > INT32_MAX ? INT32_MAX : (int32_t)run;
+}
+// Upper bounds on the parts, and on those of them that are shares, of `tiles` row tiles at most.
+__host__ inline int64_t attn_parts(int64_t tiles, int slots, int waves) {
+    return tiles * 2 <= slots ? slots : tiles + (int64_t)slots * waves;
+}
+
+// Part number `index` of `heads` heads (head fastest), the block's work in shared memory.
+// `need(n)` gives what sequence n needs.  False: there is no such part.
+template <int THREADS, typename Need>
+__device__ __forceinline__ bool attn_split_part(int N, int heads, int64_t index, int slots, int waves, int least,
+                                                Need need, AttnPart *part, int64_t *sh, int64_t *all_slots) {
+    const int per = (N + THREADS - 1) / THREADS;
+    const int lo = (int)threadIdx.x * per, hi = min(N, lo + per);
+    int64_t tiles = 0, keys = 0, total_tiles, total_keys;
+    for (int n = lo; n < hi; ++n) {
+        const AttnNeed x = need(n);
+        tiles += x.tiles;
+        keys += (int64_t)x.tiles * x.keys;
+    }
+    block_scan<THREADS>(tiles, total_tiles, sh);
+    block_scan<THREADS>(keys, total_keys, sh);
+    const int32_t run = attn_run(total_tiles * heads, total_keys * heads, slots, waves, least);
+    int64_t parts = 0, shares = 0, total_parts, total_shares;
+    for (int n = lo; n < hi; ++n) {
+        const AttnNeed x = need(n);
+        const int64_t splits = x.keys > run ? (x.keys + run - 1) / run : 1;
+        parts += x.tiles * splits;
+        if (splits > 1) shares += x.tiles * splits;
+    }
+    int64_t before = block_scan<THREADS>(parts, total_parts, sh);
+    int64_t shares_before = block_scan<THREADS>(shares, total_shares, sh);
+    *all_slots = total_shares * heads;
+    if (index >= total_parts * heads) return false;
+    const int64_t at = index / heads;
+    if (at >= before && at < before + parts) {
+        for (int n = lo; n < hi; ++n) {
+            const AttnNeed x = need(n);
+            const int64_t splits = x.keys > run ? (x.keys + run - 1) / run : 1;
+            if (at < before + x.tiles * splits) {
+                const int32_t in = (int32_t)(at - before);
+                part->n = n;
+                part->head = (int32_t)(index % heads);
+                part->tile = (int32_t)(in / splits);
+                part->split = (int32_t)(in % splits);
+                part->splits = (int32_t)splits;
+                part->j0 = splits > 1 ? part->split * run : 0;
+                part->j1 = splits > 1 ? min(x.keys, part->j0 + run) : x.keys;
+                part->slot = splits > 1 ? (int32_t)((shares_before + in / splits * splits) * heads +
+                                                    (int64_t)part->head * splits + part->split)
+                                        : -1;
+                break;
+            }
+            before += x.tiles * splits;
+            if (splits > 1) shares_before += x.tiles * splits;
+        }
+    }
+    __syncthreads();
+    return true;
+}
+
+// Row tile number `index` from the last to the first (the later tiles of a causal sequence
+// see more keys and so start first).
+template <int THREADS, typename Tiles>
+__device__ __forceinline__ bool attn_whole_part(int N, int heads, int64_t index, Tiles tiles_of, AttnPart *part,
+                                                int64_t *sh) {
+    const int per = (N + THREADS - 1) / THREADS;
+    const int lo = (int)threadIdx.x * per, hi = min(N, lo + per);
+    int64_t tiles = 0, total;
+    for (int n = lo; n < hi; ++n) tiles += tiles_of(n);
+    int64_t before = block_scan<THREADS>(tiles, total, sh);
+    if (index >= total * heads) return false;
+    const int64_t at = total - 1 - index / heads;
+    if (at >= before && at < before + tiles) {
+        for (int n = lo; n < hi; ++n) {
+            const int64_t x = tiles_of(n);
+            if (at < before + x) {
+                part->n = n;
+                part->head = (int32_t)(index % heads);
+                part->tile = (int32_t)(at - before);
+                part->slot = -1;
+                part->splits = 1;
+                break;
+            }
+            before += x;
+        }
+    }
+    __syncthreads();
+    return true;
+}
+
+}  // namespace kda

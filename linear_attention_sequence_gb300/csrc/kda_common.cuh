@@ -37,6 +37,8 @@ __host__ __device__ __forceinline__ void seq_bounds(const int32_t *cu, int n, in
 // backward's missing chunk-state rows); the other bits are bounded waits that
 // gave up.
 constexpr unsigned kBwdMissingState = 0x1000u;
+// The same of the cache calls: a page number outside the cache, or a length past the table.
+constexpr unsigned kCacheBadPage = 0x2000u;
 
 // Host-side launch parameters after validation.
 struct Problem {
@@ -169,6 +171,7 @@ cudaError_t kda_launch_backward_tc(const kda::Problem &P, const void *q, const v
                                    void *dv, float *dg, float *dbeta, float *d_init,
                                    cudaStream_t stream);
 cudaError_t kda_bwdtc_read_status(unsigned *status);
+cudaError_t kda_attn_read_status(unsigned *status);
 bool kda_prefill_noalloc_fits(const kda::Problem &P, const void *q, const void *k, const void *v,
                               const float *g, const void *out);
 cudaError_t kda_launch_prefill_noalloc(const kda::Problem &P, const void *q, const void *k,
