@@ -705,6 +705,110 @@ kda_status kda_attn_paged(const kda_attn_dims *dims, const kda_cache_dims *cache
                           const int32_t *cu_seqlens, void *out, float *lse, void *workspace,
                           int64_t workspace_bytes, kda_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The pages of a cache
+ * ---------------------------------------------------------------------------
+ * A cache is, on the device: pages of keys and values (one pair of tensors a layer), and
+ * for all layers together
+ *
+ *   page_refs  int32 [P]: how many table entries name a page; 0: it is free.
+ *   page_table int32 [N, max_pages]: the pages of each sequence, -1 behind the last.
+ *   kv_lens    int32 [N]: tokens of each sequence (0: the row is empty).
+ *
+ * An empty cache is page_refs 0, page_table -1, kv_lens 0.  The calls keep this state; none
+ * waits for the host, and what they decide follows from the state alone: free pages are
+ * given out lowest number first, to the sequences (or children) in their order.  A last
+ * page that is not full belongs to one sequence only (kda_cache_fork copies it), so that
+ * kda_cache_append never writes into a shared page.  A sequence or page number out of range
+ * is passed by and recorded in the device status word (kda_get_last_device_error then
+ * returns KDA_ERR_INVALID_ARGUMENT).  Conventions as in the softmax attention calls.
+ */
+
+/* Bytes of the workspace of kda_cache_reserve, kda_cache_fork and kda_cache_compact (16-byte
+ * aligned): a number a page.  -1 for dims that the calls refuse. */
+int64_t kda_cache_workspace(const kda_cache_dims *cache);
+
+/*
+ * kda_cache_reserve -- pages for new tokens: kv_lens[n] grows by new_lens[n] (int32 [N], < 0
+ * counts as 0) and the table by the pages that the new length needs.  A sequence gets all
+ * of its pages or none: once they run out, those in front have theirs and every later
+ * one that needs a page keeps its old length, as does one whose row in the table is too
+ * short.
+ *
+ *   missing    int32 [1] or NULL: pages that were lacking (0: all were served; short rows
+ *              are not counted).
+ */
+kda_status kda_cache_reserve(const kda_cache_dims *cache, int32_t num_seqs, int32_t *page_refs,
+                             int32_t *page_table, int32_t *kv_lens, const int32_t *new_lens,
+                             int32_t *missing, void *workspace, int64_t workspace_bytes,
+                             kda_stream_t stream);
+
+/*
+ * kda_cache_append -- writes the new tokens' keys and values into one layer's pages: of the
+ * n new tokens of a sequence, token i goes to place kv_lens - n + i (kv_lens counts them
+ * already; places below 0 are passed by).
+ *
+ *   k, v       heads [T, H_kv, d], bf16 or fp16 (16-bit elements are moved as they are);
+ *              head_dim a multiple of 8.
+ *   k_pages, v_pages  [P, page_size, H_kv, d], each element of its own.
+ *   cu_seqlens int32 [N+1] of the new tokens, or NULL (T / N each).
+ */
+kda_status kda_cache_append(const kda_cache_dims *cache, int32_t num_seqs, int32_t total_tokens,
+                            int32_t kv_heads, int32_t head_dim, const kda_heads *k,
+                            const kda_heads *v, const kda_pages *k_pages, const kda_pages *v_pages,
+                            const int32_t *page_table, const int32_t *kv_lens,
+                            const int32_t *cu_seqlens, kda_stream_t stream);
+
+/*
+ * kda_cache_free -- gives pages back: of each of `count` sequences (seqs, int32) the first
+ * keep tokens stay (int32 [count], < 0 counts as 0; NULL: none), its length becomes that if it was
+ * more, and the pages behind are freed unless another sequence shares them.  A sequence may be
+ * listed more than once: the smallest keep holds.
+ */
+kda_status kda_cache_free(const kda_cache_dims *cache, int32_t num_seqs, int32_t *page_refs,
+                          int32_t *page_table, int32_t *kv_lens, int32_t count,
+                          const int32_t *seqs, const int32_t *keep, kda_stream_t stream);
+
+/*
+ * kda_cache_fork -- children[i] becomes a continuation of parents[i], i < count: it shares the
+ * parent's full pages, and has a page of its own where the last is not full.  The children
+ * are empty rows, all different, and none of them a parent; a parent may have many.  A
+ * child for which no page is left stays empty, as does every later one that needs a page.
+ *
+ *   src, dst   int32 [count]: for every layer, page src[i] is to be copied to dst[i]
+ *              (kda_cache_copy); -1 where there is nothing to copy.
+ *   missing    int32 [1] or NULL: pages that were lacking.
+ */
+kda_status kda_cache_fork(const kda_cache_dims *cache, int32_t num_seqs, int32_t *page_refs,
+                          int32_t *page_table, int32_t *kv_lens, int32_t count,
+                          const int32_t *parents, const int32_t *children, int32_t *src,
+                          int32_t *dst, int32_t *missing, void *workspace, int64_t workspace_bytes,
+                          kda_stream_t stream);
+
+/*
+ * kda_cache_compact -- renumbers the pages so that the L in use are 0 .. L-1: those from L on
+ * move, lowest first, to the free numbers below L, lowest first.
+ *
+ *   refs_out, table_out  as page_refs and page_table; may be page_refs and page_table themselves.
+ *   src, dst   int32 [P]: for every layer, page src[i] is to be copied to dst[i]
+ *              (kda_cache_copy); -1 from the number of moved pages on.
+ */
+kda_status kda_cache_compact(const kda_cache_dims *cache, int32_t num_seqs,
+                             const int32_t *page_refs, const int32_t *page_table,
+                             const int32_t *kv_lens, int32_t *refs_out, int32_t *table_out,
+                             int32_t *src, int32_t *dst, void *workspace, int64_t workspace_bytes,
+                             kda_stream_t stream);
+
+/*
+ * kda_cache_copy -- page dst[i] of one layer's keys and values becomes a copy of page src[i]
+ * (int32 [count]; an entry with a number below 0 is passed by).  No page may be both copied
+ * from and to, or be copied to twice, in one call: what such a page then holds is unspecified.
+ * The lists of kda_cache_fork and kda_cache_compact keep to that.
+ */
+kda_status kda_cache_copy(const kda_cache_dims *cache, int32_t kv_heads, int32_t head_dim,
+                          const kda_pages *k_pages, const kda_pages *v_pages, int32_t count,
+                          const int32_t *src, const int32_t *dst, kda_stream_t stream);
+
 /*
  * kda_get_last_device_error -- report, then clear, the device-side status.
  *

@@ -31,6 +31,9 @@ Softmax attention, for the layers of a hybrid stack that keep it, and its paged 
 
     kda_attn_prefill(q, k, v, ...)      causal attention over packed prompts, grouped heads
     kda_attn_paged(q, k_pages, v_pages, page_table, kv_lens, ...)   new tokens over a paged cache
+    kda_cache_reserve / _append         pages for new tokens; their keys and values into them
+    kda_cache_fork / _free              continuations that share a prompt's pages; pages back
+    kda_cache_compact / _copy           the pages in use moved together; one layer's pages copied
 """
 from __future__ import annotations
 
@@ -47,6 +50,8 @@ __all__ = ["KdaError", "kda_prefill", "kda_prefill_noalloc", "kda_prefill_checkp
            "kda_act_pack8", "kda_ssm_conv", "kda_ssm_conv_backward", "kda_ssm_scan",
            "kda_ssm_step", "kda_ssm_scan_backward", "PACK_GROUP",
            "kda_attn_prefill", "kda_attn_paged",
+           "kda_cache_reserve", "kda_cache_append", "kda_cache_free", "kda_cache_fork", "kda_cache_compact",
+           "kda_cache_copy",
            "PREFILL_DEFAULT", "PREFILL_FP32", "PREFILL_TC", "PREFILL_TC_SPLIT", "PREFILL_TC_2PASS", "Dims"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -118,6 +123,7 @@ def lib():
         L.kda_decode.restype = ctypes.c_int
         _declare_ssm(L)
         _declare_attn(L)
+        _declare_cache(L)
         L.kda_status_string.argtypes = [ctypes.c_int]
         L.kda_status_string.restype = ctypes.c_char_p
         L.kda_last_cuda_error.restype = ctypes.c_char_p
@@ -501,3 +507,6 @@ from ._ssm import (PACK_GROUP, kda_act_pack8, kda_ssm_conv, kda_ssm_conv_backwar
 from ._ssm import declare as _declare_ssm  # noqa: E402
 from ._attn import kda_attn_paged, kda_attn_prefill  # noqa: E402
 from ._attn import declare as _declare_attn  # noqa: E402
+from ._cache import (kda_cache_append, kda_cache_compact, kda_cache_copy, kda_cache_fork,  # noqa: E402
+                     kda_cache_free, kda_cache_reserve)
+from ._cache import declare as _declare_cache  # noqa: E402

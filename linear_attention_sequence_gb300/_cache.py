@@ -1,0 +1,166 @@
+"""Binding of the calls on the pages of a cache (see ``include/kda.h``).  As in the rest of
+the package: pointers, sizes and checks, no arithmetic of the method and no fallback.
+
+The state of a cache is three int32 tensors on the device, kept by the caller and written
+in place: ``page_refs`` [P] (0: free), ``page_table`` [N, max_pages] (-1: none) and ``kv_lens``
+[N].  An empty cache is zeros, -1 and zeros.  No call waits for the host."""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+import linear_attention_sequence_gb300 as _kda
+
+from ._attn import _CACHE, _TYPES, _heads, _pages
+from ._ssm import _is, _on, _run, _sequences
+
+_vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+_I32 = torch.int32
+
+
+def declare(L):
+    """Argument types of the C entry points (structures go in as bytes)."""
+    for name, args in (("kda_cache_reserve", [_vp, _i32] + [_vp] * 6 + [_i64, _vp]),
+                       ("kda_cache_append", [_vp] + [_i32] * 4 + [_vp] * 8),
+                       ("kda_cache_free", [_vp, _i32] + [_vp] * 3 + [_i32] + [_vp] * 3),
+                       ("kda_cache_fork", [_vp, _i32] + [_vp] * 3 + [_i32] + [_vp] * 6 + [_i64, _vp]),
+                       ("kda_cache_compact", [_vp, _i32] + [_vp] * 8 + [_i64, _vp]),
+                       ("kda_cache_copy", [_vp] + [_i32] * 2 + [_vp] * 2 + [_i32] + [_vp] * 3)):
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = ctypes.c_int
+    L.kda_cache_workspace.argtypes = [_vp]
+    L.kda_cache_workspace.restype = _i64
+
+
+def _state(page_refs, page_table, kv_lens, page_size):
+    """(device, N, cache dims, addresses of refs, table and lens) of a cache's state."""
+    if page_refs is None or not page_refs.is_cuda or page_refs.dim() != 1:
+        raise ValueError("page_refs must be a CUDA tensor [P]")
+    if page_table is None or page_table.dim() != 2:
+        raise ValueError("page_table must be [N, max_pages]")
+    dev = page_refs.get_device()
+    N, wide = page_table.shape
+    P = page_refs.shape[0]
+    return (dev, N, _CACHE.pack(P, page_size, wide), _is(page_refs, "page_refs", dev, _I32, (P,)),
+            _is(page_table, "page_table", dev, _I32, (N, wide)), _is(kv_lens, "kv_lens", dev, _I32, (N,)))
+
+
+def _scratch(cache, device):
+    n = _kda.lib().kda_cache_workspace(cache)
+    if n < 0:
+        raise _kda.KdaError(2, "kda_cache_workspace")
+    return torch.empty((n,), dtype=torch.uint8, device=device), n
+
+
+def _layer(k_pages, v_pages):
+    """(device, P, page size, H, d, bytes of both) of one layer's pages."""
+    if k_pages.dim() != 4 or not k_pages.is_cuda:
+        raise ValueError("k_pages must be a CUDA tensor [P, page_size, H, d]")
+    if k_pages.dtype not in _TYPES:
+        raise ValueError("k_pages must be bf16 or fp16")
+    dev, shape = k_pages.get_device(), k_pages.shape
+    return (dev, *shape, _pages(k_pages, "k_pages", dev, k_pages.dtype, shape),
+            _pages(v_pages, "v_pages", dev, k_pages.dtype, shape))
+
+
+def kda_cache_reserve(page_refs, page_table, kv_lens, new_lens, page_size, *, missing=None, stream=None):
+    """Pages for ``new_lens`` (int32 [N]) more tokens of each sequence, in place (C entry point
+    ``kda_cache_reserve``): kv_lens grows and the table gets the lowest free pages, for the
+    sequences in their order; one that cannot have all of its pages keeps its length.
+    ``missing`` (int32 [1] or None) gets the number of pages that were lacking."""
+    dev, N, cache, refs, table, lens = _state(page_refs, page_table, kv_lens, page_size)
+    new = _is(new_lens, "new_lens", dev, _I32, (N,))
+    lacking = _is(missing, "missing", dev, _I32, (1,))
+    with _on(dev, stream):
+        ws, n = _scratch(cache, page_refs.device)
+        _run("kda_cache_reserve", dev, cache, N, refs, table, lens, new, lacking, ws.data_ptr(), n)
+
+
+def kda_cache_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *, stream=None):
+    """Writes the new tokens' k and v [T, H, d] into one layer's pages [P, page_size, H, d] (C
+    entry point ``kda_cache_append``): of the n new tokens of a sequence, token i goes to place
+    kv_lens - n + i, so that kda_cache_reserve comes first.  cu_seqlens int32 [N+1] of the new
+    tokens, or None: T / N each."""
+    dev, P, page, H, d, kp, vp = _layer(k_pages, v_pages)
+    if page_table.dim() != 2 or k.dim() != 3:
+        raise ValueError("page_table must be [N, max_pages] and k [T, H, d]")
+    N, wide = page_table.shape
+    if cu_seqlens is not None and _sequences(cu_seqlens, None, dev) != N:
+        raise ValueError("cu_seqlens must hold N + 1 entries")
+    T = k.shape[0]
+    rk, rv = (_heads(x, name, dev, k_pages.dtype, (T, H, d)) for x, name in ((k, "k"), (v, "v")))
+    table = _is(page_table, "page_table", dev, _I32, (N, wide))
+    lens = _is(kv_lens, "kv_lens", dev, _I32, (N,))
+    with _on(dev, stream):
+        _run("kda_cache_append", dev, _CACHE.pack(P, page, wide), N, T, H, d, rk, rv, kp, vp, table, lens,
+             0 if cu_seqlens is None else cu_seqlens.data_ptr())
+
+
+def kda_cache_free(page_refs, page_table, kv_lens, seqs, page_size, *, keep=None, stream=None):
+    """Gives pages back, in place (C entry point ``kda_cache_free``): of each sequence in ``seqs``
+    (int32 [M]) the first ``keep`` tokens stay (int32 [M]; None: none of them); the pages
+    behind are free unless another sequence shares them."""
+    dev, N, cache, refs, table, lens = _state(page_refs, page_table, kv_lens, page_size)
+    if seqs is None or seqs.dim() != 1:
+        raise ValueError("seqs must be [M]")
+    M = seqs.shape[0]
+    with _on(dev, stream):
+        _run("kda_cache_free", dev, cache, N, refs, table, lens, M, _is(seqs, "seqs", dev, _I32, (M,)),
+             _is(keep, "keep", dev, _I32, (M,)))
+
+
+def kda_cache_fork(page_refs, page_table, kv_lens, parents, children, page_size, *, src=None, dst=None,
+                   missing=None, stream=None):
+    """children[i] (an empty row) becomes a continuation of parents[i] (both int32 [M]), in place
+    (C entry point ``kda_cache_fork``): it shares the parent's full pages and has one of its
+    own where the last is not full.  Returns ``(src, dst)``, int32 [M]: the pages to copy with
+    kda_cache_copy in every layer (-1: none)."""
+    dev, N, cache, refs, table, lens = _state(page_refs, page_table, kv_lens, page_size)
+    if parents is None or parents.dim() != 1:
+        raise ValueError("parents must be [M]")
+    M = parents.shape[0]
+    p, c = _is(parents, "parents", dev, _I32, (M,)), _is(children, "children", dev, _I32, (M,))
+    lacking = _is(missing, "missing", dev, _I32, (1,))
+    with _on(dev, stream):
+        if src is None:
+            src = torch.empty((M,), dtype=_I32, device=page_refs.device)
+        if dst is None:
+            dst = torch.empty((M,), dtype=_I32, device=page_refs.device)
+        ws, n = _scratch(cache, page_refs.device)
+        _run("kda_cache_fork", dev, cache, N, refs, table, lens, M, p, c, _is(src, "src", dev, _I32, (M,)),
+             _is(dst, "dst", dev, _I32, (M,)), lacking, ws.data_ptr(), n)
+    return src, dst
+
+
+def kda_cache_compact(page_refs, page_table, kv_lens, page_size, *, refs_out=None, table_out=None, src=None,
+                      dst=None, stream=None):
+    """Renumbers the pages so that those in use come first (C entry point ``kda_cache_compact``).
+    Returns ``(refs_out, table_out, src, dst)``: the new counts and table (new tensors unless
+    given; page_refs and page_table themselves may be given), and int32 [P] lists of the pages to
+    copy with kda_cache_copy in every layer (-1: none)."""
+    dev, N, cache, refs, table, lens = _state(page_refs, page_table, kv_lens, page_size)
+    P, shape = page_refs.shape[0], tuple(page_table.shape)
+    with _on(dev, stream):
+        def new(given, shape):
+            return torch.empty(shape, dtype=_I32, device=page_refs.device) if given is None else given
+
+        refs_out, table_out = new(refs_out, (P,)), new(table_out, shape)
+        src, dst = new(src, (P,)), new(dst, (P,))
+        ws, n = _scratch(cache, page_refs.device)
+        _run("kda_cache_compact", dev, cache, N, refs, table, lens, _is(refs_out, "refs_out", dev, _I32, (P,)),
+             _is(table_out, "table_out", dev, _I32, shape), _is(src, "src", dev, _I32, (P,)),
+             _is(dst, "dst", dev, _I32, (P,)), ws.data_ptr(), n)
+    return refs_out, table_out, src, dst
+
+
+def kda_cache_copy(k_pages, v_pages, src, dst, *, stream=None):
+    """Page dst[i] of one layer's keys and values becomes a copy of page src[i] (int32 [M]; -1: no
+    copy) (C entry point ``kda_cache_copy``)."""
+    dev, P, page, H, d, kp, vp = _layer(k_pages, v_pages)
+    if src is None or src.dim() != 1:
+        raise ValueError("src must be [M]")
+    M = src.shape[0]
+    with _on(dev, stream):
+        _run("kda_cache_copy", dev, _CACHE.pack(P, page, 1), H, d, kp, vp, M, _is(src, "src", dev, _I32, (M,)),
+             _is(dst, "dst", dev, _I32, (M,)))
