@@ -679,6 +679,29 @@ kda_status kda_attn_prefill(const kda_attn_dims *dims, const kda_heads *q, const
                             kda_stream_t stream);
 
 /*
+ * kda_attn_backward -- gradients of kda_attn_prefill for d_out = dL/d out: with
+ * P = e^(s - lse), delta_i = d_out_i . out_i and dS_ij = P_ij (d_out_i . v_j - delta_i),
+ *
+ *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij d_out_i
+ *
+ * (the sums of dk and dv over the query heads of the group too).  P and dS are rounded to the
+ * 16-bit type for the products, sums are fp32, and none depends on timing.
+ *
+ *   out, lse   the forward's (out in in_dtype, heads [T, H_q, d]; lse fp32 [T, H_q]).
+ *   d_out      in_dtype, heads [T, H_q, d].
+ *   dq, dk, dv device, out_dtype, contiguous [T, H_q, d], [T, H_kv, d], [T, H_kv, d], 16-byte
+ *              aligned.
+ *   workspace  kda_attn_backward_workspace(dims) bytes, 16-byte aligned: two floats a token
+ *              and query head.
+ */
+int64_t kda_attn_backward_workspace(const kda_attn_dims *dims);
+kda_status kda_attn_backward(const kda_attn_dims *dims, const kda_heads *q, const kda_heads *k,
+                             const kda_heads *v, const kda_heads *out, const float *lse,
+                             const kda_heads *d_out, const int32_t *cu_seqlens, void *dq, void *dk,
+                             void *dv, void *workspace, int64_t workspace_bytes,
+                             kda_stream_t stream);
+
+/*
  * kda_attn_paged -- attention of each sequence's new tokens over its pages of a cache, in
  * which the new tokens' keys and values are already (kda_cache_append).  One token a
  * sequence is the decode step; pieces of prompts and single tokens may be mixed.

@@ -30,6 +30,7 @@ packing of the activations their gradients read:
 Softmax attention, for the layers of a hybrid stack that keep it, and its paged cache:
 
     kda_attn_prefill(q, k, v, ...)      causal attention over packed prompts, grouped heads
+    kda_attn_backward(q, k, v, out, lse, d_out, ...)   its gradients
     kda_attn_paged(q, k_pages, v_pages, page_table, kv_lens, ...)   new tokens over a paged cache
     kda_cache_reserve / _append         pages for new tokens; their keys and values into them
     kda_cache_fork / _free              continuations that share a prompt's pages; pages back
@@ -49,7 +50,7 @@ __all__ = ["KdaError", "kda_prefill", "kda_prefill_noalloc", "kda_prefill_checkp
            "kda_get_last_device_error", "kda_selftest_timeout",
            "kda_act_pack8", "kda_ssm_conv", "kda_ssm_conv_backward", "kda_ssm_scan",
            "kda_ssm_step", "kda_ssm_scan_backward", "PACK_GROUP",
-           "kda_attn_prefill", "kda_attn_paged",
+           "kda_attn_prefill", "kda_attn_backward", "kda_attn_paged",
            "kda_cache_reserve", "kda_cache_append", "kda_cache_free", "kda_cache_fork", "kda_cache_compact",
            "kda_cache_copy",
            "PREFILL_DEFAULT", "PREFILL_FP32", "PREFILL_TC", "PREFILL_TC_SPLIT", "PREFILL_TC_2PASS", "Dims"]
@@ -505,7 +506,7 @@ def kda_decode(q, k, v, g, beta, state, *, out=None, out_dtype=None, stream=None
 from ._ssm import (PACK_GROUP, kda_act_pack8, kda_ssm_conv, kda_ssm_conv_backward,  # noqa: E402
                    kda_ssm_scan, kda_ssm_scan_backward, kda_ssm_step)
 from ._ssm import declare as _declare_ssm  # noqa: E402
-from ._attn import kda_attn_paged, kda_attn_prefill  # noqa: E402
+from ._attn import kda_attn_backward, kda_attn_paged, kda_attn_prefill  # noqa: E402
 from ._attn import declare as _declare_attn  # noqa: E402
 from ._cache import (kda_cache_append, kda_cache_compact, kda_cache_copy, kda_cache_fork,  # noqa: E402
                      kda_cache_free, kda_cache_reserve)

@@ -13,7 +13,7 @@ import torch
 
 import linear_attention_sequence_gb300 as _kda
 
-from ._ssm import _is, _on, _run, _sequences
+from ._ssm import _is, _on, _run, _sequences, _workspace
 
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 _F32, _I32 = torch.float32, torch.int32
@@ -30,11 +30,14 @@ _CACHE = struct.Struct("3i")                       # P, page_size, max_pages
 def declare(L):
     """Argument types of the C entry points (structures go in as bytes)."""
     for name, args in (("kda_attn_prefill", [_vp] * 8),
+                       ("kda_attn_backward", [_vp] * 12 + [_i64, _vp]),
                        ("kda_attn_paged", [_vp] * 11 + [_i64, _vp])):
         getattr(L, name).argtypes = args
         getattr(L, name).restype = ctypes.c_int
     L.kda_attn_paged_workspace.argtypes = [_vp] * 3
     L.kda_attn_paged_workspace.restype = _i64
+    L.kda_attn_backward_workspace.argtypes = [_vp]
+    L.kda_attn_backward_workspace.restype = _i64
 
 
 def _heads(t, name, dev, dtype, shape):
@@ -116,6 +119,36 @@ def kda_attn_prefill(q, k, v, cu_seqlens=None, *, num_seqs=None, scale=None, out
         _run("kda_attn_prefill", dev, dims, rq, rk, rv, 0 if cu_seqlens is None else cu_seqlens.data_ptr(),
              _is(out, "out", dev, odt, (T, H, d)), _is(lse, "lse", dev, _F32, (T, H)))
     return out if lse is None else (out, lse)
+
+
+def kda_attn_backward(q, k, v, out, lse, d_out, cu_seqlens=None, *, num_seqs=None, scale=None,
+                      grad_dtype=None, dq=None, dk=None, dv=None, stream=None):
+    """Gradients of kda_attn_prefill (C entry point ``kda_attn_backward``) for d_out [T, H, d].
+
+    q, k, v, cu_seqlens and scale as in the forward call, out (in q's dtype) and lse its results;
+    all activations may have strides.  Returns a dict with dq, dk and dv (``grad_dtype``,
+    default q's dtype)."""
+    if k.dim() != 3 or out is None or lse is None or d_out is None:
+        raise ValueError("k must be [T, H, d]; out, lse and d_out are needed")
+    gdt = grad_dtype or q.dtype
+    dev = q.get_device()
+    N = _sequences(cu_seqlens, num_seqs, dev)
+    dims = _query(q, k.shape[1], N, scale, gdt)
+    T, H, d = q.shape
+    own, kv = (T, H, d), (T, k.shape[1], d)
+    rq, ro, ry = (_heads(x, n, dev, q.dtype, own) for x, n in ((q, "q"), (out, "out"), (d_out, "d_out")))
+    rk, rv = (_heads(x, n, dev, q.dtype, kv) for x, n in ((k, "k"), (v, "v")))
+    sums = _is(lse, "lse", dev, _F32, (T, H))
+    with _on(dev, stream):
+        def new(given, shape):
+            return torch.empty(shape, dtype=gdt, device=q.device) if given is None else given
+
+        dq, dk, dv = new(dq, own), new(dk, kv), new(dv, kv)
+        ws = _workspace("kda_attn_backward_workspace", dims, q.device)
+        _run("kda_attn_backward", dev, dims, rq, rk, rv, ro, sums, ry,
+             0 if cu_seqlens is None else cu_seqlens.data_ptr(), _is(dq, "dq", dev, gdt, own),
+             _is(dk, "dk", dev, gdt, kv), _is(dv, "dv", dev, gdt, kv), ws.data_ptr(), ws.shape[0])
+    return dict(dq=dq, dk=dk, dv=dv)
 
 
 def kda_attn_paged(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *, scale=None, out=None,

@@ -132,6 +132,44 @@ kda_status kda_attn_prefill(const kda_attn_dims *dims, const kda_heads *q, const
     return e == cudaSuccess ? KDA_OK : kda_cuda_fail(e, "kda_attn_prefill");
 }
 
+int64_t kda_attn_backward_workspace(const kda_attn_dims *dims) {
+    Attn A;
+    if (check_dims(dims, A) != KDA_OK) return -1;
+    return kda_attn_backward_ws(A);
+}
+
+kda_status kda_attn_backward(const kda_attn_dims *dims, const kda_heads *q, const kda_heads *k, const kda_heads *v,
+                             const kda_heads *out, const float *lse, const kda_heads *d_out, const int32_t *cu_seqlens,
+                             void *dq, void *dk, void *dv, void *workspace, int64_t workspace_bytes,
+                             kda_stream_t stream) {
+    Attn A;
+    kda_status st = check_dims(dims, A);
+    if (st == KDA_OK) st = check_lengths(A, cu_seqlens);
+    if (st != KDA_OK) return st;
+    if (A.T == 0 || A.N == 0) return KDA_OK;
+    if (bad_heads(q, A.T, A.Hq, A.d) || bad_heads(k, A.T, A.Hkv, A.d) || bad_heads(v, A.T, A.Hkv, A.d) ||
+        bad_heads(out, A.T, A.Hq, A.d) || bad_heads(d_out, A.T, A.Hq, A.d) || !lse || misaligned(lse, 4))
+        return KDA_ERR_INVALID_ARGUMENT;
+    for (const void *p : {(const void *)dq, (const void *)dk, (const void *)dv})
+        if (!p || misaligned(p, 16)) return KDA_ERR_INVALID_ARGUMENT;
+    const int64_t need = kda_attn_backward_ws(A);
+    if (workspace_bytes < need || !workspace || misaligned(workspace, 16)) return KDA_ERR_INVALID_ARGUMENT;
+    const size_t rows = (size_t)A.T * A.Hq, nq = rows * A.d * osize(A), nk = (size_t)A.T * A.Hkv * A.d * osize(A);
+    if (conflict({{dq, nq}, {dk, nk}, {dv, nk}, {workspace, (size_t)need}},
+                 {span_of(q, A.T, A.Hq, A.d), span_of(k, A.T, A.Hkv, A.d), span_of(v, A.T, A.Hkv, A.d),
+                  span_of(out, A.T, A.Hq, A.d), span_of(d_out, A.T, A.Hq, A.d), {lse, rows * 4},
+                  {cu_seqlens, cu_bytes(A)}}))
+        return KDA_ERR_INVALID_ARGUMENT;
+    A.q = q->data, A.q_t = q->token_stride, A.q_h = q->head_stride;
+    A.k = k->data, A.k_t = k->token_stride, A.k_h = k->head_stride;
+    A.v = v->data, A.v_t = v->token_stride, A.v_h = v->head_stride;
+    A.lse = const_cast<float *>(lse);
+    const kda::AttnGrads X{out->data, d_out->data, out->token_stride, out->head_stride, d_out->token_stride,
+                           d_out->head_stride, dq, dk, dv};
+    cudaError_t e = kda_launch_attn_backward(A, X, (float *)workspace, (cudaStream_t)stream);
+    return e == cudaSuccess ? KDA_OK : kda_cuda_fail(e, "kda_attn_backward");
+}
+
 static kda_status check_paged(const kda_attn_dims *dims, const kda_cache_dims *cache, const int32_t *cu_seqlens, Attn &A) {
     kda_status st = check_dims(dims, A);
     if (st == KDA_OK) st = check_lengths(A, cu_seqlens);

@@ -1,0 +1,558 @@
+// kda_attn_bwd.cu -- gradients of causal softmax attention over packed prompts
+// (kda_attn_backward) on the tensor cores (sm_103a).
+//
+//   P = e^(scale Q K^T - lse),  dP = dO V^T,  delta = rowsum(dO O),  dS = P (dP - delta)
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
+//
+// P is formed again from the forward's log-sums; nothing of size T x T is kept.  dK and dV sum
+// over the queries and over the heads of a group, dQ over the keys.  Two kinds of blocks
+// share one launch, each with its sum in tensor memory from first to last, so that no sum
+// depends on timing and nothing is added in global memory:
+//
+//   key blocks    128 keys of a key head against all query tiles that see them, head by head
+//                 of the group.  The products are taken with the keys as rows (S^T = K Q^T, dP^T
+//                 = V dO^T), so that P^T and dS^T stand in tensor memory as the A operands of
+//                 dV and dK.  4 products a tile pair.
+//   query blocks  128 queries of a head against the key tiles they see.  3 products.
+//
+// That is 7 products where a single pass with additions of dQ in global memory needs 5; the two
+// more are the price of results that repeat bit by bit.
+//
+// In both, two threads a row: warps 0-3 have the first 64 columns of a score tile and warps 4-7
+// the others.  P and dS are rounded to the inputs' 16-bit type because the tensor cores read
+// them so; all sums are fp32.
+#include "kda_attn_plan.cuh"
+
+using namespace kda;
+
+namespace {
+
+__device__ unsigned g_attn_bwd_status;
+
+constexpr int kThreads = 352;   // eight compute warps, products, loads, row statistics
+constexpr int kProductWarp = 8, kLoadWarp = 9, kStatWarp = 10;
+constexpr int kTile = 128;
+
+struct Grads {
+    const void *out, *d_out;
+    int64_t o_t, o_h, do_t, do_h;
+    void *dq, *dk, *dv;
+    float *delta, *lse2;     // [Hq][T]
+    int64_t key_blocks;      // blocks below this one are key blocks
+};
+
+template <int D>
+struct Lay {
+    static constexpr int kBytes = kTile * D * 2;   // a tile of 128 rows
+    static constexpr int kBlock = kTile * 128;     // 64 channels of it
+    static constexpr int kPairs = D == 128 ? 2 : 4;   // pairs of tiles in flight
+    static constexpr int kSmem = 1024 + (2 + 2 * kPairs) * kBytes;
+};
+
+struct Control {
+    uint64_t own_full, a_full[4], a_empty[4], b_full[4], b_empty[4], stat_full[4], stat_empty[4];
+    uint64_t s_full[2], p_ready, dp_full, dp_free, ds_ready, done;
+    uint32_t tmem;
+    AttnPart part;
+    int64_t scan[kThreads / 32];
+    float stat[4][2][kTile];
+};
+
+// delta and lse log2(e), head-major.  16 (8) lanes a row.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) kda_attn_delta_kernel(const Attn A, const Grads B) {
+    constexpr int LANES = D / 8;
+    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
+    const int c = threadIdx.x % LANES;
+    const int64_t rows = (int64_t)A.T * A.Hq;
+    float sum = 0.f;
+    const int64_t t = row / A.Hq, h = row - t * A.Hq;
+    if (row < rows) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(B.out) + t * B.o_t + h * B.o_h) + c);
+        const uint4 y = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(B.d_out) + t * B.do_t + h * B.do_h) + c);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b, e, f;
+            unpack16<BF16>(xs[i], a, b);
+            unpack16<BF16>(ys[i], e, f);
+            sum = fmaf(a, e, fmaf(b, f, sum));
+        }
+    }
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (row < rows && c == 0) {
+        B.delta[h * A.T + t] = sum;
+        // a row that saw nothing has weights 0
+        const float l = A.lse[row];
+        B.lse2[h * A.T + t] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
+    }
+}
+
+// Rows [from, 128) of a tile in shared memory cleared, by a warp: they belong to another
+// sequence, and 0 * NaN is NaN.
+template <int D>
+__device__ __forceinline__ void clear_rows(uint8_t *tile, int from) {
+    for (int x = threadIdx.x & 31; x < (kTile - from) * (D / 8); x += 32)
+        *reinterpret_cast<uint4 *>(tile + (x % (D / 8)) / 8 * Lay<D>::kBlock + (from + x / (D / 8)) * 128 + (x % 8) * 16) =
+            make_uint4(0, 0, 0, 0);
+    sm100::fence_proxy_async_smem();
+    __syncwarp();
+}
+
+template <int D>
+__device__ __forceinline__ void load_tile(uint8_t *to, const CUtensorMap *map, uint64_t *bar, int head, int64_t row) {
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) tma_load_4d(to + b * Lay<D>::kBlock, map, bar, b * 64, head, (int)row, 0);
+}
+
+// D[128, d] += A B: A [128, 128] 16-bit in tensor memory (its halves of 64 columns at a_tmem and
+// a_tmem + 64), B a tile of 128 rows.
+template <int D, bool BF16>
+__device__ __forceinline__ void mma_sum(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_saddr, bool more) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+        mma16_ts(d_tmem, a_tmem + (s >> 2) * 64 + (s & 3) * 8, sdesc_mn(b_saddr + s * 2048, Lay<D>::kBlock),
+                 idesc_16(BF16, 128, D, true), more || s > 0);
+}
+
+// 64 fp32 columns of the thread's row.
+__device__ __forceinline__ void load64(uint32_t at, float (&x)[64]) {
+    tmem_ld32_nowait(at, x);
+    tmem_ld32_nowait(at + 32, x + 32);
+    tmem_wait_ld(x);
+}
+// 64 columns as 16-bit pairs into the 32 columns at `at`.
+template <bool BF16>
+__device__ __forceinline__ void store64(uint32_t at, const float (&x)[64]) {
+    uint32_t p[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) p[i] = pack16<BF16>(x[2 * i], x[2 * i + 1]);
+    tmem_st16_raw(at, p);
+    tmem_st16_raw(at + 16, p + 16);
+    sm100::tmem_wait_st();
+    sm100::tc_fence_before();
+}
+
+// A result row: COLS channels of tensor memory, scaled, to `at` elements into `to`.
+template <int COLS, bool BF16>
+__device__ __forceinline__ void write_row(void *to, bool f32, int64_t at, uint32_t tmem, float scale, bool live) {
+#pragma unroll 1
+    for (int x = 0; x < COLS; x += 32) {
+        float v[32];
+        tmem_ld32_nowait(tmem + x, v);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int y = 0; y < 32; ++y) v[y] *= scale;
+        if (live)
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) store8<BF16>(to, f32, at + x + y, v + y);
+    }
+}
+
+template <int D, bool BF16>
+__device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CUtensorMap *vm, const CUtensorMap *om,
+                          const Attn &A, const Grads &B, Control &ct, uint8_t *base, const AttnSeq &sq, uint32_t tmem) {
+    using L = Lay<D>;
+    constexpr int NST = L::kPairs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *Ks = base, *Vs = base + L::kBytes, *ring = base + 2 * L::kBytes;   // pairs: queries, dO
+    const int kt = ct.part.tile, hk = ct.part.head, G = A.G;
+    const int len = (int)(sq.b - sq.a), tiles = (len + kTile - 1) / kTile;
+    const int per = tiles - kt, n = per * G;   // step j: head j / per of the group, query tile kt + j % per
+    const int tail = len - (tiles - 1) * kTile;   // rows of the last tile
+    constexpr uint32_t S = 0, DP = 128, DV = 256, DK = 256 + D;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, int phase) { return attn_wait(bar, phase & 1, &g_attn_bwd_status); };
+
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            sm100::mbar_arrive_expect_tx(&ct.own_full, 2 * L::kBytes);
+            load_tile<D>(Ks, km, &ct.own_full, hk, sq.a + kt * kTile);
+            load_tile<D>(Vs, vm, &ct.own_full, hk, sq.a + kt * kTile);
+        }
+        __syncwarp();
+        int a = 0, b = 0;   // tiles issued
+        for (int j = 0; j < n; ++j) {
+            const int st = j % NST, h = hk * G + j / per;
+            const int64_t row = sq.a + (int64_t)(kt + j % per) * kTile;
+            if (j >= NST) ok = wait(&ct.a_empty[st], j / NST - 1);
+            if (!ok) break;
+            if (lane == 0) {
+                sm100::mbar_arrive_expect_tx(&ct.a_full[st], L::kBytes);
+                load_tile<D>(ring + 2 * st * L::kBytes, qm, &ct.a_full[st], h, row);
+            }
+            __syncwarp();
+            ++a;
+            if (j >= NST) ok = wait(&ct.b_empty[st], j / NST - 1);
+            if (!ok) break;
+            if (lane == 0) {
+                sm100::mbar_arrive_expect_tx(&ct.b_full[st], L::kBytes);
+                load_tile<D>(ring + (2 * st + 1) * L::kBytes, om, &ct.b_full[st], h, row);
+            }
+            __syncwarp();
+            ++b;
+        }
+        // no copy may land after the block's end
+        attn_wait(&ct.own_full, 0, &g_attn_bwd_status);
+        for (int j = max(0, a - NST); j < a; ++j) wait(&ct.a_full[j % NST], j / NST);
+        for (int j = max(0, b - NST); j < b; ++j) wait(&ct.b_full[j % NST], j / NST);
+    } else if (warp == kStatWarp) {
+        for (int j = 0; j < n; ++j) {
+            const int st = j % NST;
+            const int64_t h = hk * G + j / per, at = h * A.T + sq.a, row = (int64_t)(kt + j % per) * kTile + lane * 4;
+            float x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = row + i < len ? B.lse2[at + row + i] : INFINITY;
+                y[i] = row + i < len ? B.delta[at + row + i] : 0.f;
+            }
+            if (j >= NST) ok = wait(&ct.stat_empty[st], j / NST - 1);
+            if (!ok) break;
+            *reinterpret_cast<float4 *>(&ct.stat[st][0][lane * 4]) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(&ct.stat[st][1][lane * 4]) = make_float4(y[0], y[1], y[2], y[3]);
+            sm100::mbar_arrive(&ct.stat_full[st]);
+        }
+    } else if (warp == kProductWarp) {
+        const uint32_t k_at = sm100::smem_u32(Ks), v_at = sm100::smem_u32(Vs), r_at = sm100::smem_u32(ring);
+        // the tile of step j, its rows behind the sequence cleared
+        auto arrived = [&](uint64_t *bars, int j, int which) {
+            if (!wait(&bars[j % NST], j / NST)) return false;
+            if (tail < kTile && j % per == per - 1) clear_rows<D>(ring + (2 * (j % NST) + which) * L::kBytes, tail);
+            return true;
+        };
+        auto scores = [&](int j) {
+            sm100::tc_fence_after();
+            mma_rows<D, BF16, 128>(tmem + S, k_at, r_at + 2 * (j % NST) * L::kBytes, L::kBlock, L::kBlock);
+            sm100::mma_commit_el(&ct.s_full[0]);
+        };
+        auto dscores = [&](int j) {
+            sm100::tc_fence_after();
+            mma_rows<D, BF16, 128>(tmem + DP, v_at, r_at + (2 * (j % NST) + 1) * L::kBytes, L::kBlock, L::kBlock);
+            sm100::mma_commit_el(&ct.dp_full);
+        };
+        ok = wait(&ct.own_full, 0) && arrived(ct.a_full, 0, 0);
+        if (ok) {
+            scores(0);
+            ok = arrived(ct.b_full, 0, 1);
+            if (ok) dscores(0);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+            const int st = j % NST;
+            ok = wait(&ct.p_ready, j);
+            if (!ok) break;
+            sm100::tc_fence_after();
+            mma_sum<D, BF16>(tmem + DV, tmem + S, r_at + (2 * st + 1) * L::kBytes, j > 0);
+            sm100::mma_commit_el(&ct.b_empty[st]);
+            if (j + 1 < n) {
+                ok = arrived(ct.a_full, j + 1, 0);
+                if (!ok) break;
+                scores(j + 1);
+            }
+            ok = wait(&ct.ds_ready, j);
+            if (!ok) break;
+            sm100::tc_fence_after();
+            mma_sum<D, BF16>(tmem + DK, tmem + DP, r_at + 2 * st * L::kBytes, j > 0);
+            sm100::mma_commit_el(&ct.a_empty[st]);
+            if (j + 1 < n) {
+                ok = arrived(ct.b_full, j + 1, 1);
+                if (!ok) break;
+                dscores(j + 1);
+            }
+        }
+        sm100::mma_commit_el(&ct.done);
+        attn_wait(&ct.done, 0, &g_attn_bwd_status);
+    } else {
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const float c = A.scale_log2;
+        for (int j = 0; j < n; ++j) {
+            const int st = j % NST, qt = kt + j % per;
+            ok = wait(&ct.stat_full[st], j / NST) && wait(&ct.s_full[0], j);
+            if (!ok) break;
+            sm100::tc_fence_after();
+            float p[64];
+            load64(lanes + S + half * 64, p);
+            const float4 *l4 = reinterpret_cast<const float4 *>(&ct.stat[st][0][half * 64]);
+            const uint64_t c2 = pack2(c, c);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                const float4 l = l4[x];
+                unpack2(fma2(pack2(p[4 * x], p[4 * x + 1]), c2, pack2(-l.x, -l.y)), p[4 * x], p[4 * x + 1]);
+                unpack2(fma2(pack2(p[4 * x + 2], p[4 * x + 3]), c2, pack2(-l.z, -l.w)), p[4 * x + 2], p[4 * x + 3]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) p[4 * x + y] = ex2(p[4 * x + y]);
+            }
+            // query column x of this half: seen from key row r, and a token of the sequence
+            const bool masked = qt == kt || (tail < kTile && qt == tiles - 1);
+            const int lo = qt == kt ? r - half * 64 : 0, hi = len - qt * kTile - half * 64;
+            if (masked) {
+#pragma unroll
+                for (int x = 0; x < 64; ++x) p[x] = x >= lo && x < hi ? p[x] : 0.f;
+            }
+            store64<BF16>(lanes + S + half * 64, p);
+            sm100::mbar_arrive(&ct.p_ready);
+            ok = wait(&ct.dp_full, j);
+            if (!ok) break;
+            sm100::tc_fence_after();
+            float dp[64];
+            load64(lanes + DP + half * 64, dp);
+            const float4 *d4 = reinterpret_cast<const float4 *>(&ct.stat[st][1][half * 64]);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                const float4 d = d4[x];
+                unpack2(mul2(pack2(p[4 * x], p[4 * x + 1]), add2(pack2(dp[4 * x], dp[4 * x + 1]), pack2(-d.x, -d.y))),
+                        dp[4 * x], dp[4 * x + 1]);
+                unpack2(mul2(pack2(p[4 * x + 2], p[4 * x + 3]), add2(pack2(dp[4 * x + 2], dp[4 * x + 3]), pack2(-d.z, -d.w))),
+                        dp[4 * x + 2], dp[4 * x + 3]);
+            }
+            if (masked) {
+#pragma unroll
+                for (int x = 0; x < 64; ++x) dp[x] = x >= lo && x < hi ? dp[x] : 0.f;
+            }
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(&ct.stat_empty[st]);
+            store64<BF16>(lanes + DP + half * 64, dp);
+            sm100::mbar_arrive(&ct.ds_ready);
+        }
+        ok = ok && wait(&ct.done, 0);
+        if (ok) {
+            sm100::tc_fence_after();
+            const int64_t at = ((sq.a + kt * kTile + r) * A.Hkv + hk) * D;
+            const bool live = kt * kTile + r < len, f32 = A.out_dtype == KDA_DTYPE_F32;
+            if (half == 0)
+                write_row<D, BF16>(B.dv, f32, at, lanes + DV, 1.f, live);
+            else
+                write_row<D, BF16>(B.dk, f32, at, lanes + DK, A.scale, live);
+        }
+        sm100::tc_fence_before();
+    }
+}
+
+template <int D, bool BF16>
+__device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const CUtensorMap *vm, const CUtensorMap *om,
+                            const Attn &A, const Grads &B, Control &ct, uint8_t *base, const AttnSeq &sq, uint32_t tmem) {
+    using L = Lay<D>;
+    constexpr int NST = L::kPairs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *Qs = base, *Os = base + L::kBytes, *ring = base + 2 * L::kBytes;   // pairs: keys, values
+    const int qt = ct.part.tile, h = ct.part.head, hk = h / A.G;
+    const int len = (int)(sq.b - sq.a), n = qt + 1;
+    const int tail = len - qt * kTile;   // rows of the last key tile (the diagonal one), if below 128
+    constexpr uint32_t S[2] = {0, 128}, DP = 256, DQ = 384;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, int phase) { return attn_wait(bar, phase & 1, &g_attn_bwd_status); };
+
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            sm100::mbar_arrive_expect_tx(&ct.own_full, 2 * L::kBytes);
+            load_tile<D>(Qs, qm, &ct.own_full, h, sq.a + (int64_t)qt * kTile);
+            load_tile<D>(Os, om, &ct.own_full, h, sq.a + (int64_t)qt * kTile);
+        }
+        __syncwarp();
+        int a = 0, b = 0;
+        for (int j = 0; j < n; ++j) {
+            const int st = j % NST;
+            const int64_t row = sq.a + (int64_t)j * kTile;
+            if (j >= NST) ok = wait(&ct.a_empty[st], j / NST - 1);
+            if (!ok) break;
+            if (lane == 0) {
+                sm100::mbar_arrive_expect_tx(&ct.a_full[st], L::kBytes);
+                load_tile<D>(ring + 2 * st * L::kBytes, km, &ct.a_full[st], hk, row);
+            }
+            __syncwarp();
+            ++a;
+            if (j >= NST) ok = wait(&ct.b_empty[st], j / NST - 1);
+            if (!ok) break;
+            if (lane == 0) {
+                sm100::mbar_arrive_expect_tx(&ct.b_full[st], L::kBytes);
+                load_tile<D>(ring + (2 * st + 1) * L::kBytes, vm, &ct.b_full[st], hk, row);
+            }
+            __syncwarp();
+            ++b;
+        }
+        attn_wait(&ct.own_full, 0, &g_attn_bwd_status);
+        for (int j = max(0, a - NST); j < a; ++j) wait(&ct.a_full[j % NST], j / NST);
+        for (int j = max(0, b - NST); j < b; ++j) wait(&ct.b_full[j % NST], j / NST);
+    } else if (warp == kProductWarp) {
+        const uint32_t q_at = sm100::smem_u32(Qs), o_at = sm100::smem_u32(Os), r_at = sm100::smem_u32(ring);
+        auto scores = [&](int j) {
+            if (!wait(&ct.a_full[j % NST], j / NST)) return false;
+            if (j == n - 1 && tail < kTile) clear_rows<D>(ring + 2 * (j % NST) * L::kBytes, tail);
+            sm100::tc_fence_after();
+            mma_rows<D, BF16, 128>(tmem + S[j & 1], q_at, r_at + 2 * (j % NST) * L::kBytes, L::kBlock, L::kBlock);
+            sm100::mma_commit_el(&ct.s_full[j & 1]);
+            return true;
+        };
+        auto dscores = [&](int j) {
+            if (!wait(&ct.b_full[j % NST], j / NST)) return false;
+            sm100::tc_fence_after();
+            mma_rows<D, BF16, 128>(tmem + DP, o_at, r_at + (2 * (j % NST) + 1) * L::kBytes, L::kBlock, L::kBlock);
+            sm100::mma_commit_el(&ct.dp_full);
+            sm100::mma_commit_el(&ct.b_empty[j % NST]);
+            return true;
+        };
+        ok = wait(&ct.own_full, 0) && scores(0) && dscores(0);
+        for (int j = 0; j < n && ok; ++j) {
+            if (j + 1 < n) {
+                ok = scores(j + 1) && wait(&ct.dp_free, j) && dscores(j + 1);
+                if (!ok) break;
+            }
+            ok = wait(&ct.ds_ready, j);
+            if (!ok) break;
+            sm100::tc_fence_after();
+            mma_sum<D, BF16>(tmem + DQ, tmem + S[j & 1], r_at + 2 * (j % NST) * L::kBytes, j > 0);
+            sm100::mma_commit_el(&ct.a_empty[j % NST]);
+        }
+        sm100::mma_commit_el(&ct.done);
+        attn_wait(&ct.done, 0, &g_attn_bwd_status);
+    } else if (warp < 8) {
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const bool live = qt * kTile + r < len;
+        const int64_t at = (int64_t)h * A.T + sq.a + qt * kTile + r;
+        const float lse2 = live ? B.lse2[at] : INFINITY, delta = live ? B.delta[at] : 0.f;
+        const float c = A.scale_log2;
+        const uint64_t c2 = pack2(c, c), l2 = pack2(-lse2, -lse2), d2 = pack2(-delta, -delta);
+        for (int j = 0; j < n; ++j) {
+            ok = wait(&ct.s_full[j & 1], j >> 1);
+            if (!ok) break;
+            sm100::tc_fence_after();
+            float p[64];
+            load64(lanes + S[j & 1] + half * 64, p);
+#pragma unroll
+            for (int x = 0; x < 64; x += 2) {
+                float a, b;
+                unpack2(fma2(pack2(p[x], p[x + 1]), c2, l2), a, b);
+                p[x] = ex2(a);
+                p[x + 1] = ex2(b);
+            }
+            ok = wait(&ct.dp_full, j);
+            if (!ok) break;
+            sm100::tc_fence_after();
+            float dp[64];
+            load64(lanes + DP + half * 64, dp);
+            sm100::tc_fence_before();
+            sm100::mbar_arrive(&ct.dp_free);
+#pragma unroll
+            for (int x = 0; x < 64; x += 2)
+                unpack2(mul2(pack2(p[x], p[x + 1]), add2(pack2(dp[x], dp[x + 1]), d2)), dp[x], dp[x + 1]);
+            if (j == n - 1) {
+#pragma unroll
+                for (int x = 0; x < 64; ++x) dp[x] = x + half * 64 <= r ? dp[x] : 0.f;
+            }
+            store64<BF16>(lanes + S[j & 1] + half * 64, dp);
+            sm100::mbar_arrive(&ct.ds_ready);
+        }
+        ok = ok && wait(&ct.done, 0);
+        if (ok) {
+            sm100::tc_fence_after();
+            write_row<D / 2, BF16>(B.dq, A.out_dtype == KDA_DTYPE_F32,
+                                   ((sq.a + qt * kTile + r) * A.Hq + h) * D + half * (D / 2), lanes + DQ + half * (D / 2),
+                                   A.scale, live);
+        }
+        sm100::tc_fence_before();
+    }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+kda_attn_backward_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
+                         const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap om, const Attn A,
+                         const Grads B) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ Control ct;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const bool keys = blockIdx.x < B.key_blocks;
+    if (tid == 0) {
+        sm100::mbar_init(&ct.own_full, 1);
+        for (int i = 0; i < 4; ++i) {
+            sm100::mbar_init(&ct.a_full[i], 1);
+            sm100::mbar_init(&ct.a_empty[i], 1);
+            sm100::mbar_init(&ct.b_full[i], 1);
+            sm100::mbar_init(&ct.b_empty[i], 1);
+            sm100::mbar_init(&ct.stat_full[i], 32);
+            sm100::mbar_init(&ct.stat_empty[i], 8);
+        }
+        sm100::mbar_init(&ct.s_full[0], 1);
+        sm100::mbar_init(&ct.s_full[1], 1);
+        sm100::mbar_init(&ct.dp_full, 1);
+        sm100::mbar_init(&ct.done, 1);
+        sm100::mbar_init(&ct.p_ready, 256);
+        sm100::mbar_init(&ct.dp_free, 256);
+        sm100::mbar_init(&ct.ds_ready, 256);
+        sm100::fence_mbar_init();
+    }
+    auto tiles = [&](int n) {
+        const AttnSeq s = attn_seq<false>(A, n);
+        return (s.b - s.a + kTile - 1) / kTile;
+    };
+    // the first key tiles are seen by the most queries, the last query tiles see the most keys:
+    // those start first
+    const bool some = keys ? attn_whole_part<kThreads>(A.N, A.Hkv, blockIdx.x, false, tiles, &ct.part, ct.scan)
+                           : attn_whole_part<kThreads>(A.N, A.Hq, blockIdx.x - B.key_blocks, true, tiles, &ct.part, ct.scan);
+    if (!some) return;
+    const AttnSeq sq = attn_seq<false>(A, ct.part.n);
+    if (warp == kProductWarp) {
+        sm100::tmem_alloc(&ct.tmem, 512);
+        sm100::tmem_relinquish();
+    }
+    sm100::tc_fence_before();
+    __syncthreads();
+    sm100::tc_fence_after();
+    const uint32_t tmem = ct.tmem;
+    if (keys)
+        key_block<D, BF16>(&qm, &km, &vm, &om, A, B, ct, base, sq, tmem);
+    else
+        query_block<D, BF16>(&qm, &km, &vm, &om, A, B, ct, base, sq, tmem);
+    __syncthreads();
+    if (warp == kProductWarp) sm100::tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool BF16>
+cudaError_t backward(const Attn &A, Grads &B, cudaStream_t stream) {
+    CUtensorMap qm, km, vm, om;
+    if (!kda_make_attn_map(&qm, A.q, BF16, D, A.Hq, A.T, 1, A.q_h, A.q_t, 0, kTile) ||
+        !kda_make_attn_map(&km, A.k, BF16, D, A.Hkv, A.T, 1, A.k_h, A.k_t, 0, kTile) ||
+        !kda_make_attn_map(&vm, A.v, BF16, D, A.Hkv, A.T, 1, A.v_h, A.v_t, 0, kTile) ||
+        !kda_make_attn_map(&om, B.d_out, BF16, D, A.Hq, A.T, 1, B.do_h, B.do_t, 0, kTile))
+        return cudaErrorInvalidValue;
+    const auto kernel = kda_attn_backward_kernel<D, BF16>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = (int64_t)A.T * A.Hq;
+    kda_attn_delta_kernel<D, BF16><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, stream>>>(A, B);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int64_t tiles = A.cu ? (int64_t)A.T / kTile + A.N : (A.seq_len + kTile - 1) / kTile * A.N;
+    B.key_blocks = tiles * A.Hkv;
+    kernel<<<(unsigned)(B.key_blocks + tiles * A.Hq), kThreads, Lay<D>::kSmem, stream>>>(qm, km, vm, om, A, B);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t kda_attn_backward_ws(const Attn &A) { return (int64_t)A.T * A.Hq * 8; }
+
+cudaError_t kda_launch_attn_backward(const Attn &A, const AttnGrads &X, float *workspace, cudaStream_t stream) {
+    Grads B{};
+    B.out = X.out, B.o_t = X.o_t, B.o_h = X.o_h;
+    B.d_out = X.d_out, B.do_t = X.do_t, B.do_h = X.do_h;
+    B.dq = X.dq, B.dk = X.dk, B.dv = X.dv;
+    B.delta = workspace;
+    B.lse2 = workspace + (int64_t)A.T * A.Hq;
+    const bool b = A.in_dtype == KDA_DTYPE_BF16;
+    if (A.d == 128) return b ? backward<128, true>(A, B, stream) : backward<128, false>(A, B, stream);
+    return b ? backward<64, true>(A, B, stream) : backward<64, false>(A, B, stream);
+}
+
+cudaError_t kda_attn_bwd_read_status(unsigned *status) {
+    unsigned w = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&w, g_attn_bwd_status, sizeof(w));
+    if (e == cudaSuccess && w) {
+        *status |= w;
+        w = 0;
+        e = cudaMemcpyToSymbol(g_attn_bwd_status, &w, sizeof(w));
+    }
+    return e;
+}

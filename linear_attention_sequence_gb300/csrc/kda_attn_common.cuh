@@ -31,7 +31,14 @@ struct Attn {
     int64_t k_p, v_p;         // strides of a page
     // results
     void *out;                // [T, Hq, d], contiguous
-    float *lse;               // [T, Hq] or nullptr
+    float *lse;               // [T, Hq] or nullptr; the backward reads it
+};
+
+// What the backward reads and writes besides.
+struct AttnGrads {
+    const void *out, *d_out;  // [T, Hq, d], strides in elements
+    int64_t o_t, o_h, do_t, do_h;
+    void *dq, *dk, *dv;       // contiguous
 };
 
 // Sequence n of the call: its tokens [a, b) and the keys it has.
@@ -225,6 +232,8 @@ __device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity, unsign
 // Launchers (kda_attn_*.cu).
 int64_t kda_attn_paged_ws(const kda::Attn &A);
 cudaError_t kda_launch_attn_prefill(const kda::Attn &A, cudaStream_t stream);
+int64_t kda_attn_backward_ws(const kda::Attn &A);
+cudaError_t kda_launch_attn_backward(const kda::Attn &A, const kda::AttnGrads &X, float *workspace, cudaStream_t stream);
 cudaError_t kda_launch_attn_paged(const kda::Attn &A, void *workspace, cudaStream_t stream);
 
 // A TMA view of [pages, rows, heads, d] 16-bit elements with strides in elements; a box is

@@ -103,7 +103,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const AttnSeq s = attn_seq<false>(A, n);
             return ((s.b - s.a) * G + kTileRows - 1) / kTileRows;
         };
-        some = attn_whole_part<kThreads>(A.N, A.Hkv, blockIdx.x, tiles, &ct.part, ct.scan);
+        some = attn_whole_part<kThreads>(A.N, A.Hkv, blockIdx.x, true, tiles, &ct.part, ct.scan);
     }
     if (!some) return;
     const AttnPart part = ct.part;
@@ -133,6 +133,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     sm100::tc_fence_after();
     const uint32_t tmem = ct.tmem;
     bool ok = true;
+    int issued = 0;   // tiles asked for by the load warp
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------ keys and values
@@ -167,6 +168,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             if (issues)
                 tma_load_4d(to + mine * L::kBlockBytes + which * box * 128, values ? &vmap : &kmap, &ct.full[st],
                             mine * 64, part.head, at, page);
+            ++issued;
         }
         if (bad) atomicOr(&g_attn_status, kCacheBadPage);
         __syncwarp();
@@ -364,9 +366,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     }
     if (warp == kLoadWarp) {
         // no copy may land after the block's end: the last ones of each stage
-        const int loads = 2 * n;
-        for (int c = max(0, loads - NST); c < loads && ok; ++c)
-            attn_wait(&ct.full[c % NST], (c / NST) & 1, &g_attn_status);
+        for (int c = max(0, issued - NST); c < issued; ++c) attn_wait(&ct.full[c % NST], (c / NST) & 1, &g_attn_status);
     }
     __syncthreads();
     if (warp == kProductWarp) sm100::tmem_dealloc(tmem, 512);
@@ -515,6 +515,7 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         const bool values = lane >= boxes * (D / 64), issues = lane < 2 * boxes * (D / 64);
         const int32_t *row = A.table + (int64_t)part.n * A.wide;
         bool bad = false;
+        int issued = 0;
         for (int j = 0; j < n; ++j) {
             const int64_t first = (int64_t)(part.j0 + j) * kFewKeys + which * box;
             int page = A.P;   // past the cache: reads zeros
@@ -531,9 +532,10 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             if (issues)
                 tma_load_4d(to + mine * L::kBlock + which * box * 128, values ? &vmap : &kmap, &ct.full[st], mine * 64,
                             part.head, (int)(first % A.page), page);
+            ++issued;
         }
         if (bad) atomicOr(&g_attn_status, kCacheBadPage);
-        for (int j = max(0, n - NST); j < n && ok; ++j) attn_wait(&ct.full[j % NST], (j / NST) & 1, &g_attn_status);
+        for (int j = max(0, issued - NST); j < issued; ++j) attn_wait(&ct.full[j % NST], (j / NST) & 1, &g_attn_status);
         __syncthreads();
         __syncthreads();
         return;

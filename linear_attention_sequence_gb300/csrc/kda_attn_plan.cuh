@@ -113,18 +113,18 @@ __device__ __forceinline__ bool attn_split_part(int N, int heads, int64_t index,
     return true;
 }
 
-// Row tile number `index` from the last to the first (the later tiles of a causal sequence
-// see more keys and so start first).
+// Tile number `index` of `heads` heads (head fastest), from the first tile to the last or, with
+// `reverse`, from the last to the first: what takes longest starts first.
 template <int THREADS, typename Tiles>
-__device__ __forceinline__ bool attn_whole_part(int N, int heads, int64_t index, Tiles tiles_of, AttnPart *part,
-                                                int64_t *sh) {
+__device__ __forceinline__ bool attn_whole_part(int N, int heads, int64_t index, bool reverse, Tiles tiles_of,
+                                                AttnPart *part, int64_t *sh) {
     const int per = (N + THREADS - 1) / THREADS;
     const int lo = (int)threadIdx.x * per, hi = min(N, lo + per);
     int64_t tiles = 0, total;
     for (int n = lo; n < hi; ++n) tiles += tiles_of(n);
     int64_t before = block_scan<THREADS>(tiles, total, sh);
     if (index >= total * heads) return false;
-    const int64_t at = total - 1 - index / heads;
+    const int64_t at = reverse ? total - 1 - index / heads : index / heads;
     if (at >= before && at < before + tiles) {
         for (int n = lo; n < hi; ++n) {
             const int64_t x = tiles_of(n);

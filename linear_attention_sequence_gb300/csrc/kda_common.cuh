@@ -172,6 +172,7 @@ cudaError_t kda_launch_backward_tc(const kda::Problem &P, const void *q, const v
                                    cudaStream_t stream);
 cudaError_t kda_bwdtc_read_status(unsigned *status);
 cudaError_t kda_attn_read_status(unsigned *status);
+cudaError_t kda_attn_bwd_read_status(unsigned *status);
 cudaError_t kda_cache_read_status(unsigned *status);
 bool kda_prefill_noalloc_fits(const kda::Problem &P, const void *q, const void *k, const void *v,
                               const float *g, const void *out);

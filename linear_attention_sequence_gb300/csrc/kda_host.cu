@@ -86,6 +86,7 @@ cudaError_t kda_read_device_status(cudaStream_t stream, unsigned *status) {
     if (e == cudaSuccess) e = kda_bwdtc_read_status(status);
     if (e == cudaSuccess) e = kda_ssm_read_status(status);
     if (e == cudaSuccess) e = kda_attn_read_status(status);
+    if (e == cudaSuccess) e = kda_attn_bwd_read_status(status);
     if (e == cudaSuccess) e = kda_cache_read_status(status);
     return e;
 }

@@ -51,6 +51,9 @@ def check_rows(out, lse, q, k, v, first, scale, what=""):
     tol = (U[q.dtype] + 2 * e + (n / 16 + 64) * U[torch.float32]) * mag + U[out.dtype] * want.abs()
     if out.dtype == torch.float16:
         tol = tol + 2.0 ** -25   # half a step of the smallest numbers
+    if q.dtype == torch.float16:
+        # the same of each weight, next to one that is 1 or more
+        tol = tol + 2.0 ** -25 * v.double().abs().nan_to_num(0.0).sum(0).repeat_interleave(q.shape[1] // v.shape[1], 0)
     off = (out.double() - want).abs()
     bad = ~(off <= tol)
     assert not bad.any(), f"{what} out: off by {float(off[bad].max())}, {int(bad.sum())} of {bad.numel()} outside"
@@ -59,3 +62,53 @@ def check_rows(out, lse, q, k, v, first, scale, what=""):
         off = torch.where(torch.isinf(wl), (lse.double() != wl).double() * 1e9, (lse.double() - wl).abs())
         bad = ~(off <= torch.where(torch.isinf(wl), torch.zeros_like(tol), tol))
         assert not bad.any(), f"{what} lse: off by {float(off[bad].max())}"
+
+
+def backward(q, k, v, out, lse, dy, scale):
+    """The documented formulas of one sequence in fp64, and for each gradient the magnitudes that
+    its bound counts: (grads, of the weights' (dS's) rounding, of the other factors of dS)."""
+    T, H, d = q.shape
+    Hkv = k.shape[1]
+    qd, kd, vd, od, yd, ld = (x.double() for x in (q, k, v, out, dy, lse))
+    g = {n: torch.zeros_like(x) for n, x in (("dq", qd), ("dk", kd), ("dv", vd))}
+    mag, err = {n: torch.zeros_like(x) for n, x in g.items()}, {n: torch.zeros_like(x) for n, x in g.items()}
+    seen = torch.ones(T, T, dtype=torch.bool, device=q.device).tril()
+    most = 0.0
+    for h in range(H):
+        c = h // (H // Hkv)
+        s = qd[:, h] @ kd[:, c].T * scale
+        most = max(most, float((qd[:, h].abs() @ kd[:, c].abs().T).max()) * scale)
+        p = torch.where(seen, torch.exp(s - ld[:, h:h + 1]), torch.zeros_like(s))
+        delta = (yd[:, h] * od[:, h]).sum(1, keepdim=True)
+        ds = p * (yd[:, h] @ vd[:, c].T - delta)
+        # fp32 sums of dP and delta: in units of u32
+        e = p * (yd[:, h].abs() @ vd[:, c].abs().T + (yd[:, h] * od[:, h]).abs().sum(1, keepdim=True))
+        g["dv"][:, c] += p.T @ yd[:, h]
+        mag["dv"][:, c] += p.T @ yd[:, h].abs()
+        for n, x, y, at in (("dq", ds, kd[:, c], h), ("dk", ds.T, qd[:, h], c)):
+            g[n][:, at] += scale * (x @ y)
+            mag[n][:, at] += scale * (x.abs() @ y.abs())
+            err[n][:, at] += scale * ((e if n == "dq" else e.T) @ y.abs())
+    return g, mag, err, most
+
+
+def backward_bounds(g, mag, err, most, q, k, lse, dy, scale, dtype):
+    """How far each gradient may be off: the weights (dS) rounded to 16 bits, moved by the errors of
+    the scores and of lse, fp32 sums, and the result's own rounding."""
+    T, _, d = q.shape
+    u = U[torch.float32]
+    e = 2 * (score_error(most, d) + 4 * u * float(lse.abs().max().clamp(min=1)))
+    H = q.shape[1]
+    tol = {}
+    small = dict(dq=scale * k.double().abs().sum(0).repeat_interleave(H // k.shape[1], 0),
+                 dk=scale * q.double().abs().sum(0).unflatten(0, (k.shape[1], -1)).sum(1),
+                 dv=dy.double().abs().sum(0).unflatten(0, (k.shape[1], -1)).sum(1))
+    for n in g:
+        sums = (T * (H if n != "dq" else 1) / 16 + 64) * u
+        tol[n] = (U[q.dtype] + e + sums) * mag[n] + (4 * d / 16 + 8) * u * err[n] + U[dtype] * g[n].abs()
+        if dtype == torch.float16:
+            tol[n] = tol[n] + 2.0 ** -25
+        if q.dtype == torch.float16:
+            # a weight (dS) below fp16's normal numbers is off by half a step of 2^-24
+            tol[n] = tol[n] + 2.0 ** -25 * small[n]
+    return tol

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import linear_attention_sequence_gb300 as kda
-from attn_reference import check_rows
+from attn_reference import backward as ref_backward, backward_bounds, check_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -114,4 +114,37 @@ def test_paged(dtype, d, page, new, total, H, Hkv):
     check_paged(out, lse, q, new, total, ks, vs)
     rounded = kda.kda_attn_paged(q, kp, vp, table, lens, cu)
     assert rounded.dtype == dtype and torch.equal(rounded, out.to(dtype))
+    assert kda.kda_get_last_device_error() == 0
+
+
+def check_backward(got, q, k, v, out, lse, dy, lens, first=0, scale=None):
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    at = starts(lens, first)
+    for n, (a, b) in enumerate(zip(at[:-1], at[1:])):
+        if a == b:
+            continue
+        args = (q[a:b], k[a:b], v[a:b], out[a:b], lse[a:b], dy[a:b])
+        want, mag, err, most = ref_backward(*args, scale)
+        tol = backward_bounds(want, mag, err, most, q[a:b], k[a:b], lse[a:b], dy[a:b], scale, got["dq"].dtype)
+        for name in want:
+            off = (got[name][a:b].double() - want[name]).abs()
+            bad = ~(off <= tol[name])
+            assert not bad.any(), (f"sequence {n} {name}: off by {float(off[bad].max())}, bound there "
+                                   f"{float(tol[name][bad].min())}, {int(bad.sum())} of {bad.numel()} outside")
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F16, 64), (F16, 128), (BF16, 64)])
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 1), (8, 2), (5, 5), (12, 1)])
+@pytest.mark.parametrize("lens", [[1], [2], [127], [128], [129], [255, 1, 0, 257], [37, 0, 0, 64, 130], [700]])
+def test_backward(lens, H, Hkv, d, dtype):
+    T = sum(lens)
+    q, k, v = prompt_inputs(T, H, Hkv, d, dtype, 50 + T)
+    dy = rnd(60 + T, dtype, T, H, d)
+    cu = None if len(lens) == 1 else cu_of(lens)
+    out, lse = kda.kda_attn_prefill(q, k, v, cu, return_lse=True)
+    grads = kda.kda_attn_backward(q, k, v, out, lse, dy, cu, grad_dtype=F32)
+    check_backward(grads, q, k, v, out, lse, dy, lens)
+    rounded = kda.kda_attn_backward(q, k, v, out, lse, dy, cu)
+    for n in grads:
+        assert rounded[n].dtype == dtype and torch.equal(rounded[n], grads[n].to(dtype))
     assert kda.kda_get_last_device_error() == 0
