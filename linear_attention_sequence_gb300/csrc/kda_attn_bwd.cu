@@ -21,6 +21,8 @@
 // In both, two threads a row: warps 0-3 have the first 64 columns of a score tile and warps 4-7
 // the others.  P and dS are rounded to the inputs' 16-bit type because the tensor cores read
 // them so; all sums are fp32.
+#include <stddef.h>
+
 #include "kda_attn_plan.cuh"
 
 using namespace kda;
@@ -49,14 +51,15 @@ struct Lay {
     static constexpr int kSmem = 1024 + (2 + 2 * kPairs) * kBytes;
 };
 
-struct Control {
+struct alignas(16) Control {
     uint64_t own_full, a_full[4], a_empty[4], b_full[4], b_empty[4], stat_full[4], stat_empty[4];
-    uint64_t s_full[2], p_ready, dp_full, dp_free, ds_ready, done;
+    uint64_t s_full[2], p_ready, dp_full, dp_free, ds_ready[2], done;
     uint32_t tmem;
     AttnPart part;
     int64_t scan[kThreads / 32];
-    float stat[4][2][kTile];
+    alignas(16) float stat[4][2][kTile];   // read as float4
 };
+static_assert(offsetof(Control, stat) % 16 == 0 && alignof(Control) % 16 == 0, "vector reads of stat");
 
 // delta and lse log2(e), head-major.  16 (8) lanes a row.
 template <int D, bool BF16>
@@ -152,10 +155,10 @@ __device__ __forceinline__ void write_row(void *to, bool f32, int64_t at, uint32
 
 template <int D, bool BF16>
 __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CUtensorMap *vm, const CUtensorMap *om,
-                          const Attn &A, const Grads &B, Control &ct, uint8_t *base, const AttnSeq &sq, uint32_t tmem) {
+                          const Attn &A, const Grads &B, Control &ct, uint8_t *base, const AttnSeq &sq, uint32_t tmem, int warp) {
     using L = Lay<D>;
     constexpr int NST = L::kPairs;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
     uint8_t *Ks = base, *Vs = base + L::kBytes, *ring = base + 2 * L::kBytes;   // pairs: queries, dO
     const int kt = ct.part.tile, hk = ct.part.head, G = A.G;
     const int len = (int)(sq.b - sq.a), tiles = (len + kTile - 1) / kTile;
@@ -249,7 +252,7 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
                 if (!ok) break;
                 scores(j + 1);
             }
-            ok = wait(&ct.ds_ready, j);
+            ok = wait(&ct.ds_ready[0], j);
             if (!ok) break;
             sm100::tc_fence_after();
             mma_sum<D, BF16>(tmem + DK, tmem + DP, r_at + 2 * st * L::kBytes, j > 0);
@@ -313,7 +316,7 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(&ct.stat_empty[st]);
             store64<BF16>(lanes + DP + half * 64, dp);
-            sm100::mbar_arrive(&ct.ds_ready);
+            sm100::mbar_arrive(&ct.ds_ready[0]);
         }
         ok = ok && wait(&ct.done, 0);
         if (ok) {
@@ -331,10 +334,10 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
 
 template <int D, bool BF16>
 __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const CUtensorMap *vm, const CUtensorMap *om,
-                            const Attn &A, const Grads &B, Control &ct, uint8_t *base, const AttnSeq &sq, uint32_t tmem) {
+                            const Attn &A, const Grads &B, Control &ct, uint8_t *base, const AttnSeq &sq, uint32_t tmem, int warp) {
     using L = Lay<D>;
     constexpr int NST = L::kPairs;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
     uint8_t *Qs = base, *Os = base + L::kBytes, *ring = base + 2 * L::kBytes;   // pairs: keys, values
     const int qt = ct.part.tile, h = ct.part.head, hk = h / A.G;
     const int len = (int)(sq.b - sq.a), n = qt + 1;
@@ -398,7 +401,9 @@ __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const 
                 ok = scores(j + 1) && wait(&ct.dp_free, j) && dscores(j + 1);
                 if (!ok) break;
             }
-            ok = wait(&ct.ds_ready, j);
+            // (two barriers in turn: the compute warps may be through step j + 1, whose scores are
+            // there already, before this wait is reached, but not through j + 2)
+            ok = wait(&ct.ds_ready[j & 1], j >> 1);
             if (!ok) break;
             sm100::tc_fence_after();
             mma_sum<D, BF16>(tmem + DQ, tmem + S[j & 1], r_at + 2 * (j % NST) * L::kBytes, j > 0);
@@ -442,7 +447,7 @@ __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const 
                 for (int x = 0; x < 64; ++x) dp[x] = x + half * 64 <= r ? dp[x] : 0.f;
             }
             store64<BF16>(lanes + S[j & 1] + half * 64, dp);
-            sm100::mbar_arrive(&ct.ds_ready);
+            sm100::mbar_arrive(&ct.ds_ready[j & 1]);
         }
         ok = ok && wait(&ct.done, 0);
         if (ok) {
@@ -463,7 +468,7 @@ kda_attn_backward_kernel(const __grid_constant__ CUtensorMap qm, const __grid_co
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     __shared__ Control ct;
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = attn_warp();
     const bool keys = blockIdx.x < B.key_blocks;
     if (tid == 0) {
         sm100::mbar_init(&ct.own_full, 1);
@@ -481,7 +486,8 @@ kda_attn_backward_kernel(const __grid_constant__ CUtensorMap qm, const __grid_co
         sm100::mbar_init(&ct.done, 1);
         sm100::mbar_init(&ct.p_ready, 256);
         sm100::mbar_init(&ct.dp_free, 256);
-        sm100::mbar_init(&ct.ds_ready, 256);
+        sm100::mbar_init(&ct.ds_ready[0], 256);
+        sm100::mbar_init(&ct.ds_ready[1], 256);
         sm100::fence_mbar_init();
     }
     auto tiles = [&](int n) {
@@ -490,8 +496,10 @@ kda_attn_backward_kernel(const __grid_constant__ CUtensorMap qm, const __grid_co
     };
     // the first key tiles are seen by the most queries, the last query tiles see the most keys:
     // those start first
-    const bool some = keys ? attn_whole_part<kThreads>(A.N, A.Hkv, blockIdx.x, false, tiles, &ct.part, ct.scan)
-                           : attn_whole_part<kThreads>(A.N, A.Hq, blockIdx.x - B.key_blocks, true, tiles, &ct.part, ct.scan);
+    const int same = A.cu ? -1 : (int)((A.seq_len + kTile - 1) / kTile);
+    const bool some =
+        keys ? attn_whole_part<kThreads>(A.N, A.Hkv, blockIdx.x, false, same, tiles, &ct.part, ct.scan)
+             : attn_whole_part<kThreads>(A.N, A.Hq, blockIdx.x - (uint32_t)B.key_blocks, true, same, tiles, &ct.part, ct.scan);
     if (!some) return;
     const AttnSeq sq = attn_seq<false>(A, ct.part.n);
     if (warp == kProductWarp) {
@@ -503,9 +511,9 @@ kda_attn_backward_kernel(const __grid_constant__ CUtensorMap qm, const __grid_co
     sm100::tc_fence_after();
     const uint32_t tmem = ct.tmem;
     if (keys)
-        key_block<D, BF16>(&qm, &km, &vm, &om, A, B, ct, base, sq, tmem);
+        key_block<D, BF16>(&qm, &km, &vm, &om, A, B, ct, base, sq, tmem, warp);
     else
-        query_block<D, BF16>(&qm, &km, &vm, &om, A, B, ct, base, sq, tmem);
+        query_block<D, BF16>(&qm, &km, &vm, &om, A, B, ct, base, sq, tmem, warp);
     __syncthreads();
     if (warp == kProductWarp) sm100::tmem_dealloc(tmem, 512);
 }

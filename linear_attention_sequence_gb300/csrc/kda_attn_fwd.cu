@@ -1,9 +1,9 @@
 // kda_attn_fwd.cu -- causal softmax attention on the tensor cores (sm_103a): whole prompts
 // of a packed batch (kda_attn_prefill) and chunks of new tokens over a paged cache
-// (kda_attn_paged, sequences of more than kAttnFewRows query rows).
+// (kda_attn_paged, sequences of more than kFewRows query rows).
 //
-// A block takes 256 query rows of one key head.  A row is a (token, query head of the
-// group) pair, token major, so that a group of any size fills the tiles and few tokens of a
+// A block takes 256 query rows of one key head at a time.  A row is a (token, query head of
+// the group) pair, token major, so that a group of any size fills the tiles and few tokens of a
 // large group still make one.  The rows are two tiles of 128; keys and values pass
 // through a ring of 128-key tiles in shared memory (TMA, 128-byte swizzle).  For each key
 // tile and row tile
@@ -14,15 +14,28 @@
 //
 // While one tile's softmax runs, the tensor cores work on the other's products.  m is the
 // running maximum of the row.  O and the running sum are rescaled only when the maximum
-// has grown by more than 2^8 (of the 16-bit types' range P then uses no more than it has,
-// and the fp32 sums nothing): after the first tiles hardly ever, and it is the softmax threads
-// themselves that do it, between the products.  P is rounded to 16 bits because the tensor
-// cores read it so (half a step of P's own value); sums, maxima and O are fp32.
+// has grown by more than 2^8 (with less, P and the sums lose nothing in their types'
+// ranges): after the first tiles hardly ever, and it is the softmax threads themselves
+// that do it, between the products.  P is rounded to 16 bits because the tensor cores
+// read it so (half a step of P's own value); sums, maxima and O are fp32.
 //
 // Keys that a row may not see get the score -inf by a select, and value rows behind a
 // sequence's last key are cleared in shared memory before the product (0 * NaN is NaN).
-#include <mutex>
-
+//
+// Prompts: a block a row tile, the longest of a sequence first.  (Blocks that stay and take the
+// next row tile as they come, by cancelling launches, were no faster: 354 us against 350 us for
+// 8192 tokens, 32 on 8 heads of 128.  These now take 340 us; at the sustained rate of the card's own
+// matrix product it would be 323 us.)  Chunks over a cache: few row tiles and a long
+// axis of keys, so that the keys of all row tiles are laid end to end and cut into as many
+// equal runs as there are SMs (512 tokens behind 32k: 277 -> 217 us, and 203 us now); a warp finds the
+// next piece of the block's run while the others are busy with this one, and a row tile that
+// is cut leaves shares, which a second kernel joins.
+//
+// Registers: the softmax warps need their 128 scores and as much again, more than a
+// 384-thread block gives each thread (168), so that the third warpgroup hands over its own: 345
+// us for the 8192 tokens instead of 376 us, when that was tried.  One warp issues both tiles' products (two
+// warps: 525 us), and P is handed over whole (in halves: 415 us).  The ring's depth counts
+// up to four tiles (three: 450 us, four: 351 us, five: 350 us).
 #include "kda_attn_plan.cuh"
 
 using namespace kda;
@@ -31,33 +44,122 @@ namespace {
 
 __device__ unsigned g_attn_status;
 
-constexpr int kThreads = 320;      // two softmax warpgroups, the product warp, the load warp
-constexpr int kProductWarp = 8, kLoadWarp = 9;
+constexpr int kThreads = 384;      // two softmax warpgroups; products, loads, the search for work, one idle warp
+constexpr int kProductWarp = 8, kLoadWarp = 9, kWorkWarp = 10;
 constexpr int kTileRows = 256;
 constexpr float kGrowth = 8.f;     // log2 of the growth of a maximum that O is rescaled for
+constexpr int kSMs = 152;
+constexpr int kRuns = 128;         // runs of sequences whose work is summed up
 
 template <int D>
 struct Lay {
     static constexpr int kTileBytes = kAttnKeys * D * 2;              // a tile of keys, values, or 128 queries
     static constexpr int kBlockBytes = kAttnKeys * 128;               // 64 channels of it
-    static constexpr int kStages = D == 128 ? 4 : 8;
-    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + 1024;
+        static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes;
+};
+
+// A piece of work: query rows from tile * kTileRows on of sequence n (tokens [a, a + tokens),
+// `keys` keys), one key head, key tiles [j0, j0 + n_of[i]) for row tile i.
+struct Work {
+    int32_t some, n, tile, head;
+    int64_t a;
+    int32_t tokens, keys, rows;    // rows of the sequence from this tile on
+    int32_t j0, n_of[2];
+    int32_t slot;                  // where its share goes; -1: it is the whole
 };
 
 struct Control {
-    uint64_t q_full, full[8], empty[8], s_full[2], p_ready[2], o_full[2], done;
+    uint64_t q_full[2][2], full[8], empty[8], s_full[2], p_ready[2], o_full[2], work_full[2], work_empty[2], done;
     uint32_t tmem;
-    AttnPart part;
+    Work work[2];
+    int64_t before[kRuns];         // units of work in front of each run of sequences
     int64_t scan[kThreads / 32];
 };
 
-// Where the shares of split row tiles go, and what the joining kernel needs to know of them.
+// Shares of split row tiles, and what the joining kernel needs to know of them.
 struct Shares {
-    int32_t *count;   // [1] shares in all
-    int32_t *rec;     // [slots][8]: n, tile, head, split, splits
+    int32_t *rec;     // [records][4]
     float *lse;       // [slots][rows]
     float *out;       // [slots][rows][d]
 };
+
+// ---------------------------------------------------------------- the next piece of work
+// Sequence that holds unit u of the batch: by the threads' sums, then within the run of one
+// thread; `first`: its first unit.
+template <typename Cost>
+__device__ __forceinline__ int find_sequence(const Control &ct, int N, int64_t u, Cost cost, int64_t &first) {
+    int lo = 0, hi = kRuns;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (ct.before[mid] <= u) lo = mid; else hi = mid;
+    }
+    const int per = (N + kRuns - 1) / kRuns;
+    int64_t at = ct.before[lo];
+    for (int n = lo * per; n < min(N, lo * per + per); ++n) {
+        const int64_t c = cost(n);
+        if (u < at + c) {
+            first = at;
+            return n;
+        }
+        at += c;
+    }
+    first = at;
+    return -1;
+}
+
+// What the roles need of a piece of work.
+template <bool PAGED>
+__device__ __forceinline__ void fill(Work &w, const Attn &A, const AttnSeq &sq, int n, int tile, int head) {
+    w.some = 1;
+    w.n = n;
+    w.tile = tile;
+    w.head = head;
+    w.a = sq.a;
+    w.tokens = (int32_t)(sq.b - sq.a);
+    w.keys = (int32_t)sq.keys;
+    w.rows = w.tokens * A.G - tile * kTileRows;
+    w.slot = -1;
+    w.j0 = 0;
+}
+// Key tiles that the rows of row tile i see.
+__device__ __forceinline__ int32_t tiles_seen(const Work &w, int G, int i) {
+    const int32_t last = min(w.rows, (i + 1) * 128) - 1;   // last row of the tile
+    if (last < i * 128) return 0;
+    const int32_t seen = w.keys - w.tokens + (w.tile * kTileRows + last) / G + 1;
+    return (max(0, min(seen, w.keys)) + kAttnKeys - 1) / kAttnKeys;
+}
+
+// Chunks over a cache: the cost of a sequence's first t row tiles, in key tiles; two more a
+// row tile for what it costs however few they are.
+constexpr int kOver = 2;
+struct Chunk {
+    int32_t tiles;
+    int64_t behind;
+    int32_t G;
+    __device__ __forceinline__ int64_t upto(int64_t t) const {
+        return kOver * t + (t * behind + kTileRows / 2 * t * (t + 1) / G) / kAttnKeys;
+    }
+};
+__device__ __forceinline__ Chunk chunk_of(const Attn &A, int n, int few) {
+    const AttnSeq s = attn_seq<true>(A, n);
+    const int64_t tokens = s.b - s.a, rows = tokens * A.G;
+    return Chunk{rows > few ? (int32_t)((rows + kTileRows - 1) / kTileRows) : 0, s.keys > tokens ? s.keys - tokens : 0, A.G};
+}
+
+// Row number r of a sequence as (token, head of the group), walked without divisions.
+struct Row {
+    int tok, g;
+    __device__ __forceinline__ Row(int r, int G) : tok(r / G), g(r - r / G * G) {}
+    __device__ __forceinline__ void add(const Row &s, int G) {
+        tok += s.tok;
+        g += s.g;
+        if (g >= G) g -= G, ++tok;
+    }
+};
+__device__ __forceinline__ void cp_async16(uint32_t to, const void *from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
 
 template <int D, bool BF16, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -69,365 +171,524 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *Qs = base, *ring = base + 2 * L::kTileBytes;
     __shared__ Control ct;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = attn_warp();
     const int G = A.G;
 
     if (tid == 0) {
-        sm100::mbar_init(&ct.q_full, 256);
         for (int i = 0; i < NST; ++i) {
             sm100::mbar_init(&ct.full[i], 1);
             sm100::mbar_init(&ct.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            sm100::mbar_init(&ct.q_full[i][0], 128);
+            sm100::mbar_init(&ct.q_full[i][1], 128);
             sm100::mbar_init(&ct.s_full[i], 1);
             sm100::mbar_init(&ct.p_ready[i], 128);
             sm100::mbar_init(&ct.o_full[i], 1);
+            sm100::mbar_init(&ct.work_full[i], 1);
+            sm100::mbar_init(&ct.work_empty[i], 10);
         }
         sm100::mbar_init(&ct.done, 1);
         sm100::fence_mbar_init();
     }
-    // which part
-    bool some;
-    if (PAGED) {
-        auto need = [&](int n) {
-            const AttnSeq s = attn_seq<true>(A, n);
-            const int64_t rows = (s.b - s.a) * G;
-            return AttnNeed{rows > few ? (int32_t)((rows + kTileRows - 1) / kTileRows) : 0,
-                            (int32_t)((s.keys + kAttnKeys - 1) / kAttnKeys)};
-        };
-        int64_t slots;
-        some = attn_split_part<kThreads>(A.N, A.Hkv, blockIdx.x, 152, 3, 4, need, &ct.part, ct.scan, &slots);
-        if (blockIdx.x == 0 && tid == 0) *sh.count = (int32_t)slots;
-    } else {
-        auto tiles = [&](int n) {
-            const AttnSeq s = attn_seq<false>(A, n);
-            return ((s.b - s.a) * G + kTileRows - 1) / kTileRows;
-        };
-        some = attn_whole_part<kThreads>(A.N, A.Hkv, blockIdx.x, true, tiles, &ct.part, ct.scan);
-    }
-    if (!some) return;
-    const AttnPart part = ct.part;
-    const AttnSeq sq = attn_seq<PAGED>(A, part.n);
-    const int32_t tokens = (int32_t)(sq.b - sq.a), rows = tokens * G - part.tile * kTileRows;   // rows from this tile on
-    const int32_t behind = (int32_t)sq.keys - tokens;   // key index that the first token sees last
-    // of each row tile, the key tiles [j0, j0 + n[i]) that some row of it sees
-    int32_t n_of[2], n = 0;
-    const int32_t j0 = PAGED ? part.j0 : 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int32_t last = min(rows, (i + 1) * 128) - 1;   // last row of the tile
-        int32_t seen = 0;
-        if (last >= i * 128) seen = behind + (part.tile * kTileRows + last) / G + 1;
-        seen = max(0, min(seen, (int32_t)sq.keys));
-        int32_t tiles = (seen + kAttnKeys - 1) / kAttnKeys;
-        if (PAGED) tiles = min(tiles, part.j1);
-        n_of[i] = max(0, tiles - j0);
-        n = max(n, n_of[i]);
-    }
     if (warp == kProductWarp) {
         sm100::tmem_alloc(&ct.tmem, 512);
         sm100::tmem_relinquish();
+    }
+    // how much work there is in front of each thread's run of sequences
+    auto tiles_of = [&](int n) {   // prompts: a unit is a row tile
+        const AttnSeq s = attn_seq<false>(A, n);
+        return ((s.b - s.a) * G + kTileRows - 1) / kTileRows;
+    };
+    auto cost_of = [&](int n) {    // chunks
+        const Chunk c = chunk_of(A, n, few);
+        return c.upto(c.tiles);
+    };
+    const int same = PAGED || A.cu ? -1 : (int)((A.seq_len * G + kTileRows - 1) / kTileRows);
+    int64_t total = (int64_t)A.N * same;
+    if (PAGED || same < 0) {
+        const int per = (A.N + kRuns - 1) / kRuns, lo = tid * per, hi = tid < kRuns ? min(A.N, lo + per) : 0;
+        int64_t mine = 0;
+        for (int n = lo; n < hi; ++n) mine += PAGED ? cost_of(n) : tiles_of(n);
+        mine = block_scan<kThreads>(mine, total, ct.scan);
+        if (tid < kRuns) ct.before[tid] = mine;
     }
     sm100::tc_fence_before();
     __syncthreads();
     sm100::tc_fence_after();
     const uint32_t tmem = ct.tmem;
     bool ok = true;
-    int issued = 0;   // tiles asked for by the load warp
+    constexpr int kPieces = PAGED ? INT32_MAX : 1;
+    // Piece k of the block's work; chunks: from the warp that finds them; prompts: the row tile of the
+    // block's number.
+    auto piece = [&](int k, Work &w) {
+        if (PAGED) {
+            ok = attn_wait_long(&ct.work_full[k & 1], (k / 2) & 1, &g_attn_status);
+            if (ok) w = ct.work[k & 1];
+            return ok && w.some;
+        }
+        const uint32_t head = blockIdx.x % (uint32_t)A.Hkv, tile = blockIdx.x / (uint32_t)A.Hkv;
+        if (tile >= total) return false;
+        const uint32_t at = (uint32_t)total - 1 - tile;
+        int n;
+        int64_t first;
+        if (same >= 0) {
+            n = (int)(at / (uint32_t)same);
+            first = (int64_t)n * same;
+        } else {
+            n = find_sequence(ct, A.N, at, tiles_of, first);
+        }
+        fill<false>(w, A, attn_seq<false>(A, n), n, (int)(at - first), (int)head);
+        w.n_of[0] = tiles_seen(w, G, 0);
+        w.n_of[1] = tiles_seen(w, G, 1);
+        return true;
+    };
+    // the piece's entry may be written again
+    auto read = [&](int k) {
+        if (!PAGED) return;
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&ct.work_empty[k & 1]);
+    };
 
-    if (warp == kLoadWarp) {
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (PAGED && warp == kWorkWarp) {
+        // ------------------------------------------------ the next piece of work
+        // units [u, end) of heads * total
+        const int64_t all = total * A.Hkv;
+        const int64_t blocks = max((int64_t)1, min((int64_t)gridDim.x, all / 8));
+        auto edge = [&](int64_t b) { return all * b / blocks; };
+        int64_t u = 0, end = 0;
+        if (lane == 0) sh.rec[blockIdx.x * 4] = 0;
+        if (blockIdx.x < blocks) u = edge(blockIdx.x), end = edge(blockIdx.x + 1);
+        for (int k = 0;; ++k) {
+            if (k >= 2) {
+                ok = attn_wait_long(&ct.work_empty[k & 1], (k / 2 - 1) & 1, &g_attn_status);
+            }
+            Work w;
+            w.some = 0;
+            while (ok && u < end && !w.some) {
+                const int64_t head = u / total, in = u - head * total;
+                int64_t first;
+                const int n = find_sequence(ct, A.N, in, cost_of, first);
+                if (n < 0) break;
+                const Chunk c = chunk_of(A, n, few);
+                int lo = 0, hi = c.tiles;   // row tile
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (first + c.upto(mid) <= in) lo = mid; else hi = mid;
+                }
+                // its units [t0, t1); an edge next to either end counts as that end
+                const int64_t t0 = head * total + first + c.upto(lo), t1 = head * total + first + c.upto(lo + 1);
+                auto snap = [&](int64_t x) { return x <= t0 + kOver + 1 ? t0 : x >= t1 - 2 ? t1 : x; };
+                const int64_t from = blockIdx.x == 0 && u == edge(0) ? t0 : snap(u), to = end >= t1 ? t1 : snap(end);
+                u = t1;
+                if (from >= to) continue;
+                fill<true>(w, A, attn_seq<true>(A, n), n, lo, (int)head);
+                const int32_t seen[2] = {tiles_seen(w, G, 0), tiles_seen(w, G, 1)};
+                const int32_t most = max(seen[0], seen[1]);
+                // edges inside: the first belongs to the block that begins the tile
+                const int64_t b0 = ((t0 + kOver + 2) * blocks + all - 1) / all, b1 = ((t1 - 2) * blocks + all - 1) / all - 1;
+                const int32_t splits = b1 >= b0 ? (int32_t)(b1 - b0) + 2 : 1;
+                auto key = [&](int64_t x) {   // units of the tile before x -> key tiles
+                    if (x >= t1) return most;
+                    if (x <= t0 + kOver) return 0;
+                    return (int32_t)((x - t0 - kOver) * most / (t1 - t0 - kOver));
+                };
+                w.j0 = key(from);
+                const int32_t j1 = key(to);
+                w.n_of[0] = max(0, min(seen[0], j1) - w.j0);
+                w.n_of[1] = max(0, min(seen[1], j1) - w.j0);
+                if (splits > 1) {
+                    const bool begins = from == t0;
+                    w.slot = begins ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
+                    if (begins && lane == 0) {
+                        int32_t *rec = sh.rec + blockIdx.x * 4;
+                        rec[1] = n;
+                        rec[2] = lo;
+                        rec[3] = (int32_t)head;
+                        rec[0] = splits;
+                    }
+                }
+            }
+            if (lane == 0) {
+                ct.work[k & 1] = w;
+                sm100::mbar_arrive(&ct.work_full[k & 1]);
+            }
+            __syncwarp();
+            if (!w.some) break;
+        }
+    } else if (warp == kLoadWarp) {
         // ------------------------------------------------ keys and values
         const int boxes = kAttnKeys / box;             // boxes of 64 channels that make a block
         const int mine = lane / boxes, which = lane % boxes;
         const bool issues = lane < boxes * (D / 64);
-        const int loads = 2 * n;
-        const int32_t *row = PAGED ? A.table + (int64_t)part.n * A.wide : nullptr;
+        uint32_t c = 0;   // tiles asked for
         bool bad = false;
-        for (int c = 0; c < loads && ok; ++c) {
-            // order: K0, K1, V0, K2, V1, ...
-            const bool values = c == loads - 1 || (c > 0 && (c & 1) == 0);
-            const int j = j0 + (values ? (c == loads - 1 ? n - 1 : c / 2 - 1) : (c + 1) / 2);
-            int page = 0, at;
-            if (PAGED) {
-                const int64_t first = (int64_t)j * kAttnKeys + which * box;
-                page = A.P;   // past the cache: reads zeros
-                at = (int)(first % A.page);
-                if (issues && first < sq.keys) {
-                    const int p = row[first / A.page];
-                    if (p >= 0 && p < A.P) page = p; else bad = true;
+        for (int k = 0; ok && k < kPieces; ++k) {
+            Work w;
+            if (!piece(k, w)) break;
+            const int n = max(w.n_of[0], w.n_of[1]), j0 = w.j0, head = w.head, keys = w.keys;
+            const int64_t a = w.a;
+            const int32_t *row = PAGED ? A.table + (int64_t)w.n * A.wide : nullptr;
+            read(k);
+            for (int x = 0; x < 2 * n; ++x, ++c) {
+                // order: K0, K1, V0, K2, V1, ...
+                const bool last = x == 2 * n - 1, values = last || (x > 0 && (x & 1) == 0);
+                const int j = j0 + (values ? (last ? n - 1 : x / 2 - 1) : (x + 1) / 2);
+                int page = 0, at;
+                if (PAGED) {
+                    const int64_t first = (int64_t)j * kAttnKeys + which * box;
+                    page = A.P;   // past the cache: reads zeros
+                    at = (int)(first % A.page);
+                    if (issues && first < keys) {
+                        const int p = row[first / A.page];
+                        if (p >= 0 && p < A.P) page = p; else bad = true;
+                    }
+                } else {
+                    at = (int)(a + (int64_t)j * kAttnKeys);
                 }
-            } else {
-                at = (int)(sq.a + (int64_t)j * kAttnKeys);
+                const uint32_t st = c % NST;
+                if (c >= NST) ok = attn_wait(&ct.empty[st], (c / NST - 1) & 1, &g_attn_status);
+                if (!ok) break;
+                uint8_t *to = ring + st * L::kTileBytes;
+                if (lane == 0) sm100::mbar_arrive_expect_tx(&ct.full[st], L::kTileBytes);
+                __syncwarp();
+                if (issues)
+                    tma_load_4d(to + mine * L::kBlockBytes + which * box * 128, values ? &vmap : &kmap, &ct.full[st],
+                                mine * 64, head, at, page);
             }
-            const int st = c % NST;
-            if (c >= NST) ok = attn_wait(&ct.empty[st], (c / NST - 1) & 1, &g_attn_status);
-            if (!ok) break;
-            uint8_t *to = ring + st * L::kTileBytes;
-            if (lane == 0) sm100::mbar_arrive_expect_tx(&ct.full[st], L::kTileBytes);
-            __syncwarp();
-            if (issues)
-                tma_load_4d(to + mine * L::kBlockBytes + which * box * 128, values ? &vmap : &kmap, &ct.full[st],
-                            mine * 64, part.head, at, page);
-            ++issued;
         }
         if (bad) atomicOr(&g_attn_status, kCacheBadPage);
         __syncwarp();
+        // no copy may land after the block's end
+        for (uint32_t x = c > NST ? c - NST : 0; x < c; ++x) attn_wait(&ct.full[x % NST], (x / NST) & 1, &g_attn_status);
     } else if (warp == kProductWarp) {
         // ------------------------------------------------ products
         const uint32_t q_at = sm100::smem_u32(Qs), ring_at = sm100::smem_u32(ring);
-        constexpr uint32_t S[2] = {0, 128}, O[2] = {256, 256 + D};
-        auto full = [&](int c) { return attn_wait(&ct.full[c % NST], (c / NST) & 1, &g_attn_status); };
-        if (n > 0) {
-            ok = attn_wait(&ct.q_full, 0, &g_attn_status) && full(0);
-            if (ok) {
-                sm100::tc_fence_after();
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (n_of[i] == 0) continue;
-                    mma_rows<D, BF16, 128>(tmem + S[i], q_at + i * L::kTileBytes, ring_at, L::kBlockBytes, L::kBlockBytes);
-                    sm100::mma_commit_el(&ct.s_full[i]);
-                }
-                sm100::mma_commit_el(&ct.empty[0]);
-            }
-        }
-        for (int j = 0; j < n && ok; ++j) {
-            const bool more = j + 1 < n;
-            const int ck = 2 * j + 1, cv = more ? 2 * j + 2 : 2 * j + 1;
-            if (more) ok = full(ck);
-            ok = ok && full(cv);
-            if (!ok) break;
-            const uint32_t k_at = ring_at + (ck % NST) * L::kTileBytes, v_at = ring_at + (cv % NST) * L::kTileBytes;
-            const int32_t left = (int32_t)sq.keys - (j0 + j) * kAttnKeys;   // keys from this tile on
-            if (left < kAttnKeys) {
-                // value rows behind the last key hold anything
-                uint8_t *v = ring + (cv % NST) * L::kTileBytes;
-                for (int x = lane; x < (kAttnKeys - left) * (D / 8); x += 32)
-                    *reinterpret_cast<uint4 *>(v + (x % (D / 64 * 8)) / 8 * L::kBlockBytes +
-                                               (left + x / (D / 8)) * 128 + (x % 8) * 16) = make_uint4(0, 0, 0, 0);
-                sm100::fence_proxy_async_smem();
-                __syncwarp();
-            }
+        auto wait = [&](uint64_t *bar, uint32_t parity) { return attn_wait(bar, parity, &g_attn_status); };
+        auto full = [&](uint32_t c) { return wait(&ct.full[c % NST], (c / NST) & 1); };
+        auto scores = [&](int i, uint32_t c) {
+            mma_rows<D, BF16, 128>(tmem + i * 128, q_at + i * L::kTileBytes, ring_at + (c % NST) * L::kTileBytes,
+                                   L::kBlockBytes, L::kBlockBytes);
+            sm100::mma_commit_el(&ct.s_full[i]);
+        };
+        uint32_t c0 = 0;           // tiles of the pieces before
+        uint32_t done[2] = {0, 0}; // key tiles of each row tile before
+        for (int k = 0; ok && k < kPieces; ++k) {
+            Work w;
+            if (!piece(k, w)) break;
+            const int n_of[2] = {w.n_of[0], w.n_of[1]}, n = max(n_of[0], n_of[1]), j0 = w.j0, keys = w.keys;
+            ok = n == 0 || full(c0);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (j < n_of[i]) {
-                    ok = ok && attn_wait(&ct.p_ready[i], j & 1, &g_attn_status);
-                    if (!ok) break;
-                    sm100::tc_fence_after();
-#pragma unroll
-                    for (int s = 0; s < kAttnKeys / 16; ++s)
-                        mma16_ts(tmem + O[i], tmem + S[i] + s * 8, sdesc_mn(v_at + s * 2048, L::kBlockBytes),
-                                 idesc_16(BF16, 128, D, true), j > 0 || s > 0);
-                    if (j == n_of[i] - 1) sm100::mma_commit_el(&ct.o_full[i]);
-                }
-                if (j + 1 < n_of[i]) {
-                    mma_rows<D, BF16, 128>(tmem + S[i], q_at + i * L::kTileBytes, k_at, L::kBlockBytes, L::kBlockBytes);
-                    sm100::mma_commit_el(&ct.s_full[i]);
-                }
+                // (the queries of a tile are there when its results of the piece before have been read)
+                ok = ok && wait(&ct.q_full[i][k & 1], (k / 2) & 1);
+                if (!ok) break;
+                sm100::tc_fence_after();
+                if (n_of[i] > 0) scores(i, c0);
             }
-            sm100::mma_commit_el(&ct.empty[cv % NST]);
-            if (more) sm100::mma_commit_el(&ct.empty[ck % NST]);
+            // (only now: a softmax warpgroup without keys here may be a piece ahead, but not two)
+            read(k);
+            if (ok && n > 0) sm100::mma_commit_el(&ct.empty[c0 % NST]);
+            for (int j = 0; j < n && ok; ++j) {
+                const bool more = j + 1 < n;
+                const uint32_t ck = c0 + 2 * j + 1, cv = c0 + (more ? 2 * j + 2 : 2 * j + 1);
+                if (more) ok = full(ck);
+                ok = ok && full(cv);
+                if (!ok) break;
+                const uint32_t v_at = ring_at + (cv % NST) * L::kTileBytes;
+                const int32_t left = keys - (j0 + j) * kAttnKeys;   // keys from this tile on
+                if (left < kAttnKeys) {
+                    // value rows behind the last key hold anything
+                    uint8_t *v = ring + (cv % NST) * L::kTileBytes;
+                    for (int x = lane; x < (kAttnKeys - left) * (D / 8); x += 32)
+                        *reinterpret_cast<uint4 *>(v + (x % (D / 8)) / 8 * L::kBlockBytes + (left + x / (D / 8)) * 128 +
+                                                   (x % 8) * 16) = make_uint4(0, 0, 0, 0);
+                    sm100::fence_proxy_async_smem();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (j < n_of[i]) {
+                        ok = wait(&ct.p_ready[i], (done[i] + j) & 1);
+                        if (!ok) break;
+                        sm100::tc_fence_after();
+#pragma unroll
+                        for (int s = 0; s < kAttnKeys / 16; ++s)
+                            mma16_ts(tmem + 256 + i * D, tmem + i * 128 + s * 8, sdesc_mn(v_at + s * 2048, L::kBlockBytes),
+                                     idesc_16(BF16, 128, D, true), j > 0 || s > 0);
+                        if (j == n_of[i] - 1) sm100::mma_commit_el(&ct.o_full[i]);
+                    }
+                    if (j + 1 < n_of[i]) scores(i, ck);
+                }
+                if (!ok) break;
+                sm100::mma_commit_el(&ct.empty[cv % NST]);
+                if (more) sm100::mma_commit_el(&ct.empty[ck % NST]);
+            }
+            c0 += 2 * n;
+            done[0] += n_of[0];
+            done[1] += n_of[1];
         }
         // whatever was issued is over before the block ends
         sm100::mma_commit_el(&ct.done);
         attn_wait(&ct.done, 0, &g_attn_status);
-    } else {
+    } else if (warp < 8) {
         // ------------------------------------------------ softmax: one thread a row
-        {
-            const uint16_t *q = static_cast<const uint16_t *>(A.q);
-            constexpr int CH = D / 8;   // 16-byte pieces of a row
-            for (int x = tid; x < kTileRows * CH; x += 256) {
-                const int r = x / CH, c = x % CH;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < rows) {
-                    const int fr = part.tile * kTileRows + r, tok = fr / G;
-                    v = __ldg(reinterpret_cast<const uint4 *>(q + (sq.a + tok) * A.q_t +
-                                                              (int64_t)(part.head * G + fr - tok * G) * A.q_h + c * 8));
-                }
-                *reinterpret_cast<uint4 *>(Qs + (r >> 7) * L::kTileBytes + (c >> 3) * L::kBlockBytes + (r & 127) * 128 +
-                                           (((c & 7) ^ (r & 7)) << 4)) = v;
-            }
-            sm100::fence_proxy_async_smem();
-            sm100::mbar_arrive(&ct.q_full);
-        }
-        const int i = warp >> 2, r = tid;                    // row tile, row of the block
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int i = warp >> 2, rt = tid & 127;             // row tile, row of it
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t S = lanes + i * 128, O = lanes + 256 + i * D;
-        const int fr = part.tile * kTileRows + r, tok = fr / G, g = fr - tok * G;
-        const bool live = r < rows;
-        const int32_t seen = live ? max(0, min(behind + tok + 1, (int32_t)sq.keys)) : 0;
         const float c = A.scale_log2;
-        float m = -INFINITY, l = 0.f;
-        for (int j = 0; j < n_of[i]; ++j) {
-            ok = attn_wait(&ct.s_full[i], j & 1, &g_attn_status);
-            if (!ok) break;
-            sm100::tc_fence_after();
-            float s[128];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_ld32_nowait(S + x * 32, s + x * 32);
-            tmem_wait_ld(s);
-            const int32_t vis = seen - (j0 + j) * kAttnKeys;
-            if (__any_sync(0xffffffffu, vis < kAttnKeys)) {
-#pragma unroll
-                for (int x = 0; x < 128; ++x) s[x] = x < vis ? s[x] : -INFINITY;
-            }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int x = 4; x < 128; x += 4)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], s[x + y]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const bool grown = top > m && (top - m) * c > kGrowth;   // also from -inf
-            if (j > 0 && __any_sync(0xffffffffu, grown)) {
-                // S of this tile is complete, and so, issued before it, is the product before
-                const float f = grown ? ex2((m - top) * c) : 1.f;
-                l *= f;
+        const uint64_t c2 = pack2(c, c);
+        uint32_t done = 0, outs = 0;   // key tiles, and pieces with any, before
+        for (int k = 0; ok && k < kPieces; ++k) {
+            Work w;
+            if (!piece(k, w)) break;
+            const int32_t tile = w.tile, head = w.head, rows = w.rows, j0 = w.j0, mine = i ? w.n_of[1] : w.n_of[0], slot = w.slot, keys = w.keys;
+            const int32_t behind = keys - w.tokens;   // key index that the first token sees last
+            const int64_t a = w.a;
+            read(k);
+            if (k > 0) sm100::named_sync(1 + i, 128);   // the tile's results have left its place
+            {
+                // 16 bytes a thread and pass, all passes in flight; a loop, because code that runs once a
+                // block is paid by its length
+                constexpr int CH = D / 8, PER = 128 / CH;   // 16-byte pieces of a row; rows a pass
+                const int p = rt % CH;
+                int r = rt / CH;
+                Row at(tile * kTileRows + i * 128 + r, G);
+                const Row step(PER, G);
+                const uint16_t *q = static_cast<const uint16_t *>(A.q) + a * A.q_t + (int64_t)head * G * A.q_h + p * 8;
+                uint32_t to = sm100::smem_u32(Qs + i * L::kTileBytes + (p >> 3) * L::kBlockBytes + ((p & 7) << 4));
 #pragma unroll 1
-                for (int x = 0; x < D; x += 16) {
-                    float o[16];
-                    sm100::tmem_ld16(O + x, o);
-#pragma unroll
-                    for (int y = 0; y < 16; ++y) o[y] *= f;
-                    sm100::tmem_st16(O + x, o);
+                for (int x = 0; x < CH; ++x, r += PER) {
+                    const bool some = i * 128 + r < rows;   // else zeros
+                    cp_async16(to + r * 128 ^ ((r & 7) << 4), some ? q + at.tok * A.q_t + at.g * A.q_h : q, some ? 16 : 0);
+                    at.add(step, G);
                 }
+                sm100::cp_async_wait_all();
+                sm100::fence_proxy_async_smem();
+                sm100::mbar_arrive(&ct.q_full[i][k & 1]);
+            }
+            const int r = i * 128 + rt, fr = tile * kTileRows + r, tok = fr / G, g = fr - tok * G;
+            const bool live = r < rows;
+            const int32_t seen = live ? max(0, min(behind + tok + 1, keys)) : 0;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < mine; ++j) {
+                ok = attn_wait(&ct.s_full[i], (done + j) & 1, &g_attn_status);
+                if (!ok) break;
+                sm100::tc_fence_after();
+                float s[128];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tmem_ld32_nowait(S + x * 32, s + x * 32);
+                tmem_wait_ld(s);
+                const int32_t vis = seen - (j0 + j) * kAttnKeys;
+                if (__any_sync(0xffffffffu, vis < kAttnKeys)) {
+#pragma unroll
+                    for (int x = 0; x < 128; ++x) s[x] = x < vis ? s[x] : -INFINITY;
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int x = 4; x < 128; x += 4)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], s[x + y]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const bool grown = top > m && (top - m) * c > kGrowth;   // also from -inf
+                if (j > 0 && __any_sync(0xffffffffu, grown)) {
+                    // S of this tile is complete, and so, issued before it, is the product before
+                    const float f = grown ? ex2((m - top) * c) : 1.f;
+                    l *= f;
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 16) {
+                        float o[16];
+                        sm100::tmem_ld16(O + x, o);
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) o[y] *= f;
+                        sm100::tmem_st16(O + x, o);
+                    }
+                    sm100::tmem_wait_st();
+                }
+                if (grown) m = top;
+                const float shift = m == -INFINITY ? 0.f : -m * c;
+                const uint64_t s2 = pack2(shift, shift);
+                uint64_t sum[2] = {0, 0};
+                uint32_t p[64];
+#pragma unroll
+                for (int x = 0; x < 64; ++x) {
+                    float y, z;
+                    unpack2(fma2(pack2(s[2 * x], s[2 * x + 1]), c2, s2), y, z);
+                    y = ex2(y);
+                    z = ex2(z);
+                    sum[x & 1] = add2(sum[x & 1], pack2(y, z));
+                    p[x] = pack16<BF16>(y, z);
+                    if ((x & 15) == 15) tmem_st16_raw(S + (x & ~15), p + (x & ~15));
+                }
+                float y, z;
+                unpack2(add2(sum[0], sum[1]), y, z);
+                l += y + z;
                 sm100::tmem_wait_st();
+                sm100::tc_fence_before();
+                sm100::mbar_arrive(&ct.p_ready[i]);
             }
-            if (grown) m = top;
-            const float shift = m == -INFINITY ? 0.f : -m * c;
-            const uint64_t c2 = pack2(c, c), s2 = pack2(shift, shift);
-            uint64_t sum[2] = {0, 0};
-            uint32_t p[64];
-#pragma unroll
-            for (int x = 0; x < 64; ++x) {
-                float a, b;
-                unpack2(fma2(pack2(s[2 * x], s[2 * x + 1]), c2, s2), a, b);
-                a = ex2(a);
-                b = ex2(b);
-                sum[x & 1] = add2(sum[x & 1], pack2(a, b));
-                p[x] = pack16<BF16>(a, b);
-                if ((x & 15) == 15) tmem_st16_raw(S + (x & ~15), p + (x & ~15));
+            done += mine;
+            if (mine > 0) {
+                ok = ok && attn_wait(&ct.o_full[i], outs++ & 1, &g_attn_status);
+                sm100::tc_fence_after();
             }
-            float a, b;
-            unpack2(add2(sum[0], sum[1]), a, b);
-            l += a + b;
-            sm100::tmem_wait_st();
-            sm100::tc_fence_before();
-            sm100::mbar_arrive(&ct.p_ready[i]);
-        }
-        if (n_of[i] > 0) {
-            ok = ok && attn_wait(&ct.o_full[i], 0, &g_attn_status);
-            sm100::tc_fence_after();
-        }
-        // ------------------------------------------------ results
-        // With m still -inf the row has seen no key (or scores of -inf only): out 0.  A sum
-        // that is NaN reaches the row through 1 / l.
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-        const float lse = l > 0.f || l != l ? m * A.scale + logf(l) : -INFINITY;
-        const bool share = PAGED && part.slot >= 0;
-        const int64_t at = sq.a + tok;
-        const int h = part.head * G + g;
-        if (ok) {
+            if (!ok) break;
+            // ------------------------------------------------ results
+            // A row whose sum is 0 has seen no key (or scores of -inf only): out 0.  A sum that is
+            // NaN reaches the row through 1 / l.
+            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+            const float lse = l > 0.f || l != l ? m * A.scale + logf(l) : -INFINITY;
+            const bool share = PAGED && slot >= 0;
+            const int64_t at = a + tok;
+            const int h = head * G + g;
+            // Through the tile's queries in shared memory (their products are over), so that a warp
+            // writes whole rows.
+            uint8_t *stage = Qs + i * L::kTileBytes + (rt & ~31) * (D * 2);
+            const bool f32 = share || A.out_dtype == KDA_DTYPE_F32;
+            const int rounds = f32 ? 2 : 1, width = f32 ? D / 2 : D;   // D * 2 bytes of a row a round
 #pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
-                float o[32];
-                if (n_of[i] > 0) {
-                    tmem_ld32_nowait(O + x, o);
-                    tmem_wait_ld(o);
-                } else {
+            for (int round = 0; round < rounds; ++round) {
+#pragma unroll 1
+                for (int x = 0; x < width; x += 32) {
+                    float o[32];
+                    if (mine > 0) {
+                        tmem_ld32_nowait(O + round * width + x, o);
+                        tmem_wait_ld(o);
+                    }
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) o[y] = 0.f;
+                    for (int y = 0; y < 32; ++y) o[y] = inv == 0.f ? 0.f : o[y] * inv;
+                    // piece x / 8 (16-bit) or x / 4 (fp32) of the row, turned within eight
+                    uint8_t *row = stage + lane * (D * 2);
+                    if (f32) {
+#pragma unroll
+                        for (int y = 0; y < 32; y += 4)
+                            *reinterpret_cast<float4 *>(row + ((((x + y) >> 2) ^ (lane & 7)) << 4)) =
+                                make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; y += 8)
+                            *reinterpret_cast<uint4 *>(row + ((((x + y) >> 3) ^ (lane & 7)) << 4)) =
+                                make_uint4(pack16<BF16>(o[y], o[y + 1]), pack16<BF16>(o[y + 2], o[y + 3]),
+                                           pack16<BF16>(o[y + 4], o[y + 5]), pack16<BF16>(o[y + 6], o[y + 7]));
+                    }
                 }
-#pragma unroll
-                for (int y = 0; y < 32; ++y) o[y] = inv == 0.f ? 0.f : o[y] * inv;
-                if (!live) continue;
-#pragma unroll
-                for (int y = 0; y < 32; y += 8) {
-                    if (share)
-                        store8<BF16>(sh.out, true, ((int64_t)part.slot * kTileRows + r) * D + x + y, o + y);
-                    else
-                        store8<BF16>(A.out, A.out_dtype == KDA_DTYPE_F32, (at * A.Hq + h) * D + x + y, o + y);
+                __syncwarp();
+                constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;   // lanes a row, rows a pass
+                const int p = lane % LANES;
+                int rr = lane / LANES, br = i * 128 + (rt & ~31) + rr;   // row of the warp, of the block
+                Row here(tile * kTileRows + br, G);
+                const Row step(AT_ONCE, G);
+                uint8_t *to = static_cast<uint8_t *>(share ? (void *)sh.out : A.out) + round * (D * 2) + p * 16;
+#pragma unroll 1
+                for (; rr < 32 && br < rows; rr += AT_ONCE, br += AT_ONCE) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * (D * 2) + ((p ^ (rr & 7)) << 4));
+                    const int64_t row = share ? (int64_t)slot * kTileRows + br : (a + here.tok) * A.Hq + head * G + here.g;
+                    *reinterpret_cast<uint4 *>(to + row * rounds * (D * 2)) = v;
+                    here.add(step, G);
                 }
+                __syncwarp();
             }
             if (live) {
                 if (share)
-                    sh.lse[(int64_t)part.slot * kTileRows + r] = lse;
+                    sh.lse[(int64_t)slot * kTileRows + r] = lse;
                 else if (A.lse)
                     A.lse[at * A.Hq + h] = lse;
             }
-        }
-        if (PAGED && share && tid == 0) {
-            int32_t *rec = sh.rec + (int64_t)part.slot * 8;
-            rec[0] = part.n;
-            rec[1] = part.tile;
-            rec[2] = part.head;
-            rec[3] = part.split;
-            rec[4] = part.splits;
+            sm100::tc_fence_before();
         }
         sm100::tc_fence_before();
-    }
-    if (warp == kLoadWarp) {
-        // no copy may land after the block's end: the last ones of each stage
-        for (int c = max(0, issued - NST); c < issued; ++c) attn_wait(&ct.full[c % NST], (c / NST) & 1, &g_attn_status);
     }
     __syncthreads();
     if (warp == kProductWarp) sm100::tmem_dealloc(tmem, 512);
 }
 
-// Joins the shares of split row tiles: out = sum_s w_s out_s with w_s = e^(lse_s - lse) in
-// the order of the shares.  One warp a row, four channels a lane.
+// Joins the shares of a split row tile: out = sum_s w_s out_s with w_s = e^(lse_s - lse), in the
+// order of the shares.  One warp has a row, or the four of a block together where there are many
+// shares (a lane has D / 32 channels; all loads of a warp are in flight at once).
 template <int D, bool BF16>
-__global__ void __launch_bounds__(128) kda_attn_join_kernel(const Attn A, const Shares sh, const int tile_rows) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int slot = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (slot >= *sh.count) return;
-    const int32_t *rec = sh.rec + (int64_t)slot * 8;
-    if (rec[3] != 0) return;
-    const int n = rec[0], tile = rec[1], head = rec[2], splits = rec[4];
-    int64_t a, b;
-    seq_bounds(A.cu, n, A.T, A.seq_len, a, b);
-    const int64_t rows = (b - a) * A.G - (int64_t)tile * tile_rows;
-    for (int r = blockIdx.y * 4 + warp; r < tile_rows && r < rows; r += gridDim.y * 4) {
-        const float *lse = sh.lse + (int64_t)slot * tile_rows + r;
-        const float *out = sh.out + ((int64_t)slot * tile_rows + r) * D;
-        float top = -INFINITY;
-        for (int s = lane; s < splits; s += 32) top = fmaxf(top, lse[(int64_t)s * tile_rows]);
+__device__ __forceinline__ void join_row(const Attn &A, const float *lse, const float *out, int rows, int second, int step,
+                                         int splits, int64_t at, bool together, float (*part)[D + 2]) {
+    // the first share's row is at lse and out; the others' slots (of `rows` rows) follow
+    auto off = [&](int s) { return s ? (int64_t)(second + (s - 1) * step) * rows : 0; };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = together ? warp : 0, stride = together ? 4 : 1;
+    constexpr int PER = D / 32;
+    float top = -INFINITY;
+    for (int s = lane; s < splits; s += 32) top = fmaxf(top, lse[off(s)]);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float ref = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-        for (int s = lane; s < splits; s += 32) sum += __expf(lse[(int64_t)s * tile_rows] - ref);
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, acc[PER] = {};
+    for (int s0 = first; s0 < splits; s0 += stride * 8) {
+        float w[8], v[8][PER];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        constexpr int PER = D / 32;
-        float acc[PER] = {};
-#pragma unroll 4
-        for (int s = 0; s < splits; ++s) {
-            const float w = __expf(lse[(int64_t)s * tile_rows] - ref);
-            const float *o = out + (int64_t)s * tile_rows * D + lane * PER;
-            float v[PER];
-            if (PER == 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(o);
-                v[0] = x.x, v[1] = x.y, v[2 % PER] = x.z, v[3 % PER] = x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2 *>(o);
-                v[0] = x.x, v[1] = x.y;
+        for (int x = 0; x < 8; ++x) {
+            const int s = s0 + x * stride;
+            w[x] = s < splits ? lse[off(s)] : -INFINITY;
+#pragma unroll
+            for (int y = 0; y < PER; y += 2) {
+                const float2 z = s < splits ? *reinterpret_cast<const float2 *>(out + off(s) * D + lane * PER + y)
+                                            : make_float2(0.f, 0.f);
+                v[x][y] = z.x;
+                v[x][y + 1] = z.y;
             }
-#pragma unroll
-            for (int y = 0; y < PER; ++y) acc[y] += w == 0.f ? 0.f : w * v[y];
         }
-        const bool none = !(sum > 0.f) && sum == sum;   // no key seen anywhere
-        const float inv = none ? 0.f : 1.f / sum;
-        const int64_t fr = (int64_t)tile * tile_rows + r, tok = fr / A.G;
-        const int64_t at = (a + tok) * A.Hq + head * A.G + (fr - tok * A.G);
-        if (A.out_dtype == KDA_DTYPE_F32) {
 #pragma unroll
-            for (int y = 0; y < PER; ++y) static_cast<float *>(A.out)[at * D + lane * PER + y] = acc[y] * inv;
-        } else {
+        for (int x = 0; x < 8; ++x) {
+            w[x] = __expf(w[x] - ref);
+            sum += w[x];
 #pragma unroll
-            for (int y = 0; y < PER; y += 2)
-                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(A.out) + at * D + lane * PER + y) =
-                    pack16<BF16>(acc[y] * inv, acc[y + 1] * inv);
+            for (int y = 0; y < PER; ++y) acc[y] += w[x] == 0.f ? 0.f : w[x] * v[x][y];
         }
-        if (lane == 0 && A.lse) A.lse[at] = none ? -INFINITY : top + logf(sum);
+    }
+    if (together) {
+        if (lane == 0) part[warp][D] = sum;
+#pragma unroll
+        for (int y = 0; y < PER; ++y) part[warp][lane * PER + y] = acc[y];
+        __syncthreads();
+        sum = (part[0][D] + part[1][D]) + (part[2][D] + part[3][D]);
+#pragma unroll
+        for (int y = 0; y < PER; ++y) {
+            const int ch = lane * PER + y;
+            acc[y] = (part[0][ch] + part[1][ch]) + (part[2][ch] + part[3][ch]);
+        }
+        __syncthreads();
+        if (warp != 0) return;
+    }
+    const bool none = !(sum > 0.f) && sum == sum;   // no key seen anywhere
+    const float inv = none ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int y = 0; y < PER; y += 2) {
+        if (A.out_dtype == KDA_DTYPE_F32)
+            *reinterpret_cast<float2 *>(static_cast<float *>(A.out) + at * D + lane * PER + y) =
+                make_float2(acc[y] * inv, acc[y + 1] * inv);
+        else
+            *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(A.out) + at * D + lane * PER + y) =
+                pack16<BF16>(acc[y] * inv, acc[y + 1] * inv);
+    }
+    if (lane == 0 && A.lse) A.lse[at] = none ? -INFINITY : top + logf(sum);
+}
+
+// Shares of kda_attn_tc_kernel: the block that began a row tile left a record; its share is the
+// second of that block's two slots, the others are the first of the next blocks'.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) kda_attn_join_kernel(const Attn A, const Shares sh) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int b = blockIdx.x;
+    const int32_t splits = sh.rec[b * 4];
+    if (splits == 0) return;
+    const int n = sh.rec[b * 4 + 1], tile = sh.rec[b * 4 + 2], head = sh.rec[b * 4 + 3];
+    int64_t a, e;
+    seq_bounds(A.cu, n, A.T, A.seq_len, a, e);
+    const int64_t rows = (e - a) * A.G - (int64_t)tile * kTileRows;
+    for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < kTileRows && r < rows; r += gridDim.y * 4) {
+        const int64_t fr = (int64_t)tile * kTileRows + r, tok = fr / A.G;
+        const int64_t slot = 2 * (int64_t)b + 1;
+        join_row<D, BF16>(A, sh.lse + slot * kTileRows + r, sh.out + (slot * kTileRows + r) * D, kTileRows, 1, 2, splits,
+                          (a + tok) * A.Hq + head * A.G + (fr - tok * A.G), false, nullptr);
     }
 }
 
@@ -501,10 +762,14 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     int64_t slots;
     const bool some = attn_split_part<kFewThreads>(A.N, A.Hkv, blockIdx.x, slots_at_once, 8, 4, need, &ct.part, ct.scan,
                                                    &slots);
-    if (blockIdx.x == 0 && tid == 0) *sh.count = (int32_t)slots;
     if (!some) return;
     const AttnPart part = ct.part;
     const AttnSeq sq = attn_seq<true>(A, part.n);
+    if (part.split == 0 && tid == 0) {
+        int32_t *rec = sh.rec + ((int64_t)part.n * A.Hkv + part.head) * 4;
+        rec[0] = part.splits;
+        rec[1] = part.slot;
+    }
     const int32_t tokens = (int32_t)(sq.b - sq.a), rows = tokens * G;
     const int32_t behind = (int32_t)sq.keys - tokens, keys = (int32_t)sq.keys;
     const int n = part.j1 - part.j0;
@@ -694,13 +959,25 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             if (ch == 0 && A.lse) A.lse[at] = lse;
         }
     }
-    if (part.slot >= 0 && tid == 0) {
-        int32_t *rec = sh.rec + (int64_t)part.slot * 8;
-        rec[0] = part.n;
-        rec[1] = 0;
-        rec[2] = part.head;
-        rec[3] = part.split;
-        rec[4] = part.splits;
+}
+
+// Joins the shares of kda_attn_few_kernel: a block has the rows of one sequence and key head,
+// every gridDim.y-th of them.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) kda_attn_few_join_kernel(const Attn A, const Shares sh) {
+    __shared__ float part[4][D + 2];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int n = blockIdx.x / A.Hkv, head = blockIdx.x - n * A.Hkv;
+    int64_t a, b;
+    seq_bounds(A.cu, n, A.T, A.seq_len, a, b);
+    const int64_t rows = (b - a) * A.G;
+    if (rows == 0 || rows > kFewRows) return;
+    const int32_t splits = sh.rec[(int64_t)blockIdx.x * 4], slot = sh.rec[(int64_t)blockIdx.x * 4 + 1];
+    if (splits <= 1) return;
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        const int tok = r / A.G;
+        join_row<D, BF16>(A, sh.lse + (int64_t)slot * kFewRows + r, sh.out + ((int64_t)slot * kFewRows + r) * D, kFewRows, 1, 1,
+                          splits, (a + tok) * A.Hq + head * A.G + (r - tok * A.G), true, part);
     }
 }
 
@@ -709,57 +986,34 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 // only (unless all are alike): each kernel passes by those that are the other's.
 struct Sizes {
     bool many, few;               // launch the kernel of many rows, of few rows
-    int64_t tiles, few_tiles;     // upper bounds on row tiles times heads
-    int64_t parts, few_parts;     // blocks
-    int64_t slots, few_slots;     // shares
+    int64_t few_tiles, few_parts, few_slots;
 };
 constexpr int kFewAtOnce = 304;   // two blocks an SM
-
-int64_t shares_bound(int64_t tiles, int at_once, int waves) {
-    // a row tile that is cut has more than one run of keys: at most two parts a run
-    const int64_t parts = attn_parts(tiles, at_once, waves);
-    return parts < 2 * (int64_t)at_once * waves ? parts : 2 * (int64_t)at_once * waves;
-}
 
 Sizes sizes_of(const Attn &A) {
     Sizes z{};
     if (A.N == 0 || A.T == 0) return z;
-    const int64_t rows = (int64_t)A.T * A.G;
-    if (A.cu) {
-        z.few = true;
-        z.many = rows > kFewRows;
-        z.tiles = rows / kTileRows + A.N;
-        z.few_tiles = A.N;
-    } else {
-        z.few = A.seq_len * A.G <= kFewRows;
-        z.many = !z.few;
-        z.tiles = (A.seq_len * A.G + kTileRows - 1) / kTileRows * A.N;
-        z.few_tiles = A.N;
-    }
-    z.tiles *= A.Hkv;
-    z.few_tiles *= A.Hkv;
-    if (z.many) {
-        // the device knows the real number of row tiles: few of them, and it cuts for one
-        // wave; more, for three
-        z.parts = z.tiles * 2 <= 152 ? 152 : z.tiles + 3 * 152;
-        z.slots = shares_bound(z.tiles, 152, 3);
-    }
+    z.few = A.cu ? true : A.seq_len * A.G <= kFewRows;
+    z.many = A.cu ? (int64_t)A.T * A.G > kFewRows : !z.few;
     if (z.few) {
+        z.few_tiles = (int64_t)A.N * A.Hkv;
         z.few_parts = attn_parts(z.few_tiles, kFewAtOnce, 8);
-        z.few_slots = shares_bound(z.few_tiles, kFewAtOnce, 8);
+        // a sequence that is cut has more than one run of keys: at most two parts a run
+        z.few_slots = z.few_parts < 16 * kFewAtOnce ? z.few_parts : 16 * kFewAtOnce;
     }
     return z;
 }
 
 int64_t up(int64_t x) { return (x + 255) / 256 * 256; }
-int64_t shares_bytes(int64_t slots, int rows, int d) { return 256 + up(slots * 32) + up(slots * rows * 4) + slots * rows * d * 4; }
+int64_t shares_bytes(int64_t records, int64_t slots, int rows, int d) {
+    return up(records * 16) + up(slots * rows * 4) + up(slots * rows * d * 4);
+}
 
-Shares shares_at(char *ws, int64_t slots, int rows) {
+Shares shares_at(char *ws, int64_t records, int64_t slots, int rows) {
     Shares s;
-    s.count = reinterpret_cast<int32_t *>(ws);
-    s.rec = reinterpret_cast<int32_t *>(ws + 256);
-    s.lse = reinterpret_cast<float *>(ws + 256 + up(slots * 32));
-    s.out = reinterpret_cast<float *>(ws + 256 + up(slots * 32) + up(slots * rows * 4));
+    s.rec = reinterpret_cast<int32_t *>(ws);
+    s.lse = reinterpret_cast<float *>(ws + up(records * 16));
+    s.out = reinterpret_cast<float *>(ws + up(records * 16) + up(slots * rows * 4));
     return s;
 }
 
@@ -809,16 +1063,17 @@ cudaError_t paged(const Attn &A, char *ws, cudaStream_t stream) {
         if (!kda_make_attn_map(&km, A.k, BF16, D, A.Hkv, A.page, A.P, A.k_h, A.k_t, A.k_p, box) ||
             !kda_make_attn_map(&vm, A.v, BF16, D, A.Hkv, A.page, A.P, A.v_h, A.v_t, A.v_p, box))
             return cudaErrorInvalidValue;
-        const Shares sh = shares_at(ws, z.few_slots, kFewRows);
+        const Shares sh = shares_at(ws, z.few_tiles, z.few_slots, kFewRows);
         const auto kernel = kda_attn_few_kernel<D, BF16>;
         e = roomy(kernel, FewLay<D>::kSmem);
         if (e == cudaSuccess)
             e = launch(false, kernel, dim3((unsigned)z.few_parts), kFewThreads, FewLay<D>::kSmem, stream, km, vm, A, sh,
                        box, kFewAtOnce);
         if (e == cudaSuccess)
-            e = launch(true, kda_attn_join_kernel<D, BF16>, dim3((unsigned)z.few_slots, 4), 128, 0, stream, A, sh,
-                       kFewRows);
-        ws += up(shares_bytes(z.few_slots, kFewRows, D));
+            e = launch(true, kda_attn_few_join_kernel<D, BF16>,
+                       dim3((unsigned)z.few_tiles, (unsigned)(z.few_tiles < kFewAtOnce ? (A.G < kFewRows ? A.G : kFewRows) : 1)),
+                       128, 0, stream, A, sh);
+        ws += shares_bytes(z.few_tiles, z.few_slots, kFewRows, D);
     }
     if (z.many && e == cudaSuccess) {
         const int box = A.page < kAttnKeys ? A.page : kAttnKeys;
@@ -826,15 +1081,14 @@ cudaError_t paged(const Attn &A, char *ws, cudaStream_t stream) {
         if (!kda_make_attn_map(&km, A.k, BF16, D, A.Hkv, A.page, A.P, A.k_h, A.k_t, A.k_p, box) ||
             !kda_make_attn_map(&vm, A.v, BF16, D, A.Hkv, A.page, A.P, A.v_h, A.v_t, A.v_p, box))
             return cudaErrorInvalidValue;
-        const Shares sh = shares_at(ws, z.slots, kTileRows);
+        const Shares sh = shares_at(ws, kSMs, 2 * kSMs, kTileRows);
         const auto kernel = kda_attn_tc_kernel<D, BF16, true>;
         e = roomy(kernel, Lay<D>::kSmem);
         if (e == cudaSuccess)
-            e = launch(false, kernel, dim3((unsigned)z.parts), kThreads, Lay<D>::kSmem, stream, km, vm, A, sh, box,
+            e = launch(false, kernel, dim3(kSMs), kThreads, Lay<D>::kSmem, stream, km, vm, A, sh, box,
                        z.few ? kFewRows : 0);
         if (e == cudaSuccess)
-            e = launch(true, kda_attn_join_kernel<D, BF16>, dim3((unsigned)z.slots, 16), 128, 0, stream, A, sh,
-                       kTileRows);
+            e = launch(true, kda_attn_join_kernel<D, BF16>, dim3(kSMs, 16), 128, 0, stream, A, sh);
     }
     return e;
 }
@@ -843,8 +1097,8 @@ cudaError_t paged(const Attn &A, char *ws, cudaStream_t stream) {
 
 int64_t kda_attn_paged_ws(const Attn &A) {
     const Sizes z = sizes_of(A);
-    return (z.few ? up(shares_bytes(z.few_slots, kFewRows, A.d)) : 0) +
-           (z.many ? up(shares_bytes(z.slots, kTileRows, A.d)) : 0);
+    return (z.few ? shares_bytes(z.few_tiles, z.few_slots, kFewRows, A.d) : 0) +
+           (z.many ? shares_bytes(kSMs, 2 * kSMs, kTileRows, A.d) : 0);
 }
 
 cudaError_t kda_launch_attn_prefill(const Attn &A, cudaStream_t stream) {

@@ -114,23 +114,38 @@ __device__ __forceinline__ bool attn_split_part(int N, int heads, int64_t index,
 }
 
 // Tile number `index` of `heads` heads (head fastest), from the first tile to the last or, with
-// `reverse`, from the last to the first: what takes longest starts first.
+// `reverse`, from the last to the first: what takes longest starts first.  `same` >= 0: every
+// sequence has that many tiles.
 template <int THREADS, typename Tiles>
-__device__ __forceinline__ bool attn_whole_part(int N, int heads, int64_t index, bool reverse, Tiles tiles_of,
+__device__ __forceinline__ bool attn_whole_part(int N, int heads, uint32_t index, bool reverse, int same, Tiles tiles_of,
                                                 AttnPart *part, int64_t *sh) {
+    const uint32_t head = index % (uint32_t)heads, tile = index / (uint32_t)heads;
+    if (same >= 0) {
+        const uint32_t total = (uint32_t)N * (uint32_t)same;   // (fits: the grid holds that many blocks)
+        if (threadIdx.x == 0 && tile < total) {
+            const uint32_t at = reverse ? total - 1 - tile : tile;
+            part->n = (int32_t)(at / (uint32_t)same);
+            part->head = (int32_t)head;
+            part->tile = (int32_t)(at % (uint32_t)same);
+            part->slot = -1;
+            part->splits = 1;
+        }
+        __syncthreads();
+        return tile < total;
+    }
     const int per = (N + THREADS - 1) / THREADS;
     const int lo = (int)threadIdx.x * per, hi = min(N, lo + per);
     int64_t tiles = 0, total;
     for (int n = lo; n < hi; ++n) tiles += tiles_of(n);
     int64_t before = block_scan<THREADS>(tiles, total, sh);
-    if (index >= total * heads) return false;
-    const int64_t at = reverse ? total - 1 - index / heads : index / heads;
+    if (tile >= total) return false;
+    const int64_t at = reverse ? total - 1 - tile : tile;
     if (at >= before && at < before + tiles) {
         for (int n = lo; n < hi; ++n) {
             const int64_t x = tiles_of(n);
             if (at < before + x) {
                 part->n = n;
-                part->head = (int32_t)(index % heads);
+                part->head = (int32_t)head;
                 part->tile = (int32_t)(at - before);
                 part->slot = -1;
                 part->splits = 1;
