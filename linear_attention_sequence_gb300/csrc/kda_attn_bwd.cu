@@ -47,17 +47,20 @@ template <int D>
 struct Lay {
     static constexpr int kBytes = kTile * D * 2;   // a tile of 128 rows
     static constexpr int kBlock = kTile * 128;     // 64 channels of it
-    static constexpr int kPairs = D == 128 ? 2 : 4;   // pairs of tiles in flight
-    static constexpr int kSmem = 1024 + (2 + 2 * kPairs) * kBytes;
+    // Two rings of tiles.  A: queries (key blocks) or keys (query blocks), held from the scores to the
+    // last product of a step; B: dO or values, held for less.
+    static constexpr int kA = D == 128 ? 3 : 4, kB = D == 128 ? 2 : 4;
+    static constexpr int kTiles = (2 + kA + kB) * kBytes;
 };
+constexpr int kStats = 2;   // steps of row statistics in flight
 
 struct alignas(16) Control {
-    uint64_t own_full, a_full[4], a_empty[4], b_full[4], b_empty[4], stat_full[4], stat_empty[4];
+    uint64_t own_full, a_full[4], a_empty[4], b_full[4], b_empty[4], stat_full[kStats], stat_empty[kStats];
     uint64_t s_full[2], p_ready, dp_full, dp_free, ds_ready[2], done;
     uint32_t tmem;
     AttnPart part;
     int64_t scan[kThreads / 32];
-    alignas(16) float stat[4][2][kTile];   // read as float4
+    alignas(16) float stat[kStats][2][kTile];   // read as float4
 };
 static_assert(offsetof(Control, stat) % 16 == 0 && alignof(Control) % 16 == 0, "vector reads of stat");
 
@@ -157,9 +160,9 @@ template <int D, bool BF16>
 __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CUtensorMap *vm, const CUtensorMap *om,
                           const Attn &A, const Grads &B, Control &ct, uint8_t *base, const AttnSeq &sq, uint32_t tmem, int warp) {
     using L = Lay<D>;
-    constexpr int NST = L::kPairs;
+    constexpr int NA = L::kA, NB = L::kB;
     const int lane = threadIdx.x & 31;
-    uint8_t *Ks = base, *Vs = base + L::kBytes, *ring = base + 2 * L::kBytes;   // pairs: queries, dO
+    uint8_t *Ks = base, *Vs = base + L::kBytes, *ra = base + 2 * L::kBytes, *rb = ra + NA * L::kBytes;   // queries, dO
     const int kt = ct.part.tile, hk = ct.part.head, G = A.G;
     const int len = (int)(sq.b - sq.a), tiles = (len + kTile - 1) / kTile;
     const int per = tiles - kt, n = per * G;   // step j: head j / per of the group, query tile kt + j % per
@@ -177,32 +180,32 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
         __syncwarp();
         int a = 0, b = 0;   // tiles issued
         for (int j = 0; j < n; ++j) {
-            const int st = j % NST, h = hk * G + j / per;
+            const int sa = j % NA, sb = j % NB, h = hk * G + j / per;
             const int64_t row = sq.a + (int64_t)(kt + j % per) * kTile;
-            if (j >= NST) ok = wait(&ct.a_empty[st], j / NST - 1);
+            if (j >= NA) ok = wait(&ct.a_empty[sa], j / NA - 1);
             if (!ok) break;
             if (lane == 0) {
-                sm100::mbar_arrive_expect_tx(&ct.a_full[st], L::kBytes);
-                load_tile<D>(ring + 2 * st * L::kBytes, qm, &ct.a_full[st], h, row);
+                sm100::mbar_arrive_expect_tx(&ct.a_full[sa], L::kBytes);
+                load_tile<D>(ra + sa * L::kBytes, qm, &ct.a_full[sa], h, row);
             }
             __syncwarp();
             ++a;
-            if (j >= NST) ok = wait(&ct.b_empty[st], j / NST - 1);
+            if (j >= NB) ok = wait(&ct.b_empty[sb], j / NB - 1);
             if (!ok) break;
             if (lane == 0) {
-                sm100::mbar_arrive_expect_tx(&ct.b_full[st], L::kBytes);
-                load_tile<D>(ring + (2 * st + 1) * L::kBytes, om, &ct.b_full[st], h, row);
+                sm100::mbar_arrive_expect_tx(&ct.b_full[sb], L::kBytes);
+                load_tile<D>(rb + sb * L::kBytes, om, &ct.b_full[sb], h, row);
             }
             __syncwarp();
             ++b;
         }
         // no copy may land after the block's end
         attn_wait(&ct.own_full, 0, &g_attn_bwd_status);
-        for (int j = max(0, a - NST); j < a; ++j) wait(&ct.a_full[j % NST], j / NST);
-        for (int j = max(0, b - NST); j < b; ++j) wait(&ct.b_full[j % NST], j / NST);
+        for (int j = max(0, a - NA); j < a; ++j) wait(&ct.a_full[j % NA], j / NA);
+        for (int j = max(0, b - NB); j < b; ++j) wait(&ct.b_full[j % NB], j / NB);
     } else if (warp == kStatWarp) {
         for (int j = 0; j < n; ++j) {
-            const int st = j % NST;
+            const int st = j % kStats;
             const int64_t h = hk * G + j / per, at = h * A.T + sq.a, row = (int64_t)(kt + j % per) * kTile + lane * 4;
             float x[4], y[4];
 #pragma unroll
@@ -210,55 +213,59 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
                 x[i] = row + i < len ? B.lse2[at + row + i] : INFINITY;
                 y[i] = row + i < len ? B.delta[at + row + i] : 0.f;
             }
-            if (j >= NST) ok = wait(&ct.stat_empty[st], j / NST - 1);
+            if (j >= kStats) ok = wait(&ct.stat_empty[st], j / kStats - 1);
             if (!ok) break;
             *reinterpret_cast<float4 *>(&ct.stat[st][0][lane * 4]) = make_float4(x[0], x[1], x[2], x[3]);
             *reinterpret_cast<float4 *>(&ct.stat[st][1][lane * 4]) = make_float4(y[0], y[1], y[2], y[3]);
             sm100::mbar_arrive(&ct.stat_full[st]);
         }
     } else if (warp == kProductWarp) {
-        const uint32_t k_at = sm100::smem_u32(Ks), v_at = sm100::smem_u32(Vs), r_at = sm100::smem_u32(ring);
-        // the tile of step j, its rows behind the sequence cleared
-        auto arrived = [&](uint64_t *bars, int j, int which) {
-            if (!wait(&bars[j % NST], j / NST)) return false;
-            if (tail < kTile && j % per == per - 1) clear_rows<D>(ring + (2 * (j % NST) + which) * L::kBytes, tail);
+        const uint32_t k_at = sm100::smem_u32(Ks), v_at = sm100::smem_u32(Vs), a_at = sm100::smem_u32(ra), b_at = sm100::smem_u32(rb);
+        // the tiles of step j, their rows behind the sequence cleared
+        auto arrived_a = [&](int j) {
+            if (!wait(&ct.a_full[j % NA], j / NA)) return false;
+            if (tail < kTile && j % per == per - 1) clear_rows<D>(ra + (j % NA) * L::kBytes, tail);
+            return true;
+        };
+        auto arrived_b = [&](int j) {
+            if (!wait(&ct.b_full[j % NB], j / NB)) return false;
+            if (tail < kTile && j % per == per - 1) clear_rows<D>(rb + (j % NB) * L::kBytes, tail);
             return true;
         };
         auto scores = [&](int j) {
             sm100::tc_fence_after();
-            mma_rows<D, BF16, 128>(tmem + S, k_at, r_at + 2 * (j % NST) * L::kBytes, L::kBlock, L::kBlock);
+            mma_rows<D, BF16, 128>(tmem + S, k_at, a_at + (j % NA) * L::kBytes, L::kBlock, L::kBlock);
             sm100::mma_commit_el(&ct.s_full[0]);
         };
         auto dscores = [&](int j) {
             sm100::tc_fence_after();
-            mma_rows<D, BF16, 128>(tmem + DP, v_at, r_at + (2 * (j % NST) + 1) * L::kBytes, L::kBlock, L::kBlock);
+            mma_rows<D, BF16, 128>(tmem + DP, v_at, b_at + (j % NB) * L::kBytes, L::kBlock, L::kBlock);
             sm100::mma_commit_el(&ct.dp_full);
         };
-        ok = wait(&ct.own_full, 0) && arrived(ct.a_full, 0, 0);
+        ok = wait(&ct.own_full, 0) && arrived_a(0);
         if (ok) {
             scores(0);
-            ok = arrived(ct.b_full, 0, 1);
+            ok = arrived_b(0);
             if (ok) dscores(0);
         }
         for (int j = 0; j < n && ok; ++j) {
-            const int st = j % NST;
             ok = wait(&ct.p_ready, j);
             if (!ok) break;
             sm100::tc_fence_after();
-            mma_sum<D, BF16>(tmem + DV, tmem + S, r_at + (2 * st + 1) * L::kBytes, j > 0);
-            sm100::mma_commit_el(&ct.b_empty[st]);
+            mma_sum<D, BF16>(tmem + DV, tmem + S, b_at + (j % NB) * L::kBytes, j > 0);
+            sm100::mma_commit_el(&ct.b_empty[j % NB]);
             if (j + 1 < n) {
-                ok = arrived(ct.a_full, j + 1, 0);
+                ok = arrived_a(j + 1);
                 if (!ok) break;
                 scores(j + 1);
             }
             ok = wait(&ct.ds_ready[0], j);
             if (!ok) break;
             sm100::tc_fence_after();
-            mma_sum<D, BF16>(tmem + DK, tmem + DP, r_at + 2 * st * L::kBytes, j > 0);
-            sm100::mma_commit_el(&ct.a_empty[st]);
+            mma_sum<D, BF16>(tmem + DK, tmem + DP, a_at + (j % NA) * L::kBytes, j > 0);
+            sm100::mma_commit_el(&ct.a_empty[j % NA]);
             if (j + 1 < n) {
-                ok = arrived(ct.b_full, j + 1, 1);
+                ok = arrived_b(j + 1);
                 if (!ok) break;
                 dscores(j + 1);
             }
@@ -270,8 +277,8 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float c = A.scale_log2;
         for (int j = 0; j < n; ++j) {
-            const int st = j % NST, qt = kt + j % per;
-            ok = wait(&ct.stat_full[st], j / NST) && wait(&ct.s_full[0], j);
+            const int st = j % kStats, qt = kt + j % per;
+            ok = wait(&ct.stat_full[st], j / kStats) && wait(&ct.s_full[0], j);
             if (!ok) break;
             sm100::tc_fence_after();
             float p[64];
@@ -336,9 +343,9 @@ template <int D, bool BF16>
 __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const CUtensorMap *vm, const CUtensorMap *om,
                             const Attn &A, const Grads &B, Control &ct, uint8_t *base, const AttnSeq &sq, uint32_t tmem, int warp) {
     using L = Lay<D>;
-    constexpr int NST = L::kPairs;
+    constexpr int NA = L::kA, NB = L::kB;
     const int lane = threadIdx.x & 31;
-    uint8_t *Qs = base, *Os = base + L::kBytes, *ring = base + 2 * L::kBytes;   // pairs: keys, values
+    uint8_t *Qs = base, *Os = base + L::kBytes, *ra = base + 2 * L::kBytes, *rb = ra + NA * L::kBytes;   // keys, values
     const int qt = ct.part.tile, h = ct.part.head, hk = h / A.G;
     const int len = (int)(sq.b - sq.a), n = qt + 1;
     const int tail = len - qt * kTile;   // rows of the last key tile (the diagonal one), if below 128
@@ -355,44 +362,44 @@ __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const 
         __syncwarp();
         int a = 0, b = 0;
         for (int j = 0; j < n; ++j) {
-            const int st = j % NST;
+            const int sa = j % NA, sb = j % NB;
             const int64_t row = sq.a + (int64_t)j * kTile;
-            if (j >= NST) ok = wait(&ct.a_empty[st], j / NST - 1);
+            if (j >= NA) ok = wait(&ct.a_empty[sa], j / NA - 1);
             if (!ok) break;
             if (lane == 0) {
-                sm100::mbar_arrive_expect_tx(&ct.a_full[st], L::kBytes);
-                load_tile<D>(ring + 2 * st * L::kBytes, km, &ct.a_full[st], hk, row);
+                sm100::mbar_arrive_expect_tx(&ct.a_full[sa], L::kBytes);
+                load_tile<D>(ra + sa * L::kBytes, km, &ct.a_full[sa], hk, row);
             }
             __syncwarp();
             ++a;
-            if (j >= NST) ok = wait(&ct.b_empty[st], j / NST - 1);
+            if (j >= NB) ok = wait(&ct.b_empty[sb], j / NB - 1);
             if (!ok) break;
             if (lane == 0) {
-                sm100::mbar_arrive_expect_tx(&ct.b_full[st], L::kBytes);
-                load_tile<D>(ring + (2 * st + 1) * L::kBytes, vm, &ct.b_full[st], hk, row);
+                sm100::mbar_arrive_expect_tx(&ct.b_full[sb], L::kBytes);
+                load_tile<D>(rb + sb * L::kBytes, vm, &ct.b_full[sb], hk, row);
             }
             __syncwarp();
             ++b;
         }
         attn_wait(&ct.own_full, 0, &g_attn_bwd_status);
-        for (int j = max(0, a - NST); j < a; ++j) wait(&ct.a_full[j % NST], j / NST);
-        for (int j = max(0, b - NST); j < b; ++j) wait(&ct.b_full[j % NST], j / NST);
+        for (int j = max(0, a - NA); j < a; ++j) wait(&ct.a_full[j % NA], j / NA);
+        for (int j = max(0, b - NB); j < b; ++j) wait(&ct.b_full[j % NB], j / NB);
     } else if (warp == kProductWarp) {
-        const uint32_t q_at = sm100::smem_u32(Qs), o_at = sm100::smem_u32(Os), r_at = sm100::smem_u32(ring);
+        const uint32_t q_at = sm100::smem_u32(Qs), o_at = sm100::smem_u32(Os), a_at = sm100::smem_u32(ra), b_at = sm100::smem_u32(rb);
         auto scores = [&](int j) {
-            if (!wait(&ct.a_full[j % NST], j / NST)) return false;
-            if (j == n - 1 && tail < kTile) clear_rows<D>(ring + 2 * (j % NST) * L::kBytes, tail);
+            if (!wait(&ct.a_full[j % NA], j / NA)) return false;
+            if (j == n - 1 && tail < kTile) clear_rows<D>(ra + (j % NA) * L::kBytes, tail);
             sm100::tc_fence_after();
-            mma_rows<D, BF16, 128>(tmem + S[j & 1], q_at, r_at + 2 * (j % NST) * L::kBytes, L::kBlock, L::kBlock);
+            mma_rows<D, BF16, 128>(tmem + S[j & 1], q_at, a_at + (j % NA) * L::kBytes, L::kBlock, L::kBlock);
             sm100::mma_commit_el(&ct.s_full[j & 1]);
             return true;
         };
         auto dscores = [&](int j) {
-            if (!wait(&ct.b_full[j % NST], j / NST)) return false;
+            if (!wait(&ct.b_full[j % NB], j / NB)) return false;
             sm100::tc_fence_after();
-            mma_rows<D, BF16, 128>(tmem + DP, o_at, r_at + (2 * (j % NST) + 1) * L::kBytes, L::kBlock, L::kBlock);
+            mma_rows<D, BF16, 128>(tmem + DP, o_at, b_at + (j % NB) * L::kBytes, L::kBlock, L::kBlock);
             sm100::mma_commit_el(&ct.dp_full);
-            sm100::mma_commit_el(&ct.b_empty[j % NST]);
+            sm100::mma_commit_el(&ct.b_empty[j % NB]);
             return true;
         };
         ok = wait(&ct.own_full, 0) && scores(0) && dscores(0);
@@ -406,8 +413,8 @@ __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const 
             ok = wait(&ct.ds_ready[j & 1], j >> 1);
             if (!ok) break;
             sm100::tc_fence_after();
-            mma_sum<D, BF16>(tmem + DQ, tmem + S[j & 1], r_at + 2 * (j % NST) * L::kBytes, j > 0);
-            sm100::mma_commit_el(&ct.a_empty[j % NST]);
+            mma_sum<D, BF16>(tmem + DQ, tmem + S[j & 1], a_at + (j % NA) * L::kBytes, j > 0);
+            sm100::mma_commit_el(&ct.a_empty[j % NA]);
         }
         sm100::mma_commit_el(&ct.done);
         attn_wait(&ct.done, 0, &g_attn_bwd_status);
@@ -465,9 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 kda_attn_backward_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
                          const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap om, const Attn A,
                          const Grads B) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    __shared__ Control ct;
+    // the tiles, and behind them what the warps tell each other (there is no room for both and a gap)
+    extern __shared__ __align__(1024) uint8_t base[];
+    Control &ct = *reinterpret_cast<Control *>(base + Lay<D>::kTiles);
+    if (sm100::smem_u32(base) & 1023) {   // the swizzled tiles need it
+        if (threadIdx.x == 0) atomicOr(&g_attn_bwd_status, kAttnTimeout);
+        return;
+    }
     const int tid = threadIdx.x, warp = attn_warp();
     const bool keys = blockIdx.x < B.key_blocks;
     if (tid == 0) {
@@ -477,6 +488,8 @@ kda_attn_backward_kernel(const __grid_constant__ CUtensorMap qm, const __grid_co
             sm100::mbar_init(&ct.a_empty[i], 1);
             sm100::mbar_init(&ct.b_full[i], 1);
             sm100::mbar_init(&ct.b_empty[i], 1);
+        }
+        for (int i = 0; i < kStats; ++i) {
             sm100::mbar_init(&ct.stat_full[i], 32);
             sm100::mbar_init(&ct.stat_empty[i], 8);
         }
@@ -527,14 +540,16 @@ cudaError_t backward(const Attn &A, Grads &B, cudaStream_t stream) {
         !kda_make_attn_map(&om, B.d_out, BF16, D, A.Hq, A.T, 1, B.do_h, B.do_t, 0, kTile))
         return cudaErrorInvalidValue;
     const auto kernel = kda_attn_backward_kernel<D, BF16>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kSmem);
+    constexpr int smem = Lay<D>::kTiles + (int)sizeof(Control);
+    static_assert(smem <= 232448, "shared memory of a block");
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)A.T * A.Hq;
     kda_attn_delta_kernel<D, BF16><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, stream>>>(A, B);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t tiles = A.cu ? (int64_t)A.T / kTile + A.N : (A.seq_len + kTile - 1) / kTile * A.N;
     B.key_blocks = tiles * A.Hkv;
-    kernel<<<(unsigned)(B.key_blocks + tiles * A.Hq), kThreads, Lay<D>::kSmem, stream>>>(qm, km, vm, om, A, B);
+    kernel<<<(unsigned)(B.key_blocks + tiles * A.Hq), kThreads, smem, stream>>>(qm, km, vm, om, A, B);
     return cudaGetLastError();
 }
 
