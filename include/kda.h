@@ -741,8 +741,9 @@ kda_status kda_attn_paged(const kda_attn_dims *dims, const kda_cache_dims *cache
  * An empty cache is page_refs 0, page_table -1, kv_lens 0.  The calls keep this state; none
  * waits for the host, and what they decide follows from the state alone: free pages are
  * given out lowest number first, to the sequences (or children) in their order.  A last
- * page that is not full belongs to one sequence only (kda_cache_fork copies it), so that
- * kda_cache_append never writes into a shared page.  A sequence or page number out of range
+ * page that is not full and grows belongs to one sequence only (kda_cache_fork copies it, and
+ * kda_cache_reserve one that a sequence was shortened into), so that kda_cache_append never
+ * writes into a shared page.  A sequence or page number out of range
  * is passed by and recorded in the device status word (kda_get_last_device_error then
  * returns KDA_ERR_INVALID_ARGUMENT).  Conventions as in the softmax attention calls.
  */
@@ -758,13 +759,19 @@ int64_t kda_cache_workspace(const kda_cache_dims *cache);
  * one that needs a page keeps its old length, as does one whose row in the table is too
  * short.
  *
+ *   src, dst   int32 [N], or both NULL.  A sequence that grows from the middle of a page that
+ *              others share (kda_cache_fork, then kda_cache_free with keep) gets a page of its
+ *              own in its place: for every layer, page src[n] is to be copied to dst[n]
+ *              (kda_cache_copy) before anything else takes pages; -1 where there is nothing to
+ *              copy.  Without the lists such a sequence keeps its old length, and the device
+ *              status word records it.
  *   missing    int32 [1] or NULL: pages that were lacking (0: all were served; short rows
  *              are not counted).
  */
 kda_status kda_cache_reserve(const kda_cache_dims *cache, int32_t num_seqs, int32_t *page_refs,
                              int32_t *page_table, int32_t *kv_lens, const int32_t *new_lens,
-                             int32_t *missing, void *workspace, int64_t workspace_bytes,
-                             kda_stream_t stream);
+                             int32_t *src, int32_t *dst, int32_t *missing, void *workspace,
+                             int64_t workspace_bytes, kda_stream_t stream);
 
 /*
  * kda_cache_append -- writes the new tokens' keys and values into one layer's pages: of the

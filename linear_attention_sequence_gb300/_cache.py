@@ -21,7 +21,7 @@ _I32 = torch.int32
 
 def declare(L):
     """Argument types of the C entry points (structures go in as bytes)."""
-    for name, args in (("kda_cache_reserve", [_vp, _i32] + [_vp] * 6 + [_i64, _vp]),
+    for name, args in (("kda_cache_reserve", [_vp, _i32] + [_vp] * 8 + [_i64, _vp]),
                        ("kda_cache_append", [_vp] + [_i32] * 4 + [_vp] * 8),
                        ("kda_cache_free", [_vp, _i32] + [_vp] * 3 + [_i32] + [_vp] * 3),
                        ("kda_cache_fork", [_vp, _i32] + [_vp] * 3 + [_i32] + [_vp] * 6 + [_i64, _vp]),
@@ -64,17 +64,30 @@ def _layer(k_pages, v_pages):
             _pages(v_pages, "v_pages", dev, k_pages.dtype, shape))
 
 
-def kda_cache_reserve(page_refs, page_table, kv_lens, new_lens, page_size, *, missing=None, stream=None):
+def kda_cache_reserve(page_refs, page_table, kv_lens, new_lens, page_size, *, src=None, dst=None,
+                      return_copies=False, missing=None, stream=None):
     """Pages for ``new_lens`` (int32 [N]) more tokens of each sequence, in place (C entry point
     ``kda_cache_reserve``): kv_lens grows and the table gets the lowest free pages, for the
     sequences in their order; one that cannot have all of its pages keeps its length.
-    ``missing`` (int32 [1] or None) gets the number of pages that were lacking."""
+    ``missing`` (int32 [1] or None) gets the number of pages that were lacking.
+
+    A sequence that was shortened into a page that others share (kda_cache_free with ``keep``
+    after kda_cache_fork) gets a page of its own when it grows again: with ``return_copies``
+    (or buffers given) returns ``(src, dst)``, int32 [N], the pages to copy with kda_cache_copy in
+    every layer (-1: none); without, such a sequence keeps its length and the device status
+    says so."""
     dev, N, cache, refs, table, lens = _state(page_refs, page_table, kv_lens, page_size)
     new = _is(new_lens, "new_lens", dev, _I32, (N,))
     lacking = _is(missing, "missing", dev, _I32, (1,))
     with _on(dev, stream):
+        if return_copies and src is None:
+            src = torch.empty((N,), dtype=_I32, device=page_refs.device)
+        if return_copies and dst is None:
+            dst = torch.empty((N,), dtype=_I32, device=page_refs.device)
         ws, n = _scratch(cache, page_refs.device)
-        _run("kda_cache_reserve", dev, cache, N, refs, table, lens, new, lacking, ws.data_ptr(), n)
+        _run("kda_cache_reserve", dev, cache, N, refs, table, lens, new, _is(src, "src", dev, _I32, (N,)),
+             _is(dst, "dst", dev, _I32, (N,)), lacking, ws.data_ptr(), n)
+    return None if src is None else (src, dst)
 
 
 def kda_cache_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *, stream=None):

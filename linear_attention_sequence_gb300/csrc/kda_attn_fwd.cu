@@ -331,6 +331,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const int n = max(w.n_of[0], w.n_of[1]), j0 = w.j0, head = w.head, keys = w.keys;
             const int64_t a = w.a;
             const int32_t *row = PAGED ? A.table + (int64_t)w.n * A.wide : nullptr;
+            if (PAGED) bad = bad || A.lens[w.n] > (int64_t)A.wide * A.page;
             read(k);
             for (int x = 0; x < 2 * n; ++x, ++c) {
                 // order: K0, K1, V0, K2, V1, ...
@@ -779,7 +780,7 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         const int unit = lane % (boxes * (D / 64)), mine = unit / boxes, which = unit % boxes;
         const bool values = lane >= boxes * (D / 64), issues = lane < 2 * boxes * (D / 64);
         const int32_t *row = A.table + (int64_t)part.n * A.wide;
-        bool bad = false;
+        bool bad = A.lens[part.n] > (int64_t)A.wide * A.page;
         int issued = 0;
         for (int j = 0; j < n; ++j) {
             const int64_t first = (int64_t)(part.j0 + j) * kFewKeys + which * box;

@@ -86,22 +86,36 @@ __device__ int free_pages(const int32_t *refs, int P, int want, int32_t *list, i
 }
 
 // ---------------------------------------------------------------- reserve
-__global__ void __launch_bounds__(kBlock) kda_cache_reserve_kernel(const Cache C, const int32_t *new_lens, int32_t *missing,
-                                                                   int32_t *list) {
+// A last page that is not full and that others share (a sequence was shortened into it) is replaced
+// by one of the sequence's own.  Which sequences that is, is settled before any count changes (src).
+__global__ void __launch_bounds__(kBlock) kda_cache_reserve_kernel(const Cache C, const int32_t *new_lens, int32_t *src,
+                                                                   int32_t *dst, int32_t *missing, int32_t *list) {
     __shared__ int sh[32];
-    auto needs = [&](int n, int &len, int &add, int &have) {
+    auto shared_page = [&](int n, int len, int add) {
+        if (add == 0 || (len & ((1 << C.shift) - 1)) == 0) return -1;
+        const int p = C.table[(int64_t)n * C.wide + (len >> C.shift)];
+        return p >= 0 && p < C.P && C.refs[p] > 1 ? p : -1;
+    };
+    // (new pages; -1: the table's row is too short, or a page to copy and nowhere to say so)
+    auto needs = [&](int n, bool first, int &len, int &add, int &have, int &old) {
         len = length_of(C, n);
         add = max(0, new_lens[n]);
         have = pages_of(len, C.shift);
+        old = src && !first ? src[n] : shared_page(n, len, add);
         const int64_t want = ((int64_t)len + add + (1 << C.shift) - 1) >> C.shift;
-        return want > C.wide ? -1 : (int)want - have;   // -1: the table's row is too short
+        if (first && src) src[n] = old;
+        if (old >= 0 && !src) {
+            if (first) atomicOr(&g_cache_status, kCacheBadPage);
+            return -1;
+        }
+        return want > C.wide ? -1 : (int)want - have + (old >= 0);
     };
     // how many pages in all (no more than there are matter)
     int64_t want = 0;
     for (int base = 0; base < C.N; base += kBlock) {
         const int n = base + threadIdx.x;
-        int len, add, have, total;
-        const int need = n < C.N ? max(0, needs(n, len, add, have)) : 0;
+        int len, add, have, old, total;
+        const int need = n < C.N ? max(0, needs(n, true, len, add, have, old)) : 0;
         scan1024(min(need, C.P + 1), total, sh);
         want += total;
     }
@@ -111,14 +125,23 @@ __global__ void __launch_bounds__(kBlock) kda_cache_reserve_kernel(const Cache C
     int64_t before = 0;
     for (int base = 0; base < C.N; base += kBlock) {
         const int n = base + threadIdx.x;
-        int len = 0, add = 0, have = 0, total;
-        const int need = n < C.N ? needs(n, len, add, have) : -1;
+        int len = 0, add = 0, have = 0, old = -1, total;
+        const int need = n < C.N ? needs(n, false, len, add, have, old) : -1;
         const int64_t at = before + scan1024(min(max(0, need), C.P + 1), total, sh);
         before += total;
-        if (need < 0 || (need > 0 && at + need > got)) continue;
+        if (n >= C.N) continue;
+        const bool served = need >= 0 && (need == 0 || at + need <= got);
+        const int copies = served && old >= 0 ? 1 : 0;
+        if (src) {
+            src[n] = copies ? old : -1;
+            dst[n] = copies ? list[at] : -1;
+        }
+        if (!served) continue;
+        int32_t *row = C.table + (int64_t)n * C.wide + have - copies;
+        if (copies) atomicSub(C.refs + old, 1);
         for (int j = 0; j < need; ++j) {
             const int p = list[at + j];
-            C.table[(int64_t)n * C.wide + have + j] = p;
+            row[j] = p;
             C.refs[p] = 1;
         }
         C.lens[n] = len + add;
@@ -432,9 +455,9 @@ cudaError_t launch_behind(void (*kernel)(Params...), unsigned blocks, int thread
 
 }  // namespace
 
-cudaError_t kda_launch_cache_reserve(const Cache &C, const int32_t *new_lens, int32_t *missing, int32_t *list,
-                                     cudaStream_t stream) {
-    kda_cache_reserve_kernel<<<1, kBlock, 0, stream>>>(C, new_lens, missing, list);
+cudaError_t kda_launch_cache_reserve(const Cache &C, const int32_t *new_lens, int32_t *src, int32_t *dst, int32_t *missing,
+                                     int32_t *list, cudaStream_t stream) {
+    kda_cache_reserve_kernel<<<1, kBlock, 0, stream>>>(C, new_lens, src, dst, missing, list);
     return cudaGetLastError();
 }
 

@@ -95,20 +95,23 @@ int64_t kda_cache_workspace(const kda_cache_dims *cache) {
 }
 
 kda_status kda_cache_reserve(const kda_cache_dims *cache, int32_t num_seqs, int32_t *page_refs, int32_t *page_table,
-                             int32_t *kv_lens, const int32_t *new_lens, int32_t *missing, void *workspace,
-                             int64_t workspace_bytes, kda_stream_t stream) {
+                             int32_t *kv_lens, const int32_t *new_lens, int32_t *src, int32_t *dst, int32_t *missing,
+                             void *workspace, int64_t workspace_bytes, kda_stream_t stream) {
     Cache C;
     const kda_status st = check_cache(cache, num_seqs, page_refs, page_table, kv_lens, C);
     if (st != KDA_OK) return st;
     const int64_t need = (int64_t)C.P * 4 + 16;
     if (bad(page_refs) || (C.N > 0 && (bad(page_table) || bad(kv_lens) || bad(new_lens))) || misaligned(missing, 4) ||
-        !workspace || workspace_bytes < need || misaligned(workspace, 16))
+        (src == nullptr) != (dst == nullptr) || misaligned(src, 4) || misaligned(dst, 4) || !workspace ||
+        workspace_bytes < need || misaligned(workspace, 16))
         return KDA_ERR_INVALID_ARGUMENT;
-    if (conflict({refs_of(C), table_of(C), lens_of(C), {missing, 4}, {workspace, (size_t)need}},
+    if (conflict({refs_of(C), table_of(C), lens_of(C), {src, (size_t)C.N * 4}, {dst, (size_t)C.N * 4}, {missing, 4},
+                  {workspace, (size_t)need}},
                  {{new_lens, (size_t)C.N * 4}}))
         return KDA_ERR_INVALID_ARGUMENT;
     if (C.N == 0 && !missing) return KDA_OK;
-    return done(kda_launch_cache_reserve(C, new_lens, missing, (int32_t *)workspace, (cudaStream_t)stream), "kda_cache_reserve");
+    return done(kda_launch_cache_reserve(C, new_lens, src, dst, missing, (int32_t *)workspace, (cudaStream_t)stream),
+                "kda_cache_reserve");
 }
 
 kda_status kda_cache_append(const kda_cache_dims *cache, int32_t num_seqs, int32_t total_tokens, int32_t kv_heads,

@@ -174,10 +174,9 @@ def test_empty_batches_are_ok(L):
 
 
 def reserve(L, c=None, **kw):
-    a = dict(N=5, refs=at(1), table=at(2), lens=at(3), new=at(4), missing=None, ws=at(5), size=1 << 20)
+    a = dict(N=5, refs=at(1), table=at(2), lens=at(3), new=at(4), src=at(6), dst=at(7), missing=None, ws=at(5), size=1 << 20)
     a.update(kw)
-    return L.kda_cache_reserve(R(c or cache()), *(a[n] for n in ("N", "refs", "table", "lens", "new", "missing", "ws", "size")),
-                               None)
+    return L.kda_cache_reserve(R(c or cache()), *a.values(), None)
 
 
 def append(L, c=None, **kw):
@@ -218,7 +217,8 @@ def copy(L, c=None, **kw):
 @pytest.mark.parametrize("call,over", [
     (reserve, o) for o in (dict(N=-1), dict(refs=None), dict(table=None), dict(lens=None), dict(new=None), dict(refs=at(1) + 2),
                            dict(missing=at(9) + 1), dict(ws=None), dict(ws=at(5) + 8), dict(size=100), dict(new=at(3)),
-                           dict(lens=at(2)), dict(ws=at(1)), dict(missing=at(3) + 4))] + [
+                           dict(lens=at(2)), dict(ws=at(1)), dict(missing=at(3) + 4), dict(src=None), dict(dst=None),
+                           dict(dst=at(6) + 4), dict(src=at(6) + 2))] + [
     (append, o) for o in (dict(N=-1), dict(T=-1), dict(T=21), dict(H=0), dict(d=0), dict(k=None), dict(v=None), dict(kp=None),
                           dict(vp=None), dict(table=None), dict(lens=None), dict(lens=at(6) + 2), dict(cu=at(7) + 2),
                           dict(k=heads(1, 2, data=at(1) + 4)), dict(v=heads(2, 2, token_stride=12)),

@@ -31,20 +31,28 @@ class Plain:
         return [p for p in range(self.P) if self.refs[p] == 0]
 
     def reserve(self, new):
-        free, upto = self.free_list(), 0
+        free, upto, src, dst = self.free_list(), 0, [-1] * self.N, [-1] * self.N
+        last = [self.table[n][self.lens[n] // self.page] if self.lens[n] % self.page else -1 for n in range(self.N)]
+        shared = [p >= 0 and self.refs[p] > 1 for p in last]
         for n, add in enumerate(new):
             add = max(0, add)
             have, want = self.pages(self.lens[n]), self.pages(self.lens[n] + add)
             if want > self.wide:
                 continue
-            at, upto = upto, upto + want - have
-            if want > have and upto > len(free):
+            copies = add > 0 and shared[n]
+            need = want - have + copies
+            at, upto = upto, upto + need
+            if need and upto > len(free):
                 continue
+            if copies:
+                src[n], dst[n] = last[n], free[at]
+                self.refs[last[n]] -= 1
+                have -= 1
             for j in range(have, want):
                 p = free[at + j - have]
                 self.table[n][j], self.refs[p] = p, 1
             self.lens[n] += add
-        return max(0, upto - len(free))
+        return max(0, upto - len(free)), src, dst
 
     def free(self, seqs, keep=None):
         for i, n in enumerate(seqs):
@@ -120,10 +128,10 @@ class Both:
         assert used == self.plain.refs
 
     def reserve(self, new):
-        kda.kda_cache_reserve(*self.state, ints(new), self.page, missing=self.missing)
-        want = self.plain.reserve(new)
+        src, dst = kda.kda_cache_reserve(*self.state, ints(new), self.page, missing=self.missing, return_copies=True)
+        want, s, d = self.plain.reserve(new)
         self.check()
-        assert self.missing.item() == want
+        assert self.missing.item() == want and src.tolist() == s and dst.tolist() == d
 
     def free(self, seqs, keep=None):
         kda.kda_cache_free(*self.state, ints(seqs), self.page, keep=None if keep is None else ints(keep))
@@ -177,6 +185,25 @@ def test_bookkeeping(P, N, wide, page, seed):
             c.compact(r.random() < 0.5)
     c.compact(True)
     assert kda.kda_get_last_device_error() == 0
+
+
+def test_shared_pages_that_grow():
+    """Continuations cut back into the page they share: each gets one of its own, and without
+    lists for the copies none is served."""
+    c = Both(20, 5, 6, 8)
+    c.reserve([30, 0, 0, 0, 7])
+    c.fork([0, 0], [1, 2])
+    c.free([0, 1, 2], [21, 13, 16])
+    c.reserve([1, 4, 0, 9, 1])
+    c.free([0, 1], [5, 5])                                       # both in the page of tokens 0..7, and 2 has it too
+    before = [x.clone() for x in c.state]
+    kda.kda_cache_reserve(*c.state, ints([3, 0, 0, 0, 0]), 8)
+    assert kda.kda_get_last_device_error() == 1
+    assert all(torch.equal(a, b) for a, b in zip(before, c.state))
+    kda.kda_cache_reserve(*c.state, ints([0, 0, 3, 0, 0]), 8)    # 2 ends with a full page: nothing to copy
+    c.plain.reserve([0, 0, 3, 0, 0])
+    c.check()
+    c.reserve([3, 3, 0, 0, 0])
 
 
 def test_aligned_or_not():
