@@ -13,7 +13,7 @@ import torch
 
 import linear_attention_sequence_gb300 as _kda
 
-from ._ssm import _is, _on, _run, _sequences, _workspace
+from ._ssm import _is, _on, _run, _sequences
 
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 _F32, _I32 = torch.float32, torch.int32
@@ -25,6 +25,45 @@ _HEADS = struct.Struct("Pqq")                      # data, token stride, head st
 _PAGES = struct.Struct("Pqqq")                     # data, page, token, head stride
 _DIMS = struct.Struct("7if")                       # N, T, H_q, H_kv, d, in, out, scale
 _CACHE = struct.Struct("3i")                       # P, page_size, max_pages
+
+
+# What a small call costs the host is mostly checks, so that they ask each tensor for as little as
+# they can.  The current device, without making sure of the runtime first (a CUDA tensor has).
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+class _Here:
+    """Nothing to change: the call's device is current, and its stream the current one."""
+
+    __slots__ = ()
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
+
+
+def _place(dev, stream):
+    return _HERE if stream is None and _current() == dev else _on(dev, stream)
+
+
+_sizes = {}   # bytes of a workspace, by the query and the dims it was asked for
+
+
+def _workspace(query, dims, device, *more):
+    n = _sizes.get((query, dims, *more))
+    if n is None:
+        n = getattr(_kda.lib(), query)(dims, *more)
+        if n < 0:
+            raise _kda.KdaError(2, query)
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        _sizes[(query, dims, *more)] = n
+    return torch.empty((n,), dtype=torch.uint8, device=device), n
 
 
 def declare(L):
@@ -42,21 +81,22 @@ def declare(L):
 
 def _heads(t, name, dev, dtype, shape):
     """The bytes of a [T, H, d] activation whose tokens and heads may lie strides apart."""
-    if t.dtype != dtype or t.shape != shape or t.get_device() != dev:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         if t.get_device() != dev:
             raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     a, b, c = t.stride()
-    if c != 1:
-        raise ValueError(f"{name}'s channels must be contiguous")
     T, H, d = shape
+    if c != 1 and d > 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
     if T <= 1:
         a = H * d
     if H == 1:
         b = d
-    if a % 8 or b % 8 or t.data_ptr() % 16:
+    at = t.data_ptr()
+    if (a | b) & 7 or at & 15:
         raise ValueError(f"{name} must be 16-byte aligned, in its strides too")
-    return _HEADS.pack(t.data_ptr(), a, b)
+    return _HEADS.pack(at, a, b)
 
 
 def _pages(t, name, dev, dtype, shape):
@@ -111,13 +151,15 @@ def kda_attn_prefill(q, k, v, cu_seqlens=None, *, num_seqs=None, scale=None, out
     kv = (T, k.shape[1], d)
     rq, rk, rv = (_heads(q, "q", dev, q.dtype, (T, H, d)), _heads(k, "k", dev, q.dtype, kv),
                   _heads(v, "v", dev, q.dtype, kv))
-    with _on(dev, stream):
+    o, s = _is(out, "out", dev, odt, (T, H, d)), _is(lse, "lse", dev, _F32, (T, H))
+    with _place(dev, stream):
         if out is None:
             out = torch.empty((T, H, d), dtype=odt, device=q.device)
+            o = out.data_ptr()
         if lse is None and return_lse:
             lse = torch.empty((T, H), dtype=_F32, device=q.device)
-        _run("kda_attn_prefill", dev, dims, rq, rk, rv, 0 if cu_seqlens is None else cu_seqlens.data_ptr(),
-             _is(out, "out", dev, odt, (T, H, d)), _is(lse, "lse", dev, _F32, (T, H)))
+            s = lse.data_ptr()
+        _run("kda_attn_prefill", dev, dims, rq, rk, rv, 0 if cu_seqlens is None else cu_seqlens.data_ptr(), o, s)
     return out if lse is None else (out, lse)
 
 
@@ -139,15 +181,16 @@ def kda_attn_backward(q, k, v, out, lse, d_out, cu_seqlens=None, *, num_seqs=Non
     rq, ro, ry = (_heads(x, n, dev, q.dtype, own) for x, n in ((q, "q"), (out, "out"), (d_out, "d_out")))
     rk, rv = (_heads(x, n, dev, q.dtype, kv) for x, n in ((k, "k"), (v, "v")))
     sums = _is(lse, "lse", dev, _F32, (T, H))
-    with _on(dev, stream):
+    for x, n, shape in ((dq, "dq", own), (dk, "dk", kv), (dv, "dv", kv)):
+        _is(x, n, dev, gdt, shape)
+    with _place(dev, stream):
         def new(given, shape):
             return torch.empty(shape, dtype=gdt, device=q.device) if given is None else given
 
         dq, dk, dv = new(dq, own), new(dk, kv), new(dv, kv)
-        ws = _workspace("kda_attn_backward_workspace", dims, q.device)
+        ws, n = _workspace("kda_attn_backward_workspace", dims, q.device)
         _run("kda_attn_backward", dev, dims, rq, rk, rv, ro, sums, ry,
-             0 if cu_seqlens is None else cu_seqlens.data_ptr(), _is(dq, "dq", dev, gdt, own),
-             _is(dk, "dk", dev, gdt, kv), _is(dv, "dv", dev, gdt, kv), ws.data_ptr(), ws.shape[0])
+             0 if cu_seqlens is None else cu_seqlens.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), n)
     return dict(dq=dq, dk=dk, dv=dv)
 
 
@@ -178,15 +221,15 @@ def kda_attn_paged(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *,
     table = _is(page_table, "page_table", dev, _I32, (N, wide))
     lens = _is(kv_lens, "kv_lens", dev, _I32, (N,))
     cu = 0 if cu_seqlens is None else cu_seqlens.data_ptr()
-    with _on(dev, stream):
+    o, s = _is(out, "out", dev, odt, (T, H, d)), _is(lse, "lse", dev, _F32, (T, H))
+    with _place(dev, stream):
         if out is None:
             out = torch.empty((T, H, d), dtype=odt, device=q.device)
+            o = out.data_ptr()
         if lse is None and return_lse:
             lse = torch.empty((T, H), dtype=_F32, device=q.device)
-        n = _kda.lib().kda_attn_paged_workspace(dims, cache, cu)
-        if n < 0:
-            raise _kda.KdaError(2 if T else 1, "kda_attn_paged_workspace")
-        ws = torch.empty((n,), dtype=torch.uint8, device=q.device)
-        _run("kda_attn_paged", dev, dims, cache, rq, rk, rv, table, lens, cu,
-             _is(out, "out", dev, odt, (T, H, d)), _is(lse, "lse", dev, _F32, (T, H)), ws.data_ptr(), n)
+            s = lse.data_ptr()
+        # (of cu_seqlens it matters only whether there are any; any address stands for them)
+        ws, n = _workspace("kda_attn_paged_workspace", dims, q.device, cache, 16 if cu else 0)
+        _run("kda_attn_paged", dev, dims, cache, rq, rk, rv, table, lens, cu, o, s, ws.data_ptr(), n)
     return out if lse is None else (out, lse)

@@ -12,8 +12,8 @@ import torch
 
 import linear_attention_sequence_gb300 as _kda
 
-from ._attn import _CACHE, _TYPES, _heads, _pages
-from ._ssm import _is, _on, _run, _sequences
+from ._attn import _CACHE, _TYPES, _heads, _pages, _place, _workspace
+from ._ssm import _is, _run, _sequences
 
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 _I32 = torch.int32
@@ -33,24 +33,29 @@ def declare(L):
     L.kda_cache_workspace.restype = _i64
 
 
+def _int(t, name, dev, shape):
+    """The address of a contiguous int32 tensor of this shape on this device (_is, for the usual case
+    in fewer steps)."""
+    if t is not None and t.dtype is _I32 and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _is(t, name, dev, _I32, shape)
+
+
 def _state(page_refs, page_table, kv_lens, page_size):
     """(device, N, cache dims, addresses of refs, table and lens) of a cache's state."""
-    if page_refs is None or not page_refs.is_cuda or page_refs.dim() != 1:
+    if page_refs is None or page_refs.dim() != 1 or page_refs.get_device() < 0:
         raise ValueError("page_refs must be a CUDA tensor [P]")
     if page_table is None or page_table.dim() != 2:
         raise ValueError("page_table must be [N, max_pages]")
     dev = page_refs.get_device()
-    N, wide = page_table.shape
-    P = page_refs.shape[0]
-    return (dev, N, _CACHE.pack(P, page_size, wide), _is(page_refs, "page_refs", dev, _I32, (P,)),
-            _is(page_table, "page_table", dev, _I32, (N, wide)), _is(kv_lens, "kv_lens", dev, _I32, (N,)))
+    shape, own = page_table.shape, page_refs.shape
+    N = shape[0]
+    return (dev, N, _CACHE.pack(own[0], page_size, shape[1]), _int(page_refs, "page_refs", dev, own),
+            _int(page_table, "page_table", dev, shape), _int(kv_lens, "kv_lens", dev, (N,)))
 
 
 def _scratch(cache, device):
-    n = _kda.lib().kda_cache_workspace(cache)
-    if n < 0:
-        raise _kda.KdaError(2, "kda_cache_workspace")
-    return torch.empty((n,), dtype=torch.uint8, device=device), n
+    return _workspace("kda_cache_workspace", cache, device)
 
 
 def _layer(k_pages, v_pages):
@@ -77,16 +82,16 @@ def kda_cache_reserve(page_refs, page_table, kv_lens, new_lens, page_size, *, sr
     every layer (-1: none); without, such a sequence keeps its length and the device status
     says so."""
     dev, N, cache, refs, table, lens = _state(page_refs, page_table, kv_lens, page_size)
-    new = _is(new_lens, "new_lens", dev, _I32, (N,))
-    lacking = _is(missing, "missing", dev, _I32, (1,))
-    with _on(dev, stream):
+    new = _int(new_lens, "new_lens", dev, (N,))
+    lacking = _int(missing, "missing", dev, (1,))
+    with _place(dev, stream):
         if return_copies and src is None:
             src = torch.empty((N,), dtype=_I32, device=page_refs.device)
         if return_copies and dst is None:
             dst = torch.empty((N,), dtype=_I32, device=page_refs.device)
         ws, n = _scratch(cache, page_refs.device)
-        _run("kda_cache_reserve", dev, cache, N, refs, table, lens, new, _is(src, "src", dev, _I32, (N,)),
-             _is(dst, "dst", dev, _I32, (N,)), lacking, ws.data_ptr(), n)
+        _run("kda_cache_reserve", dev, cache, N, refs, table, lens, new, _int(src, "src", dev, (N,)),
+             _int(dst, "dst", dev, (N,)), lacking, ws.data_ptr(), n)
     return None if src is None else (src, dst)
 
 
@@ -103,9 +108,9 @@ def kda_cache_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens=Non
         raise ValueError("cu_seqlens must hold N + 1 entries")
     T = k.shape[0]
     rk, rv = (_heads(x, name, dev, k_pages.dtype, (T, H, d)) for x, name in ((k, "k"), (v, "v")))
-    table = _is(page_table, "page_table", dev, _I32, (N, wide))
-    lens = _is(kv_lens, "kv_lens", dev, _I32, (N,))
-    with _on(dev, stream):
+    table = _int(page_table, "page_table", dev, (N, wide))
+    lens = _int(kv_lens, "kv_lens", dev, (N,))
+    with _place(dev, stream):
         _run("kda_cache_append", dev, _CACHE.pack(P, page, wide), N, T, H, d, rk, rv, kp, vp, table, lens,
              0 if cu_seqlens is None else cu_seqlens.data_ptr())
 
@@ -118,9 +123,9 @@ def kda_cache_free(page_refs, page_table, kv_lens, seqs, page_size, *, keep=None
     if seqs is None or seqs.dim() != 1:
         raise ValueError("seqs must be [M]")
     M = seqs.shape[0]
-    with _on(dev, stream):
-        _run("kda_cache_free", dev, cache, N, refs, table, lens, M, _is(seqs, "seqs", dev, _I32, (M,)),
-             _is(keep, "keep", dev, _I32, (M,)))
+    with _place(dev, stream):
+        _run("kda_cache_free", dev, cache, N, refs, table, lens, M, _int(seqs, "seqs", dev, (M,)),
+             _int(keep, "keep", dev, (M,)))
 
 
 def kda_cache_fork(page_refs, page_table, kv_lens, parents, children, page_size, *, src=None, dst=None,
@@ -133,16 +138,16 @@ def kda_cache_fork(page_refs, page_table, kv_lens, parents, children, page_size,
     if parents is None or parents.dim() != 1:
         raise ValueError("parents must be [M]")
     M = parents.shape[0]
-    p, c = _is(parents, "parents", dev, _I32, (M,)), _is(children, "children", dev, _I32, (M,))
-    lacking = _is(missing, "missing", dev, _I32, (1,))
-    with _on(dev, stream):
+    p, c = _int(parents, "parents", dev, (M,)), _int(children, "children", dev, (M,))
+    lacking = _int(missing, "missing", dev, (1,))
+    with _place(dev, stream):
         if src is None:
             src = torch.empty((M,), dtype=_I32, device=page_refs.device)
         if dst is None:
             dst = torch.empty((M,), dtype=_I32, device=page_refs.device)
         ws, n = _scratch(cache, page_refs.device)
-        _run("kda_cache_fork", dev, cache, N, refs, table, lens, M, p, c, _is(src, "src", dev, _I32, (M,)),
-             _is(dst, "dst", dev, _I32, (M,)), lacking, ws.data_ptr(), n)
+        _run("kda_cache_fork", dev, cache, N, refs, table, lens, M, p, c, _int(src, "src", dev, (M,)),
+             _int(dst, "dst", dev, (M,)), lacking, ws.data_ptr(), n)
     return src, dst
 
 
@@ -154,16 +159,16 @@ def kda_cache_compact(page_refs, page_table, kv_lens, page_size, *, refs_out=Non
     copy with kda_cache_copy in every layer (-1: none)."""
     dev, N, cache, refs, table, lens = _state(page_refs, page_table, kv_lens, page_size)
     P, shape = page_refs.shape[0], tuple(page_table.shape)
-    with _on(dev, stream):
+    with _place(dev, stream):
         def new(given, shape):
             return torch.empty(shape, dtype=_I32, device=page_refs.device) if given is None else given
 
         refs_out, table_out = new(refs_out, (P,)), new(table_out, shape)
         src, dst = new(src, (P,)), new(dst, (P,))
         ws, n = _scratch(cache, page_refs.device)
-        _run("kda_cache_compact", dev, cache, N, refs, table, lens, _is(refs_out, "refs_out", dev, _I32, (P,)),
-             _is(table_out, "table_out", dev, _I32, shape), _is(src, "src", dev, _I32, (P,)),
-             _is(dst, "dst", dev, _I32, (P,)), ws.data_ptr(), n)
+        _run("kda_cache_compact", dev, cache, N, refs, table, lens, _int(refs_out, "refs_out", dev, (P,)),
+             _int(table_out, "table_out", dev, shape), _int(src, "src", dev, (P,)),
+             _int(dst, "dst", dev, (P,)), ws.data_ptr(), n)
     return refs_out, table_out, src, dst
 
 
@@ -174,6 +179,6 @@ def kda_cache_copy(k_pages, v_pages, src, dst, *, stream=None):
     if src is None or src.dim() != 1:
         raise ValueError("src must be [M]")
     M = src.shape[0]
-    with _on(dev, stream):
-        _run("kda_cache_copy", dev, _CACHE.pack(P, page, 1), H, d, kp, vp, M, _is(src, "src", dev, _I32, (M,)),
-             _is(dst, "dst", dev, _I32, (M,)))
+    with _place(dev, stream):
+        _run("kda_cache_copy", dev, _CACHE.pack(P, page, 1), H, d, kp, vp, M, _int(src, "src", dev, (M,)),
+             _int(dst, "dst", dev, (M,)))

@@ -1089,7 +1089,7 @@ cudaError_t paged(const Attn &A, char *ws, cudaStream_t stream) {
             e = launch(false, kernel, dim3(kSMs), kThreads, Lay<D>::kSmem, stream, km, vm, A, sh, box,
                        z.few ? kFewRows : 0);
         if (e == cudaSuccess)
-            e = launch(true, kda_attn_join_kernel<D, BF16>, dim3(kSMs, 16), 128, 0, stream, A, sh);
+            e = launch(true, kda_attn_join_kernel<D, BF16>, dim3(kSMs, 32), 128, 0, stream, A, sh);
     }
     return e;
 }

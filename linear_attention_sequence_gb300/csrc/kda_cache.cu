@@ -30,28 +30,32 @@ __device__ __forceinline__ int length_of(const Cache &C, int n) {
     return len < 0 ? 0 : min(len, C.wide << C.shift);
 }
 
-// Exclusive sum over the 1024 threads, and the total.
-__device__ __forceinline__ int scan1024(int x, int &total, int *sh) {
+// Exclusive sum over the 1024 threads, and the total (of one count, or of two in the halves of 64
+// bits).
+template <typename T>
+__device__ __forceinline__ T scan1024(T x, T &total, T *sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = x;
+    T s = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        const T y = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += y;
     }
     __syncthreads();
     if (lane == 31) sh[warp] = s;
     __syncthreads();
-    int w = sh[lane];
+    T w = sh[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        const T y = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += y;
     }
     total = __shfl_sync(0xffffffffu, w, 31);
-    const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    const T before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
     return (warp ? before : 0) + s - x;
 }
+typedef unsigned long long Two;   // a count in the low half, another in the high half
+__device__ __forceinline__ Two two(int a, int b) { return (Two)(unsigned)a | (Two)(unsigned)b << 32; }
 
 // The first `want` free pages, lowest first, into `list`; returns how many there are (no
 // more than `want`).  The counts are read 16 a thread and step, the next step's ahead.
@@ -311,47 +315,47 @@ __global__ void __launch_bounds__(256) kda_cache_fork_rows_kernel(const Cache C,
 constexpr int kCluster = 8;
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kBlock)
     kda_cache_plan_kernel(const int32_t *refs, int P, int32_t *src, int32_t *dst, int32_t *to, int32_t *live_out) {
-    __shared__ int sh[32];
-    __shared__ int counts[3];   // in use, free below L, in use from L on
+    __shared__ Two sh[32];
+    __shared__ int in_use;
+    __shared__ Two counts;   // free below L, in use from L on
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank();
     const int per = ((P + kCluster - 1) / kCluster + 3) & ~3;
     const int lo = min(P, rank * per), hi = min(P, lo + per);
-    int mine = 0, total;
+    Two total;
+    int mine = 0;
     for (int i = lo + threadIdx.x; i < hi; i += kBlock) mine += refs[i] > 0;
-    scan1024(mine, total, sh);
-    if (threadIdx.x == 0) counts[0] = total;
+    scan1024(two(mine, 0), total, sh);
+    if (threadIdx.x == 0) in_use = (int)total;
     cluster.sync();
     int live = 0;
-    for (int r = 0; r < kCluster; ++r) live += *cluster.map_shared_rank(&counts[0], r);
-    int free_below = 0, live_above = 0;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) live += *cluster.map_shared_rank(&in_use, r);
+    Two both = 0;
     for (int i = lo + threadIdx.x; i < hi; i += kBlock) {
         const bool used = refs[i] > 0;
-        free_below += !used && i < live;
-        live_above += used && i >= live;
+        both += two(!used && i < live, used && i >= live);
     }
-    scan1024(free_below, total, sh);
-    if (threadIdx.x == 0) counts[1] = total;
-    scan1024(live_above, total, sh);
-    if (threadIdx.x == 0) counts[2] = total;
+    scan1024(both, total, sh);
+    if (threadIdx.x == 0) counts = total;
     cluster.sync();
-    int f = 0, u = 0, moved = 0;
+    Two before = 0, all = 0;
+#pragma unroll
     for (int r = 0; r < kCluster; ++r) {
-        const int a = *cluster.map_shared_rank(&counts[1], r), b = *cluster.map_shared_rank(&counts[2], r);
-        if (r < rank) f += a, u += b;
-        moved += a;
+        const Two c = *cluster.map_shared_rank(&counts, r);
+        if (r < rank) before += c;
+        all += c;
     }
+    const int moved = (int)all;
     for (int base = lo; base < hi; base += kBlock) {
         const int i = base + threadIdx.x;
         const bool used = i < hi && refs[i] > 0;
         const bool fb = i < hi && !used && i < live, la = used && i >= live;
-        const int at_f = f + scan1024(fb, total, sh);
-        f += total;
-        const int at_u = u + scan1024(la, total, sh);
-        u += total;
-        if (fb) dst[at_f] = i;
-        if (la) src[at_u] = i;
+        const Two at = before + scan1024(two(fb, la), total, sh);
+        before += total;
+        if (fb) dst[(int)at] = i;
+        if (la) src[(int)(at >> 32)] = i;
     }
     // entries behind the moved ones
     for (int i = lo + threadIdx.x; i < hi; i += kBlock)
@@ -398,8 +402,11 @@ __global__ void __launch_bounds__(256) kda_cache_renumber_kernel(const Cache C, 
 }
 
 // ---------------------------------------------------------------- copy
-// A unit is a part of one page's keys or values: 16 KB.  Blocks take units in turn.
-constexpr int kCopyThreads = 256, kCopyInFlight = 4;
+// A unit is a part of one page's keys or values: 16 KB, eight accesses in flight a thread
+// (half of a cache of 16384 pages, 0.54 GB: 87 us; with four in flight 101 us, with two 115 us).
+// Blocks take units in turn; a lane each looks at the next 32, because a long list may be mostly
+// empty entries.
+constexpr int kCopyThreads = 128, kCopyInFlight = 8;
 template <bool DENSE>
 __global__ void __launch_bounds__(kCopyThreads) kda_cache_copy_kernel(const Cache C, const Pages kp, const Pages vp, int M,
                                                                       const int32_t *src, const int32_t *dst) {
@@ -407,14 +414,17 @@ __global__ void __launch_bounds__(kCopyThreads) kda_cache_copy_kernel(const Cach
     const int page = (C.H * pieces) << C.shift;           // 16-byte pieces of a page
     const int per = (page + kCopyThreads * kCopyInFlight - 1) / (kCopyThreads * kCopyInFlight);
     const int64_t units = (int64_t)M * per * 2;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int m = (int)(u / (per * 2)), part = (int)(u - (int64_t)m * (per * 2));
-        const int a = src[m], b = dst[m];
-        if (a < 0 || b < 0) continue;                     // an empty entry
-        if (a >= C.P || b >= C.P) {
-            if (threadIdx.x == 0) atomicOr(&g_cache_status, kCacheBadPage);
-            continue;
-        }
+    const int lane = threadIdx.x & 31;
+    for (int64_t base = blockIdx.x; base < units; base += 32 * (int64_t)gridDim.x) {
+      const int64_t mine = base + lane * (int64_t)gridDim.x;
+      const int m_of = (int)(mine / (per * 2)), part_of = (int)(mine - (int64_t)m_of * (per * 2));
+      const int a_of = mine < units ? src[m_of] : -1, b_of = mine < units ? dst[m_of] : -1;
+      const bool some = a_of >= 0 && b_of >= 0, bad = some && (a_of >= C.P || b_of >= C.P);
+      if (bad) atomicOr(&g_cache_status, kCacheBadPage);
+      for (uint32_t left = __ballot_sync(0xffffffffu, some && !bad); left; left &= left - 1) {
+        const int who = __ffs(left) - 1;
+        const int a = __shfl_sync(0xffffffffu, a_of, who), b = __shfl_sync(0xffffffffu, b_of, who);
+        const int part = __shfl_sync(0xffffffffu, part_of, who);
         const Pages &x = part < per ? kp : vp;
         const int first = (part < per ? part : part - per) * kCopyThreads * kCopyInFlight + threadIdx.x;
         uint4 v[kCopyInFlight];
@@ -436,6 +446,7 @@ __global__ void __launch_bounds__(kCopyThreads) kda_cache_copy_kernel(const Cach
 #pragma unroll
         for (int i = 0; i < kCopyInFlight; ++i)
             if (at[i] >= 0) *reinterpret_cast<uint4 *>(x.p + b * x.page + at[i]) = v[i];
+      }
     }
 }
 
@@ -488,7 +499,7 @@ cudaError_t kda_launch_cache_compact(const Cache &C, int32_t *refs_out, int32_t 
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t most = C.P > (int64_t)C.N * C.wide ? C.P : (int64_t)C.N * C.wide;
-    const int64_t blocks = (most + 1023) / 1024;
+    const int64_t blocks = (most + 255) / 256;
     return launch_behind(kda_cache_renumber_kernel, (unsigned)(blocks > 1216 ? 1216 : blocks), 256, stream, C,
                          (const int32_t *)src, (const int32_t *)dst, (const int32_t *)to, (const int32_t *)counts, refs_out,
                          table_out);
@@ -505,7 +516,7 @@ cudaError_t kda_launch_cache_copy(const Cache &C, const Pages &kp, const Pages &
     };
     const int64_t page = (int64_t)(C.H * (C.d / 8)) << C.shift;
     const int64_t units = (page + kCopyThreads * kCopyInFlight - 1) / (kCopyThreads * kCopyInFlight) * 2 * M;
-    const unsigned grid = (unsigned)(units < 152 * 8 ? units : 152 * 8);
+    const unsigned grid = (unsigned)(units < 152 * 16 ? units : 152 * 16);
     if (dense(kp) && dense(vp))
         kda_cache_copy_kernel<true><<<grid, kCopyThreads, 0, stream>>>(C, kp, vp, M, src, dst);
     else
