@@ -27,7 +27,7 @@
 // 8192 tokens, 32 on 8 heads of 128.  These now take 340 us; at the sustained rate of the card's own
 // matrix product it would be 323 us.)  Chunks over a cache: few row tiles and a long
 // axis of keys, so that the keys of all row tiles are laid end to end and cut into as many
-// equal runs as there are SMs (512 tokens behind 32k: 277 -> 217 us, and 203 us now); a warp finds the
+// equal runs as there are SMs (512 tokens behind 32k: 277 -> 217 us); a warp finds the
 // next piece of the block's run while the others are busy with this one, and a row tile that
 // is cut leaves shares, which a second kernel joins.
 //
@@ -66,6 +66,7 @@ struct Work {
     int64_t a;
     int32_t tokens, keys, rows;    // rows of the sequence from this tile on
     int32_t j0, n_of[2];
+    int32_t turn;                  // the walk begins with key tile j0 + turn, and j0 follows on the last
     int32_t slot;                  // where its share goes; -1: it is the whole
 };
 
@@ -121,6 +122,7 @@ __device__ __forceinline__ void fill(Work &w, const Attn &A, const AttnSeq &sq, 
     w.rows = w.tokens * A.G - tile * kTileRows;
     w.slot = -1;
     w.j0 = 0;
+    w.turn = 0;
 }
 // Key tiles that the rows of row tile i see.
 __device__ __forceinline__ int32_t tiles_seen(const Work &w, int G, int i) {
@@ -254,10 +256,11 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (PAGED && warp == kWorkWarp) {
         // ------------------------------------------------ the next piece of work
-        // units [u, end) of heads * total
+        // units [u, end) of heads * total, the last piece first (see where turn is set)
         const int64_t all = total * A.Hkv;
         const int64_t blocks = max((int64_t)1, min((int64_t)gridDim.x, all / 8));
         auto edge = [&](int64_t b) { return all * b / blocks; };
+        const int64_t run = max((int64_t)1, all / blocks);
         int64_t u = 0, end = 0;
         if (lane == 0) sh.rec[blockIdx.x * 4] = 0;
         if (blockIdx.x < blocks) u = edge(blockIdx.x), end = edge(blockIdx.x + 1);
@@ -268,7 +271,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             Work w;
             w.some = 0;
             while (ok && u < end && !w.some) {
-                const int64_t head = u / total, in = u - head * total;
+                const int64_t head = (end - 1) / total, in = end - 1 - head * total;
                 int64_t first;
                 const int n = find_sequence(ct, A.N, in, cost_of, first);
                 if (n < 0) break;
@@ -281,8 +284,8 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 // its units [t0, t1); an edge next to either end counts as that end
                 const int64_t t0 = head * total + first + c.upto(lo), t1 = head * total + first + c.upto(lo + 1);
                 auto snap = [&](int64_t x) { return x <= t0 + kOver + 1 ? t0 : x >= t1 - 2 ? t1 : x; };
-                const int64_t from = blockIdx.x == 0 && u == edge(0) ? t0 : snap(u), to = end >= t1 ? t1 : snap(end);
-                u = t1;
+                const int64_t from = u <= t0 ? t0 : snap(u), to = end >= t1 ? t1 : snap(end);
+                end = t0;
                 if (from >= to) continue;
                 fill<true>(w, A, attn_seq<true>(A, n), n, lo, (int)head);
                 const int32_t seen[2] = {tiles_seen(w, G, 0), tiles_seen(w, G, 1)};
@@ -299,6 +302,18 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 const int32_t j1 = key(to);
                 w.n_of[0] = max(0, min(seen[0], j1) - w.j0);
                 w.n_of[1] = max(0, min(seen[1], j1) - w.j0);
+                // The row tiles of a head read the same keys, each in blocks of their own: they should do so at
+                // about the same time, or HBM delivers every key once a row tile.  So a block begins
+                // with the piece that starts a row tile, and every piece with a multiple of the run
+                // (512 tokens behind 32k: 960 -> 142 MB from HBM, 203 -> 183 us).
+                const int64_t begin = (w.j0 + run - 1) / run * run;
+                const int32_t walk = max(w.n_of[0], w.n_of[1]);
+                if (begin > w.j0 && begin < w.j0 + walk) {
+                    w.turn = (int32_t)(begin - w.j0);
+                    // (both row tiles walk all key tiles then: what they do not see is masked)
+                    w.n_of[0] = walk;
+                    w.n_of[1] = w.rows > 128 ? walk : 0;
+                }
                 if (splits > 1) {
                     const bool begins = from == t0;
                     w.slot = begins ? 2 * blockIdx.x + 1 : 2 * blockIdx.x;
@@ -328,7 +343,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         for (int k = 0; ok && k < kPieces; ++k) {
             Work w;
             if (!piece(k, w)) break;
-            const int n = max(w.n_of[0], w.n_of[1]), j0 = w.j0, head = w.head, keys = w.keys;
+            const int n = max(w.n_of[0], w.n_of[1]), j0 = w.j0, head = w.head, keys = w.keys, turn = w.turn;
             const int64_t a = w.a;
             const int32_t *row = PAGED ? A.table + (int64_t)w.n * A.wide : nullptr;
             if (PAGED) bad = bad || A.lens[w.n] > (int64_t)A.wide * A.page;
@@ -336,7 +351,8 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             for (int x = 0; x < 2 * n; ++x, ++c) {
                 // order: K0, K1, V0, K2, V1, ...
                 const bool last = x == 2 * n - 1, values = last || (x > 0 && (x & 1) == 0);
-                const int j = j0 + (values ? (last ? n - 1 : x / 2 - 1) : (x + 1) / 2);
+                int j = (values ? (last ? n - 1 : x / 2 - 1) : (x + 1) / 2) + turn;
+                j = j0 + (j < n ? j : j - n);
                 int page = 0, at;
                 if (PAGED) {
                     const int64_t first = (int64_t)j * kAttnKeys + which * box;
@@ -379,7 +395,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         for (int k = 0; ok && k < kPieces; ++k) {
             Work w;
             if (!piece(k, w)) break;
-            const int n_of[2] = {w.n_of[0], w.n_of[1]}, n = max(n_of[0], n_of[1]), j0 = w.j0, keys = w.keys;
+            const int n_of[2] = {w.n_of[0], w.n_of[1]}, n = max(n_of[0], n_of[1]), j0 = w.j0, keys = w.keys, turn = w.turn;
             ok = n == 0 || full(c0);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -399,7 +415,8 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 ok = ok && full(cv);
                 if (!ok) break;
                 const uint32_t v_at = ring_at + (cv % NST) * L::kTileBytes;
-                const int32_t left = keys - (j0 + j) * kAttnKeys;   // keys from this tile on
+                const int at = j + turn < n ? j + turn : j + turn - n;
+                const int32_t left = keys - (j0 + at) * kAttnKeys;   // keys from this tile on
                 if (left < kAttnKeys) {
                     // value rows behind the last key hold anything
                     uint8_t *v = ring + (cv % NST) * L::kTileBytes;
@@ -447,6 +464,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             Work w;
             if (!piece(k, w)) break;
             const int32_t tile = w.tile, head = w.head, rows = w.rows, j0 = w.j0, mine = i ? w.n_of[1] : w.n_of[0], slot = w.slot, keys = w.keys;
+            const int32_t n = max(w.n_of[0], w.n_of[1]), turn = w.turn;
             const int32_t behind = keys - w.tokens;   // key index that the first token sees last
             const int64_t a = w.a;
             read(k);
@@ -483,7 +501,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 #pragma unroll
                 for (int x = 0; x < 4; ++x) tmem_ld32_nowait(S + x * 32, s + x * 32);
                 tmem_wait_ld(s);
-                const int32_t vis = seen - (j0 + j) * kAttnKeys;
+                const int32_t vis = seen - (j0 + (j + turn < n ? j + turn : j + turn - n)) * kAttnKeys;
                 if (__any_sync(0xffffffffu, vis < kAttnKeys)) {
 #pragma unroll
                     for (int x = 0; x < 128; ++x) s[x] = x < vis ? s[x] : -INFINITY;
