@@ -680,12 +680,15 @@ kda_status kda_attn_prefill(const kda_attn_dims *dims, const kda_heads *q, const
 
 /*
  * kda_attn_backward -- gradients of kda_attn_prefill for d_out = dL/d out: with
- * P = e^(s - lse), delta_i = d_out_i . out_i and dS_ij = P_ij (d_out_i . v_j - delta_i),
+ * P = e^(s - lse), delta_i = d_out_i . out_i and dS_ij = P_ij (d_out_i . v_j - delta_i) for
+ * the keys j that token i sees (0 for the others),
  *
  *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij d_out_i
  *
  * (the sums of dk and dv over the query heads of the group too).  P and dS are rounded to the
- * 16-bit type for the products, sums are fp32, and none depends on timing.
+ * 16-bit type for the products, sums are fp32, and none depends on timing.  An infinity or a
+ * NaN in a sequence may reach gradients of that sequence up to 127 tokens to either side of
+ * where the formulas have it, and no other sequence's.
  *
  *   out, lse   the forward's (out in in_dtype, heads [T, H_q, d]; lse fp32 [T, H_q]).
  *   d_out      in_dtype, heads [T, H_q, d].
@@ -718,7 +721,8 @@ kda_status kda_attn_backward(const kda_attn_dims *dims, const kda_heads *q, cons
  *   out, lse   as in kda_attn_prefill.
  *   workspace  kda_attn_paged_workspace(dims, cache, cu_seqlens) bytes, 16-byte aligned
  *              (of cu_seqlens it matters only whether it is NULL): shares of rows whose
- *              keys are split over blocks, 21 MB for one token of 8 key heads of 128 channels.
+ *              keys are split over blocks (d = 128: 2.5 MB for one token, 40 MB for a chunk, up
+ *              to 81 MB for a large batch that may hold both).
  */
 int64_t kda_attn_paged_workspace(const kda_attn_dims *dims, const kda_cache_dims *cache,
                                  const int32_t *cu_seqlens);

@@ -225,9 +225,9 @@ __device__ __forceinline__ void store8(void *base, bool f32, int64_t at, const f
 // its lanes see the phase complete, or all give up: what they wait for is one word).  A wait
 // that gives up records the status word; the warp then leaves its loop, and so do, each by
 // its own bounded wait, those that depend on it.
-constexpr uint32_t kAttnPolls = 1u << 19;
-constexpr uint32_t kAttnLongPolls = 1u << 21;   // for waits that last as long as a piece of work
-// The thread is suspended until the phase completes, or for about a microsecond a poll (a
+constexpr uint32_t kAttnPolls = 1u << 20;
+constexpr uint32_t kAttnLongPolls = 1u << 24;   // for waits that last as long as a piece of work
+// The thread is suspended until the phase completes, or for up to a microsecond a poll (a
 // sleep between polls would wake too late: 100 cycles count here).
 __device__ __forceinline__ bool attn_poll(uint64_t *bar, uint32_t parity, uint32_t polls) {
 #pragma unroll 1

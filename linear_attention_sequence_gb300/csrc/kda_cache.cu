@@ -114,13 +114,13 @@ __global__ void __launch_bounds__(kBlock) kda_cache_reserve_kernel(const Cache C
         }
         return want > C.wide ? -1 : (int)want - have + (old >= 0);
     };
-    // how many pages in all (no more than there are matter)
+    // how many pages in all
     int64_t want = 0;
     for (int base = 0; base < C.N; base += kBlock) {
         const int n = base + threadIdx.x;
         int len, add, have, old, total;
         const int need = n < C.N ? max(0, needs(n, true, len, add, have, old)) : 0;
-        scan1024(min(need, C.P + 1), total, sh);
+        scan1024(need, total, sh);   // (N * wide fits 32 bits)
         want += total;
     }
     const int ask = (int)min(want, (int64_t)C.P);
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kBlock) kda_cache_reserve_kernel(const Cache C
         const int n = base + threadIdx.x;
         int len = 0, add = 0, have = 0, old = -1, total;
         const int need = n < C.N ? needs(n, false, len, add, have, old) : -1;
-        const int64_t at = before + scan1024(min(max(0, need), C.P + 1), total, sh);
+        const int64_t at = before + scan1024(max(0, need), total, sh);
         before += total;
         if (n >= C.N) continue;
         const bool served = need >= 0 && (need == 0 || at + need <= got);
