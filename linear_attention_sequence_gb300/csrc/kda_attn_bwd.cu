@@ -68,6 +68,7 @@ static_assert(offsetof(Control, stat) % 16 == 0 && alignof(Control) % 16 == 0, "
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) kda_attn_delta_kernel(const Attn A, const Grads B) {
     constexpr int LANES = D / 8;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
     const int c = threadIdx.x % LANES;
     const int64_t rows = (int64_t)A.T * A.Hq;
@@ -204,6 +205,7 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
         for (int j = max(0, a - NA); j < a; ++j) wait(&ct.a_full[j % NA], j / NA);
         for (int j = max(0, b - NB); j < b; ++j) wait(&ct.b_full[j % NB], j / NB);
     } else if (warp == kStatWarp) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernel in front writes delta and lse2
         for (int j = 0; j < n; ++j) {
             const int st = j % kStats;
             const int64_t h = hk * G + j / per, at = h * A.T + sq.a, row = (int64_t)(kt + j % per) * kTile + lane * 4;
@@ -423,6 +425,7 @@ __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const 
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const bool live = qt * kTile + r < len;
         const int64_t at = (int64_t)h * A.T + sq.a + qt * kTile + r;
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernel in front writes delta and lse2
         const float lse2 = live ? B.lse2[at] : INFINITY, delta = live ? B.delta[at] : 0.f;
         const float c = A.scale_log2;
         const uint64_t c2 = pack2(c, c), l2 = pack2(-lse2, -lse2), d2 = pack2(-delta, -delta);
@@ -482,6 +485,10 @@ kda_attn_backward_kernel(const __grid_constant__ CUtensorMap qm, const __grid_co
     const int tid = threadIdx.x, warp = attn_warp();
     const bool keys = blockIdx.x < B.key_blocks;
     if (tid == 0) {
+        sm100::prefetch_tmap(&qm);
+        sm100::prefetch_tmap(&km);
+        sm100::prefetch_tmap(&vm);
+        sm100::prefetch_tmap(&om);
         sm100::mbar_init(&ct.own_full, 1);
         for (int i = 0; i < 4; ++i) {
             sm100::mbar_init(&ct.a_full[i], 1);
@@ -513,7 +520,10 @@ kda_attn_backward_kernel(const __grid_constant__ CUtensorMap qm, const __grid_co
     const bool some =
         keys ? attn_whole_part<kThreads>(A.N, A.Hkv, blockIdx.x, false, same, tiles, &ct.part, ct.scan)
              : attn_whole_part<kThreads>(A.N, A.Hq, blockIdx.x - (uint32_t)B.key_blocks, true, same, tiles, &ct.part, ct.scan);
-    if (!some) return;
+    if (!some) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // no kernel ends before the one in front of it
+        return;
+    }
     const AttnSeq sq = attn_seq<false>(A, ct.part.n);
     if (warp == kProductWarp) {
         sm100::tmem_alloc(&ct.tmem, 512);
@@ -542,15 +552,26 @@ cudaError_t backward(const Attn &A, Grads &B, cudaStream_t stream) {
     const auto kernel = kda_attn_backward_kernel<D, BF16>;
     constexpr int smem = Lay<D>::kTiles + (int)sizeof(Control);
     static_assert(smem <= 232448, "shared memory of a block");
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = kda_allow_smem<kda_attn_backward_kernel<D, BF16>>(smem);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)A.T * A.Hq;
     kda_attn_delta_kernel<D, BF16><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, stream>>>(A, B);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t tiles = A.cu ? (int64_t)A.T / kTile + A.N : (A.seq_len + kTile - 1) / kTile * A.N;
     B.key_blocks = tiles * A.Hkv;
-    kernel<<<(unsigned)(B.key_blocks + tiles * A.Hq), kThreads, smem, stream>>>(qm, km, vm, om, A, B);
-    return cudaGetLastError();
+    // The gradients' kernel starts behind the first blocks of delta's; what it reads but delta and lse2 was
+    // there before that one started, and its results are written after it has waited.
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(B.key_blocks + tiles * A.Hq));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, qm, km, vm, om, A, B);
 }
 
 }  // namespace

@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "kda_common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -245,6 +247,21 @@ __device__ __forceinline__ bool attn_wait_long(uint64_t *bar, uint32_t parity, u
 }
 
 }  // namespace kda
+
+// Allows a kernel `bytes` of dynamic shared memory on the current device, once a device (the call
+// costs as much as a third of a launch).
+template <auto Kernel>
+cudaError_t kda_allow_smem(int bytes) {
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = (uint64_t)1 << (dev & 63);
+    if (dev < 64 && (allowed.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Launchers (kda_attn_*.cu).
 int64_t kda_attn_paged_ws(const kda::Attn &A);

@@ -178,6 +178,8 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const int G = A.G;
 
     if (tid == 0) {
+        sm100::prefetch_tmap(&kmap);
+        sm100::prefetch_tmap(&vmap);
         for (int i = 0; i < NST; ++i) {
             sm100::mbar_init(&ct.full[i], 1);
             sm100::mbar_init(&ct.empty[i], 1);
@@ -470,7 +472,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             read(k);
             if (k > 0) sm100::named_sync(1 + i, 128);   // the tile's results have left its place
             {
-                // 16 bytes a thread and pass, all passes in flight; a loop, because code that runs once a
+                // 16 bytes a thread and pass, all passes in flight; a short loop, because code that runs once a
                 // block is paid by its length
                 constexpr int CH = D / 8, PER = 128 / CH;   // 16-byte pieces of a row; rows a pass
                 const int p = rt % CH;
@@ -479,7 +481,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 const Row step(PER, G);
                 const uint16_t *q = static_cast<const uint16_t *>(A.q) + a * A.q_t + (int64_t)head * G * A.q_h + p * 8;
                 uint32_t to = sm100::smem_u32(Qs + i * L::kTileBytes + (p >> 3) * L::kBlockBytes + ((p & 7) << 4));
-#pragma unroll 1
+#pragma unroll 4
                 for (int x = 0; x < CH; ++x, r += PER) {
                     const bool some = i * 128 + r < rows;   // else zeros
                     cp_async16(to + r * 128 ^ ((r & 7) << 4), some ? q + at.tok * A.q_t + at.g * A.q_h : q, some ? 16 : 0);
@@ -767,6 +769,8 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     const int G = A.G;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
+        sm100::prefetch_tmap(&kmap);
+        sm100::prefetch_tmap(&vmap);
         for (int i = 0; i < NST; ++i) {
             sm100::mbar_init(&ct.full[i], 1);
             sm100::mbar_init(&ct.empty[i], 4);
@@ -778,11 +782,8 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         const int64_t rows = (s.b - s.a) * G;
         return AttnNeed{rows > 0 && rows <= kFewRows ? 1 : 0, (int32_t)((s.keys + kFewKeys - 1) / kFewKeys)};
     };
-    int64_t slots;
-    const bool some = attn_split_part<kFewThreads>(A.N, A.Hkv, blockIdx.x, slots_at_once, 8, 4, need, &ct.part, ct.scan,
-                                                   &slots);
-    if (!some) return;
-    const AttnPart part = ct.part;
+    AttnPart part;
+    if (!attn_split_part<kFewThreads>(A.N, A.Hkv, blockIdx.x, slots_at_once, 8, 4, need, part, &ct.part, ct.scan)) return;
     const AttnSeq sq = attn_seq<true>(A, part.n);
     if (part.split == 0 && tid == 0) {
         int32_t *rec = sh.rec + ((int64_t)part.n * A.Hkv + part.head) * 4;
@@ -1036,11 +1037,6 @@ Shares shares_at(char *ws, int64_t records, int64_t slots, int rows) {
     return s;
 }
 
-template <typename Kernel>
-cudaError_t roomy(Kernel kernel, int smem) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-}
-
 template <typename... Params, typename... Args>
 cudaError_t launch(bool behind, void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
                    const Args &...args) {
@@ -1064,7 +1060,7 @@ cudaError_t prefill(const Attn &A, cudaStream_t stream) {
         !kda_make_attn_map(&vm, A.v, BF16, D, A.Hkv, A.T, 1, A.v_h, A.v_t, 0, kAttnKeys))
         return cudaErrorInvalidValue;
     const auto kernel = kda_attn_tc_kernel<D, BF16, false>;
-    cudaError_t e = roomy(kernel, Lay<D>::kSmem);
+    cudaError_t e = kda_allow_smem<kda_attn_tc_kernel<D, BF16, false>>(Lay<D>::kSmem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = A.cu ? (int64_t)A.T * A.G / kTileRows + A.N
                                : (A.seq_len * A.G + kTileRows - 1) / kTileRows * A.N;
@@ -1084,7 +1080,7 @@ cudaError_t paged(const Attn &A, char *ws, cudaStream_t stream) {
             return cudaErrorInvalidValue;
         const Shares sh = shares_at(ws, z.few_tiles, z.few_slots, kFewRows);
         const auto kernel = kda_attn_few_kernel<D, BF16>;
-        e = roomy(kernel, FewLay<D>::kSmem);
+        e = kda_allow_smem<kda_attn_few_kernel<D, BF16>>(FewLay<D>::kSmem);
         if (e == cudaSuccess)
             e = launch(false, kernel, dim3((unsigned)z.few_parts), kFewThreads, FewLay<D>::kSmem, stream, km, vm, A, sh,
                        box, kFewAtOnce);
@@ -1102,7 +1098,7 @@ cudaError_t paged(const Attn &A, char *ws, cudaStream_t stream) {
             return cudaErrorInvalidValue;
         const Shares sh = shares_at(ws, kSMs, 2 * kSMs, kTileRows);
         const auto kernel = kda_attn_tc_kernel<D, BF16, true>;
-        e = roomy(kernel, Lay<D>::kSmem);
+        e = kda_allow_smem<kda_attn_tc_kernel<D, BF16, true>>(Lay<D>::kSmem);
         if (e == cudaSuccess)
             e = launch(false, kernel, dim3(kSMs), kThreads, Lay<D>::kSmem, stream, km, vm, A, sh, box,
                        z.few ? kFewRows : 0);

@@ -59,11 +59,50 @@ __host__ inline int64_t attn_parts(int64_t tiles, int slots, int waves) {
     return tiles * 2 <= slots ? slots : tiles + (int64_t)slots * waves;
 }
 
-// Part number `index` of `heads` heads (head fastest), the block's work in shared memory.
-// `need(n)` gives what sequence n needs.  False: there is no such part.
+// Part number `index` of `heads` heads (head fastest).  `need(n)` gives what sequence n needs.  False:
+// there is no such part.  Up to 32 sequences each warp finds it by itself (and the block only
+// meets); beyond, the block does together.  Every thread calls it.
 template <int THREADS, typename Need>
 __device__ __forceinline__ bool attn_split_part(int N, int heads, int64_t index, int slots, int waves, int least,
-                                                Need need, AttnPart *part, int64_t *sh, int64_t *all_slots) {
+                                                Need need, AttnPart &part, AttnPart *shared, int64_t *sh) {
+    const int64_t at = index / heads;
+    auto fill = [&](AttnPart &p, int n, const AttnNeed &x, int32_t run, int64_t splits, int64_t in, int64_t shares_before) {
+        p.n = n;
+        p.head = (int32_t)(index - at * heads);
+        p.tile = (int32_t)(in / splits);
+        p.split = (int32_t)(in - p.tile * splits);
+        p.splits = (int32_t)splits;
+        p.j0 = splits > 1 ? p.split * run : 0;
+        p.j1 = splits > 1 ? min(x.keys, p.j0 + run) : x.keys;
+        p.slot = splits > 1 ? (int32_t)((shares_before + p.tile * splits) * heads + (int64_t)p.head * splits + p.split) : -1;
+    };
+    auto splits_of = [](const AttnNeed &x, int32_t run) { return x.keys > run ? (int64_t)(x.keys + run - 1) / run : (int64_t)1; };
+    if (N <= 32) {
+        const int lane = threadIdx.x & 31;
+        const AttnNeed x = lane < N ? need(lane) : AttnNeed{0, 0};
+        int64_t tiles = x.tiles, keys = (int64_t)x.tiles * x.keys;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+            keys += __shfl_xor_sync(0xffffffffu, keys, o);
+        }
+        const int32_t run = attn_run(tiles * heads, keys * heads, slots, waves, least);
+        const int64_t splits = splits_of(x, run), parts = x.tiles * splits, shares = splits > 1 ? parts : 0;
+        int64_t p = parts, s = shares;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, p, o), z = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) p += y, s += z;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, at >= p - parts && at < p);
+        __syncthreads();
+        if (!here) return false;
+        const int n = __ffs(here) - 1;
+        const AttnNeed y{__shfl_sync(0xffffffffu, x.tiles, n), __shfl_sync(0xffffffffu, x.keys, n)};
+        fill(part, n, y, run, __shfl_sync(0xffffffffu, splits, n), at - __shfl_sync(0xffffffffu, p - parts, n),
+             __shfl_sync(0xffffffffu, s - shares, n));
+        return true;
+    }
     const int per = (N + THREADS - 1) / THREADS;
     const int lo = (int)threadIdx.x * per, hi = min(N, lo + per);
     int64_t tiles = 0, keys = 0, total_tiles, total_keys;
@@ -78,31 +117,19 @@ __device__ __forceinline__ bool attn_split_part(int N, int heads, int64_t index,
     int64_t parts = 0, shares = 0, total_parts, total_shares;
     for (int n = lo; n < hi; ++n) {
         const AttnNeed x = need(n);
-        const int64_t splits = x.keys > run ? (x.keys + run - 1) / run : 1;
+        const int64_t splits = splits_of(x, run);
         parts += x.tiles * splits;
         if (splits > 1) shares += x.tiles * splits;
     }
     int64_t before = block_scan<THREADS>(parts, total_parts, sh);
     int64_t shares_before = block_scan<THREADS>(shares, total_shares, sh);
-    *all_slots = total_shares * heads;
-    if (index >= total_parts * heads) return false;
-    const int64_t at = index / heads;
+    if (at >= total_parts) return false;
     if (at >= before && at < before + parts) {
         for (int n = lo; n < hi; ++n) {
             const AttnNeed x = need(n);
-            const int64_t splits = x.keys > run ? (x.keys + run - 1) / run : 1;
+            const int64_t splits = splits_of(x, run);
             if (at < before + x.tiles * splits) {
-                const int32_t in = (int32_t)(at - before);
-                part->n = n;
-                part->head = (int32_t)(index % heads);
-                part->tile = (int32_t)(in / splits);
-                part->split = (int32_t)(in % splits);
-                part->splits = (int32_t)splits;
-                part->j0 = splits > 1 ? part->split * run : 0;
-                part->j1 = splits > 1 ? min(x.keys, part->j0 + run) : x.keys;
-                part->slot = splits > 1 ? (int32_t)((shares_before + in / splits * splits) * heads +
-                                                    (int64_t)part->head * splits + part->split)
-                                        : -1;
+                fill(*shared, n, x, run, splits, at - before, shares_before);
                 break;
             }
             before += x.tiles * splits;
@@ -110,6 +137,7 @@ __device__ __forceinline__ bool attn_split_part(int N, int heads, int64_t index,
         }
     }
     __syncthreads();
+    part = *shared;
     return true;
 }
 
