@@ -159,12 +159,12 @@ __device__ __forceinline__ void write_row(void *to, bool f32, int64_t at, uint32
 
 template <int D, bool BF16>
 __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CUtensorMap *vm, const CUtensorMap *om,
-                          const Attn &A, const Grads &B, Control &ct, uint8_t *base, const AttnSeq &sq, uint32_t tmem, int warp) {
+                          const Attn &A, const Grads &B, Control &ct, const AttnPart &part, uint8_t *base, const AttnSeq &sq, uint32_t tmem, int warp) {
     using L = Lay<D>;
     constexpr int NA = L::kA, NB = L::kB;
     const int lane = threadIdx.x & 31;
     uint8_t *Ks = base, *Vs = base + L::kBytes, *ra = base + 2 * L::kBytes, *rb = ra + NA * L::kBytes;   // queries, dO
-    const int kt = ct.part.tile, hk = ct.part.head, G = A.G;
+    const int kt = part.tile, hk = part.head, G = A.G;
     const int len = (int)(sq.b - sq.a), tiles = (len + kTile - 1) / kTile;
     const int per = tiles - kt, n = per * G;   // step j: head j / per of the group, query tile kt + j % per
     const int tail = len - (tiles - 1) * kTile;   // rows of the last tile
@@ -343,12 +343,12 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
 
 template <int D, bool BF16>
 __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const CUtensorMap *vm, const CUtensorMap *om,
-                            const Attn &A, const Grads &B, Control &ct, uint8_t *base, const AttnSeq &sq, uint32_t tmem, int warp) {
+                            const Attn &A, const Grads &B, Control &ct, const AttnPart &part, uint8_t *base, const AttnSeq &sq, uint32_t tmem, int warp) {
     using L = Lay<D>;
     constexpr int NA = L::kA, NB = L::kB;
     const int lane = threadIdx.x & 31;
     uint8_t *Qs = base, *Os = base + L::kBytes, *ra = base + 2 * L::kBytes, *rb = ra + NA * L::kBytes;   // keys, values
-    const int qt = ct.part.tile, h = ct.part.head, hk = h / A.G;
+    const int qt = part.tile, h = part.head, hk = h / A.G;
     const int len = (int)(sq.b - sq.a), n = qt + 1;
     const int tail = len - qt * kTile;   // rows of the last key tile (the diagonal one), if below 128
     constexpr uint32_t S[2] = {0, 128}, DP = 256, DQ = 384;
@@ -517,14 +517,14 @@ kda_attn_backward_kernel(const __grid_constant__ CUtensorMap qm, const __grid_co
     // the first key tiles are seen by the most queries, the last query tiles see the most keys:
     // those start first
     const int same = A.cu ? -1 : (int)((A.seq_len + kTile - 1) / kTile);
-    const bool some =
-        keys ? attn_whole_part<kThreads>(A.N, A.Hkv, blockIdx.x, false, same, tiles, &ct.part, ct.scan)
-             : attn_whole_part<kThreads>(A.N, A.Hq, blockIdx.x - (uint32_t)B.key_blocks, true, same, tiles, &ct.part, ct.scan);
+    AttnPart part;
+    const bool some = attn_whole_part<kThreads>(A.N, keys ? A.Hkv : A.Hq, blockIdx.x - (keys ? 0u : (uint32_t)B.key_blocks),
+                                                !keys, same, tiles, part, &ct.part, ct.scan);
     if (!some) {
         asm volatile("griddepcontrol.wait;" ::: "memory");   // no kernel ends before the one in front of it
         return;
     }
-    const AttnSeq sq = attn_seq<false>(A, ct.part.n);
+    const AttnSeq sq = attn_seq<false>(A, part.n);
     if (warp == kProductWarp) {
         sm100::tmem_alloc(&ct.tmem, 512);
         sm100::tmem_relinquish();
@@ -534,9 +534,9 @@ kda_attn_backward_kernel(const __grid_constant__ CUtensorMap qm, const __grid_co
     sm100::tc_fence_after();
     const uint32_t tmem = ct.tmem;
     if (keys)
-        key_block<D, BF16>(&qm, &km, &vm, &om, A, B, ct, base, sq, tmem, warp);
+        key_block<D, BF16>(&qm, &km, &vm, &om, A, B, ct, part, base, sq, tmem, warp);
     else
-        query_block<D, BF16>(&qm, &km, &vm, &om, A, B, ct, base, sq, tmem, warp);
+        query_block<D, BF16>(&qm, &km, &vm, &om, A, B, ct, part, base, sq, tmem, warp);
     __syncthreads();
     if (warp == kProductWarp) sm100::tmem_dealloc(tmem, 512);
 }

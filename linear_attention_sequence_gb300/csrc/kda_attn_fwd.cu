@@ -200,7 +200,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         sm100::tmem_alloc(&ct.tmem, 512);
         sm100::tmem_relinquish();
     }
-    // how much work there is in front of each thread's run of sequences
+    // how much work there is in front of each run of sequences
     auto tiles_of = [&](int n) {   // prompts: a unit is a row tile
         const AttnSeq s = attn_seq<false>(A, n);
         return ((s.b - s.a) * G + kTileRows - 1) / kTileRows;
@@ -210,8 +210,9 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         return c.upto(c.tiles);
     };
     const int same = PAGED || A.cu ? -1 : (int)((A.seq_len * G + kTileRows - 1) / kTileRows);
+    const bool small = !PAGED && A.N <= 32;   // each warp forms the sums itself
     int64_t total = (int64_t)A.N * same;
-    if (PAGED || same < 0) {
+    if ((PAGED || same < 0) && !small) {
         const int per = (A.N + kRuns - 1) / kRuns, lo = tid * per, hi = tid < kRuns ? min(A.N, lo + per) : 0;
         int64_t mine = 0;
         for (int n = lo; n < hi; ++n) mine += PAGED ? cost_of(n) : tiles_of(n);
@@ -233,15 +234,22 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             return ok && w.some;
         }
         const uint32_t head = blockIdx.x % (uint32_t)A.Hkv, tile = blockIdx.x / (uint32_t)A.Hkv;
-        if (tile >= total) return false;
-        const uint32_t at = (uint32_t)total - 1 - tile;
         int n;
-        int64_t first;
-        if (same >= 0) {
-            n = (int)(at / (uint32_t)same);
-            first = (int64_t)n * same;
+        int64_t first, at;
+        if (same < 0 && small) {
+            const int64_t tiles = lane < A.N ? tiles_of(lane) : 0, all = __shfl_sync(0xffffffffu, warp_scan(tiles), 31);
+            if (tile >= all) return false;
+            at = all - 1 - tile;
+            n = warp_find(tiles, at, first);
         } else {
-            n = find_sequence(ct, A.N, at, tiles_of, first);
+            if (tile >= total) return false;
+            at = total - 1 - tile;
+            if (same >= 0) {
+                n = (int)((uint32_t)at / (uint32_t)same);
+                first = (int64_t)n * same;
+            } else {
+                n = find_sequence(ct, A.N, at, tiles_of, first);
+            }
         }
         fill<false>(w, A, attn_seq<false>(A, n), n, (int)(at - first), (int)head);
         w.n_of[0] = tiles_seen(w, G, 0);

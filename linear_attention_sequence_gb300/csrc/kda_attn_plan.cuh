@@ -141,25 +141,55 @@ __device__ __forceinline__ bool attn_split_part(int N, int heads, int64_t index,
     return true;
 }
 
+// A warp's inclusive sums.
+__device__ __forceinline__ int64_t warp_scan(int64_t x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+// Of up to 32 sequences, the one that holds unit `at`, by a warp: lane n has the `units` of sequence n.
+// `first`: its first unit; -1: none holds it.
+__device__ __forceinline__ int warp_find(int64_t units, int64_t at, int64_t &first) {
+    const int64_t upto = warp_scan(units);
+    const uint32_t here = __ballot_sync(0xffffffffu, at >= upto - units && at < upto);
+    const int n = __ffs(here) - 1;
+    first = __shfl_sync(0xffffffffu, upto - units, n < 0 ? 0 : n);
+    return n;
+}
+
 // Tile number `index` of `heads` heads (head fastest), from the first tile to the last or, with
 // `reverse`, from the last to the first: what takes longest starts first.  `same` >= 0: every
-// sequence has that many tiles.
+// sequence has that many tiles.  Then, and up to 32 sequences, each warp finds it by itself;
+// beyond, the block does together.  Every thread calls it.
 template <int THREADS, typename Tiles>
 __device__ __forceinline__ bool attn_whole_part(int N, int heads, uint32_t index, bool reverse, int same, Tiles tiles_of,
-                                                AttnPart *part, int64_t *sh) {
+                                                AttnPart &part, AttnPart *shared, int64_t *sh) {
     const uint32_t head = index % (uint32_t)heads, tile = index / (uint32_t)heads;
+    part.head = (int32_t)head;
+    part.slot = -1;
+    part.splits = 1;
     if (same >= 0) {
         const uint32_t total = (uint32_t)N * (uint32_t)same;   // (fits: the grid holds that many blocks)
-        if (threadIdx.x == 0 && tile < total) {
-            const uint32_t at = reverse ? total - 1 - tile : tile;
-            part->n = (int32_t)(at / (uint32_t)same);
-            part->head = (int32_t)head;
-            part->tile = (int32_t)(at % (uint32_t)same);
-            part->slot = -1;
-            part->splits = 1;
-        }
-        __syncthreads();
-        return tile < total;
+        if (tile >= total) return false;
+        const uint32_t at = reverse ? total - 1 - tile : tile;
+        part.n = (int32_t)(at / (uint32_t)same);
+        part.tile = (int32_t)(at % (uint32_t)same);
+        return true;
+    }
+    if (N <= 32) {
+        const int lane = threadIdx.x & 31;
+        const int64_t tiles = lane < N ? tiles_of(lane) : 0, total = __shfl_sync(0xffffffffu, warp_scan(tiles), 31);
+        if (tile >= total) return false;
+        int64_t first;
+        const int64_t at = reverse ? total - 1 - tile : tile;
+        part.n = warp_find(tiles, at, first);
+        part.tile = (int32_t)(at - first);
+        return true;
     }
     const int per = (N + THREADS - 1) / THREADS;
     const int lo = (int)threadIdx.x * per, hi = min(N, lo + per);
@@ -172,17 +202,16 @@ __device__ __forceinline__ bool attn_whole_part(int N, int heads, uint32_t index
         for (int n = lo; n < hi; ++n) {
             const int64_t x = tiles_of(n);
             if (at < before + x) {
-                part->n = n;
-                part->head = (int32_t)head;
-                part->tile = (int32_t)(at - before);
-                part->slot = -1;
-                part->splits = 1;
+                shared->n = n;
+                shared->tile = (int32_t)(at - before);
                 break;
             }
             before += x;
         }
     }
     __syncthreads();
+    part.n = shared->n;
+    part.tile = shared->tile;
     return true;
 }
 
