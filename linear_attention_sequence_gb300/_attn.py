@@ -101,19 +101,25 @@ def _heads(t, name, dev, dtype, shape):
 
 def _pages(t, name, dev, dtype, shape):
     """The bytes of a cache [P, page, H, d] with strides."""
-    if t.dtype != dtype or t.shape != shape or t.get_device() != dev:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         if t.get_device() != dev:
             raise ValueError(f"{name} must be a CUDA tensor on device {dev}")
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    s = list(t.stride())
-    if s[3] != 1:
+    p, s, h, c = t.stride()
+    P, page, H, d = shape
+    if c != 1 and d > 1:
         raise ValueError(f"{name}'s channels must be contiguous")
-    for i in (2, 1, 0):
-        if shape[i] == 1:
-            s[i] = s[i + 1] * shape[i + 1]
-    if any(x % 8 for x in s[:3]) or t.data_ptr() % 16:
+    # (the stride of a dimension of one is any)
+    if H == 1:
+        h = d
+    if page == 1:
+        s = h * H
+    if P == 1:
+        p = max(s * page, h * H)
+    at = t.data_ptr()
+    if (p | s | h) & 7 or at & 15:
         raise ValueError(f"{name} must be 16-byte aligned, in its strides too")
-    return _PAGES.pack(t.data_ptr(), *s[:3])
+    return _PAGES.pack(at, p, s, h)
 
 
 def _query(q, kv_heads, N, scale, out_dtype):

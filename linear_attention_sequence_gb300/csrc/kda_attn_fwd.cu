@@ -923,6 +923,17 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
         const uint32_t pa[4] = {pack16<BF16>(s[0][0], s[0][1]), pack16<BF16>(s[0][2], s[0][3]),
                                 pack16<BF16>(s[1][0], s[1][1]), pack16<BF16>(s[1][2], s[1][3])};
+        // what bf16 leaves of a weight is a second operand: the products have time for it here, and the
+        // result then is as good as fp32 weights would make it (fp16 leaves an eighth of that)
+        uint32_t rest[4];
+        if (BF16) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                float lo, hi;
+                unpack16<BF16>(pa[x], lo, hi);
+                rest[x] = pack16<BF16>(s[x >> 1][(x & 1) * 2] - lo, s[x >> 1][(x & 1) * 2 + 1] - hi);
+            }
+        }
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
             uint32_t b[4];
@@ -930,6 +941,10 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             ldsm4_t(b, vb + (piece >> 3) * L::kBlock + vrow * 128 + (((piece & 7) ^ (vrow & 7)) << 4));
             mma16816<BF16>(o[2 * x], pa, b[0], b[1]);
             mma16816<BF16>(o[2 * x + 1], pa, b[2], b[3]);
+            if (BF16) {
+                mma16816<BF16>(o[2 * x], rest, b[0], b[1]);
+                mma16816<BF16>(o[2 * x + 1], rest, b[2], b[3]);
+            }
         }
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(&ct.empty[st]);

@@ -239,10 +239,29 @@ __global__ void __launch_bounds__(256) kda_cache_free_kernel(const Cache C, cons
 
 // ---------------------------------------------------------------- fork
 // First a page for each child whose parent's last page is not full (one block; src and dst
-// are the pages to be copied), then the children's rows, a block each.
+// are the pages to be copied), then the children's rows: a block each in a second kernel, or, where
+// they are few entries, a warp each in the first (a launch costs the host as much as the work).
+__device__ __forceinline__ void fork_row(const Cache &C, int parent, int child, int own, int first, int step) {
+    const int len = length_of(C, child), whole = len >> C.shift;
+    const int32_t *from = C.table + (int64_t)parent * C.wide;
+    int32_t *to = C.table + (int64_t)child * C.wide;
+    for (int j = first; j < C.wide; j += step) {
+        int p = -1;
+        if (j < whole) {
+            p = from[j];
+            if (p >= 0 && p < C.P)
+                atomicAdd(C.refs + p, 1);
+            else
+                atomicOr(&g_cache_status, kCacheBadPage);
+        } else if (j == whole) {
+            p = own;
+        }
+        to[j] = p;
+    }
+}
 __global__ void __launch_bounds__(kBlock) kda_cache_fork_pages_kernel(const Cache C, int M, const int32_t *parents,
                                                                       const int32_t *children, int32_t *src, int32_t *dst,
-                                                                      int32_t *missing, int32_t *list) {
+                                                                      int32_t *missing, int32_t *list, bool rows) {
     __shared__ int sh[32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     auto partial = [&](int m, int &parent, int &child, int &len) {
@@ -284,28 +303,20 @@ __global__ void __launch_bounds__(kBlock) kda_cache_fork_pages_kernel(const Cach
         src[m] = from;
         dst[m] = to;
     }
+    if (!rows) return;
+    __syncthreads();
+    for (int m = threadIdx.x >> 5; m < M; m += kBlock / 32) {
+        parent = parents[m], child = children[m];
+        if (parent >= 0 && parent < C.N && child >= 0 && child < C.N && parent != child)
+            fork_row(C, parent, child, dst[m], threadIdx.x & 31, 32);
+    }
 }
 __global__ void __launch_bounds__(256) kda_cache_fork_rows_kernel(const Cache C, const int32_t *parents, const int32_t *children,
                                                                   const int32_t *dst) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int parent = parents[blockIdx.x], child = children[blockIdx.x];
     if (parent < 0 || parent >= C.N || child < 0 || child >= C.N || parent == child) return;
-    const int len = length_of(C, child), whole = len >> C.shift, own = dst[blockIdx.x];
-    const int32_t *from = C.table + (int64_t)parent * C.wide;
-    int32_t *to = C.table + (int64_t)child * C.wide;
-    for (int j = threadIdx.x; j < C.wide; j += 256) {
-        int p = -1;
-        if (j < whole) {
-            p = from[j];
-            if (p >= 0 && p < C.P)
-                atomicAdd(C.refs + p, 1);
-            else
-                atomicOr(&g_cache_status, kCacheBadPage);
-        } else if (j == whole) {
-            p = own;
-        }
-        to[j] = p;
-    }
+    fork_row(C, parent, child, dst[blockIdx.x], threadIdx.x, 256);
 }
 
 // ---------------------------------------------------------------- compact
@@ -486,9 +497,10 @@ cudaError_t kda_launch_cache_free(const Cache &C, int M, const int32_t *seqs, co
 
 cudaError_t kda_launch_cache_fork(const Cache &C, int M, const int32_t *parents, const int32_t *children, int32_t *src,
                                   int32_t *dst, int32_t *missing, int32_t *list, cudaStream_t stream) {
-    kda_cache_fork_pages_kernel<<<1, kBlock, 0, stream>>>(C, M, parents, children, src, dst, missing, list);
+    const bool rows = (int64_t)M * C.wide <= 8 * kBlock;
+    kda_cache_fork_pages_kernel<<<1, kBlock, 0, stream>>>(C, M, parents, children, src, dst, missing, list, rows);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || rows) return e;
     return launch_behind(kda_cache_fork_rows_kernel, (unsigned)M, 256, stream, C, parents, children, (const int32_t *)dst);
 }
 
