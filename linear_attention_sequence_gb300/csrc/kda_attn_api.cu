@@ -42,7 +42,7 @@ kda_status check_dims(const kda_attn_dims *d, Attn &A) {
     if (d->head_dim != 64 && d->head_dim != 128) return KDA_ERR_UNSUPPORTED;
     // rows (token, query head) and blocks are counted in 32 bits
     if ((int64_t)d->total_tokens * d->q_heads > INT32_MAX / 2 ||
-        (int64_t)d->num_seqs * d->kv_heads > INT32_MAX / 4)
+        (int64_t)d->num_seqs * d->q_heads > INT32_MAX / 4)
         return KDA_ERR_UNSUPPORTED;
     A = Attn{};
     A.N = d->num_seqs;

@@ -277,3 +277,15 @@ def test_binding_refuses():
         kda.kda_cache_append(x, x, torch.zeros(3, 8, 2, 64, dtype=torch.bfloat16), x, i[:, None], i)
     with pytest.raises(ValueError, match="CUDA"):
         kda.kda_cache_copy(torch.zeros(3, 8, 2, 64, dtype=torch.bfloat16), x, i, i)
+
+
+def test_more_blocks_than_a_grid_holds(L):
+    """Every sequence has a block a query head at the least in the gradients: 2^20 of them with
+    4096 heads are more than 2^31 blocks, and a number that wraps would be a grid of few."""
+    d = dims(num_seqs=1 << 20, total_tokens=16, q_heads=4096, kv_heads=1)
+    q, k = heads(1, 4096), heads(2, 1)
+    cu = at(14)
+    assert L.kda_attn_backward_workspace(R(d)) == -1
+    assert backward(L, d, q=q, k=k, v=heads(3, 1), o=heads(4, 4096), y=heads(6, 4096), cu=cu) == UNSUPPORTED
+    assert prefill(L, d, q=q, k=k, v=heads(3, 1), cu=cu) == UNSUPPORTED
+    assert paged(L, d, q=q, k=pages(2, 1), v=pages(3, 1), cu=cu) == UNSUPPORTED
