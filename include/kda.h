@@ -693,7 +693,8 @@ kda_status kda_attn_prefill(const kda_attn_dims *dims, const kda_heads *q, const
  *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij d_out_i
  *
  * (the sums of dk and dv over the query heads of the group too).  P and dS are rounded to the
- * 16-bit type for the products, sums are fp32, and none depends on timing.  An infinity or a
+ * 16-bit type for the products (in sequences of up to 128 tokens what that leaves is a second
+ * operand: twice the bits), sums are fp32, and none depends on timing.  An infinity or a
  * NaN in a sequence may reach gradients of that sequence up to 127 tokens to either side of
  * where the formulas have it, and no other sequence's.
  *

@@ -20,7 +20,9 @@
 //
 // In both, two threads a row: warps 0-3 have the first 64 columns of a score tile and warps 4-7
 // the others.  P and dS are rounded to the inputs' 16-bit type because the tensor cores read
-// them so; all sums are fp32.
+// them so; all sums are fp32.  A sequence of one tile (128 tokens) has few rows over which
+// that rounding averages out, and time to spare: what it leaves follows as a second operand, in the
+// columns of tensor memory that the 16-bit values leave free.
 #include <stddef.h>
 
 #include "kda_attn_plan.cuh"
@@ -141,6 +143,20 @@ __device__ __forceinline__ void store64(uint32_t at, const float (&x)[64]) {
     sm100::tc_fence_before();
 }
 
+// What that rounding leaves, into the 32 columns behind (store64 follows and waits).
+template <bool BF16>
+__device__ __forceinline__ void store64_rest(uint32_t at, const float (&x)[64]) {
+    uint32_t p[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        float a, b;
+        unpack16<BF16>(pack16<BF16>(x[2 * i], x[2 * i + 1]), a, b);
+        p[i] = pack16<BF16>(x[2 * i] - a, x[2 * i + 1] - b);
+    }
+    tmem_st16_raw(at + 32, p);
+    tmem_st16_raw(at + 48, p + 16);
+}
+
 // A result row: COLS channels of tensor memory, scaled, to `at` elements into `to`.
 template <int COLS, bool BF16>
 __device__ __forceinline__ void write_row(void *to, bool f32, int64_t at, uint32_t tmem, float scale, bool live) {
@@ -168,6 +184,7 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
     const int len = (int)(sq.b - sq.a), tiles = (len + kTile - 1) / kTile;
     const int per = tiles - kt, n = per * G;   // step j: head j / per of the group, query tile kt + j % per
     const int tail = len - (tiles - 1) * kTile;   // rows of the last tile
+    const bool rest = tiles == 1;                 // (see the top)
     constexpr uint32_t S = 0, DP = 128, DV = 256, DK = 256 + D;
     bool ok = true;
     auto wait = [&](uint64_t *bar, int phase) { return attn_wait(bar, phase & 1, &g_attn_bwd_status); };
@@ -255,6 +272,7 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
             if (!ok) break;
             sm100::tc_fence_after();
             mma_sum<D, BF16>(tmem + DV, tmem + S, b_at + (j % NB) * L::kBytes, j > 0);
+            if (rest) mma_sum<D, BF16>(tmem + DV, tmem + S + 32, b_at + (j % NB) * L::kBytes, true);
             sm100::mma_commit_el(&ct.b_empty[j % NB]);
             if (j + 1 < n) {
                 ok = arrived_a(j + 1);
@@ -265,6 +283,7 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
             if (!ok) break;
             sm100::tc_fence_after();
             mma_sum<D, BF16>(tmem + DK, tmem + DP, a_at + (j % NA) * L::kBytes, j > 0);
+            if (rest) mma_sum<D, BF16>(tmem + DK, tmem + DP + 32, a_at + (j % NA) * L::kBytes, true);
             sm100::mma_commit_el(&ct.a_empty[j % NA]);
             if (j + 1 < n) {
                 ok = arrived_b(j + 1);
@@ -302,6 +321,7 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
 #pragma unroll
                 for (int x = 0; x < 64; ++x) p[x] = x >= lo && x < hi ? p[x] : 0.f;
             }
+            if (rest) store64_rest<BF16>(lanes + S + half * 64, p);
             store64<BF16>(lanes + S + half * 64, p);
             sm100::mbar_arrive(&ct.p_ready);
             ok = wait(&ct.dp_full, j);
@@ -324,6 +344,7 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
             }
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(&ct.stat_empty[st]);
+            if (rest) store64_rest<BF16>(lanes + DP + half * 64, dp);
             store64<BF16>(lanes + DP + half * 64, dp);
             sm100::mbar_arrive(&ct.ds_ready[0]);
         }
@@ -351,6 +372,7 @@ __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const 
     const int qt = part.tile, h = part.head, hk = h / A.G;
     const int len = (int)(sq.b - sq.a), n = qt + 1;
     const int tail = len - qt * kTile;   // rows of the last key tile (the diagonal one), if below 128
+    const bool rest = len <= kTile;      // (see the top)
     constexpr uint32_t S[2] = {0, 128}, DP = 256, DQ = 384;
     bool ok = true;
     auto wait = [&](uint64_t *bar, int phase) { return attn_wait(bar, phase & 1, &g_attn_bwd_status); };
@@ -416,6 +438,7 @@ __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const 
             if (!ok) break;
             sm100::tc_fence_after();
             mma_sum<D, BF16>(tmem + DQ, tmem + S[j & 1], a_at + (j % NA) * L::kBytes, j > 0);
+            if (rest) mma_sum<D, BF16>(tmem + DQ, tmem + S[j & 1] + 32, a_at + (j % NA) * L::kBytes, true);
             sm100::mma_commit_el(&ct.a_empty[j % NA]);
         }
         sm100::mma_commit_el(&ct.done);
@@ -456,6 +479,7 @@ __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const 
 #pragma unroll
                 for (int x = 0; x < 64; ++x) dp[x] = x + half * 64 <= r ? dp[x] : 0.f;
             }
+            if (rest) store64_rest<BF16>(lanes + S[j & 1] + half * 64, dp);
             store64<BF16>(lanes + S[j & 1] + half * 64, dp);
             sm100::mbar_arrive(&ct.ds_ready[j & 1]);
         }

@@ -500,3 +500,31 @@ def test_serving(dtype, d, page, order):
                 kda.kda_cache_copy(kp[y], vp[y], src, dst)
             assert bool((refs[:int((refs > 0).sum())] > 0).all())
         assert lens.tolist() == [x[0][0].shape[0] for x in past]
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F16, 64), (F16, 128), (BF16, 64)])
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (8, 2), (12, 1)])
+@pytest.mark.parametrize("lens", [[1], [2], [3, 0, 5], [128], [127, 2, 64]])
+def test_gradients_of_short_sequences(lens, H, Hkv, d, dtype):
+    """Sequences of one tile keep what the rounding of P and dS to 16 bits leaves as a second operand: the
+    rest is at most u16 of the value and is itself off by u16 of that, so that u16^2 stands in the
+    bound for u16 (the 2^-25 of small fp16 values holds for the rest as for the value).  The sums have
+    twice as many products: (2 T H / 16 + 64) u32 of the magnitudes, the half of it counted already."""
+    T = sum(lens)
+    q, k, v = prompt_inputs(T, H, Hkv, d, dtype, 150 + T)
+    dy = rnd(160 + T, dtype, T, H, d)
+    out, lse = kda.kda_attn_prefill(q, k, v, cu_of(lens), return_lse=True)
+    got = kda.kda_attn_backward(q, k, v, out, lse, dy, cu_of(lens), grad_dtype=F32)
+    at = starts(lens)
+    for a, b in zip(at[:-1], at[1:]):
+        if a == b:
+            continue
+        x = [t[a:b] for t in (q, k, v, out, lse, dy)]
+        want, mag, err, most = ref_backward(*x, d ** -0.5)
+        tol = backward_bounds(want, mag, err, most, x[0], x[1], x[4], x[5], d ** -0.5, F32)
+        for n in want:
+            sums = (b - a) * (H if n != "dq" else 1) / 16 * U[F32]
+            bound = tol[n] - (U[dtype] - U[dtype] ** 2 - sums) * mag[n]
+            off = (got[n][a:b].double() - want[n]).abs()
+            assert bool((off <= bound).all()), f"{n} of {b - a} tokens: off by {float((off / bound).max())} bounds"
+    assert kda.kda_get_last_device_error() == 0
