@@ -740,6 +740,19 @@ kda_status kda_attn_paged(const kda_attn_dims *dims, const kda_cache_dims *cache
                           const int32_t *cu_seqlens, void *out, float *lse, void *workspace,
                           int64_t workspace_bytes, kda_stream_t stream);
 
+/*
+ * kda_attn_paged_granted -- the same behind a reservation that may have refused sequences.
+ *
+ *   granted    device int32 [N] or NULL, as kda_cache_reserve_granted wrote it: the tokens of a
+ *              sequence that was granted fewer than it has in this call see nothing (out 0, lse -inf).
+ */
+kda_status kda_attn_paged_granted(const kda_attn_dims *dims, const kda_cache_dims *cache,
+                                  const kda_heads *q, const kda_pages *k_pages,
+                                  const kda_pages *v_pages, const int32_t *page_table,
+                                  const int32_t *kv_lens, const int32_t *cu_seqlens,
+                                  const int32_t *granted, void *out, float *lse, void *workspace,
+                                  int64_t workspace_bytes, kda_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * The pages of a cache
  * ---------------------------------------------------------------------------
@@ -755,7 +768,10 @@ kda_status kda_attn_paged(const kda_attn_dims *dims, const kda_cache_dims *cache
  * given out lowest number first, to the sequences (or children) in their order.  A last
  * page that is not full and grows belongs to one sequence only (kda_cache_fork copies it, and
  * kda_cache_reserve one that a sequence was shortened into), so that kda_cache_append never
- * writes into a shared page.  A sequence or page number out of range
+ * writes into a shared page where every sequence got its pages.  Where a reservation may refuse one,
+ * take kda_cache_reserve_granted and hand what it granted to kda_cache_append_granted and
+ * kda_attn_paged_granted: the length of a refused sequence does not count its new tokens, and
+ * without that word they would be written over the last ones that it has.  A sequence or page number out of range
  * is passed by and recorded in the device status word (kda_get_last_device_error then
  * returns KDA_ERR_INVALID_ARGUMENT).  Conventions as in the softmax attention calls.
  */
@@ -777,13 +793,25 @@ int64_t kda_cache_workspace(const kda_cache_dims *cache);
  *              (kda_cache_copy) before anything else takes pages; -1 where there is nothing to
  *              copy.  Without the lists such a sequence keeps its old length, and the device
  *              status word records it.
- *   missing    int32 [1] or NULL: pages that were lacking (0: all were served; short rows
- *              are not counted).
+ *   missing    int32 [1] or NULL: pages that were lacking (short rows are not counted).
+ *
+ * kda_cache_reserve_granted also says who was served:
+ *
+ *   granted    int32 [N] or NULL: the new tokens of each sequence that have a place: new_lens[n]
+ *              (0 for what is below 0), or 0 where the sequence kept its old length.
+ *
+ * Without both missing and granted a refusal is recorded in the device status word
+ * (KDA_ERR_INVALID_ARGUMENT).
  */
 kda_status kda_cache_reserve(const kda_cache_dims *cache, int32_t num_seqs, int32_t *page_refs,
                              int32_t *page_table, int32_t *kv_lens, const int32_t *new_lens,
                              int32_t *src, int32_t *dst, int32_t *missing, void *workspace,
                              int64_t workspace_bytes, kda_stream_t stream);
+kda_status kda_cache_reserve_granted(const kda_cache_dims *cache, int32_t num_seqs,
+                                     int32_t *page_refs, int32_t *page_table, int32_t *kv_lens,
+                                     const int32_t *new_lens, int32_t *src, int32_t *dst,
+                                     int32_t *missing, int32_t *granted, void *workspace,
+                                     int64_t workspace_bytes, kda_stream_t stream);
 
 /*
  * kda_cache_append -- writes the new tokens' keys and values into one layer's pages: of the
@@ -794,12 +822,20 @@ kda_status kda_cache_reserve(const kda_cache_dims *cache, int32_t num_seqs, int3
  *              head_dim a multiple of 8.
  *   k_pages, v_pages  [P, page_size, H_kv, d], each element of its own.
  *   cu_seqlens int32 [N+1] of the new tokens, or NULL (T / N each).
+ *   granted    (kda_cache_append_granted) int32 [N] or NULL, as kda_cache_reserve_granted wrote it:
+ *              a sequence that was granted fewer than it has new tokens here is passed by.
  */
 kda_status kda_cache_append(const kda_cache_dims *cache, int32_t num_seqs, int32_t total_tokens,
                             int32_t kv_heads, int32_t head_dim, const kda_heads *k,
                             const kda_heads *v, const kda_pages *k_pages, const kda_pages *v_pages,
                             const int32_t *page_table, const int32_t *kv_lens,
                             const int32_t *cu_seqlens, kda_stream_t stream);
+kda_status kda_cache_append_granted(const kda_cache_dims *cache, int32_t num_seqs,
+                                    int32_t total_tokens, int32_t kv_heads, int32_t head_dim,
+                                    const kda_heads *k, const kda_heads *v, const kda_pages *k_pages,
+                                    const kda_pages *v_pages, const int32_t *page_table,
+                                    const int32_t *kv_lens, const int32_t *cu_seqlens,
+                                    const int32_t *granted, kda_stream_t stream);
 
 /*
  * kda_cache_free -- gives pages back: of each of `count` sequences (seqs, int32) the first

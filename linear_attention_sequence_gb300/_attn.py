@@ -70,7 +70,8 @@ def declare(L):
     """Argument types of the C entry points (structures go in as bytes)."""
     for name, args in (("kda_attn_prefill", [_vp] * 8),
                        ("kda_attn_backward", [_vp] * 12 + [_i64, _vp]),
-                       ("kda_attn_paged", [_vp] * 11 + [_i64, _vp])):
+                       ("kda_attn_paged", [_vp] * 11 + [_i64, _vp]),
+                       ("kda_attn_paged_granted", [_vp] * 12 + [_i64, _vp])):
         getattr(L, name).argtypes = args
         getattr(L, name).restype = ctypes.c_int
     L.kda_attn_paged_workspace.argtypes = [_vp] * 3
@@ -200,7 +201,7 @@ def kda_attn_backward(q, k, v, out, lse, d_out, cu_seqlens=None, *, num_seqs=Non
     return dict(dq=dq, dk=dk, dv=dv)
 
 
-def kda_attn_paged(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *, scale=None, out=None,
+def kda_attn_paged(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *, granted=None, scale=None, out=None,
                    out_dtype=None, lse=None, return_lse=False, stream=None):
     """Attention of each sequence's new tokens over its pages of a cache, which holds their
     keys and values already (C entry point ``kda_attn_paged``).
@@ -210,7 +211,8 @@ def kda_attn_paged(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *,
     from 8 to 1024; page_table int32 [N, max_pages]; kv_lens int32 [N], the tokens in the
     cache with the new ones; cu_seqlens int32 [N+1] of the new tokens, or None: T / N each
     (T == N is the decode step).  Returns ``out`` [T, H, d], and with ``return_lse`` (or
-    a buffer given) ``(out, lse)``.  A token that sees no key has out 0 and lse -inf."""
+    a buffer given) ``(out, lse)``.  A token that sees no key has out 0 and lse -inf; so has, with
+    granted (int32 [N], what kda_cache_reserve granted), every token of a sequence that was refused."""
     if k_pages.dim() != 4 or page_table.dim() != 2:
         raise ValueError("k_pages must be [P, page_size, H, d] and page_table [N, max_pages]")
     odt = out_dtype or q.dtype
@@ -227,6 +229,7 @@ def kda_attn_paged(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *,
     table = _is(page_table, "page_table", dev, _I32, (N, wide))
     lens = _is(kv_lens, "kv_lens", dev, _I32, (N,))
     cu = 0 if cu_seqlens is None else cu_seqlens.data_ptr()
+    got = _is(granted, "granted", dev, _I32, (N,))
     o, s = _is(out, "out", dev, odt, (T, H, d)), _is(lse, "lse", dev, _F32, (T, H))
     with _place(dev, stream):
         if out is None:
@@ -237,5 +240,5 @@ def kda_attn_paged(q, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *,
             s = lse.data_ptr()
         # (of cu_seqlens it matters only whether there are any; any address stands for them)
         ws, n = _workspace("kda_attn_paged_workspace", dims, q.device, cache, 16 if cu else 0)
-        _run("kda_attn_paged", dev, dims, cache, rq, rk, rv, table, lens, cu, o, s, ws.data_ptr(), n)
+        _run("kda_attn_paged_granted", dev, dims, cache, rq, rk, rv, table, lens, cu, got, o, s, ws.data_ptr(), n)
     return out if lse is None else (out, lse)

@@ -22,7 +22,9 @@ _I32 = torch.int32
 def declare(L):
     """Argument types of the C entry points (structures go in as bytes)."""
     for name, args in (("kda_cache_reserve", [_vp, _i32] + [_vp] * 8 + [_i64, _vp]),
+                       ("kda_cache_reserve_granted", [_vp, _i32] + [_vp] * 9 + [_i64, _vp]),
                        ("kda_cache_append", [_vp] + [_i32] * 4 + [_vp] * 8),
+                       ("kda_cache_append_granted", [_vp] + [_i32] * 4 + [_vp] * 9),
                        ("kda_cache_free", [_vp, _i32] + [_vp] * 3 + [_i32] + [_vp] * 3),
                        ("kda_cache_fork", [_vp, _i32] + [_vp] * 3 + [_i32] + [_vp] * 6 + [_i64, _vp]),
                        ("kda_cache_compact", [_vp, _i32] + [_vp] * 8 + [_i64, _vp]),
@@ -70,7 +72,7 @@ def _layer(k_pages, v_pages):
 
 
 def kda_cache_reserve(page_refs, page_table, kv_lens, new_lens, page_size, *, src=None, dst=None,
-                      return_copies=False, missing=None, stream=None):
+                      return_copies=False, missing=None, granted=None, return_granted=False, stream=None):
     """Pages for ``new_lens`` (int32 [N]) more tokens of each sequence, in place (C entry point
     ``kda_cache_reserve``): kv_lens grows and the table gets the lowest free pages, for the
     sequences in their order; one that cannot have all of its pages keeps its length.
@@ -80,7 +82,13 @@ def kda_cache_reserve(page_refs, page_table, kv_lens, new_lens, page_size, *, sr
     after kda_cache_fork) gets a page of its own when it grows again: with ``return_copies``
     (or buffers given) returns ``(src, dst)``, int32 [N], the pages to copy with kda_cache_copy in
     every layer (-1: none); without, such a sequence keeps its length and the device status
-    says so."""
+    says so.
+
+    Where pages or rows may run out: with ``return_granted`` (or a buffer given) also returns
+    ``granted``, int32 [N], the new tokens of each sequence that have a place (0 for one that keeps
+    its length).  Hand it to kda_cache_append and kda_attn_paged, or the tokens of a refused sequence are
+    written over the last ones that it has.  Without ``missing`` and ``granted`` the device status
+    tells of a refusal."""
     dev, N, cache, refs, table, lens = _state(page_refs, page_table, kv_lens, page_size)
     new = _int(new_lens, "new_lens", dev, (N,))
     lacking = _int(missing, "missing", dev, (1,))
@@ -89,17 +97,22 @@ def kda_cache_reserve(page_refs, page_table, kv_lens, new_lens, page_size, *, sr
             src = torch.empty((N,), dtype=_I32, device=page_refs.device)
         if return_copies and dst is None:
             dst = torch.empty((N,), dtype=_I32, device=page_refs.device)
+        if return_granted and granted is None:
+            granted = torch.empty((N,), dtype=_I32, device=page_refs.device)
         ws, n = _scratch(cache, page_refs.device)
-        _run("kda_cache_reserve", dev, cache, N, refs, table, lens, new, _int(src, "src", dev, (N,)),
-             _int(dst, "dst", dev, (N,)), lacking, ws.data_ptr(), n)
-    return None if src is None else (src, dst)
+        _run("kda_cache_reserve_granted", dev, cache, N, refs, table, lens, new, _int(src, "src", dev, (N,)),
+             _int(dst, "dst", dev, (N,)), lacking, _int(granted, "granted", dev, (N,)), ws.data_ptr(), n)
+    if granted is None:
+        return None if src is None else (src, dst)
+    return granted if src is None else (src, dst, granted)
 
 
-def kda_cache_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *, stream=None):
+def kda_cache_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens=None, *, granted=None, stream=None):
     """Writes the new tokens' k and v [T, H, d] into one layer's pages [P, page_size, H, d] (C
     entry point ``kda_cache_append``): of the n new tokens of a sequence, token i goes to place
     kv_lens - n + i, so that kda_cache_reserve comes first.  cu_seqlens int32 [N+1] of the new
-    tokens, or None: T / N each."""
+    tokens, or None: T / N each.  granted int32 [N] is what kda_cache_reserve granted: sequences that
+    were refused are passed by; without it every sequence must have been served."""
     dev, P, page, H, d, kp, vp = _layer(k_pages, v_pages)
     if page_table.dim() != 2 or k.dim() != 3:
         raise ValueError("page_table must be [N, max_pages] and k [T, H, d]")
@@ -111,8 +124,8 @@ def kda_cache_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens=Non
     table = _int(page_table, "page_table", dev, (N, wide))
     lens = _int(kv_lens, "kv_lens", dev, (N,))
     with _place(dev, stream):
-        _run("kda_cache_append", dev, _CACHE.pack(P, page, wide), N, T, H, d, rk, rv, kp, vp, table, lens,
-             0 if cu_seqlens is None else cu_seqlens.data_ptr())
+        _run("kda_cache_append_granted", dev, _CACHE.pack(P, page, wide), N, T, H, d, rk, rv, kp, vp, table, lens,
+             0 if cu_seqlens is None else cu_seqlens.data_ptr(), _int(granted, "granted", dev, (N,)))
 
 
 def kda_cache_free(page_refs, page_table, kv_lens, seqs, page_size, *, keep=None, stream=None):

@@ -194,13 +194,21 @@ kda_status kda_attn_paged(const kda_attn_dims *dims, const kda_cache_dims *cache
                           const kda_pages *k_pages, const kda_pages *v_pages, const int32_t *page_table,
                           const int32_t *kv_lens, const int32_t *cu_seqlens, void *out, float *lse, void *workspace,
                           int64_t workspace_bytes, kda_stream_t stream) {
+    return kda_attn_paged_granted(dims, cache, q, k_pages, v_pages, page_table, kv_lens, cu_seqlens, nullptr, out, lse, workspace,
+                                  workspace_bytes, stream);
+}
+
+kda_status kda_attn_paged_granted(const kda_attn_dims *dims, const kda_cache_dims *cache, const kda_heads *q,
+                                  const kda_pages *k_pages, const kda_pages *v_pages, const int32_t *page_table,
+                                  const int32_t *kv_lens, const int32_t *cu_seqlens, const int32_t *granted, void *out,
+                                  float *lse, void *workspace, int64_t workspace_bytes, kda_stream_t stream) {
     Attn A;
     kda_status st = check_paged(dims, cache, cu_seqlens, A);
     if (st != KDA_OK) return st;
     if (A.T == 0 || A.N == 0) return KDA_OK;
     if (bad_heads(q, A.T, A.Hq, A.d) || bad_pages(k_pages, A.P, A.page, A.Hkv, A.d) ||
         bad_pages(v_pages, A.P, A.page, A.Hkv, A.d) || !page_table || misaligned(page_table, 4) || !kv_lens ||
-        misaligned(kv_lens, 4) || !out || misaligned(out, 16) || misaligned(lse, 4))
+        misaligned(kv_lens, 4) || misaligned(granted, 4) || !out || misaligned(out, 16) || misaligned(lse, 4))
         return KDA_ERR_INVALID_ARGUMENT;
     const int64_t need = kda_attn_paged_ws(A);
     if (workspace_bytes < need || (need > 0 && !workspace) || misaligned(workspace, 16)) return KDA_ERR_INVALID_ARGUMENT;
@@ -208,13 +216,14 @@ kda_status kda_attn_paged(const kda_attn_dims *dims, const kda_cache_dims *cache
     if (conflict({{out, rows * A.d * osize(A)}, {lse, rows * 4}, {workspace, (size_t)need}},
                  {span_of(q, A.T, A.Hq, A.d), span_of(k_pages, A.P, A.page, A.Hkv, A.d),
                   span_of(v_pages, A.P, A.page, A.Hkv, A.d), {page_table, (size_t)A.N * A.wide * 4},
-                  {kv_lens, (size_t)A.N * 4}, {cu_seqlens, cu_bytes(A)}}))
+                  {kv_lens, (size_t)A.N * 4}, {cu_seqlens, cu_bytes(A)}, {granted, (size_t)A.N * 4}}))
         return KDA_ERR_INVALID_ARGUMENT;
     A.q = q->data, A.q_t = q->token_stride, A.q_h = q->head_stride;
     A.k = k_pages->data, A.k_p = k_pages->page_stride, A.k_t = k_pages->token_stride, A.k_h = k_pages->head_stride;
     A.v = v_pages->data, A.v_p = v_pages->page_stride, A.v_t = v_pages->token_stride, A.v_h = v_pages->head_stride;
     A.table = page_table;
     A.lens = kv_lens;
+    A.granted = granted;
     A.out = out;
     A.lse = lse;
     cudaError_t e = kda_launch_attn_paged(A, workspace, (cudaStream_t)stream);

@@ -29,6 +29,7 @@ struct Attn {
     // the cache (kda_attn_paged)
     const int32_t *table;     // [N, wide]
     const int32_t *lens;      // [N]: tokens in the cache, the new ones among them
+    const int32_t *granted;   // [N] or nullptr: new tokens that got a place (all of a sequence's, or its tokens see nothing)
     int32_t P, page, wide;
     int64_t k_p, v_p;         // strides of a page
     // results
@@ -55,6 +56,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const Attn &A, int n) {
     if (PAGED) {
         const int64_t most = (int64_t)A.wide * A.page, len = A.lens[n];
         s.keys = len < 0 ? 0 : len > most ? most : len;
+        if (A.granted && A.granted[n] < s.b - s.a) s.keys = 0;
     }
     return s;
 }

@@ -93,7 +93,7 @@ __device__ int free_pages(const int32_t *refs, int P, int want, int32_t *list, i
 // A last page that is not full and that others share (a sequence was shortened into it) is replaced
 // by one of the sequence's own.  Which sequences that is, is settled before any count changes (src).
 __global__ void __launch_bounds__(kBlock) kda_cache_reserve_kernel(const Cache C, const int32_t *new_lens, int32_t *src,
-                                                                   int32_t *dst, int32_t *missing, int32_t *list) {
+                                                                   int32_t *dst, int32_t *missing, int32_t *granted, int32_t *list) {
     __shared__ int sh[32];
     auto shared_page = [&](int n, int len, int add) {
         if (add == 0 || (len & ((1 << C.shift) - 1)) == 0) return -1;
@@ -140,6 +140,11 @@ __global__ void __launch_bounds__(kBlock) kda_cache_reserve_kernel(const Cache C
             src[n] = copies ? old : -1;
             dst[n] = copies ? list[at] : -1;
         }
+        // a refusal is told to whoever appends next, or recorded
+        if (granted)
+            granted[n] = served ? add : 0;
+        else if (!served && !missing)
+            atomicOr(&g_cache_status, kCacheBadPage);
         if (!served) continue;
         int32_t *row = C.table + (int64_t)n * C.wide + have - copies;
         if (copies) atomicSub(C.refs + old, 1);
@@ -157,7 +162,8 @@ __global__ void __launch_bounds__(kBlock) kda_cache_reserve_kernel(const Cache C
 // first finds where each goes.
 constexpr int kAppendTokens = 8;
 __global__ void __launch_bounds__(256) kda_cache_append_kernel(const Cache C, const Heads k, const Heads v, const Pages kp,
-                                                               const Pages vp, const int32_t *cu, int64_t T, int64_t seq_len) {
+                                                               const Pages vp, const int32_t *cu, int64_t T, int64_t seq_len,
+                                                               const int32_t *granted) {
     __shared__ int64_t to_k[kAppendTokens], to_v[kAppendTokens];
     const int64_t first = (int64_t)blockIdx.x * kAppendTokens;
     if (threadIdx.x < kAppendTokens) {
@@ -180,7 +186,8 @@ __global__ void __launch_bounds__(256) kda_cache_append_kernel(const Cache C, co
                 if (t >= a && t < b) n = lo;
             }
         }
-        if (n >= 0) {
+        // (refused: kv_lens does not count these tokens, and the places in front of it hold others)
+        if (n >= 0 && !(granted && granted[n] < b - a)) {
             const int len = C.lens[n];
             const int64_t at = (int64_t)len - (b - a) + (t - a);
             if (len > (int64_t)C.wide << C.shift) {
@@ -478,15 +485,16 @@ cudaError_t launch_behind(void (*kernel)(Params...), unsigned blocks, int thread
 }  // namespace
 
 cudaError_t kda_launch_cache_reserve(const Cache &C, const int32_t *new_lens, int32_t *src, int32_t *dst, int32_t *missing,
-                                     int32_t *list, cudaStream_t stream) {
-    kda_cache_reserve_kernel<<<1, kBlock, 0, stream>>>(C, new_lens, src, dst, missing, list);
+                                     int32_t *granted, int32_t *list, cudaStream_t stream) {
+    kda_cache_reserve_kernel<<<1, kBlock, 0, stream>>>(C, new_lens, src, dst, missing, granted, list);
     return cudaGetLastError();
 }
 
 cudaError_t kda_launch_cache_append(const Cache &C, const Heads &k, const Heads &v, const Pages &kp, const Pages &vp,
-                                    const int32_t *cu, int64_t T, int64_t seq_len, cudaStream_t stream) {
+                                    const int32_t *cu, int64_t T, int64_t seq_len, const int32_t *granted,
+                                    cudaStream_t stream) {
     kda_cache_append_kernel<<<(unsigned)((T + kAppendTokens - 1) / kAppendTokens), 256, 0, stream>>>(C, k, v, kp, vp, cu, T,
-                                                                                                    seq_len);
+                                                                                                    seq_len, granted);
     return cudaGetLastError();
 }
 

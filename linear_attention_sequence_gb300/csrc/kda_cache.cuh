@@ -25,9 +25,10 @@ struct Pages {
 }  // namespace kda
 
 cudaError_t kda_launch_cache_reserve(const kda::Cache &C, const int32_t *new_lens, int32_t *src, int32_t *dst, int32_t *missing,
-                                     int32_t *list, cudaStream_t stream);
+                                     int32_t *granted, int32_t *list, cudaStream_t stream);
 cudaError_t kda_launch_cache_append(const kda::Cache &C, const kda::Heads &k, const kda::Heads &v, const kda::Pages &kp,
-                                    const kda::Pages &vp, const int32_t *cu, int64_t T, int64_t seq_len, cudaStream_t stream);
+                                    const kda::Pages &vp, const int32_t *cu, int64_t T, int64_t seq_len, const int32_t *granted,
+                                    cudaStream_t stream);
 cudaError_t kda_launch_cache_free(const kda::Cache &C, int M, const int32_t *seqs, const int32_t *keep, cudaStream_t stream);
 cudaError_t kda_launch_cache_fork(const kda::Cache &C, int M, const int32_t *parents, const int32_t *children, int32_t *src,
                                   int32_t *dst, int32_t *missing, int32_t *list, cudaStream_t stream);

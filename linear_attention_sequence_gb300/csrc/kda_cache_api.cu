@@ -97,20 +97,27 @@ int64_t kda_cache_workspace(const kda_cache_dims *cache) {
 kda_status kda_cache_reserve(const kda_cache_dims *cache, int32_t num_seqs, int32_t *page_refs, int32_t *page_table,
                              int32_t *kv_lens, const int32_t *new_lens, int32_t *src, int32_t *dst, int32_t *missing,
                              void *workspace, int64_t workspace_bytes, kda_stream_t stream) {
+    return kda_cache_reserve_granted(cache, num_seqs, page_refs, page_table, kv_lens, new_lens, src, dst, missing, nullptr,
+                                     workspace, workspace_bytes, stream);
+}
+
+kda_status kda_cache_reserve_granted(const kda_cache_dims *cache, int32_t num_seqs, int32_t *page_refs, int32_t *page_table,
+                                     int32_t *kv_lens, const int32_t *new_lens, int32_t *src, int32_t *dst, int32_t *missing,
+                                     int32_t *granted, void *workspace, int64_t workspace_bytes, kda_stream_t stream) {
     Cache C;
     const kda_status st = check_cache(cache, num_seqs, page_refs, page_table, kv_lens, C);
     if (st != KDA_OK) return st;
     const int64_t need = (int64_t)C.P * 4 + 16;
     if (bad(page_refs) || (C.N > 0 && (bad(page_table) || bad(kv_lens) || bad(new_lens))) || misaligned(missing, 4) ||
-        (src == nullptr) != (dst == nullptr) || misaligned(src, 4) || misaligned(dst, 4) || !workspace ||
+        (src == nullptr) != (dst == nullptr) || misaligned(src, 4) || misaligned(dst, 4) || misaligned(granted, 4) || !workspace ||
         workspace_bytes < need || misaligned(workspace, 16))
         return KDA_ERR_INVALID_ARGUMENT;
     if (conflict({refs_of(C), table_of(C), lens_of(C), {src, (size_t)C.N * 4}, {dst, (size_t)C.N * 4}, {missing, 4},
-                  {workspace, (size_t)need}},
+                  {granted, (size_t)C.N * 4}, {workspace, (size_t)need}},
                  {{new_lens, (size_t)C.N * 4}}))
         return KDA_ERR_INVALID_ARGUMENT;
     if (C.N == 0 && !missing) return KDA_OK;
-    return done(kda_launch_cache_reserve(C, new_lens, src, dst, missing, (int32_t *)workspace, (cudaStream_t)stream),
+    return done(kda_launch_cache_reserve(C, new_lens, src, dst, missing, granted, (int32_t *)workspace, (cudaStream_t)stream),
                 "kda_cache_reserve");
 }
 
@@ -118,25 +125,33 @@ kda_status kda_cache_append(const kda_cache_dims *cache, int32_t num_seqs, int32
                             int32_t head_dim, const kda_heads *k, const kda_heads *v, const kda_pages *k_pages,
                             const kda_pages *v_pages, const int32_t *page_table, const int32_t *kv_lens,
                             const int32_t *cu_seqlens, kda_stream_t stream) {
+    return kda_cache_append_granted(cache, num_seqs, total_tokens, kv_heads, head_dim, k, v, k_pages, v_pages, page_table,
+                                    kv_lens, cu_seqlens, nullptr, stream);
+}
+
+kda_status kda_cache_append_granted(const kda_cache_dims *cache, int32_t num_seqs, int32_t total_tokens, int32_t kv_heads,
+                                    int32_t head_dim, const kda_heads *k, const kda_heads *v, const kda_pages *k_pages,
+                                    const kda_pages *v_pages, const int32_t *page_table, const int32_t *kv_lens,
+                                    const int32_t *cu_seqlens, const int32_t *granted, kda_stream_t stream) {
     Cache C;
     kda_status st = check_cache(cache, num_seqs, nullptr, const_cast<int32_t *>(page_table), const_cast<int32_t *>(kv_lens), C);
     if (st == KDA_OK) st = check_heads_dims(kv_heads, head_dim, C);
     if (st != KDA_OK) return st;
     const int64_t T = total_tokens;
-    if (T < 0 || misaligned(cu_seqlens, 4)) return KDA_ERR_INVALID_ARGUMENT;
+    if (T < 0 || misaligned(cu_seqlens, 4) || misaligned(granted, 4)) return KDA_ERR_INVALID_ARGUMENT;
     if (!cu_seqlens && (C.N == 0 ? T != 0 : T % C.N != 0)) return KDA_ERR_INVALID_ARGUMENT;
     if (T == 0 || C.N == 0) return KDA_OK;
     if (bad_rows(k, T, C) || bad_rows(v, T, C) || bad_pages(k_pages, C) || bad_pages(v_pages, C) || bad(page_table) ||
         bad(kv_lens))
         return KDA_ERR_INVALID_ARGUMENT;
     // (the two caches may be parts of one tensor: their spans may interleave)
-    const Span reads[5] = {span_of(k, T, C), span_of(v, T, C), table_of(C), lens_of(C),
-                           {cu_seqlens, cu_seqlens ? (size_t)(C.N + 1) * 4 : 0}};
+    const Span reads[6] = {span_of(k, T, C), span_of(v, T, C), table_of(C), lens_of(C),
+                           {cu_seqlens, cu_seqlens ? (size_t)(C.N + 1) * 4 : 0}, {granted, (size_t)C.N * 4}};
     for (const Span &r : reads)
         if (conflict({span_of(k_pages, C)}, {r}) || conflict({span_of(v_pages, C)}, {r})) return KDA_ERR_INVALID_ARGUMENT;
     if (k_pages->data == v_pages->data) return KDA_ERR_INVALID_ARGUMENT;
     return done(kda_launch_cache_append(C, heads_at(k), heads_at(v), pages_at(k_pages), pages_at(v_pages), cu_seqlens, T,
-                                        cu_seqlens ? 0 : T / C.N, (cudaStream_t)stream),
+                                        cu_seqlens ? 0 : T / C.N, granted, (cudaStream_t)stream),
                 "kda_cache_append");
 }
 
