@@ -694,7 +694,10 @@ kda_status kda_attn_prefill(const kda_attn_dims *dims, const kda_heads *q, const
  *
  * (the sums of dk and dv over the query heads of the group too).  P and dS are rounded to the
  * 16-bit type for the products (in sequences of up to 128 tokens what that leaves is a second
- * operand: twice the bits), sums are fp32, and none depends on timing.  An infinity or a
+ * operand: twice the bits), sums are fp32, and none depends on timing.  In fp16, which has few powers of
+ * two, both are rounded behind a power of two: P down to 2^-29 and dS down to 2^-27 of the largest
+ * |d_out_i| |v_j| of the row (dq) or of the rows that see the key (dk) keep all bits of the type, however
+ * large or small d_out and v are.  An infinity or a
  * NaN in a sequence may reach gradients of that sequence up to 127 tokens to either side of
  * where the formulas have it, and no other sequence's.
  *
@@ -703,7 +706,7 @@ kda_status kda_attn_prefill(const kda_attn_dims *dims, const kda_heads *q, const
  *   dq, dk, dv device, out_dtype, contiguous [T, H_q, d], [T, H_kv, d], [T, H_kv, d], 16-byte
  *              aligned.
  *   workspace  kda_attn_backward_workspace(dims) bytes, 16-byte aligned: two floats a token
- *              and query head.
+ *              and query head (fp16: three, and one a token and key head).
  */
 int64_t kda_attn_backward_workspace(const kda_attn_dims *dims);
 kda_status kda_attn_backward(const kda_attn_dims *dims, const kda_heads *q, const kda_heads *k,

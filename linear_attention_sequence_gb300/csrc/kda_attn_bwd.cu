@@ -23,6 +23,15 @@
 // them so; all sums are fp32.  A sequence of one tile (128 tokens) has few rows over which
 // that rounding averages out, and time to spare: what it leaves follows as a second operand, in the
 // columns of tensor memory that the 16-bit values leave free.
+//
+// fp16 has few powers of two: below 2^-14 its step is fixed, above 65504 it ends.  P and dS are therefore
+// stored times powers of two that the epilogues take back.  P <= 1 is stored as 2^15 P (folded into
+// lse log2 e).  |dS| <= 2 |d_out_i| max_j |v_j| (delta is d_out_i . out_i, and out_i a mean of values), so
+// that 2^15 over that bound is safe whatever the inputs: for a query block's row with the row's own |d_out_i|, for
+// a key block, whose sums run over the queries, with the largest |d_out_i| of the queries that see it.  The
+// delta kernel leaves the norms, and each block looks for the maxima it needs before its first step: four
+// bytes a token and head next to a step's 2,000 cycles.  (Maxima kept by atomics instead, and cleared by a
+// memset: 90 us for the 13 packed prompts, which take 57.4 us like this and took 53.3 unscaled.)
 #include <stddef.h>
 
 #include "kda_attn_plan.cuh"
@@ -41,7 +50,8 @@ struct Grads {
     const void *out, *d_out;
     int64_t o_t, o_h, do_t, do_h;
     void *dq, *dk, *dv;
-    float *delta, *lse2;     // [Hq][T]
+    float *delta, *lse2;     // [Hq][T]; fp16: lse log2(e) - kPLog2
+    float *y_norm, *v_norm;  // fp16: [Hq][T], |d_out|^2; [Hkv][T], |v|^2
     int64_t key_blocks;      // blocks below this one are key blocks
 };
 
@@ -55,6 +65,7 @@ struct Lay {
     static constexpr int kTiles = (2 + kA + kB) * kBytes;
 };
 constexpr int kStats = 2;   // steps of row statistics in flight
+constexpr float kPLog2 = 15.f, kPScale = 32768.f;   // fp16: P is stored times 2^15
 
 struct alignas(16) Control {
     uint64_t own_full, a_full[4], a_empty[4], b_full[4], b_empty[4], stat_full[kStats], stat_empty[kStats];
@@ -63,8 +74,18 @@ struct alignas(16) Control {
     AttnPart part;
     int64_t scan[kThreads / 32];
     alignas(16) float stat[kStats][2][kTile];   // read as float4
+    float most[2][8];   // fp16: each compute warp's largest |d_out|^2 and |v|^2
 };
 static_assert(offsetof(Control, stat) % 16 == 0 && alignof(Control) % 16 == 0, "vector reads of stat");
+
+// fp16: the power of two that dS is stored times, from |d_out|^2 and the largest |v|^2: with x their product,
+// 2 sqrt(x) times it is at most 2^15 (1 where there is nothing to scale, or an infinity or NaN, which stays one).
+__device__ __forceinline__ float range_scale(float dd, float vv) {
+    const float x = dd * vv;   // (2^-96 ... 2^79, or 0)
+    if (!(x > 0.f && x < INFINITY)) return 1.f;
+    const int half = ((int)(__float_as_uint(x) >> 23) - 127 + 2) >> 1;   // sqrt(x) < 2^half
+    return __uint_as_float((uint32_t)(14 - half + 127) << 23);
+}
 
 // delta and lse log2(e), head-major.  16 (8) lanes a row.
 template <int D, bool BF16>
@@ -74,7 +95,7 @@ __global__ void __launch_bounds__(256) kda_attn_delta_kernel(const Attn A, const
     const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LANES;
     const int c = threadIdx.x % LANES;
     const int64_t rows = (int64_t)A.T * A.Hq;
-    float sum = 0.f;
+    float sum = 0.f, dd = 0.f, vv = 0.f;
     const int64_t t = row / A.Hq, h = row - t * A.Hq;
     if (row < rows) {
         const uint4 x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(B.out) + t * B.o_t + h * B.o_h) + c);
@@ -86,15 +107,36 @@ __global__ void __launch_bounds__(256) kda_attn_delta_kernel(const Attn A, const
             unpack16<BF16>(xs[i], a, b);
             unpack16<BF16>(ys[i], e, f);
             sum = fmaf(a, e, fmaf(b, f, sum));
+            if (!BF16) dd = fmaf(e, e, fmaf(f, f, dd));
+        }
+        if (!BF16 && h % A.G == 0) {   // the key head's values once
+            const uint4 z = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(A.v) + t * A.v_t + h / A.G * A.v_h) + c);
+            const uint32_t zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float a, b;
+                unpack16<BF16>(zs[i], a, b);
+                vv = fmaf(a, a, fmaf(b, b, vv));
+            }
         }
     }
 #pragma unroll
-    for (int o = LANES / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = LANES / 2; o; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (!BF16) {
+            dd += __shfl_xor_sync(0xffffffffu, dd, o);
+            vv += __shfl_xor_sync(0xffffffffu, vv, o);
+        }
+    }
+    if (!BF16 && row < rows && c == 0) {
+        B.y_norm[h * A.T + t] = dd;
+        if (h % A.G == 0) B.v_norm[h / A.G * A.T + t] = vv;
+    }
     if (row < rows && c == 0) {
         B.delta[h * A.T + t] = sum;
         // a row that saw nothing has weights 0
         const float l = A.lse[row];
-        B.lse2[h * A.T + t] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
+        B.lse2[h * A.T + t] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f - (BF16 ? 0.f : kPLog2);
     }
 }
 
@@ -123,6 +165,27 @@ __device__ __forceinline__ void mma_sum(uint32_t d_tmem, uint32_t a_tmem, uint32
     for (int s = 0; s < 8; ++s)
         mma16_ts(d_tmem, a_tmem + (s >> 2) * 64 + (s & 3) * 8, sdesc_mn(b_saddr + s * 2048, Lay<D>::kBlock),
                  idesc_16(BF16, 128, D, true), more || s > 0);
+}
+
+// dP - delta; fp16: times the scale in `by`, which `minus` has already.
+template <bool BF16>
+__device__ __forceinline__ uint64_t less_delta(uint64_t dp, uint64_t by, uint64_t minus) {
+    return BF16 ? add2(dp, minus) : fma2(dp, by, minus);
+}
+
+// fp16: the largest norms, by the 256 threads of the compute warps.  An infinity or NaN counts for nothing: it reaches
+// what it reaches without a scale.
+__device__ __forceinline__ float larger(float most, float x) { return fmaxf(most, x < INFINITY ? x : 0.f); }
+__device__ __forceinline__ void leave(float most, float *place) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if ((threadIdx.x & 31) == 0) place[threadIdx.x >> 5] = most;
+}
+__device__ __forceinline__ float largest(const float *place) {
+    float most = place[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) most = fmaxf(most, place[i]);
+    return most;
 }
 
 // 64 fp32 columns of the thread's row.
@@ -223,6 +286,11 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
         for (int j = max(0, b - NB); j < b; ++j) wait(&ct.b_full[j % NB], j / NB);
     } else if (warp == kStatWarp) {
         asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernel in front writes delta and lse2
+        float by = 1.f;   // what dP - delta is multiplied by: P comes times kPScale
+        if (!BF16) {
+            sm100::named_sync(1, 288);   // the compute warps have looked
+            by = range_scale(largest(ct.most[0]), largest(ct.most[1])) / kPScale;
+        }
         for (int j = 0; j < n; ++j) {
             const int st = j % kStats;
             const int64_t h = hk * G + j / per, at = h * A.T + sq.a, row = (int64_t)(kt + j % per) * kTile + lane * 4;
@@ -230,7 +298,7 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[i] = row + i < len ? B.lse2[at + row + i] : INFINITY;
-                y[i] = row + i < len ? B.delta[at + row + i] : 0.f;
+                y[i] = row + i < len ? B.delta[at + row + i] * by : 0.f;
             }
             if (j >= kStats) ok = wait(&ct.stat_empty[st], j / kStats - 1);
             if (!ok) break;
@@ -297,6 +365,24 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const float c = A.scale_log2;
+        float scale = 1.f;
+        if (!BF16) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernel in front writes the norms
+            float y = 0.f, v = 0.f;
+            const float *ys = B.y_norm + (int64_t)hk * G * A.T + sq.a, *vs = B.v_norm + (int64_t)hk * A.T + sq.a;
+#pragma unroll 2
+            for (int i = threadIdx.x; i < len; i += 256) {
+                v = larger(v, vs[i]);
+                if (i >= kt * kTile)
+#pragma unroll 4
+                    for (int g = 0; g < G; ++g) y = larger(y, ys[(int64_t)g * A.T + i]);
+            }
+            leave(y, ct.most[0]);
+            leave(v, ct.most[1]);
+            sm100::named_sync(1, 288);
+            scale = range_scale(largest(ct.most[0]), largest(ct.most[1]));
+        }
+        const uint64_t by = pack2(scale / kPScale, scale / kPScale);
         for (int j = 0; j < n; ++j) {
             const int st = j % kStats, qt = kt + j % per;
             ok = wait(&ct.stat_full[st], j / kStats) && wait(&ct.s_full[0], j);
@@ -333,9 +419,11 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
                 const float4 d = d4[x];
-                unpack2(mul2(pack2(p[4 * x], p[4 * x + 1]), add2(pack2(dp[4 * x], dp[4 * x + 1]), pack2(-d.x, -d.y))),
+                unpack2(mul2(pack2(p[4 * x], p[4 * x + 1]),
+                             less_delta<BF16>(pack2(dp[4 * x], dp[4 * x + 1]), by, pack2(-d.x, -d.y))),
                         dp[4 * x], dp[4 * x + 1]);
-                unpack2(mul2(pack2(p[4 * x + 2], p[4 * x + 3]), add2(pack2(dp[4 * x + 2], dp[4 * x + 3]), pack2(-d.z, -d.w))),
+                unpack2(mul2(pack2(p[4 * x + 2], p[4 * x + 3]),
+                             less_delta<BF16>(pack2(dp[4 * x + 2], dp[4 * x + 3]), by, pack2(-d.z, -d.w))),
                         dp[4 * x + 2], dp[4 * x + 3]);
             }
             if (masked) {
@@ -354,9 +442,9 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
             const int64_t at = ((sq.a + kt * kTile + r) * A.Hkv + hk) * D;
             const bool live = kt * kTile + r < len, f32 = A.out_dtype == KDA_DTYPE_F32;
             if (half == 0)
-                write_row<D, BF16>(B.dv, f32, at, lanes + DV, 1.f, live);
+                write_row<D, BF16>(B.dv, f32, at, lanes + DV, BF16 ? 1.f : 1.f / kPScale, live);
             else
-                write_row<D, BF16>(B.dk, f32, at, lanes + DK, A.scale, live);
+                write_row<D, BF16>(B.dk, f32, at, lanes + DK, A.scale / scale, live);
         }
         sm100::tc_fence_before();
     }
@@ -450,8 +538,19 @@ __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const 
         const int64_t at = (int64_t)h * A.T + sq.a + qt * kTile + r;
         asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernel in front writes delta and lse2
         const float lse2 = live ? B.lse2[at] : INFINITY, delta = live ? B.delta[at] : 0.f;
+        float scale = 1.f, by = 1.f;
+        if (!BF16) {
+            float v = 0.f;
+            const float *vs = B.v_norm + (int64_t)hk * A.T + sq.a;
+#pragma unroll 4
+            for (int i = threadIdx.x; i < min(len, n * kTile); i += 256) v = larger(v, vs[i]);
+            leave(v, ct.most[1]);
+            sm100::named_sync(1, 256);
+            if (live) scale = range_scale(B.y_norm[at], largest(ct.most[1]));
+            by = scale / kPScale;
+        }
         const float c = A.scale_log2;
-        const uint64_t c2 = pack2(c, c), l2 = pack2(-lse2, -lse2), d2 = pack2(-delta, -delta);
+        const uint64_t c2 = pack2(c, c), l2 = pack2(-lse2, -lse2), d2 = pack2(-delta * by, -delta * by), by2 = pack2(by, by);
         for (int j = 0; j < n; ++j) {
             ok = wait(&ct.s_full[j & 1], j >> 1);
             if (!ok) break;
@@ -474,7 +573,7 @@ __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const 
             sm100::mbar_arrive(&ct.dp_free);
 #pragma unroll
             for (int x = 0; x < 64; x += 2)
-                unpack2(mul2(pack2(p[x], p[x + 1]), add2(pack2(dp[x], dp[x + 1]), d2)), dp[x], dp[x + 1]);
+                unpack2(mul2(pack2(p[x], p[x + 1]), less_delta<BF16>(pack2(dp[x], dp[x + 1]), by2, d2)), dp[x], dp[x + 1]);
             if (j == n - 1) {
 #pragma unroll
                 for (int x = 0; x < 64; ++x) dp[x] = x + half * 64 <= r ? dp[x] : 0.f;
@@ -488,7 +587,7 @@ __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const 
             sm100::tc_fence_after();
             write_row<D / 2, BF16>(B.dq, A.out_dtype == KDA_DTYPE_F32,
                                    ((sq.a + qt * kTile + r) * A.Hq + h) * D + half * (D / 2), lanes + DQ + half * (D / 2),
-                                   A.scale, live);
+                                   A.scale / scale, live);
         }
         sm100::tc_fence_before();
     }
@@ -600,7 +699,10 @@ cudaError_t backward(const Attn &A, Grads &B, cudaStream_t stream) {
 
 }  // namespace
 
-int64_t kda_attn_backward_ws(const Attn &A) { return (int64_t)A.T * A.Hq * 8; }
+int64_t kda_attn_backward_ws(const Attn &A) {
+    const int64_t rows = (int64_t)A.T * A.Hq;
+    return A.in_dtype == KDA_DTYPE_BF16 ? rows * 8 : rows * 12 + (int64_t)A.T * A.Hkv * 4;
+}
 
 cudaError_t kda_launch_attn_backward(const Attn &A, const AttnGrads &X, float *workspace, cudaStream_t stream) {
     Grads B{};
@@ -609,6 +711,8 @@ cudaError_t kda_launch_attn_backward(const Attn &A, const AttnGrads &X, float *w
     B.dq = X.dq, B.dk = X.dk, B.dv = X.dv;
     B.delta = workspace;
     B.lse2 = workspace + (int64_t)A.T * A.Hq;
+    B.y_norm = B.lse2 + (int64_t)A.T * A.Hq;
+    B.v_norm = B.y_norm + (int64_t)A.T * A.Hq;
     const bool b = A.in_dtype == KDA_DTYPE_BF16;
     if (A.d == 128) return b ? backward<128, true>(A, B, stream) : backward<128, false>(A, B, stream);
     return b ? backward<64, true>(A, B, stream) : backward<64, false>(A, B, stream);
