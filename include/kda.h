@@ -623,9 +623,9 @@ kda_status kda_ssm_scan_backward(const kda_ssm_dims *dims, const kda_ssm_inputs 
  *
  * Conventions: activations are 16-bit (bf16 or fp16, one type a call), products are
  * accumulated in fp32 on the tensor cores, maxima, sums and log-sums are fp32, and
- * the weights e^(s - max) are rounded to the 16-bit type for the product with v (in
- * kda_attn_paged not those of bf16 sequences of up to 16 rows, that is tokens times H_q / H_kv,
- * which are kept to 16 bits of mantissa).  Heads are
+ * the weights e^(s - max) are rounded to the 16-bit type for the product with v (fp16: times 2^11, so
+ * that weights down to 2^-25 of a row's largest keep all bits).  In kda_attn_paged those of sequences of
+ * up to 16 rows, that is tokens times H_q / H_kv, keep twice the bits of the type.  Heads are
  * given with strides (kda_heads), so that parts of a projection's rows need no copy.  Keys
  * and values that a row may not see never reach it, whatever they hold, as long as
  * they belong to another sequence or lie behind the cache's length; inside a sequence an

@@ -9,14 +9,16 @@
 // tile and row tile
 //
 //   S = Q K^T               tcgen05, fp32 in tensor memory
-//   P = 2^(c S - c m)       one thread a row: its 128 scores in registers, c = scale log2 e
+//   P = 2^(c S - c m + u)   one thread a row: its 128 scores in registers, c = scale log2 e
 //   O += P V                tcgen05, P 16 bits in tensor memory over the columns of S
 //
 // While one tile's softmax runs, the tensor cores work on the other's products.  m is the
 // running maximum of the row.  O and the running sum are rescaled only when the maximum
-// has grown by more than 2^8 (with less, P and the sums lose nothing in their types'
-// ranges): after the first tiles hardly ever, and it is the softmax threads themselves
-// that do it, between the products.  P is rounded to 16 bits because the tensor cores
+// has grown by more than 2^8 (fp16: 2^4), which bf16 and fp32 have the range for: after the first tiles
+// hardly ever, and it is the softmax threads themselves that do it, between the products.  fp16
+// ends at 2^16 and has a fixed step of 2^-24 below 2^-14, so that u = 11 there (bf16: 0): P is at most
+// 2^15, and the many small weights of a long prompt next to a large one are still there (with u = 0 what is
+// below 2^-25 of the largest would be counted in the sum and be missing in O).  P is rounded to 16 bits because the tensor cores
 // read it so (half a step of P's own value); sums, maxima and O are fp32.
 //
 // Keys that a row may not see get the score -inf by a select, and value rows behind a
@@ -47,7 +49,14 @@ __device__ unsigned g_attn_status;
 constexpr int kThreads = 384;      // two softmax warpgroups; products, loads, the search for work, one idle warp
 constexpr int kProductWarp = 8, kLoadWarp = 9, kWorkWarp = 10;
 constexpr int kTileRows = 256;
-constexpr float kGrowth = 8.f;     // log2 of the growth of a maximum that O is rescaled for
+// log2 of the growth of a maximum that O is rescaled for, and of what weights are stored times (see the top)
+template <bool BF16>
+constexpr float kGrowth = BF16 ? 8.f : 4.f;
+template <bool BF16>
+constexpr float kUp = BF16 ? 0.f : 11.f;
+// A sum of weights without that factor.
+template <bool BF16>
+__device__ __forceinline__ float plain_sum(float l) { return BF16 ? l : l * (1.f / 2048.f); }
 constexpr int kSMs = 152;
 constexpr int kRuns = 128;         // runs of sequences whose work is summed up
 
@@ -522,7 +531,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 #pragma unroll
                     for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], s[x + y]);
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                const bool grown = top > m && (top - m) * c > kGrowth;   // also from -inf
+                const bool grown = top > m && (top - m) * c > kGrowth<BF16>;   // also from -inf
                 if (j > 0 && __any_sync(0xffffffffu, grown)) {
                     // S of this tile is complete, and so, issued before it, is the product before
                     const float f = grown ? ex2((m - top) * c) : 1.f;
@@ -538,7 +547,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     sm100::tmem_wait_st();
                 }
                 if (grown) m = top;
-                const float shift = m == -INFINITY ? 0.f : -m * c;
+                const float shift = m == -INFINITY ? 0.f : kUp<BF16> - m * c;
                 const uint64_t s2 = pack2(shift, shift);
                 uint64_t sum[2] = {0, 0};
                 uint32_t p[64];
@@ -569,7 +578,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             // A row whose sum is 0 has seen no key (or scores of -inf only): out 0.  A sum that is
             // NaN reaches the row through 1 / l.
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-            const float lse = l > 0.f || l != l ? m * A.scale + logf(l) : -INFINITY;
+            const float lse = l > 0.f || l != l ? m * A.scale + logf(plain_sum<BF16>(l)) : -INFINITY;
             const bool share = PAGED && slot >= 0;
             const int64_t at = a + tok;
             const int h = head * G + g;
@@ -901,7 +910,7 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
             t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
         }
-        const bool g0 = t0 > m0 && (t0 - m0) * c > kGrowth, g1 = t1 > m1 && (t1 - m1) * c > kGrowth;
+        const bool g0 = t0 > m0 && (t0 - m0) * c > kGrowth<BF16>, g1 = t1 > m1 && (t1 - m1) * c > kGrowth<BF16>;
         if (__any_sync(0xffffffffu, g0 || g1)) {
             const float f0 = g0 ? ex2((m0 - t0) * c) : 1.f, f1 = g1 ? ex2((m1 - t1) * c) : 1.f;
             l0 *= f0;
@@ -911,7 +920,7 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
             for (int x = 0; x < D / 8; ++x) o[x][0] *= f0, o[x][1] *= f0, o[x][2] *= f1, o[x][3] *= f1;
         }
-        const float h0 = m0 == -INFINITY ? 0.f : -m0 * c, h1 = m1 == -INFINITY ? 0.f : -m1 * c;
+        const float h0 = m0 == -INFINITY ? 0.f : kUp<BF16> - m0 * c, h1 = m1 == -INFINITY ? 0.f : kUp<BF16> - m1 * c;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             s[t][0] = ex2(fmaf(s[t][0], c, h0));
@@ -923,16 +932,14 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         l1 += (s[0][2] + s[0][3]) + (s[1][2] + s[1][3]);
         const uint32_t pa[4] = {pack16<BF16>(s[0][0], s[0][1]), pack16<BF16>(s[0][2], s[0][3]),
                                 pack16<BF16>(s[1][0], s[1][1]), pack16<BF16>(s[1][2], s[1][3])};
-        // what bf16 leaves of a weight is a second operand: the products have time for it here, and the
-        // result then is as good as fp32 weights would make it (fp16 leaves an eighth of that)
+        // what the 16 bits leave of a weight is a second operand: the products have time for it here, and the
+        // result then is as good as fp32 weights would make it
         uint32_t rest[4];
-        if (BF16) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                float lo, hi;
-                unpack16<BF16>(pa[x], lo, hi);
-                rest[x] = pack16<BF16>(s[x >> 1][(x & 1) * 2] - lo, s[x >> 1][(x & 1) * 2 + 1] - hi);
-            }
+        for (int x = 0; x < 4; ++x) {
+            float lo, hi;
+            unpack16<BF16>(pa[x], lo, hi);
+            rest[x] = pack16<BF16>(s[x >> 1][(x & 1) * 2] - lo, s[x >> 1][(x & 1) * 2 + 1] - hi);
         }
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
@@ -941,10 +948,8 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             ldsm4_t(b, vb + (piece >> 3) * L::kBlock + vrow * 128 + (((piece & 7) ^ (vrow & 7)) << 4));
             mma16816<BF16>(o[2 * x], pa, b[0], b[1]);
             mma16816<BF16>(o[2 * x + 1], pa, b[2], b[3]);
-            if (BF16) {
-                mma16816<BF16>(o[2 * x], rest, b[0], b[1]);
-                mma16816<BF16>(o[2 * x + 1], rest, b[2], b[3]);
-            }
+            mma16816<BF16>(o[2 * x], rest, b[0], b[1]);
+            mma16816<BF16>(o[2 * x + 1], rest, b[2], b[3]);
         }
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(&ct.empty[st]);
@@ -991,7 +996,7 @@ kda_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             for (int y = 0; y < 4; ++y) sum += w[y] * all[(y * 16 + r) * D + ch + e];
             v[e] = none ? 0.f : sum * inv;
         }
-        const float lse = none ? -INFINITY : top * A.scale + logf(l);
+        const float lse = none ? -INFINITY : top * A.scale + logf(plain_sum<BF16>(l));
         if (part.slot >= 0) {
             store8<BF16>(sh.out, true, ((int64_t)part.slot * kFewRows + r) * D + ch, v);
             if (ch == 0) sh.lse[(int64_t)part.slot * kFewRows + r] = lse;

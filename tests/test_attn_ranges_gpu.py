@@ -1,5 +1,5 @@
-"""GPU tests of the gradients of softmax attention in fp16 over the range of its inputs: upstream gradients and
-values far from 1, rows of different size, weights of long prompts.
+"""GPU tests of softmax attention in fp16 over the range of its weights and of its gradients' inputs: small weights
+next to a large one, upstream gradients and values far from 1, rows of different size, weights of long prompts.
 
 Bounds: those of attn_reference.py for roundings, and instead of its allowance for small fp16 numbers (half a
 step of 2^-24 of each weight) what the documented powers of two leave: P is stored times 2^15, so that below
@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import linear_attention_sequence_gb300 as kda
-from attn_reference import U, backward as ref_backward, backward_bounds
+from attn_reference import U, backward as ref_backward, backward_bounds, rows, score_error
 from test_attn_gpu import DEV, F16, F32, cu_of, prompt_inputs, rnd, starts
 
 pytestmark = pytest.mark.gpu
@@ -145,3 +145,56 @@ def test_weights_of_a_long_prompt():
         off = (got[n][:, 0].double() - want[n]).abs()
         bad = ~(off <= tol)
         assert not bad.any(), (n, float((off / tol)[bad].max()), int(bad.sum()))
+
+
+# ------------------------------------------------------------------ the forward's weights
+
+def check_small_weights(out, lse, q, k, v, first, rest=False):
+    """out [t, H, d] and lse of tokens that see keys 0 .. first + i.  A weight is rounded by half a step, or by 2^-25 /
+    2^11 of a row's largest (the documented factor), which the sum of weights is at least; with `rest` what that leaves
+    follows as a second operand, and of it the same is left."""
+    want, wl, mag, most = rows(q, k, v, first, 1.0)
+    n, e = k.shape[0], score_error(most, q.shape[2])
+    tol = ((U[F16] ** 2 if rest else U[F16]) + 2 * e + (n / 8 + 64) * U[F32]) * mag + U[F32] * want.abs()
+    tol = tol + 2.0 ** -36 * v.double().abs().sum(0).repeat_interleave(q.shape[1] // v.shape[1], 0)
+    off = (out.double() - want).abs()
+    assert bool((off <= tol).all()), float((off / tol).max())
+    assert bool(((lse.double() - wl).abs() <= e + (n / 16 + 64) * U[F32] + 4 * U[F32] * wl.abs()).all())
+
+
+def one_and_many(n, d, seed):
+    """Keys of which the first has a score 17.40625 above all others: their weights are 2^-25.1 next to it; values that are 0
+    there, so that the result is what those weights give."""
+    k, v = torch.zeros(n, 1, d, device=DEV, dtype=F16), rnd(seed, F16, n, 1, d).abs()
+    k[0, 0, 0], v[0] = 17.40625, 0
+    return k, v
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_small_weights_of_a_prompt(d):
+    T = 32768
+    k, v = one_and_many(T, d, 70)
+    q = torch.zeros(T, 1, d, device=DEV, dtype=F16)
+    q[:, 0, 0] = 1
+    out, lse = kda.kda_attn_prefill(q, k, v, scale=1.0, out_dtype=F32, return_lse=True)
+    for a in (1000, T - 3):
+        check_small_weights(out[a:a + 3], lse[a:a + 3], q[a:a + 3], k[:a + 3], v[:a + 3], a)
+
+
+@pytest.mark.parametrize("new", [1, 20])
+@pytest.mark.parametrize("N", [1, 2500])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_small_weights_of_a_cache(d, N, new):
+    """One sequence, whose keys are split over blocks, and so many (of the same pages) that they are not."""
+    n, page = 16384, 128
+    k, v = one_and_many(n, d, 80)
+    kp, vp = (x.view(n // page, page, 1, d) for x in (k, v))
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV).expand(N, -1).contiguous()
+    lens = torch.full((N,), n, dtype=torch.int32, device=DEV)
+    q = torch.zeros(N * new, 1, d, device=DEV, dtype=F16)
+    q[:, 0, 0] = 1
+    out, lse = kda.kda_attn_paged(q, kp, vp, table, lens, scale=1.0, out_dtype=F32, return_lse=True)
+    for i in {0, N // 2, N - 1}:
+        part = slice(i * new, (i + 1) * new)
+        check_small_weights(out[part], lse[part], q[part], k, v, n - new, rest=new == 1)
+    assert kda.kda_get_last_device_error() == 0
