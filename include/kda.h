@@ -629,8 +629,9 @@ kda_status kda_ssm_scan_backward(const kda_ssm_dims *dims, const kda_ssm_inputs 
  * given with strides (kda_heads), so that parts of a projection's rows need no copy.  Keys
  * and values that a row may not see never reach it, whatever they hold, as long as
  * they belong to another sequence or lie behind the cache's length; inside a sequence an
- * infinity or a NaN in k or v reaches the tokens that see it and may reach up to 127
- * tokens before it.  Rows of an output that belong to no sequence are left as they were.
+ * infinity or a NaN in k or v reaches the tokens that see it, and one in v may reach up to 127
+ * tokens before it (in kda_attn_paged up to 382: the row tiles of a chunk end anywhere in a key tile, and
+ * the two of a block may share their walk over the keys).  Rows of an output that belong to no sequence are left as they were.
  * A malformed cu_seqlens, length or page table never causes an access out of bounds; what
  * a call then writes to its outputs is unspecified.
  * The calls allocate nothing and give the same bits every time; calls on different streams
