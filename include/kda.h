@@ -855,7 +855,8 @@ kda_status kda_cache_free(const kda_cache_dims *cache, int32_t num_seqs, int32_t
  * kda_cache_fork -- children[i] becomes a continuation of parents[i], i < count: it shares the
  * parent's full pages, and has a page of its own where the last is not full.  The children
  * are empty rows, all different, and none of them a parent; a parent may have many.  A
- * child for which no page is left stays empty, as does every later one that needs a page.
+ * child for which no page is left stays empty, as does every later one that needs a page.  A
+ * child that has pages is passed by and recorded in the device status word.
  *
  *   src, dst   int32 [count]: for every layer, page src[i] is to be copied to dst[i]
  *              (kda_cache_copy); -1 where there is nothing to copy.

@@ -248,6 +248,11 @@ __global__ void __launch_bounds__(256) kda_cache_free_kernel(const Cache C, cons
 // First a page for each child whose parent's last page is not full (one block; src and dst
 // are the pages to be copied), then the children's rows: a block each in a second kernel, or, where
 // they are few entries, a warp each in the first (a launch costs the host as much as the work).
+// What a child must be: an empty row (a row with pages would leave their counts behind).  The rows are
+// written after the last block has asked for its pages, so that a row's own answer holds throughout.
+__device__ __forceinline__ bool may_fork(const Cache &C, int parent, int child) {
+    return parent >= 0 && parent < C.N && child >= 0 && child < C.N && parent != child && C.table[(int64_t)child * C.wide] < 0;
+}
 __device__ __forceinline__ void fork_row(const Cache &C, int parent, int child, int own, int first, int step) {
     const int len = length_of(C, child), whole = len >> C.shift;
     const int32_t *from = C.table + (int64_t)parent * C.wide;
@@ -273,7 +278,7 @@ __global__ void __launch_bounds__(kBlock) kda_cache_fork_pages_kernel(const Cach
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     auto partial = [&](int m, int &parent, int &child, int &len) {
         parent = parents[m], child = children[m];
-        if (parent < 0 || parent >= C.N || child < 0 || child >= C.N || parent == child) {
+        if (!may_fork(C, parent, child)) {
             atomicOr(&g_cache_status, kCacheBadPage);
             return -1;
         }
@@ -314,7 +319,9 @@ __global__ void __launch_bounds__(kBlock) kda_cache_fork_pages_kernel(const Cach
     __syncthreads();
     for (int m = threadIdx.x >> 5; m < M; m += kBlock / 32) {
         parent = parents[m], child = children[m];
-        if (parent >= 0 && parent < C.N && child >= 0 && child < C.N && parent != child)
+        const bool may = may_fork(C, parent, child);
+        __syncwarp();   // (asked by all lanes before one writes)
+        if (may)
             fork_row(C, parent, child, dst[m], threadIdx.x & 31, 32);
     }
 }
@@ -322,7 +329,9 @@ __global__ void __launch_bounds__(256) kda_cache_fork_rows_kernel(const Cache C,
                                                                   const int32_t *dst) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int parent = parents[blockIdx.x], child = children[blockIdx.x];
-    if (parent < 0 || parent >= C.N || child < 0 || child >= C.N || parent == child) return;
+    const bool may = may_fork(C, parent, child);
+    __syncthreads();    // (asked by all threads before one writes)
+    if (!may) return;
     fork_row(C, parent, child, dst[blockIdx.x], threadIdx.x, 256);
 }
 
