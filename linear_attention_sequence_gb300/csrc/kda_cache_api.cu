@@ -161,8 +161,9 @@ kda_status kda_cache_free(const kda_cache_dims *cache, int32_t num_seqs, int32_t
     const kda_status st = check_cache(cache, num_seqs, page_refs, page_table, kv_lens, C);
     if (st != KDA_OK) return st;
     if (count < 0) return KDA_ERR_INVALID_ARGUMENT;
-    if (count == 0 || C.N == 0) return KDA_OK;
-    if (bad(page_refs) || bad(page_table) || bad(kv_lens) || bad(seqs) || misaligned(keep, 4)) return KDA_ERR_INVALID_ARGUMENT;
+    if (count == 0) return KDA_OK;
+    if (bad(page_refs) || (C.N > 0 && (bad(page_table) || bad(kv_lens))) || bad(seqs) || misaligned(keep, 4))
+        return KDA_ERR_INVALID_ARGUMENT;
     if (conflict({refs_of(C), table_of(C), lens_of(C)}, {{seqs, (size_t)count * 4}, {keep, keep ? (size_t)count * 4 : 0}}))
         return KDA_ERR_INVALID_ARGUMENT;
     return done(kda_launch_cache_free(C, count, seqs, keep, (cudaStream_t)stream), "kda_cache_free");
@@ -174,11 +175,12 @@ kda_status kda_cache_fork(const kda_cache_dims *cache, int32_t num_seqs, int32_t
     Cache C;
     const kda_status st = check_cache(cache, num_seqs, page_refs, page_table, kv_lens, C);
     if (st != KDA_OK) return st;
-    if (count < 0) return KDA_ERR_INVALID_ARGUMENT;
-    if (count == 0 || C.N == 0) return KDA_OK;
+    if (count < 0 || misaligned(missing, 4)) return KDA_ERR_INVALID_ARGUMENT;
+    if (count == 0)   // nothing was lacking
+        return missing ? done(cudaMemsetAsync(missing, 0, 4, (cudaStream_t)stream), "kda_cache_fork") : KDA_OK;
     const int64_t need = (int64_t)C.P * 4 + 16;
-    if (bad(page_refs) || bad(page_table) || bad(kv_lens) || bad(parents) || bad(children) || bad(src) || bad(dst) ||
-        misaligned(missing, 4) || !workspace || workspace_bytes < need || misaligned(workspace, 16))
+    if (bad(page_refs) || (C.N > 0 && (bad(page_table) || bad(kv_lens))) || bad(parents) || bad(children) || bad(src) || bad(dst) ||
+        !workspace || workspace_bytes < need || misaligned(workspace, 16))
         return KDA_ERR_INVALID_ARGUMENT;
     const size_t list = (size_t)count * 4;
     if (conflict({refs_of(C), table_of(C), lens_of(C), {src, list}, {dst, list}, {missing, 4}, {workspace, (size_t)need}},

@@ -33,3 +33,26 @@ def test_children_with_pages_are_passed_by(M, wide):
     kda.kda_cache_fork(*c.state, ints(parents), ints(children), 8)
     assert kda.kda_get_last_device_error() == INVALID
     assert all(torch.equal(a, b) for a, b in zip(before, c.state))
+
+
+def test_no_children_and_no_rows():
+    """Results are written where there is nothing to fork, and a cache without rows has no sequence to name."""
+    c = Both(9, 2, 4, 8)
+    c.reserve([9, 0])
+    missing = ints([-7])
+    src, dst = kda.kda_cache_fork(*c.state, ints([]), ints([]), 8, missing=missing)
+    assert missing.item() == 0 and src.shape == dst.shape == (0,)
+    kda.kda_cache_free(*c.state, ints([]), 8)
+    c.check()
+    assert kda.kda_get_last_device_error() == 0
+    for wide in (4, 3000):
+        none = (c.refs, torch.empty((0, wide), dtype=torch.int32, device="cuda"), ints([]))
+        src, dst, missing = ints([77] * 5), ints([77] * 5), ints([-7])
+        kda.kda_cache_fork(*none, ints([0, 1, -1, 2, 0]), ints([1, 0, 5, 3, 0]), 8, src=src, dst=dst, missing=missing)
+        assert kda.kda_get_last_device_error() == INVALID
+        assert src.tolist() == dst.tolist() == [-1] * 5 and missing.item() == 0
+    kda.kda_cache_free(*none, ints([3]), 8)
+    assert kda.kda_get_last_device_error() == INVALID
+    kda.kda_cache_reserve(*none, ints([]), 8, missing=missing.fill_(-7))
+    assert missing.item() == 0 and kda.kda_get_last_device_error() == 0
+    c.check()
