@@ -31,7 +31,8 @@
 // a key block, whose sums run over the queries, with the largest |d_out_i| of the queries that see it.  The
 // delta kernel leaves the norms, and each block looks for the maxima it needs before its first step: four
 // bytes a token and head next to a step's 2,000 cycles.  (Maxima kept by atomics instead, and cleared by a
-// memset: 90 us for the 13 packed prompts, which take 57.4 us like this and took 53.3 unscaled.)
+// memset: 90 us for the 13 packed prompts, which take 57.4 us like this and took 53.4 unscaled; 8192 tokens with 32 on 8
+// heads of 128 take 1,183 us and took 1,154.)
 #include <stddef.h>
 
 #include "kda_attn_plan.cuh"
@@ -175,7 +176,15 @@ __device__ __forceinline__ uint64_t less_delta(uint64_t dp, uint64_t by, uint64_
 
 // fp16: the largest norms, by the 256 threads of the compute warps.  An infinity or NaN counts for nothing: it reaches
 // what it reaches without a scale.
-__device__ __forceinline__ float larger(float most, float x) { return fmaxf(most, x < INFINITY ? x : 0.f); }
+__device__ __forceinline__ void look(const float *x, int n, float &most) {
+    for (int i = threadIdx.x; i < n; i += 8 * 256) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = i + e * 256 < n ? x[i + e * 256] : 0.f;   // in flight together
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = fmaxf(most, v[e] < INFINITY ? v[e] : 0.f);
+    }
+}
 __device__ __forceinline__ void leave(float most, float *place) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
@@ -369,14 +378,8 @@ __device__ void key_block(const CUtensorMap *qm, const CUtensorMap *km, const CU
         if (!BF16) {
             asm volatile("griddepcontrol.wait;" ::: "memory");   // the kernel in front writes the norms
             float y = 0.f, v = 0.f;
-            const float *ys = B.y_norm + (int64_t)hk * G * A.T + sq.a, *vs = B.v_norm + (int64_t)hk * A.T + sq.a;
-#pragma unroll 2
-            for (int i = threadIdx.x; i < len; i += 256) {
-                v = larger(v, vs[i]);
-                if (i >= kt * kTile)
-#pragma unroll 4
-                    for (int g = 0; g < G; ++g) y = larger(y, ys[(int64_t)g * A.T + i]);
-            }
+            for (int g = 0; g < G; ++g) look(B.y_norm + (int64_t)(hk * G + g) * A.T + sq.a + kt * kTile, len - kt * kTile, y);
+            look(B.v_norm + (int64_t)hk * A.T + sq.a, len, v);
             leave(y, ct.most[0]);
             leave(v, ct.most[1]);
             sm100::named_sync(1, 288);
@@ -541,9 +544,7 @@ __device__ void query_block(const CUtensorMap *qm, const CUtensorMap *km, const 
         float scale = 1.f, by = 1.f;
         if (!BF16) {
             float v = 0.f;
-            const float *vs = B.v_norm + (int64_t)hk * A.T + sq.a;
-#pragma unroll 4
-            for (int i = threadIdx.x; i < min(len, n * kTile); i += 256) v = larger(v, vs[i]);
+            look(B.v_norm + (int64_t)hk * A.T + sq.a, min(len, n * kTile), v);
             leave(v, ct.most[1]);
             sm100::named_sync(1, 256);
             if (live) scale = range_scale(B.y_norm[at], largest(ct.most[1]));
