@@ -640,8 +640,8 @@ kda_status kda_ssm_scan_backward(const kda_ssm_dims *dims, const kda_ssm_inputs 
  * Errors, before any launch: KDA_ERR_INVALID_ARGUMENT for a NULL or misaligned pointer that is
  * needed, a negative size, strides that are no multiple of 8 or fall below what they step over, an
  * overlap of an output with anything else, or a workspace too small; KDA_ERR_UNSUPPORTED for
- * other types, head dims and page sizes than named here, T H_q beyond 2^30, N H_q beyond 2^29,
- * N max_pages beyond 2^31 or max_pages page_size beyond 2^30.
+ * other types, head dims and page sizes than named here, T H_q from 2^30 on, N H_q from 2^29 on,
+ * max_pages page_size from 2^30 on, or (kda_cache_*) N max_pages from 2^31 on.
  */
 
 /* [T, H, head_dim] activations: head h of token t starts at data + t * token_stride +

@@ -145,7 +145,7 @@ def kda_cache_fork(page_refs, page_table, kv_lens, parents, children, page_size,
                    missing=None, stream=None):
     """children[i] (an empty row) becomes a continuation of parents[i] (both int32 [M]), in place
     (C entry point ``kda_cache_fork``): it shares the parent's full pages and has one of its
-    own where the last is not full.  Returns ``(src, dst)``, int32 [M]: the pages to copy with
+    own where the last is not full; a row that has pages is passed by.  Returns ``(src, dst)``, int32 [M]: the pages to copy with
     kda_cache_copy in every layer (-1: none)."""
     dev, N, cache, refs, table, lens = _state(page_refs, page_table, kv_lens, page_size)
     if parents is None or parents.dim() != 1:

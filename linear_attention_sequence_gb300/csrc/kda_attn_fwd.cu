@@ -26,10 +26,12 @@
 //
 // Prompts: a block a row tile, the longest of a sequence first.  (Blocks that stay and take the
 // next row tile as they come, by cancelling launches, were no faster: 354 us against 350 us for
-// 8192 tokens, 32 on 8 heads of 128.  These now take 340 us; at the sustained rate of the card's own
-// matrix product it would be 323 us.)  Chunks over a cache: few row tiles and a long
-// axis of keys, so that the keys of all row tiles are laid end to end and cut into as many
-// equal runs as there are SMs (512 tokens behind 32k: 277 -> 217 us); a warp finds the
+// 8192 tokens, 32 on 8 heads of 128.  These take 340 us by themselves and 360 in a row of calls; at the sustained
+// rate of the card's own matrix product it would be 323 us.)  A row tile's keys are not cut here, so that prompts of few row
+// tiles are as long as the longest: 8192 tokens take 93 us with one head, and 144 with 12 on one.
+// Chunks over a cache: few row tiles and a long axis of keys, so that the keys of all row tiles are laid end to end and cut into as many
+// equal runs as there are SMs (512 tokens behind 32k: 310 -> 203 us, with the registers and uniform values
+// of the softmax warps taken in the same step); a warp finds the
 // next piece of the block's run while the others are busy with this one, and a row tile that
 // is cut leaves shares, which a second kernel joins.
 //
@@ -324,7 +326,7 @@ kda_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 // The row tiles of a head read the same keys, each in blocks of their own: they should do so at
                 // about the same time, or HBM delivers every key once a row tile.  So a block begins
                 // with the piece that starts a row tile, and every piece with a multiple of the run
-                // (512 tokens behind 32k: 960 -> 142 MB from HBM, 203 -> 183 us).
+                // (512 tokens behind 32k: 960 -> 142 MB from HBM, 203 -> 183 us by itself; 195 in a row of calls).
                 const int64_t begin = (w.j0 + run - 1) / run * run;
                 const int32_t walk = max(w.n_of[0], w.n_of[1]);
                 if (begin > w.j0 && begin < w.j0 + walk) {

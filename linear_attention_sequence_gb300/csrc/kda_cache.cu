@@ -514,6 +514,11 @@ cudaError_t kda_launch_cache_free(const Cache &C, int M, const int32_t *seqs, co
 
 cudaError_t kda_launch_cache_fork(const Cache &C, int M, const int32_t *parents, const int32_t *children, int32_t *src,
                                   int32_t *dst, int32_t *missing, int32_t *list, cudaStream_t stream) {
+    // Few entries: the rows in the same launch.  That saves the host a launch, which is what a call by itself waits for
+    // (fork and free of 4 children by 64 entries and of 96 by 70: 19 us a pair against 22).  In a graph the
+    // device alone counts, and one block is slower from some 1,500 entries on: 5.9 us a pair against 6.7 for 1 by
+    // 64, 7.7 and 8.8 for 16 by 64, 10.3 and 9.5 for 96 by 70, 18.6 and 10.0 for 96 by 512, 16.4 and 9.9 for 512
+    // by 16.  The border lies where both lose little.
     const bool rows = (int64_t)M * C.wide <= 8 * kBlock;
     kda_cache_fork_pages_kernel<<<1, kBlock, 0, stream>>>(C, M, parents, children, src, dst, missing, list, rows);
     cudaError_t e = cudaGetLastError();
