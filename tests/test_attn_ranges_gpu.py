@@ -147,6 +147,34 @@ def test_weights_of_a_long_prompt():
         assert not bad.any(), (n, float((off / tol)[bad].max()), int(bad.sum()))
 
 
+def test_captured_with_inputs_of_other_sizes():
+    """One capture, replayed for d_out and v of other sizes: the scales are each replay's own."""
+    lens, H, Hkv, d = [300, 1, 77], 6, 2, 128
+    T, cu = sum(lens), cu_of(lens)
+    q, k, v = prompt_inputs(T, H, Hkv, d, F16, 90)
+    dy = rnd(93, F16, T, H, d)
+
+    def call(**kw):
+        out, lse = kda.kda_attn_prefill(q, k, v, cu, return_lse=True, **kw)
+        return [out, lse, *kda.kda_attn_backward(q, k, v, out, lse, dy, cu, grad_dtype=F32, **kw).values()]
+
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for ystd, vstd in ((2.0 ** -14, 1.0), (2.0 ** 8, 2.0 ** 5), (2.0 ** -3, 2.0 ** -14)):
+        dy.copy_(rnd(94, F16, T, H, d, std=ystd))
+        v.copy_(rnd(95, F16, T, Hkv, d, std=vstd))
+        graph.replay()
+        torch.cuda.synchronize()
+        own = torch.cuda.Stream()
+        own.wait_stream(torch.cuda.current_stream())
+        for want in (call(), call(stream=own)):
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        check(dict(zip(("dq", "dk", "dv"), got[2:])), q, k, v, got[0], got[1], dy, lens)
+
+
 # ------------------------------------------------------------------ the forward's weights
 
 def check_small_weights(out, lse, q, k, v, first, rest=False):

@@ -195,3 +195,19 @@ def test_many_sequences_are_granted():
         left -= need
         want.append(max(0, x) if left >= 0 or need == 0 else 0)
     assert granted == want == c.lens.tolist()
+
+
+def test_binding_refuses():
+    """What was granted: int32 [N], contiguous, on the cache's device."""
+    c = Cache(9, 3, 3, 8, 1, 64, BF16)
+    new, x = ints([1, 1, 1]), rnd(1, BF16, 3, 1, 64)
+    for bad in (ints([1, 1]), ints([1, 1, 1]).long(), ints([1] * 6)[::2], torch.ones(3, dtype=torch.int32)):
+        with pytest.raises((ValueError, kda.KdaError)):
+            kda.kda_cache_reserve(*c.state, new, 8, granted=bad)
+        with pytest.raises((ValueError, kda.KdaError)):
+            kda.kda_cache_append(x, x, c.kp, c.vp, c.table, c.lens, granted=bad)
+        with pytest.raises((ValueError, kda.KdaError)):
+            kda.kda_attn_paged(x, c.kp, c.vp, c.table, c.lens, granted=bad)
+    with pytest.raises(kda.KdaError):
+        kda.kda_cache_reserve(*c.state, new, 8, granted=new)
+    c.check()
